@@ -272,9 +272,6 @@ def _plain_conv_step(s):
     return [y.to(TYPES[c["out"]]), s["init"]]
 
 
-BLOCK = 64  # tokens whose decays and inputs the plain scan forms at once
-
-
 def _steps(s):
     """Step sizes after bias and softplus; 0 behind a sequence's end, where the state stays as it is."""
     raw = s["dt"].float() + s["dt_bias"]
@@ -283,36 +280,46 @@ def _steps(s):
     return raw, d if live is None else torch.where(live, d, 0.0)
 
 
-def _per_channel(s, m):
-    """(.., g, n) rows of the groups as (.., channels, n) in fp32."""
-    return m.float().repeat_interleave(s["case"]["channels"] // s["case"]["ngroups"], dim=-2)
+def _grouped(s, v):
+    """(b, L, channels) as (b, L, groups, channels of a group, 1), beside B and C as (b, L, groups, 1, states)."""
+    return v.unflatten(2, (s["case"]["ngroups"], -1))[..., None]
 
 
-def _plain_states(s, keep):
-    """All states of the scan, token by token; with ``keep`` stacked, else only C h of each token."""
+def _recur(decay, put, first):
+    """h_t = decay_t h_{t-1} + put_t along dim 1 from h = first, for all t at once: runs of about sqrt(L) tokens beside
+    each other, then the runs one after the other.  Overwrites both; returns every state."""
+    L = put.shape[1]
+    run = max(1, math.isqrt(L))
+    cuts = range(run, L, run)
+    for k in range(1, run):
+        put[:, k::run] += decay[:, k::run] * put[:, k - 1::run][:, :put[:, k::run].shape[1]]
+        decay[:, k::run] *= decay[:, k - 1::run][:, :decay[:, k::run].shape[1]]
+    h = first
+    for t in (0, *cuts):
+        put[:, t:t + run] += decay[:, t:t + run] * h[:, None]
+        h = put[:, min(t + run, L) - 1]
+    return put
+
+
+def _plain_states(s):
+    """Step sizes, x, the initial state and every state h_t, (b, L, groups, channels of a group, states)."""
     c = s["case"]
-    b, L, d, n = c["batch"], c["seqlen"], c["channels"], c["dstate"]
+    b, d, n, g = c["batch"], c["channels"], c["dstate"], c["ngroups"]
     _, step = _steps(s)
     x = s["x"].float()
-    h = s["init"].clone() if s["init"] is not None else x.new_zeros((b, d, n))
-    hs = x.new_empty((b, L, d, n)) if keep else None
-    y = x.new_empty((b, L, d))
-    for t0 in range(0, L, BLOCK):
-        at = slice(t0, min(t0 + BLOCK, L))
-        decay = torch.exp(step[:, at, :, None] * s["A"])
-        put = (step[:, at] * x[:, at])[..., None] * _per_channel(s, s["B"][:, at])
-        part = hs[:, at] if keep else x.new_empty(put.shape)
-        for k in range(put.shape[1]):
-            h = decay[:, k] * h + put[:, k]
-            part[:, k] = h
-        y[:, at] = (part * _per_channel(s, s["C"][:, at])).sum(-1)
-    return step, x, y, h, hs
+    first = s["init"].unflatten(1, (g, -1)) if s["init"] is not None else x.new_zeros((b, g, d // g, n))
+    decay = torch.exp(_grouped(s, step) * s["A"].unflatten(0, (g, -1)))
+    return step, x, first, _recur(decay, _grouped(s, step * x) * s["B"].float()[:, :, :, None], first)
+
+
+def _readout(s, hs):
+    return (hs * s["C"].float()[:, :, :, None]).sum(-1).flatten(2)
 
 
 def _plain_scan_fwd(s):
     c = s["case"]
-    _, x, y, h, _ = _plain_states(s, False)
-    y = y + s["D"] * x
+    _, x, _, hs = _plain_states(s)
+    y = _readout(s, hs) + s["D"] * x
     if s["z"] is not None:
         z = s["z"].float()
         y = y * z / (1 + torch.exp(-z))
@@ -320,13 +327,13 @@ def _plain_scan_fwd(s):
     if live is not None:
         y = torch.where(live, y, 0.0)
     y = y.to(TYPES[c["out"]])
-    return [y, h] if c["carry"] else [y]
+    return [y, hs[:, -1].flatten(1, 2)] if c["carry"] else [y]
 
 
 def _plain_scan_bwd(s):
     c = s["case"]
-    b, L, d, n, g = c["batch"], c["seqlen"], c["channels"], c["dstate"], c["ngroups"]
-    step, x, y, _, hs = _plain_states(s, True)
+    g = c["ngroups"]
+    step, x, first, hs = _plain_states(s)
     dy = s["dy"].float()
     live = _live(s)
     if live is not None:
@@ -335,56 +342,46 @@ def _plain_scan_bwd(s):
     if s["z"] is not None:
         z = s["z"].float()
         sig = 1 / (1 + torch.exp(-z))
-        got["dz"] = dy * (y + s["D"] * x) * sig * (1 + z * (1 - sig))
+        got["dz"] = dy * (_readout(s, hs) + s["D"] * x) * sig * (1 + z * (1 - sig))
         dy = dy * z * sig
-    got["dx"] = s["D"] * dy
-    got["ddt"] = torch.empty_like(x)
-    got["dB"], got["dC"] = x.new_empty((b, L, g, n)), x.new_empty((b, L, g, n))
-    dA = torch.zeros((d, n), dtype=torch.float64, device="cuda")
-    carry = s["dfinal"].clone() if s["dfinal"] is not None else x.new_zeros((b, d, n))
-    for t0 in reversed(range(0, L, BLOCK)):
-        at = slice(t0, min(t0 + BLOCK, L))
-        decay = torch.exp(step[:, at, :, None] * s["A"])
-        Bx, Cx = _per_channel(s, s["B"][:, at]), _per_channel(s, s["C"][:, at])
-        G = Cx * dy[:, at, :, None]
-        for k in reversed(range(G.shape[1])):
-            G[:, k] += carry
-            carry = decay[:, k] * G[:, k]
-        if t0 > 0:
-            before = hs[:, t0 - 1:at.stop - 1]
-        else:
-            first = s["init"] if s["init"] is not None else x.new_zeros((b, d, n))
-            before = torch.cat([first[:, None], hs[:, :at.stop - 1]], 1)
-        gB = (G * Bx).sum(-1)
-        q = G * decay * before
-        got["ddt"][:, at] = (q * s["A"]).sum(-1) + gB * x[:, at]
-        dA += (q * step[:, at, :, None]).sum((0, 1), dtype=torch.float64)
-        got["dx"][:, at] += gB * step[:, at]
-        put = G * (step[:, at] * x[:, at])[..., None]
-        got["dB"][:, at] = put.unflatten(2, (g, d // g)).sum(3)
-        got["dC"][:, at] = (hs[:, at] * dy[:, at, :, None]).unflatten(2, (g, d // g)).sum(3)
+    A = s["A"].unflatten(0, (g, -1))
+    decay = torch.exp(_grouped(s, step) * A)
+    # the state's gradient runs backwards: G_t = C_t dy_t + decay_{t+1} G_{t+1}
+    last = s["dfinal"].unflatten(1, (g, -1)) if s["dfinal"] is not None else torch.zeros_like(first)
+    after = torch.cat([torch.ones_like(decay[:, :1]), decay.flip(1)[:, :-1]], 1)
+    G = _recur(after, (_grouped(s, dy) * s["C"].float()[:, :, :, None]).flip(1), last).flip(1)
+    got["dC"] = (hs * _grouped(s, dy)).sum(3)
+    got["dB"] = (G * _grouped(s, step * x)).sum(3)
+    gB = (G * s["B"].float()[:, :, :, None]).sum(-1).flatten(2)
+    got["dx"] = gB * step + s["D"] * dy
+    G *= decay
+    if c["carry"]:
+        got["d_initial_states"] = G[:, 0].flatten(1, 2).clone()
+    # times the state before each token: the gradient of decay_t, as one of the exponent
+    G[:, 1:] *= hs[:, :-1]
+    G[:, 0] *= first
     raw, _ = _steps(s)
-    got["ddt"] = got["ddt"] / (1 + torch.exp(-raw))
-    if live is not None:
-        got["ddt"] = torch.where(live, got["ddt"], 0.0)
-    got["dA"] = dA.float()
+    ddt = ((G * A).sum(-1).flatten(2) + gB * x) / (1 + torch.exp(-raw))
+    got["ddt"] = ddt if live is None else torch.where(live, ddt, 0.0)
+    got["dA"] = (G * _grouped(s, step)).sum((0, 1), dtype=torch.float64).flatten(0, 1).float()
     got["dD"] = (dy * x).sum((0, 1), dtype=torch.float64).float()
     got["ddt_bias"] = got["ddt"].sum((0, 1), dtype=torch.float64).float()
-    if c["carry"]:
-        got["d_initial_states"] = carry
     return got
 
 
 def _plain_scan_step(s):
     c = s["case"]
+    g = c["ngroups"]
     _, step = _steps(s)
     x = s["x"].float()
-    h = torch.exp(step[..., None] * s["A"]) * s["init"] + (step * x)[..., None] * _per_channel(s, s["B"])
-    y = (h * _per_channel(s, s["C"])).sum(-1) + s["D"] * x
+    decay = torch.exp(step[..., None] * s["A"]).unflatten(1, (g, -1))
+    put = (step * x).unflatten(1, (g, -1))[..., None] * s["B"].float()[:, :, None]
+    h = decay * s["init"].unflatten(1, (g, -1)) + put
+    y = (h * s["C"].float()[:, :, None]).sum(-1).flatten(1) + s["D"] * x
     if s["z"] is not None:
         z = s["z"].float()
         y = y * z / (1 + torch.exp(-z))
-    s["init"].copy_(h)
+    s["init"].copy_(h.flatten(1, 2))
     return [y.to(TYPES[c["out"]]), s["init"]]
 
 
