@@ -393,6 +393,167 @@ ssd_status ssd_chunk_scan_bwd_saved(const ssd_shape *shape,
                                     void *workspace, size_t workspace_bytes, void *stream,
                                     void *const *stage_events);
 
+/* ---------------------------------------------------------------------------
+ * The short causal convolution and the selective scan
+ *
+ * Two operators of the layers around and beside the chunked scan: the
+ * depthwise convolution that a layer applies to x, B and C before its scan,
+ * and the scan whose decay differs by channel and state (the chunked scan's
+ * decay is one number per head).  Each has a forward pass over prompts, a
+ * backward pass and a one-token step.  The conventions above hold, except:
+ * - Inputs with one row per token (x, dt, B, C, z, dy) may be strided, as
+ *   column slices of a wider projection are: an ssd_stride gives the elements
+ *   between batch entries and between tokens, {0, 0} meaning dense.  Within a
+ *   row the elements are contiguous.  row must be at least the row's length
+ *   when seqlen > 1; batch may be anything >= 0 (0 with a nonzero row: one
+ *   sequence read by the whole batch).  Outputs and states are dense.
+ * - Pointers need their element type's alignment only; 16-byte aligned
+ *   operands whose channels and strides are multiples of 16 bytes run on
+ *   wider loads.
+ * - lengths: device int32 (batch) or NULL.  Sequence b has
+ *   min(max(lengths[b], 0), seqlen) tokens (NULL: seqlen).  Rows behind a
+ *   sequence's end are not read; they are written as 0 in y and in the
+ *   gradients.  The final state is the state after the sequence's last token
+ *   (its initial state when it has none).
+ * - Sums over tokens and channels use fixed orders and no atomics: the same
+ *   call gives the same bits.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int64_t batch, row;
+} ssd_stride;
+
+typedef enum { SSD_ACT_NONE = 0, SSD_ACT_SILU = 1 } ssd_activation;
+
+/* Short causal convolution, one filter per channel:
+ *     p_t = bias + sum_{k < width} weight[k] x_{t - width + 1 + k},  y_t = act(p_t)
+ * with x before the first token taken from the initial state (or 0), and
+ * act(p) = p or p / (1 + exp(-p)) (SiLU). */
+typedef struct {
+    int64_t batch, seqlen; /* >= 0 */
+    int64_t channels;      /* >= 1 */
+    int32_t width;         /* taps: 2, 3 or 4 */
+    int32_t activation;    /* ssd_activation */
+    int32_t dtype;         /* ssd_dtype of x and of the states */
+    int32_t y_dtype;       /* ssd_dtype of y and dy: SSD_DTYPE_F32 or dtype */
+    int32_t dx_dtype;      /* ssd_dtype of dx: SSD_DTYPE_F32 or dtype (backward only) */
+    int32_t reserved;      /* must be 0 */
+    ssd_stride x, dy;      /* (dy: backward only) */
+} ssd_conv_shape;
+
+/* Forward pass over prompts.
+ *   x               (batch, seqlen, channels) dtype, shape->x strides
+ *   weight          (channels, width) fp32; weight[c][width - 1] meets x_t
+ *   bias            (channels) fp32, NULL => 0
+ *   initial_states  (batch, width - 1, channels) dtype, the inputs before the
+ *                   first token, oldest first; NULL => 0
+ *   lengths         see above
+ *   y               (batch, seqlen, channels) y_dtype, out
+ *   final_states    as initial_states, out, NULL => not written; may be the
+ *                   very buffer of initial_states
+ * y must not overlap an input or final_states. */
+ssd_status ssd_causal_conv_fwd(const ssd_conv_shape *shape, const void *x, const float *weight, const float *bias,
+                               const void *initial_states, const int32_t *lengths, void *y, void *final_states,
+                               void *stream);
+/* Gradients through ssd_causal_conv_fwd; x, weight, bias, initial_states and
+ * lengths as passed there.
+ *   dy                (batch, seqlen, channels) y_dtype, shape->dy strides
+ *   d_final_states    (batch, width - 1, channels) fp32, NULL => 0
+ *   dx                (batch, seqlen, channels) dx_dtype, out
+ *   dweight, dbias    (channels, width), (channels) fp32, out, summed over
+ *                     batch and tokens; dbias NULL => not written
+ *   d_initial_states  (batch, width - 1, channels) fp32, out, NULL => not
+ *                     written
+ *   workspace         256-byte aligned, at least
+ *                     ssd_causal_conv_bwd_workspace_size(shape) bytes (0 for
+ *                     an invalid shape)
+ * No output may overlap an input, the workspace or another output. */
+size_t ssd_causal_conv_bwd_workspace_size(const ssd_conv_shape *shape);
+ssd_status ssd_causal_conv_bwd(const ssd_conv_shape *shape, const void *x, const float *weight, const float *bias,
+                               const void *initial_states, const int32_t *lengths, const void *dy,
+                               const float *d_final_states, void *dx, float *dweight, float *dbias,
+                               float *d_initial_states, void *workspace, size_t workspace_bytes, void *stream);
+/* One token per sequence (shape->seqlen must be 1; x rows by shape->x.batch,
+ * both 0 => dense): y as above with the state's rows before x, and the state
+ * shifted by one row with x as its last.
+ *   x      (batch, channels) dtype
+ *   state  (batch, width - 1, channels) dtype, read and updated in place
+ *   y      (batch, channels) y_dtype, out
+ * y and state must not overlap each other or an input. */
+ssd_status ssd_causal_conv_step(const ssd_conv_shape *shape, const void *x, const float *weight, const float *bias,
+                                void *state, void *y, void *stream);
+
+/* Selective scan: for every channel c (of group g = c / (channels / ngroups))
+ * and state n,
+ *     d_t = softplus(dt_t + dt_bias)            (or dt_t + dt_bias)
+ *     h_t = exp(d_t A[c][n]) h_{t-1} + d_t x_t B_t[g][n]
+ *     y_t = (sum_n C_t[g][n] h_t + D x_t) * z_t / (1 + exp(-z_t))
+ * where the last factor stands only if z is given. */
+enum { SSD_SCAN_DT_SOFTPLUS = 1u };
+typedef struct {
+    int64_t batch, seqlen; /* >= 0 */
+    int64_t channels;      /* >= 1 */
+    int64_t dstate;        /* 1 .. 64 */
+    int64_t ngroups;       /* >= 1, divides channels; channels share B/C contiguously */
+    int32_t dtype;         /* ssd_dtype of x, dt, B, C, z */
+    int32_t y_dtype;       /* ssd_dtype of y and dy: SSD_DTYPE_F32 or dtype */
+    uint32_t flags;        /* SSD_SCAN_DT_SOFTPLUS or 0 */
+    int32_t reserved;      /* must be 0 */
+    ssd_stride x, dt, B, C, z, dy; /* (dy: backward only) */
+} ssd_selective_shape;
+
+/* Forward pass over prompts.
+ *   x, dt, z         (batch, seqlen, channels) dtype; z NULL => no gate
+ *   A                (channels, dstate) fp32, <= 0
+ *   B, C             (batch, seqlen, ngroups, dstate) dtype
+ *   D, dt_bias       (channels) fp32, NULL => 0
+ *   initial_states   (batch, channels, dstate) fp32, NULL => 0
+ *   lengths          see above
+ *   y                (batch, seqlen, channels) y_dtype, out
+ *   final_states     as initial_states, out, NULL => not written; may be the
+ *                    very buffer of initial_states
+ *   workspace        256-byte aligned, at least
+ *                    ssd_selective_scan_fwd_workspace_size(shape) bytes (which
+ *                    may be 0; also 0 for an invalid shape)
+ * Without the softplus flag d_t >= 0 is the caller's part, as A <= 0 is.
+ * Time is cut into segments run beside each other where batch and channels
+ * alone would leave compute units idle. */
+size_t ssd_selective_scan_fwd_workspace_size(const ssd_selective_shape *shape);
+ssd_status ssd_selective_scan_fwd(const ssd_selective_shape *shape, const void *x, const void *dt, const float *A,
+                                  const void *B, const void *C, const float *D, const void *z, const float *dt_bias,
+                                  const float *initial_states, const int32_t *lengths, void *y, float *final_states,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+/* Gradients through ssd_selective_scan_fwd; inputs as passed there.
+ *   dy                (batch, seqlen, channels) y_dtype, shape->dy strides
+ *   d_final_states    (batch, channels, dstate) fp32, NULL => 0
+ * Outputs, all fp32 and written (not accumulated):
+ *   dx, ddt           (batch, seqlen, channels)
+ *   dA                (channels, dstate)      summed over batch and tokens
+ *   dB, dC            (batch, seqlen, ngroups, dstate), summed over the
+ *                     channels of each group
+ *   dD, ddt_bias      (channels), each NULL => not written (dD as if D were
+ *                     given when it is NULL, ddt_bias likewise)
+ *   dz                (batch, seqlen, channels); required with z, else NULL
+ *   d_initial_states  (batch, channels, dstate), NULL => not written
+ *   workspace         256-byte aligned, at least
+ *                     ssd_selective_scan_bwd_workspace_size(shape) bytes
+ * No output may overlap an input, the workspace or another output. */
+size_t ssd_selective_scan_bwd_workspace_size(const ssd_selective_shape *shape);
+ssd_status ssd_selective_scan_bwd(const ssd_selective_shape *shape, const void *x, const void *dt, const float *A,
+                                  const void *B, const void *C, const float *D, const void *z, const float *dt_bias,
+                                  const float *initial_states, const int32_t *lengths, const void *dy,
+                                  const float *d_final_states, float *dx, float *ddt, float *dA, float *dB, float *dC,
+                                  float *dD, float *dz, float *ddt_bias, float *d_initial_states, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+/* One token per sequence (shape->seqlen must be 1; rows by the strides' batch).
+ *   x, dt, z   (batch, channels) dtype; z NULL => no gate
+ *   B, C       (batch, ngroups, dstate) dtype
+ *   state      (batch, channels, dstate) fp32, read and updated in place
+ *   y          (batch, channels) y_dtype, out
+ * y and state must not overlap each other or an input. */
+ssd_status ssd_selective_scan_step(const ssd_selective_shape *shape, const void *x, const void *dt, const float *A,
+                                   const void *B, const void *C, const float *D, const void *z, const float *dt_bias,
+                                   float *state, void *y, void *stream);
+
 /* Static, human-readable description of a status code. */
 const char *ssd_status_string(ssd_status status);
 

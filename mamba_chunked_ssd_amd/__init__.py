@@ -53,6 +53,15 @@ EXPORTS = [
     "ssd_chunk_scan_bwd",
     "ssd_chunk_scan_bwd_profiled",
     "ssd_chunk_scan_bwd_saved",
+    "ssd_causal_conv_fwd",
+    "ssd_causal_conv_bwd_workspace_size",
+    "ssd_causal_conv_bwd",
+    "ssd_causal_conv_step",
+    "ssd_selective_scan_fwd_workspace_size",
+    "ssd_selective_scan_fwd",
+    "ssd_selective_scan_bwd_workspace_size",
+    "ssd_selective_scan_bwd",
+    "ssd_selective_scan_step",
     "ssd_status_string",
     "ssd_version",
 ]
@@ -94,6 +103,52 @@ class WorkspaceLayout(ctypes.Structure):
         ("total", ctypes.c_size_t),
         ("nchunks", ctypes.c_int64),
         ("padded_len", ctypes.c_int64),
+    ]
+
+
+class Stride(ctypes.Structure):
+    """ssd_stride: elements between batch entries and between tokens ({0, 0}: dense)."""
+    _fields_ = [("batch", ctypes.c_int64), ("row", ctypes.c_int64)]
+
+
+SSD_ACT_NONE = 0
+SSD_ACT_SILU = 1
+SSD_SCAN_DT_SOFTPLUS = 1
+
+
+class ConvShape(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("seqlen", ctypes.c_int64),
+        ("channels", ctypes.c_int64),
+        ("width", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("y_dtype", ctypes.c_int32),
+        ("dx_dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("x", Stride),
+        ("dy", Stride),
+    ]
+
+
+class SelectiveShape(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("seqlen", ctypes.c_int64),
+        ("channels", ctypes.c_int64),
+        ("dstate", ctypes.c_int64),
+        ("ngroups", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("y_dtype", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
+        ("reserved", ctypes.c_int32),
+        ("x", Stride),
+        ("dt", Stride),
+        ("B", Stride),
+        ("C", Stride),
+        ("z", Stride),
+        ("dy", Stride),
     ]
 
 
@@ -176,6 +231,21 @@ def load_library(path: str | None = None):
         lib.ssd_chunk_scan_bwd_saved.argtypes = bwd_args[:11] + [vp, sz] + bwd_args[11:] + [
             ctypes.POINTER(ctypes.c_void_p)]
         lib.ssd_chunk_scan_bwd_saved.restype = ctypes.c_int
+        cp, xp = ctypes.POINTER(ConvShape), ctypes.POINTER(SelectiveShape)
+        lib.ssd_causal_conv_fwd.argtypes = [cp] + [vp] * 8
+        lib.ssd_causal_conv_bwd_workspace_size.argtypes = [cp]
+        lib.ssd_causal_conv_bwd.argtypes = [cp] + [vp] * 12 + [sz, vp]
+        lib.ssd_causal_conv_step.argtypes = [cp] + [vp] * 6
+        lib.ssd_selective_scan_fwd_workspace_size.argtypes = [xp]
+        lib.ssd_selective_scan_fwd.argtypes = [xp] + [vp] * 13 + [sz, vp]
+        lib.ssd_selective_scan_bwd_workspace_size.argtypes = [xp]
+        lib.ssd_selective_scan_bwd.argtypes = [xp] + [vp] * 22 + [sz, vp]
+        lib.ssd_selective_scan_step.argtypes = [xp] + [vp] * 11
+        for name in ("causal_conv_bwd", "selective_scan_fwd", "selective_scan_bwd"):
+            getattr(lib, "ssd_%s_workspace_size" % name).restype = sz
+        for name in ("causal_conv_fwd", "causal_conv_bwd", "causal_conv_step", "selective_scan_fwd",
+                     "selective_scan_bwd", "selective_scan_step"):
+            getattr(lib, "ssd_" + name).restype = ctypes.c_int
         lib.ssd_status_string.argtypes = [ctypes.c_int]
         lib.ssd_status_string.restype = ctypes.c_char_p
         lib.ssd_version.argtypes = []
@@ -527,3 +597,342 @@ def tune(x, dt, A, B, C, D=None, chunk_size: int = 256, initial_states=None, *, 
     if st != 0:
         raise SSDError(st, "ssd_chunk_scan_fwd_tune")
     return plan, float(us.value)
+
+
+# ---------------------------------------------------------------------------
+# The short causal convolution and the selective scan
+# ---------------------------------------------------------------------------
+
+_ACTIVATIONS = {None: SSD_ACT_NONE, "silu": SSD_ACT_SILU}
+
+
+def _storage(t, name):
+    """dtype code of an operator's first input, which its other inputs share."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.device.type != "cuda":
+        raise ValueError("tensors must be on a ROCm device (got %s)" % t.device)
+    if t.dtype == torch.bfloat16:
+        return SSD_DTYPE_BF16
+    if t.dtype == torch.float32:
+        return SSD_DTYPE_F32
+    raise TypeError("%s must be float32 or bfloat16" % name)
+
+
+def _result_dtype(dtype, given, name):
+    torch = _torch()
+    if dtype is None or dtype == torch.float32:
+        return torch.float32, SSD_DTYPE_F32
+    if dtype != given:
+        raise TypeError("%s must be float32 or the input dtype" % name)
+    return dtype, SSD_DTYPE_BF16
+
+
+def _rows(t, name, dtype, shape, device, tokens=True):
+    """Checks an input of one row per token (or, without ``tokens``, per batch
+    entry), whose rows may lie apart, and returns its ssd_stride."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.dtype != dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.is_contiguous():
+        return 0, 0
+    st = t.stride()
+    lead = 2 if tokens else 1
+    width = 1
+    for k in range(t.dim() - 1, lead - 1, -1):
+        if shape[k] != 1 and st[k] != width:
+            raise ValueError("%s: each row must be contiguous (strides %s)" % (name, st))
+        width *= shape[k]
+    row = st[1] if tokens and shape[1] > 1 else width
+    if tokens and shape[1] > 1 and row < width:
+        raise ValueError("%s: rows of different tokens overlap (strides %s)" % (name, st))
+    return (st[0] if shape[0] > 1 else row * (shape[1] if tokens else 1)), row
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(where, device, stream, run):
+    """``run(stream handle)`` with ``device`` current; what it
+    allocates belongs to the stream that the kernels run on."""
+    torch = _torch()
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _call(where, device, stream, run)
+    if stream is None:
+        st, res = run(torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+            st, res = run(stream)
+    if st != 0:
+        raise SSDError(st, where)
+    return res
+
+
+def _workspace(given, need, device):
+    """(address, bytes) of the caller's workspace or of a new one (kept by the third value)."""
+    torch = _torch()
+    if given is not None:
+        if given.device != device or not given.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on %s" % device)
+        return given.data_ptr(), given.numel() * given.element_size(), given
+    if need == 0:
+        return None, 0, None
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    return ws.data_ptr(), need, ws
+
+
+def _conv_args(x, weight, bias, lengths, activation, tokens):
+    torch = _torch()
+    code = _storage(x, "x")
+    if x.dim() != (3 if tokens else 2) or weight.dim() != 2:
+        raise ValueError("x must be (batch, %schannels) and weight (channels, width)" % ("seqlen, " if tokens else ""))
+    if activation not in _ACTIVATIONS:
+        raise ValueError("activation must be None or 'silu'")
+    dev = x.device
+    b, c, w = x.shape[0], x.shape[-1], weight.shape[1]
+    L = x.shape[1] if tokens else 1
+    xs = _rows(x, "x", x.dtype, x.shape, dev, tokens)
+    _check(weight, "weight", torch.float32, (c, w), dev)
+    if bias is not None:
+        _check(bias, "bias", torch.float32, (c,), dev)
+    if lengths is not None:
+        _check(lengths, "lengths", torch.int32, (b,), dev)
+    shape = ConvShape(b, L, c, w, _ACTIVATIONS[activation], code, 0, 0, 0, Stride(*xs), Stride(0, 0))
+    return shape, dev, b, L, c, w
+
+
+def causal_conv_fwd(x, weight, bias=None, initial_states=None, return_final_states: bool = False, *,
+                    activation="silu", lengths=None, y_dtype=None, out=None, final_out=None, stream=None):
+    """Short causal convolution over prompts (``ssd_causal_conv_fwd``):
+    y_t = act(bias + sum_k weight[:, k] x_{t - width + 1 + k}), per channel.
+
+    x (b, L, c): float32 or bfloat16, rows may lie apart (a column slice of a
+    wider tensor); weight (c, width), width 2..4, and bias (c,): float32;
+    ``initial_states`` (b, width - 1, c), the inputs before the first token, in
+    x's dtype.  ``activation``: "silu" or None.  ``lengths``: int32 (b,) device
+    tensor, tokens of each padded sequence; rows behind are 0 in y.  Returns y
+    (``y_dtype``: float32, the default, or x's dtype), or (y, final_states);
+    ``final_out`` may be ``initial_states`` itself.
+    """
+    torch = _torch()
+    shape, dev, b, L, c, w = _conv_args(x, weight, bias, lengths, activation, True)
+    if initial_states is not None:
+        _check(initial_states, "initial_states", x.dtype, (b, w - 1, c), dev)
+    ytype, shape.y_dtype = _result_dtype(y_dtype, x.dtype, "y_dtype")
+    if out is not None:
+        _check(out, "out", ytype, (b, L, c), dev)
+    if final_out is not None:
+        _check(final_out, "final_out", x.dtype, (b, w - 1, c), dev)
+
+    def run(handle):
+        y = out if out is not None else torch.empty((b, L, c), dtype=ytype, device=dev)
+        fin = final_out
+        if fin is None and return_final_states:
+            fin = torch.empty((b, max(w - 1, 0), c), dtype=x.dtype, device=dev)
+        st = load_library().ssd_causal_conv_fwd(ctypes.byref(shape), x.data_ptr(), weight.data_ptr(), _addr(bias),
+                                                _addr(initial_states), _addr(lengths), y.data_ptr(), _addr(fin),
+                                                handle)
+        return st, (y, fin) if return_final_states else y
+
+    return _call("ssd_causal_conv_fwd", dev, stream, run)
+
+
+def causal_conv_bwd(x, weight, bias, dy, initial_states=None, d_final_states=None, *, activation="silu",
+                    lengths=None, dx_dtype=None, want_d_initial: bool = True, workspace=None, stream=None):
+    """Gradients through :func:`causal_conv_fwd` (``ssd_causal_conv_bwd``).
+
+    Inputs as passed there, plus ``dy`` (b, L, c) (float32 or x's dtype, rows
+    may lie apart) and optionally ``d_final_states`` (b, width - 1, c) float32.
+    Returns a dict of ``dx`` (``dx_dtype``: float32, the default, or x's
+    dtype), ``dweight``, ``dbias`` and, when requested, ``d_initial_states``
+    (float32).
+    """
+    torch = _torch()
+    lib = load_library()
+    shape, dev, b, L, c, w = _conv_args(x, weight, bias, lengths, activation, True)
+    if initial_states is not None:
+        _check(initial_states, "initial_states", x.dtype, (b, w - 1, c), dev)
+    if d_final_states is not None:
+        _check(d_final_states, "d_final_states", torch.float32, (b, w - 1, c), dev)
+    dytype, shape.y_dtype = _result_dtype(dy.dtype, x.dtype, "dy's dtype")
+    shape.dy = Stride(*_rows(dy, "dy", dytype, x.shape, dev))
+    dxtype, shape.dx_dtype = _result_dtype(dx_dtype, x.dtype, "dx_dtype")
+
+    def run(handle):
+        f32 = dict(dtype=torch.float32, device=dev)
+        res = {"dx": torch.empty((b, L, c), dtype=dxtype, device=dev), "dweight": torch.empty((c, w), **f32),
+               "dbias": torch.empty((c,), **f32)}
+        if want_d_initial:
+            res["d_initial_states"] = torch.empty((b, max(w - 1, 0), c), **f32)
+        ws, size, _keep = _workspace(workspace, lib.ssd_causal_conv_bwd_workspace_size(ctypes.byref(shape)), dev)
+        st = lib.ssd_causal_conv_bwd(ctypes.byref(shape), x.data_ptr(), weight.data_ptr(), _addr(bias),
+                                     _addr(initial_states), _addr(lengths), dy.data_ptr(), _addr(d_final_states),
+                                     res["dx"].data_ptr(), res["dweight"].data_ptr(), res["dbias"].data_ptr(),
+                                     _addr(res.get("d_initial_states")), ws, size, handle)
+        return st, res
+
+    return _call("ssd_causal_conv_bwd", dev, stream, run)
+
+
+def causal_conv_step(x, weight, bias, state, *, activation="silu", y_dtype=None, out=None, stream=None):
+    """The convolution for one new token per sequence (``ssd_causal_conv_step``).
+
+    x (b, c); ``state`` (b, width - 1, c) in x's dtype, the inputs before it,
+    updated in place.  Returns y (b, c) (``y_dtype``: float32, the default, or
+    x's dtype).
+    """
+    torch = _torch()
+    shape, dev, b, _, c, w = _conv_args(x, weight, bias, None, activation, False)
+    _check(state, "state", x.dtype, (b, w - 1, c), dev)
+    ytype, shape.y_dtype = _result_dtype(y_dtype, x.dtype, "y_dtype")
+    if out is not None:
+        _check(out, "out", ytype, (b, c), dev)
+
+    def run(handle):
+        y = out if out is not None else torch.empty((b, c), dtype=ytype, device=dev)
+        st = load_library().ssd_causal_conv_step(ctypes.byref(shape), x.data_ptr(), weight.data_ptr(), _addr(bias),
+                                                 state.data_ptr(), y.data_ptr(), handle)
+        return st, y
+
+    return _call("ssd_causal_conv_step", dev, stream, run)
+
+
+def _scan_args(x, dt, A, B, C, D, z, dt_bias, lengths, dt_softplus, tokens):
+    torch = _torch()
+    code = _storage(x, "x")
+    lead = 2 if tokens else 1
+    if x.dim() != lead + 1 or B.dim() != lead + 2 or A.dim() != 2:
+        raise ValueError("x must be (batch, %schannels), B (batch, %sngroups, dstate) and A (channels, dstate)"
+                         % (("seqlen, ",) * 2 if tokens else ("", "")))
+    dev, dtype = x.device, x.dtype
+    b, c, g, n = x.shape[0], x.shape[-1], B.shape[-2], B.shape[-1]
+    L = x.shape[1] if tokens else 1
+    rows = torch.Size((b, L, g, n) if tokens else (b, g, n))
+    none = (0, 0)
+    shape = SelectiveShape(b, L, c, n, g, code, 0, SSD_SCAN_DT_SOFTPLUS if dt_softplus else 0, 0,
+                           _rows(x, "x", dtype, x.shape, dev, tokens), _rows(dt, "dt", dtype, x.shape, dev, tokens),
+                           _rows(B, "B", dtype, rows, dev, tokens), _rows(C, "C", dtype, rows, dev, tokens),
+                           none if z is None else _rows(z, "z", dtype, x.shape, dev, tokens), none)
+    _check(A, "A", torch.float32, (c, n), dev)
+    if D is not None:
+        _check(D, "D", torch.float32, (c,), dev)
+    if dt_bias is not None:
+        _check(dt_bias, "dt_bias", torch.float32, (c,), dev)
+    if lengths is not None:
+        _check(lengths, "lengths", torch.int32, (b,), dev)
+    return shape, dev, b, L, c, g, n
+
+
+def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, initial_states=None,
+                       return_final_states: bool = False, *, dt_softplus: bool = True, lengths=None, y_dtype=None,
+                       out=None, final_out=None, workspace=None, stream=None):
+    """Selective scan over prompts (``ssd_selective_scan_fwd``): per channel
+    and state h_t = exp(d_t A) h_{t-1} + d_t x_t B_t with d = softplus(dt +
+    dt_bias), and y_t = (C_t h_t + D x_t) silu(z_t).
+
+    x, dt, z (b, L, c) and B, C (b, L, g, n), n <= 64: float32 or bfloat16, all
+    the same dtype, rows may lie apart (column slices of wider tensors); A
+    (c, n), D and dt_bias (c,), initial_states (b, c, n): float32.  z None: no
+    gate.  ``lengths``: int32 (b,) device tensor, tokens of each padded
+    sequence; rows behind are 0 in y.  Returns y (``y_dtype``: float32, the
+    default, or x's dtype), or (y, final_states); ``final_out`` may be
+    ``initial_states`` itself.
+    """
+    torch = _torch()
+    lib = load_library()
+    shape, dev, b, L, c, g, n = _scan_args(x, dt, A, B, C, D, z, dt_bias, lengths, dt_softplus, True)
+    if initial_states is not None:
+        _check(initial_states, "initial_states", torch.float32, (b, c, n), dev)
+    ytype, shape.y_dtype = _result_dtype(y_dtype, x.dtype, "y_dtype")
+    if out is not None:
+        _check(out, "out", ytype, (b, L, c), dev)
+    if final_out is not None:
+        _check(final_out, "final_out", torch.float32, (b, c, n), dev)
+
+    def run(handle):
+        y = out if out is not None else torch.empty((b, L, c), dtype=ytype, device=dev)
+        fin = final_out
+        if fin is None and return_final_states:
+            fin = torch.empty((b, c, n), dtype=torch.float32, device=dev)
+        ws, size, _keep = _workspace(workspace, lib.ssd_selective_scan_fwd_workspace_size(ctypes.byref(shape)), dev)
+        st = lib.ssd_selective_scan_fwd(ctypes.byref(shape), x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(),
+                                        C.data_ptr(), _addr(D), _addr(z), _addr(dt_bias), _addr(initial_states),
+                                        _addr(lengths), y.data_ptr(), _addr(fin), ws, size, handle)
+        return st, (y, fin) if return_final_states else y
+
+    return _call("ssd_selective_scan_fwd", dev, stream, run)
+
+
+def selective_scan_bwd(x, dt, A, B, C, D, dy, z=None, dt_bias=None, initial_states=None, d_final_states=None, *,
+                       dt_softplus: bool = True, lengths=None, want_d_initial: bool = True, workspace=None,
+                       stream=None):
+    """Gradients through :func:`selective_scan_fwd` (``ssd_selective_scan_bwd``).
+
+    Inputs as passed there, plus ``dy`` (b, L, c) (float32 or x's dtype, rows
+    may lie apart) and optionally ``d_final_states`` (b, c, n) float32.
+    Returns a dict of float32 tensors ``dx, ddt, dA, dB, dC, dD, ddt_bias``,
+    ``dz`` when z is given and, when requested, ``d_initial_states``.
+    """
+    torch = _torch()
+    lib = load_library()
+    shape, dev, b, L, c, g, n = _scan_args(x, dt, A, B, C, D, z, dt_bias, lengths, dt_softplus, True)
+    for name, t in (("initial_states", initial_states), ("d_final_states", d_final_states)):
+        if t is not None:
+            _check(t, name, torch.float32, (b, c, n), dev)
+    dytype, shape.y_dtype = _result_dtype(dy.dtype, x.dtype, "dy's dtype")
+    shape.dy = Stride(*_rows(dy, "dy", dytype, x.shape, dev))
+
+    def run(handle):
+        def new(*dims):
+            return torch.empty(dims, dtype=torch.float32, device=dev)
+
+        res = {"dx": new(b, L, c), "ddt": new(b, L, c), "dA": new(c, n), "dB": new(b, L, g, n), "dC": new(b, L, g, n),
+               "dD": new(c), "ddt_bias": new(c)}
+        if z is not None:
+            res["dz"] = new(b, L, c)
+        if want_d_initial:
+            res["d_initial_states"] = new(b, c, n)
+        ws, size, _keep = _workspace(workspace, lib.ssd_selective_scan_bwd_workspace_size(ctypes.byref(shape)), dev)
+        st = lib.ssd_selective_scan_bwd(
+            ctypes.byref(shape), x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _addr(D),
+            _addr(z), _addr(dt_bias), _addr(initial_states), _addr(lengths), dy.data_ptr(), _addr(d_final_states),
+            res["dx"].data_ptr(), res["ddt"].data_ptr(), res["dA"].data_ptr(), res["dB"].data_ptr(),
+            res["dC"].data_ptr(), res["dD"].data_ptr(), _addr(res.get("dz")), res["ddt_bias"].data_ptr(),
+            _addr(res.get("d_initial_states")), ws, size, handle)
+        return st, res
+
+    return _call("ssd_selective_scan_bwd", dev, stream, run)
+
+
+def selective_scan_step(x, dt, A, B, C, D, state, z=None, dt_bias=None, *, dt_softplus: bool = True, y_dtype=None,
+                        out=None, stream=None):
+    """The scan for one new token per sequence (``ssd_selective_scan_step``).
+
+    x, dt, z (b, c) and B, C (b, g, n); ``state`` (b, c, n) float32 is updated
+    in place.  Returns y (b, c) (``y_dtype``: float32, the default, or x's
+    dtype).
+    """
+    torch = _torch()
+    shape, dev, b, _, c, g, n = _scan_args(x, dt, A, B, C, D, z, dt_bias, None, dt_softplus, False)
+    _check(state, "state", torch.float32, (b, c, n), dev)
+    ytype, shape.y_dtype = _result_dtype(y_dtype, x.dtype, "y_dtype")
+    if out is not None:
+        _check(out, "out", ytype, (b, c), dev)
+
+    def run(handle):
+        y = out if out is not None else torch.empty((b, c), dtype=ytype, device=dev)
+        st = load_library().ssd_selective_scan_step(
+            ctypes.byref(shape), x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _addr(D),
+            _addr(z), _addr(dt_bias), state.data_ptr(), y.data_ptr(), handle)
+        return st, y
+
+    return _call("ssd_selective_scan_step", dev, stream, run)

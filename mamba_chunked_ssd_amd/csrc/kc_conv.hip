@@ -1,0 +1,437 @@
+// kc_conv.hip -- the short causal convolution of a layer's x, B and C, one
+// filter of 2..4 taps per channel: forward over prompts, backward, one token.
+//
+//   p_t = bias + sum_k w_k x_{t-W+1+k} ,  y_t = act(p_t)
+//
+// Bound by memory: each element of x is read and each of y written once,
+// against 2 W + about 10 vector operations.  A thread owns the channels of
+// one 16-byte load and walks a run of tokens with the last W - 1 inputs in
+// registers, so only the run's first W - 1 rows are read twice (from the L2).
+// Threads of a wave take consecutive channels: every access is one contiguous
+// piece of a row.
+#include "ssd_launch.h"
+#include "ssd_ops_device.h"
+#include "ssd_ops_internal.h"
+
+namespace ssd {
+namespace {
+
+constexpr int kFwdRun = 16;  // tokens of one thread of the forward pass
+constexpr int kUnroll = 8;   // tokens whose loads are in flight together
+
+template <typename T>
+struct ConvIn {
+    const T *x, *init;
+    const float *weight, *bias;
+    const int32_t *lengths;
+    int64_t xb, xr;  // strides of x
+    int L, C, nvec, nvb;
+    bool silu;
+};
+
+__device__ __forceinline__ int conv_length(const int32_t *lengths, int b, int L) {
+    return lengths == nullptr ? L : min(max(lengths[b], 0), L);
+}
+
+template <int W, int V>
+__device__ __forceinline__ void load_filter(const float *weight, const float *bias, int c0, float (&w)[W][V],
+                                            float (&bs)[V]) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) w[k][e] = weight[(int64_t)(c0 + e) * W + k];
+        bs[e] = bias != nullptr ? bias[c0 + e] : 0.f;
+    }
+}
+
+// Input row t of a sequence: the initial state's rows stand before row 0.
+template <typename T, int W, int V>
+__device__ __forceinline__ Raw<T, V> conv_row(const ConvIn<T> &a, int b, int t, int len, int c0) {
+    Raw<T, V> r;
+    r.zero();
+    if (t < 0) {
+        if (a.init != nullptr) r.load(a.init + ((int64_t)b * (W - 1) + (W - 1) + t) * a.C + c0);
+    } else if (t < len) {
+        r.load(a.x + b * a.xb + t * a.xr + c0);
+    }
+    return r;
+}
+
+template <typename Tin, typename Tout, int W, int V>
+__global__ __launch_bounds__(256) void kc_conv_fwd(ConvIn<Tin> a, Tout *__restrict__ y, Tin *final_state) {
+    const int vec = (int)(blockIdx.x % a.nvb) * blockDim.x + threadIdx.x;
+    if (vec >= a.nvec) return;
+    const int run = (int)(blockIdx.x / a.nvb) * blockDim.y + threadIdx.y;
+    const int b = blockIdx.y, c0 = vec * V;
+    const int t0 = run * kFwdRun, t1 = min(t0 + kFwdRun, a.L);
+    if (run > 0 && t0 >= a.L) return;
+    const int len = conv_length(a.lengths, b, a.L);
+
+    float w[W][V], bs[V], win[W][V];  // win[k]: x_{t - W + 1 + k}
+    load_filter<W, V>(a.weight, a.bias, c0, w, bs);
+#pragma unroll
+    for (int k = 1; k < W; ++k) conv_row<Tin, W, V>(a, b, t0 - W + k, len, c0).unpack(win[k]);
+
+    // The first run's thread holds the initial state already when it writes
+    // the final one, so the two may be the same buffer.
+    if (run == 0 && final_state != nullptr) {
+        Raw<Tin, V> keep[W - 1];
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) keep[k] = conv_row<Tin, W, V>(a, b, len - (W - 1) + k, len, c0);
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) {
+            float f[V];
+            keep[k].unpack(f);
+            store_n<V>(final_state + ((int64_t)b * (W - 1) + k) * a.C + c0, f);  // exact: the values are Tin's
+        }
+    }
+
+    Tout *yp = y + ((int64_t)b * a.L + t0) * a.C + c0;
+    for (int t = t0; t < t1; t += kUnroll) {
+        Raw<Tin, V> in[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            in[u].zero();
+            if (t + u < min(len, t1)) in[u].load(a.x + b * a.xb + (t + u) * a.xr + c0);
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+                for (int e = 0; e < V; ++e) win[k][e] = win[k + 1][e];
+            in[u].unpack(win[W - 1]);
+            float out[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                float p = bs[e];
+#pragma unroll
+                for (int k = 0; k < W; ++k) p = fmaf(w[k][e], win[k][e], p);
+                if (a.silu) p *= logistic(p);
+                out[e] = t + u < len ? p : 0.f;
+            }
+            if (t + u < t1) store_n<V>(yp, out);
+            yp += a.C;
+        }
+    }
+}
+
+// Backward: with d_t = dy_t act'(p_t) (0 behind the end),
+//   dx_s = sum_k w_k d_{s+W-1-k} ,  dw_k = sum_t d_t x_{t-W+1+k} ,  db = sum_t d_t .
+// A thread walks t over its strip and W - 1 tokens beyond it, whose d_t it
+// forms again: dx_{t-W+1} is complete at t.  dw and db stay in registers over
+// the strip, are joined over the block's strips in LDS and leave one row of
+// partial sums per block, which kc_conv_sums adds in a fixed order.
+template <typename Tin, typename Tdy, typename Tdx, int W, int V>
+__global__ __launch_bounds__(256) void kc_conv_bwd(ConvIn<Tin> a, const Tdy *__restrict__ dy, int64_t dyb, int64_t dyr,
+                                                   const float *__restrict__ dfinal, Tdx *__restrict__ dx,
+                                                   float *__restrict__ dinit, float *__restrict__ partials, int strip,
+                                                   int nstrips) {
+    extern __shared__ float red[];  // (blockDim.y, (W + 1) * V, blockDim.x)
+    const int vec = (int)(blockIdx.x % a.nvb) * blockDim.x + threadIdx.x;
+    const int sb = blockIdx.x / a.nvb;  // block of strips
+    const int st = sb * blockDim.y + threadIdx.y;
+    const int b = blockIdx.y, c0 = vec * V;
+    const bool work = vec < a.nvec && st < nstrips;
+    const int len = conv_length(a.lengths, b, a.L);
+
+    float dw[W][V], db[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        db[e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) dw[k][e] = 0.f;
+    }
+    if (work) {
+        const int t0 = st * strip, t1 = min(t0 + strip, a.L);
+        float w[W][V], bs[V], win[W][V], dp[W][V];  // dp[k]: d_{t - W + 1 + k}
+        load_filter<W, V>(a.weight, a.bias, c0, w, bs);
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+#pragma unroll
+            for (int e = 0; e < V; ++e) dp[k][e] = 0.f;
+#pragma unroll
+        for (int k = 1; k < W; ++k) conv_row<Tin, W, V>(a, b, t0 - W + k, len, c0).unpack(win[k]);
+        const int tend = t1 + W - 1;
+        for (int t = t0; t < tend; t += kUnroll) {
+            Raw<Tin, V> in[kUnroll];
+            Raw<Tdy, V> up[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                in[u].zero();
+                up[u].zero();
+                if (t + u < min(len, tend)) {
+                    in[u].load(a.x + b * a.xb + (t + u) * a.xr + c0);
+                    up[u].load(dy + b * dyb + (t + u) * dyr + c0);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                if (t + u >= tend) break;
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        win[k][e] = win[k + 1][e];
+                        dp[k][e] = dp[k + 1][e];
+                    }
+                in[u].unpack(win[W - 1]);
+                up[u].unpack(dp[W - 1]);
+                if (a.silu) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        float p = bs[e];
+#pragma unroll
+                        for (int k = 0; k < W; ++k) p = fmaf(w[k][e], win[k][e], p);
+                        const float sg = logistic(p);
+                        // silu'(p) = s (1 + p (1 - s)); rows behind the end have dy = 0
+                        dp[W - 1][e] *= sg * fmaf(p, 1.f - sg, 1.f);
+                    }
+                }
+                if (t + u < t1) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        db[e] += dp[W - 1][e];
+#pragma unroll
+                        for (int k = 0; k < W; ++k) dw[k][e] = fmaf(dp[W - 1][e], win[k][e], dw[k][e]);
+                    }
+                }
+                const int s = t + u - (W - 1);
+                if (s >= t0 || st == 0) {
+                    float g[V];
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        g[e] = 0.f;
+#pragma unroll
+                        for (int k = 0; k < W; ++k) g[e] = fmaf(w[k][e], dp[W - 1 - k][e], g[e]);
+                    }
+                    const int i = s - len + (W - 1);  // x_s's row in the final state
+                    if (dfinal != nullptr && i >= 0 && i < W - 1) {
+                        Raw<float, V> r;
+                        float f[V];
+                        r.load(dfinal + ((int64_t)b * (W - 1) + i) * a.C + c0);
+                        r.unpack(f);
+#pragma unroll
+                        for (int e = 0; e < V; ++e) g[e] += f[e];
+                    }
+                    if (s >= 0) store_n<V>(dx + ((int64_t)b * a.L + s) * a.C + c0, g);
+                    else if (dinit != nullptr) store_n<V>(dinit + ((int64_t)b * (W - 1) + (W - 1) + s) * a.C + c0, g);
+                }
+            }
+        }
+    }
+
+    constexpr int R = (W + 1) * V;
+    float *mine = red + (threadIdx.y * R) * blockDim.x + threadIdx.x;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) mine[(k * V + e) * blockDim.x] = dw[k][e];
+        mine[(W * V + e) * blockDim.x] = db[e];
+    }
+    __syncthreads();
+    const int nsb = (nstrips + blockDim.y - 1) / blockDim.y;
+    float *out = partials + ((int64_t)b * nsb + sb) * (W + 1) * a.C;
+    const int tid = threadIdx.y * blockDim.x + threadIdx.x, n = R * blockDim.x;
+    for (int i = tid; i < n; i += 256) {
+        // consecutive threads take consecutive channels of one tap
+        const int k = i / (V * blockDim.x), cl = i % (V * blockDim.x), e = cl % V, xi = cl / V;
+        const int c = ((int)(blockIdx.x % a.nvb) * blockDim.x) * V + cl;
+        float sum = 0.f;
+        for (int q = 0; q < (int)blockDim.y; ++q) sum += red[(q * R + k * V + e) * blockDim.x + xi];
+        if (c < a.C) out[(int64_t)k * a.C + c] = sum;
+    }
+}
+
+// dweight and dbias: column (tap, channel) summed over the rows of partial
+// sums, four threads a column, in 64 bits (thousands of rows at long inputs;
+// free beside the reads).
+__global__ __launch_bounds__(256) void kc_conv_sums(const float *__restrict__ partials, int64_t parts, int C, int W,
+                                                    float *__restrict__ dweight, float *__restrict__ dbias) {
+    __shared__ double part[256];
+    const int64_t cols = (int64_t)(W + 1) * C, col = (int64_t)blockIdx.x * 64 + threadIdx.x % 64;
+    const int q = threadIdx.x / 64;
+    double sum = 0.0;
+    if (col < cols)
+        for (int64_t p = q; p < parts; p += 4) sum += (double)partials[p * cols + col];
+    part[threadIdx.x] = sum;
+    __syncthreads();
+    if (q == 0 && col < cols) {
+        sum += part[threadIdx.x + 64] + part[threadIdx.x + 128] + part[threadIdx.x + 192];
+        const int k = (int)(col / C), c = (int)(col % C);
+        if (k < W) dweight[(int64_t)c * W + k] = (float)sum;
+        else if (dbias != nullptr) dbias[c] = (float)sum;
+    }
+}
+
+// One token per sequence: all W - 1 kept rows and x in, y and the shifted rows out.
+template <typename Tin, typename Tout, int W, int V>
+__global__ __launch_bounds__(256) void kc_conv_step(ConvIn<Tin> a, Tin *state, Tout *__restrict__ y) {
+    const int64_t gid = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int b = blockIdx.y;
+    if (gid >= a.nvec) return;
+    const int c0 = (int)gid * V;
+    Raw<Tin, V> row[W];
+    Tin *sp = state + (int64_t)b * (W - 1) * a.C + c0;
+    row[W - 1].load(a.x + b * a.xb + c0);
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) row[k].load(sp + (int64_t)k * a.C);
+    float w[W][V], p[V], f[V];
+    load_filter<W, V>(a.weight, a.bias, c0, w, p);
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+        row[k].unpack(f);
+        if (k > 0) store_n<V>(sp + (int64_t)(k - 1) * a.C, f);
+#pragma unroll
+        for (int e = 0; e < V; ++e) p[e] = fmaf(w[k][e], f[e], p[e]);
+    }
+    if (a.silu) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) p[e] *= logistic(p[e]);
+    }
+    store_n<V>(y + (int64_t)b * a.C + c0, p);
+}
+
+// Whether V-element loads and stores fit: whole vectors in a row, every row
+// and buffer aligned to them.
+template <typename T>
+bool vec_ok(const void *p, int V) {
+    return (uintptr_t)p % (V * sizeof(T)) == 0;
+}
+
+template <typename Tin>
+ConvIn<Tin> conv_in(const ConvArgs &a, int V, int bx) {
+    ConvIn<Tin> in;
+    in.x = static_cast<const Tin *>(a.x);
+    in.init = static_cast<const Tin *>(a.init);
+    in.weight = a.weight;
+    in.bias = a.bias;
+    in.lengths = a.lengths;
+    in.xb = a.xs.batch;
+    in.xr = a.xs.row;
+    in.L = a.seqlen;
+    in.C = a.channels;
+    in.nvec = a.channels / V;
+    in.nvb = (in.nvec + bx - 1) / bx;
+    in.silu = a.silu;
+    return in;
+}
+
+// Threads of a block along the channel vectors: a wave's worth where there
+// are that many, else the next power of two, the rest along the tokens.
+int conv_bx(int nvec) {
+    int bx = 1;
+    while (bx < 64 && bx < nvec) bx <<= 1;
+    return bx;
+}
+
+template <typename Tin, typename Tout, int W, int V>
+hipError_t fwd(const ConvArgs &a, hipStream_t stream) {
+    const int bx = conv_bx(a.channels / V), by = 256 / bx;
+    const ConvIn<Tin> in = conv_in<Tin>(a, V, bx);
+    const int runs = a.seqlen > 0 ? (a.seqlen + kFwdRun - 1) / kFwdRun : 1;
+    const int64_t blocks = (int64_t)in.nvb * ((runs + by - 1) / by);
+    return launch_kernel(kc_conv_fwd<Tin, Tout, W, V>, dim3((unsigned)blocks, (unsigned)a.batch), dim3(bx, by), 0,
+                         stream, LaunchEvents{}, in, static_cast<Tout *>(a.y), static_cast<Tin *>(a.final_state));
+}
+
+template <typename Tin, typename Tdy, typename Tdx, int W, int V>
+hipError_t bwd(const ConvArgs &a, const ConvBwdPlan &plan, hipStream_t stream) {
+    // the plan's blocks are for 4 channels a thread; with one, the same blocks take a quarter of the channels
+    const ConvIn<Tin> in = conv_in<Tin>(a, V, plan.bx);
+    const int nsb = (plan.nstrips + plan.by - 1) / plan.by;
+    const int64_t blocks = (int64_t)in.nvb * nsb;
+    if (a.batch > 0) {
+        const size_t lds = sizeof(float) * 256 * (W + 1) * V;
+        const hipError_t e = launch_kernel(
+            kc_conv_bwd<Tin, Tdy, Tdx, W, V>, dim3((unsigned)blocks, (unsigned)a.batch), dim3(plan.bx, plan.by), lds,
+            stream, LaunchEvents{}, in, static_cast<const Tdy *>(a.dy), a.dys.batch, a.dys.row, a.dfinal,
+            static_cast<Tdx *>(a.dx), a.dinit, a.partials, plan.strip, plan.nstrips);
+        if (e != hipSuccess) return e;
+    }
+    const int64_t cols = (int64_t)(W + 1) * a.channels;
+    return launch_kernel(kc_conv_sums, dim3((unsigned)((cols + 63) / 64)), dim3(256), 0, stream, LaunchEvents{},
+                         (const float *)a.partials, plan.parts, a.channels, W, a.dweight, a.dbias);
+}
+
+template <typename Tin, typename Tout, int W, int V>
+hipError_t step(const ConvArgs &a, hipStream_t stream) {
+    const ConvIn<Tin> in = conv_in<Tin>(a, V, 256);
+    return launch_kernel(kc_conv_step<Tin, Tout, W, V>, dim3((unsigned)in.nvb, (unsigned)a.batch), dim3(256), 0, stream,
+                         LaunchEvents{}, in, static_cast<Tin *>(const_cast<void *>(a.init)), static_cast<Tout *>(a.y));
+}
+
+template <int W>
+hipError_t fwd_w(const ConvArgs &a, hipStream_t s) {
+    if (!a.in_bf16) {
+        const bool v = a.channels % 4 == 0 && a.xs.batch % 4 == 0 && a.xs.row % 4 == 0 && vec_ok<float>(a.x, 4) &&
+                       vec_ok<float>(a.init, 4) && vec_ok<float>(a.y, 4) && vec_ok<float>(a.final_state, 4);
+        return v ? fwd<float, float, W, 4>(a, s) : fwd<float, float, W, 1>(a, s);
+    }
+    const bool v = a.channels % 8 == 0 && a.xs.batch % 8 == 0 && a.xs.row % 8 == 0 && vec_ok<uint16_t>(a.x, 8) &&
+                   vec_ok<uint16_t>(a.init, 8) && (uintptr_t)a.y % 16 == 0 && vec_ok<uint16_t>(a.final_state, 8);
+    if (a.y_bf16) return v ? fwd<uint16_t, uint16_t, W, 8>(a, s) : fwd<uint16_t, uint16_t, W, 1>(a, s);
+    return v ? fwd<uint16_t, float, W, 8>(a, s) : fwd<uint16_t, float, W, 1>(a, s);
+}
+
+// four channels a thread: the sums of a wider one would halve the waves a CU holds
+template <typename Tin, typename Tdy, typename Tdx, int W>
+hipError_t bwd_v(const ConvArgs &a, const ConvBwdPlan &p, hipStream_t s) {
+    const bool v = a.channels % 4 == 0 && a.xs.batch % 4 == 0 && a.xs.row % 4 == 0 && a.dys.batch % 4 == 0 &&
+                   a.dys.row % 4 == 0 && vec_ok<Tin>(a.x, 4) && vec_ok<Tin>(a.init, 4) && vec_ok<Tdy>(a.dy, 4) &&
+                   vec_ok<Tdx>(a.dx, 4) && vec_ok<float>(a.dfinal, 4) && vec_ok<float>(a.dinit, 4);
+    return v ? bwd<Tin, Tdy, Tdx, W, 4>(a, p, s) : bwd<Tin, Tdy, Tdx, W, 1>(a, p, s);
+}
+
+template <int W>
+hipError_t bwd_w(const ConvArgs &a, const ConvBwdPlan &p, hipStream_t s) {
+    if (!a.in_bf16) return bwd_v<float, float, float, W>(a, p, s);
+    if (a.y_bf16)
+        return a.dx_bf16 ? bwd_v<uint16_t, uint16_t, uint16_t, W>(a, p, s)
+                         : bwd_v<uint16_t, uint16_t, float, W>(a, p, s);
+    return a.dx_bf16 ? bwd_v<uint16_t, float, uint16_t, W>(a, p, s) : bwd_v<uint16_t, float, float, W>(a, p, s);
+}
+
+template <int W>
+hipError_t step_w(const ConvArgs &a, hipStream_t s) {
+    if (!a.in_bf16) {
+        const bool v = a.channels % 4 == 0 && a.xs.batch % 4 == 0 && vec_ok<float>(a.x, 4) &&
+                       vec_ok<float>(a.init, 4) && vec_ok<float>(a.y, 4);
+        return v ? step<float, float, W, 4>(a, s) : step<float, float, W, 1>(a, s);
+    }
+    const bool v = a.channels % 4 == 0 && a.xs.batch % 4 == 0 && vec_ok<uint16_t>(a.x, 4) &&
+                   vec_ok<uint16_t>(a.init, 4) && (uintptr_t)a.y % 16 == 0;
+    if (a.y_bf16) return v ? step<uint16_t, uint16_t, W, 4>(a, s) : step<uint16_t, uint16_t, W, 1>(a, s);
+    return v ? step<uint16_t, float, W, 4>(a, s) : step<uint16_t, float, W, 1>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_conv_fwd(const ConvArgs &a, hipStream_t stream) {
+    switch (a.width) {
+        case 2: return fwd_w<2>(a, stream);
+        case 3: return fwd_w<3>(a, stream);
+        case 4: return fwd_w<4>(a, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t launch_conv_bwd(const ConvArgs &a, const ConvBwdPlan &plan, hipStream_t stream) {
+    switch (a.width) {
+        case 2: return bwd_w<2>(a, plan, stream);
+        case 3: return bwd_w<3>(a, plan, stream);
+        case 4: return bwd_w<4>(a, plan, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t launch_conv_step(const ConvArgs &a, hipStream_t stream) {
+    switch (a.width) {
+        case 2: return step_w<2>(a, stream);
+        case 3: return step_w<3>(a, stream);
+        case 4: return step_w<4>(a, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace ssd

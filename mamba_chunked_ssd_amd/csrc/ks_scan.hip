@@ -1,0 +1,244 @@
+// ks_scan.hip -- the selective scan's forward pass and its one-token step.
+#include "ks_scan.h"
+
+namespace ssd {
+namespace {
+
+// SUMMARY: a segment's own end state from a zero start, and the sum of its
+// step sizes (whose exponential carries a state across the segment).
+// Otherwise the outputs, from the segment's start state.
+template <typename Tin, typename Tout, int LPC, bool SUMMARY>
+__global__ __launch_bounds__(256) void ks_scan(ScanIn<Tin> a, const float *init, float *seg_state,
+                                               float *__restrict__ seg_steps, Tout *__restrict__ y,
+                                               float *final_state) {
+    constexpr int NP = 4 * LPC, TPL = kTT / LPC;
+    __shared__ float sB[2][kTT * NP], sC[2][SUMMARY ? 1 : kTT * NP];
+    const ScanPos<LPC> at(a);
+    const int n0 = 4 * at.j, b = at.b, c = at.c;
+    const int64_t bc = (int64_t)b * a.channels + c;
+    const int64_t slot = ((int64_t)b * a.nseg + at.seg) * a.channels + c;
+
+    float A2[4], h[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        A2[r] = n0 + r < a.N ? kLog2e * a.A[(int64_t)c * a.N + n0 + r] : 0.f;
+        h[r] = 0.f;
+    }
+    if (!SUMMARY) {
+        if (a.nseg > 1) load_states(seg_state + slot * NP + n0, h);
+        else load_states_n(init != nullptr ? init + bc * a.N : nullptr, n0, a.N, h);
+    }
+    const float bias = a.bias != nullptr ? a.bias[c] : 0.f;
+    const float D = !SUMMARY && a.D != nullptr ? a.D[c] : 0.f;
+    const bool gate = !SUMMARY && a.z != nullptr;
+    float steps = 0.f;
+
+    RowStage<NP, Tin> rB, rC;
+    float dr[TPL], xr[TPL], zr[TPL];
+    auto fetch = [&](int t) {
+        load_own<LPC>(a.dt, a.dts, b, c, t, at.j, at.end, dr);
+        load_own<LPC>(a.x, a.xs, b, c, t, at.j, at.end, xr);
+        if (gate) load_own<LPC>(a.z, a.zs, b, c, t, at.j, at.end, zr);
+        rB.load(a.B, a.Bs, b, at.g, a.N, t, at.end);
+        if (!SUMMARY) rC.load(a.C, a.Cs, b, at.g, a.N, t, at.end);
+    };
+    if (at.s0 < at.end) fetch(at.s0);
+    int buf = 0;
+    for (int t = at.s0; t < at.end; t += kTT, buf ^= 1) {
+        rB.store(sB[buf]);
+        if (!SUMMARY) rC.store(sC[buf]);
+        float d[TPL], x[TPL], z[TPL];
+#pragma unroll
+        for (int i = 0; i < TPL; ++i) {
+            // tokens behind the end take a step of 0: the state stays
+            const float raw = dr[i] + bias;
+            d[i] = t + i * LPC + at.j < at.end ? (a.softplus ? softplus(raw) : raw) : 0.f;
+            x[i] = xr[i];
+            z[i] = zr[i];
+        }
+        __syncthreads();  // also: the buffer stored next was last read before this barrier
+        if (t + kTT < at.end) fetch(t + kTT);
+#pragma unroll
+        for (int i = 0; i < TPL; ++i) {
+            const float u = d[i] * x[i];
+            steps += d[i];
+            float p[LPC];
+            auto token = [&](auto K) {
+                constexpr int k = decltype(K)::value;
+                const float dk = lane_bcast<LPC, k>(d[i]), uk = lane_bcast<LPC, k>(u);
+                const int row = (i * LPC + k) * NP + n0;
+                const floatx4 Bv = *reinterpret_cast<const floatx4 *>(&sB[buf][row]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) h[r] = fmaf(fast_exp2(dk * A2[r]), h[r], uk * Bv[r]);
+                if constexpr (!SUMMARY) {
+                    const floatx4 Cv = *reinterpret_cast<const floatx4 *>(&sC[buf][row]);
+                    float s = Cv[0] * h[0];
+#pragma unroll
+                    for (int r = 1; r < 4; ++r) s = fmaf(Cv[r], h[r], s);
+                    p[k] = s;
+                }
+            };
+            for_lanes<LPC>(token);
+            if constexpr (!SUMMARY) {
+                float o = fmaf(D, x[i], lane_sums<LPC>(p, at.j));
+                if (gate) o *= z[i] * logistic(z[i]);
+                const int tt = t + i * LPC + at.j;
+                float out[1] = {tt < at.end ? o : 0.f};
+                if (at.ok && tt < at.s1) store_n<1>(y + ((int64_t)b * a.L + tt) * a.channels + c, out);
+            }
+        }
+    }
+    if constexpr (SUMMARY) {
+        steps = lane_total<LPC>(steps);
+        if (at.ok) {
+            store_states(seg_state + slot * NP + n0, h);
+            if (at.j == 0) seg_steps[slot] = steps;
+        }
+    } else {
+        // tiles wholly behind the end
+        const int done = at.end > at.s0 ? at.s0 + (at.end - at.s0 + kTT - 1) / kTT * kTT : at.s0;
+        const float zero[1] = {0.f};
+        for (int tt = done + at.j; tt < at.s1; tt += LPC)
+            if (at.ok) store_n<1>(y + ((int64_t)b * a.L + tt) * a.channels + c, zero);
+        if (a.nseg == 1 && final_state != nullptr && at.ok)
+            store_states_n(final_state + bc * a.N, n0, a.N, h);
+    }
+}
+
+// The state at each segment's start, written over the segments' own end
+// states, and the final state: h <- exp(A sum of steps) h + own.
+__global__ __launch_bounds__(256) void ks_carry(const float *__restrict__ A, const float *init, float *seg_state,
+                                                const float *__restrict__ seg_steps, float *final_state, int channels,
+                                                int N, int NP, int nseg) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int b = blockIdx.y;
+    if (i >= (int64_t)channels * NP) return;
+    const int c = (int)(i / NP), n = (int)(i % NP);
+    const bool ok = n < N;
+    const int64_t bcn = ((int64_t)b * channels + c) * N + n;
+    const float A2 = ok ? kLog2e * A[(int64_t)c * N + n] : 0.f;
+    float h = ok && init != nullptr ? init[bcn] : 0.f;
+    float *s = seg_state + (int64_t)b * nseg * channels * NP + i;
+    const float *sum = seg_steps + (int64_t)b * nseg * channels + c;
+#pragma unroll 4
+    for (int k = 0; k < nseg; ++k) {
+        const float own = s[(int64_t)k * channels * NP], d = sum[(int64_t)k * channels];
+        s[(int64_t)k * channels * NP] = h;
+        h = fmaf(fast_exp2(A2 * d), h, own);
+    }
+    if (ok && final_state != nullptr) final_state[bcn] = h;
+}
+
+// One token: a stream of the state, four entries a thread (bound by memory,
+// 8 bytes a state).
+template <typename Tin, typename Tout, int LPC, bool VEC>
+__global__ __launch_bounds__(256) void ks_step(ScanIn<Tin> a, float *state, Tout *__restrict__ y) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int b = blockIdx.y, j = (int)(i % LPC), n0 = 4 * j;
+    if (i / LPC >= a.channels) return;  // whole channels: their lanes leave together
+    const int c = (int)(i / LPC), g = c / a.cpg;
+    const int64_t bc = (int64_t)b * a.channels + c;
+    float h[4], A[4], Bv[4], Cv[4];
+    if constexpr (VEC) {
+        // N = NP: every lane holds four states
+        load_states(state + bc * a.N + n0, h);
+        load_states(a.A + (int64_t)c * a.N + n0, A);
+    } else {
+        load_states_n(state + bc * a.N, n0, a.N, h);
+        load_states_n(a.A + (int64_t)c * a.N, n0, a.N, A);
+    }
+    const Tin *Bp = a.B + b * a.Bs.batch + (int64_t)g * a.N, *Cp = a.C + b * a.Cs.batch + (int64_t)g * a.N;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const bool in = VEC || n0 + r < a.N;
+        Bv[r] = in ? load_one(Bp, n0 + r) : 0.f;
+        Cv[r] = in ? load_one(Cp, n0 + r) : 0.f;
+    }
+    const float x = load_one(a.x + b * a.xs.batch, c);
+    const float raw = load_one(a.dt + b * a.dts.batch, c) + (a.bias != nullptr ? a.bias[c] : 0.f);
+    const float z = a.z != nullptr ? load_one(a.z + b * a.zs.batch, c) : 0.f;
+    const float D = a.D != nullptr ? a.D[c] : 0.f;
+    const float d = a.softplus ? softplus(raw) : raw, u = d * x;
+    float s = 0.f;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        h[r] = fmaf(fast_exp2(kLog2e * A[r] * d), h[r], u * Bv[r]);
+        s = fmaf(Cv[r], h[r], s);
+    }
+    if constexpr (VEC) store_states(state + bc * a.N + n0, h);
+    else store_states_n(state + bc * a.N, n0, a.N, h);
+    s = lane_total<LPC>(s);
+    if (j == 0) {
+        float o[1] = {fmaf(D, x, s)};
+        if (a.z != nullptr) o[0] *= z * logistic(z);
+        store_n<1>(y + bc, o);
+    }
+}
+
+template <typename Tin, typename Tout, int LPC>
+hipError_t fwd(const ScanArgs &a, const ScanPlan &plan, hipStream_t stream) {
+    const ScanIn<Tin> in = scan_in<Tin>(a, plan);
+    const dim3 grid((unsigned)(plan.nblk * plan.nseg), (unsigned)a.batch);
+    if (plan.nseg > 1) {
+        hipError_t e = launch_kernel(ks_scan<Tin, Tout, LPC, true>, grid, dim3(256), 0, stream, LaunchEvents{}, in,
+                                     a.init, a.seg_state, a.seg_steps, (Tout *)nullptr, (float *)nullptr);
+        if (e != hipSuccess) return e;
+        const int64_t n = (int64_t)a.channels * plan.np;
+        e = launch_kernel(ks_carry, dim3((unsigned)((n + 255) / 256), (unsigned)a.batch), dim3(256), 0, stream,
+                          LaunchEvents{}, a.A, a.init, a.seg_state, (const float *)a.seg_steps, a.final_state,
+                          a.channels, a.dstate, plan.np, plan.nseg);
+        if (e != hipSuccess) return e;
+    }
+    return launch_kernel(ks_scan<Tin, Tout, LPC, false>, grid, dim3(256), 0, stream, LaunchEvents{}, in, a.init,
+                         a.seg_state, a.seg_steps, static_cast<Tout *>(a.y), a.final_state);
+}
+
+template <typename Tin, typename Tout, int LPC>
+hipError_t step(const ScanArgs &a, hipStream_t stream) {
+    ScanPlan plan{};
+    plan.nblk = plan.gblocks = plan.nseg = 1;
+    const ScanIn<Tin> in = scan_in<Tin>(a, plan);
+    const dim3 grid((unsigned)(((int64_t)a.channels * LPC + 255) / 256), (unsigned)a.batch);
+    float *state = const_cast<float *>(a.init);
+    const bool vec = a.dstate == 4 * LPC && (uintptr_t)a.init % 16 == 0 && (uintptr_t)a.A % 16 == 0;
+    return vec ? launch_kernel(ks_step<Tin, Tout, LPC, true>, grid, dim3(256), 0, stream, LaunchEvents{}, in, state,
+                               static_cast<Tout *>(a.y))
+               : launch_kernel(ks_step<Tin, Tout, LPC, false>, grid, dim3(256), 0, stream, LaunchEvents{}, in, state,
+                               static_cast<Tout *>(a.y));
+}
+
+template <typename Tin, typename Tout>
+hipError_t fwd_np(const ScanArgs &a, const ScanPlan &plan, hipStream_t s) {
+    switch (plan.np) {
+        case 8: return fwd<Tin, Tout, 2>(a, plan, s);
+        case 16: return fwd<Tin, Tout, 4>(a, plan, s);
+        case 32: return fwd<Tin, Tout, 8>(a, plan, s);
+        case 64: return fwd<Tin, Tout, 16>(a, plan, s);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+template <typename Tin, typename Tout>
+hipError_t step_np(const ScanArgs &a, hipStream_t s) {
+    switch (padded_states(a.dstate)) {
+        case 8: return step<Tin, Tout, 2>(a, s);
+        case 16: return step<Tin, Tout, 4>(a, s);
+        case 32: return step<Tin, Tout, 8>(a, s);
+        case 64: return step<Tin, Tout, 16>(a, s);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_scan_fwd(const ScanArgs &a, const ScanPlan &plan, hipStream_t s) {
+    if (!a.in_bf16) return fwd_np<float, float>(a, plan, s);
+    return a.y_bf16 ? fwd_np<uint16_t, uint16_t>(a, plan, s) : fwd_np<uint16_t, float>(a, plan, s);
+}
+
+hipError_t launch_scan_step(const ScanArgs &a, hipStream_t s) {
+    if (!a.in_bf16) return step_np<float, float>(a, s);
+    return a.y_bf16 ? step_np<uint16_t, uint16_t>(a, s) : step_np<uint16_t, float>(a, s);
+}
+
+}  // namespace ssd

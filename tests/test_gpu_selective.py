@@ -1,0 +1,326 @@
+"""Parity of the selective scan (ssd_selective_scan_fwd, _bwd, _step) against
+the fp64 oracle, and of the layer paths that the convolution and the scans
+make together.
+
+Bounds: max |gpu - oracle| / rms(oracle) <= 1e-4 for every fp32 result, as for
+the chunked scan: a decay exp(d A) carries the relative error of its exponent,
+(5 + |d A|) 2^-23 or so, and a state sums as many of them as it remembers
+tokens, at most a few hundred here, so 300 * 6 * 2^-23 = 2e-4 of the largest
+term if all erred alike and a tenth of that as they do not.  A bf16 y adds half
+a step, 2^-8 |y|.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import mamba_chunked_ssd_amd as ssd
+from oracle import layer_ops as lo
+from tests.gpu_util import nerr
+
+pytestmark = pytest.mark.gpu
+
+TOL = 1e-4
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+NAMES = ("x", "dt", "A", "B", "C", "D", "z", "dt_bias", "init", "lengths")
+
+
+def inputs(b, L, c, n, g=1, dtype="f32", gate=True, state=True, ragged=False, sliced=False, seed=0, softplus=True):
+    gen = torch.Generator().manual_seed(seed + 13 * L + 3 * c + n)
+    t = TYPES[dtype]
+
+    def rows(*shape):
+        if not sliced:
+            return torch.randn(shape, generator=gen).to(t).cuda()
+        k = len(shape) - 2
+        flat = int(np.prod(shape[2:]))
+        wide = torch.randn(shape[:2] + (flat + 11,), generator=gen).to(t).cuda()
+        return wide[..., 3:3 + flat].unflatten(-1, shape[2:]) if k > 1 else wide[..., 3:3 + flat]
+
+    d = dict(x=rows(b, L, c), dt=rows(b, L, c), B=rows(b, L, g, n), C=rows(b, L, g, n))
+    if softplus:
+        d["dt_bias"] = (torch.randn(c, generator=gen) - 3).cuda()
+    else:
+        d["dt"] = (0.1 * d["dt"].float().abs()).to(t)
+        d["dt_bias"] = torch.full((c,), 0.01).cuda()
+    d["A"] = -(torch.arange(1, n + 1).float() * torch.exp(0.3 * torch.randn((c, n), generator=gen))).cuda()
+    d["D"] = torch.randn(c, generator=gen).cuda()
+    d["z"] = rows(b, L, c) if gate else None
+    d["init"] = (0.5 * torch.randn((b, c, n), generator=gen)).cuda() if state else None
+    d["dfinal"] = torch.randn((b, c, n), generator=gen).cuda() if state else None
+    d["dy"] = torch.randn((b, L, c), generator=gen).cuda()
+    d["lengths"] = None
+    if ragged:
+        d["lengths"] = torch.randint(0, L + 1, (b,), generator=gen, dtype=torch.int32).cuda()
+        d["lengths"][-1] = 0
+        if b > 1:
+            d["lengths"][0] = L
+    return d
+
+
+def host(t):
+    return None if t is None else t.double().cpu().numpy() if t.is_floating_point() else t.cpu().numpy()
+
+
+def fwd(d, **kw):
+    return ssd.selective_scan_fwd(*[d[k] for k in NAMES[:9]], True, lengths=d["lengths"], **kw)
+
+
+def bwd(d, dy=None, **kw):
+    return ssd.selective_scan_bwd(d["x"], d["dt"], d["A"], d["B"], d["C"], d["D"], d["dy"] if dy is None else dy,
+                                  d["z"], d["dt_bias"], d["init"], d["dfinal"], lengths=d["lengths"], **kw)
+
+
+# b, L, c, n, g, dtype, y, gate, state, ragged, sliced, softplus: lengths around the tile of 16 and the segments,
+# channels around a block (256 / lanes of a channel), every lane layout (n <= 8, 16, 32, 64) and padded states
+CASES = [
+    (1, 1, 1, 1, 1, "f32", "f32", False, False, False, False, True),
+    (2, 5, 3, 2, 1, "bf16", "bf16", True, True, False, False, True),
+    (1, 16, 64, 16, 1, "f32", "f32", True, True, False, False, True),
+    (3, 17, 65, 16, 1, "bf16", "f32", True, True, True, True, True),
+    (2, 40, 130, 8, 2, "f32", "f32", False, True, False, True, True),
+    (2, 33, 36, 32, 4, "bf16", "bf16", True, True, True, False, True),
+    (1, 50, 20, 64, 2, "f32", "f32", True, True, False, False, True),
+    (2, 70, 9, 23, 3, "f32", "f32", True, False, True, True, False),
+    (1, 300, 70, 16, 1, "bf16", "bf16", True, True, False, True, True),
+    (4, 200, 24, 12, 2, "f32", "f32", True, True, True, False, True),
+    (2, 0, 8, 16, 1, "f32", "f32", True, True, False, False, True),
+    (1, 257, 40, 45, 1, "bf16", "f32", False, True, False, False, False),
+]
+
+
+def ids(c):
+    return "b%d_L%d_c%d_n%d_g%d_%s_%s%s%s%s%s%s" % (c[:7] + ("_gate" * c[7], "_state" * c[8], "_ragged" * c[9],
+                                                         "_sliced" * c[10], "_softplus" * c[11]))
+
+
+def make(case):
+    b, L, c, n, g, dtype, _, gate, state, ragged, sliced, softplus = case
+    return inputs(b, L, c, n, g, dtype, gate, state, ragged, sliced, softplus=softplus)
+
+
+@pytest.mark.parametrize("case", CASES, ids=ids)
+def test_forward(case):
+    d = make(case)
+    y, fin = fwd(d, y_dtype=TYPES[case[6]], dt_softplus=case[11])
+    torch.cuda.synchronize()
+    ref, rfin = lo.scan(*[host(d[k]) for k in NAMES], use_softplus=case[11])
+    rms = np.sqrt(np.mean(ref ** 2)) if ref.size else 0.0
+    assert np.all(np.abs(host(y) - ref) <= TOL * rms * (ref != 0) + (2.0 ** -8 * np.abs(ref) if case[6] == "bf16" else 0))
+    assert nerr(host(fin), rfin) <= TOL
+
+
+@pytest.mark.parametrize("case", CASES, ids=ids)
+def test_backward(case):
+    d = make(case)
+    dy = d["dy"].to(TYPES[case[6]])
+    got = bwd(d, dy, dt_softplus=case[11])
+    torch.cuda.synchronize()
+    a = {k: host(d[k]) for k in NAMES}
+    ref = lo.scan_bwd(a["x"], a["dt"], a["A"], a["B"], a["C"], a["D"], host(dy), a["z"], a["dt_bias"], a["init"],
+                      host(d["dfinal"]), a["lengths"], use_softplus=case[11])
+    assert set(got) == set(ref)
+    errs = {k: nerr(host(got[k]), r) for k, r in ref.items()}
+    print(errs)
+    assert all(e <= TOL for e in errs.values()), errs
+    if d["lengths"] is not None:
+        for i, end in enumerate(host(d["lengths"])):
+            assert not any(bool(got[k][i, end:].any()) for k in ("dx", "ddt", "dB", "dC"))
+
+
+@pytest.mark.parametrize("c,n,g", [(1, 1, 1), (70, 16, 1), (36, 8, 2), (20, 32, 4), (9, 64, 3), (33, 21, 1)])
+@pytest.mark.parametrize("dtype,out", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+def test_steps_follow_the_forward_pass(c, n, g, dtype, out):
+    d = inputs(3, 7, c, n, g, dtype, sliced=True)
+    ref, rfin = lo.scan(*[host(d[k]) for k in NAMES])
+    state = d["init"].clone()
+    rms = np.sqrt(np.mean(ref ** 2))
+    for t in range(7):
+        y = ssd.selective_scan_step(d["x"][:, t], d["dt"][:, t], d["A"], d["B"][:, t], d["C"][:, t], d["D"], state,
+                                    d["z"][:, t], d["dt_bias"], y_dtype=TYPES[out])
+        r = ref[:, t]
+        assert np.all(np.abs(host(y) - r) <= TOL * rms + (2.0 ** -8 * np.abs(r) if out == "bf16" else 0))
+    assert nerr(host(state), rfin) <= TOL
+
+
+def test_long_sequence_of_few_channels():
+    # many segments: the states carried across them against the oracle
+    d = inputs(1, 3000, 5, 16, gate=False)
+    y, fin = fwd(d)
+    ref, rfin = lo.scan(*[host(d[k]) for k in NAMES])
+    assert nerr(host(y), ref) <= TOL and nerr(host(fin), rfin) <= TOL
+    got = bwd(d)
+    a = {k: host(d[k]) for k in NAMES}
+    r = lo.scan_bwd(a["x"], a["dt"], a["A"], a["B"], a["C"], a["D"], host(d["dy"]), a["z"], a["dt_bias"], a["init"],
+                    host(d["dfinal"]))
+    assert all(nerr(host(got[k]), v) <= TOL for k, v in r.items())
+
+
+def test_rows_behind_the_end_are_not_read():
+    d = inputs(4, 90, 24, 16, ragged=True, seed=3)
+    clean, gclean = fwd(d), bwd(d)
+    bad = dict(d)
+    for k in ("x", "dt", "z", "B", "C", "dy"):
+        bad[k] = d[k].clone()
+        for i, end in enumerate(d["lengths"].tolist()):
+            bad[k][i, end:] = float("nan")
+    got, ggot = fwd(bad), bwd(bad)
+    assert all(torch.equal(p, q) for p, q in zip(got, clean))
+    assert all(torch.equal(ggot[k], gclean[k]) for k in gclean)
+
+
+def test_extreme_steps():
+    # steps from 1e-12 to 60: decays of exactly 1 and 0, no NaN
+    d = inputs(1, 48, 8, 16, gate=False)
+    d["dt"] = torch.linspace(-30, 60, 48, device="cuda")[None, :, None].expand(1, 48, 8).contiguous()
+    y, fin = fwd(d)
+    ref, rfin = lo.scan(*[host(d[k]) for k in NAMES])
+    assert nerr(host(y), ref) <= TOL and nerr(host(fin), rfin) <= TOL
+    got = bwd(d)
+    assert all(bool(torch.isfinite(v).all()) for v in got.values())
+
+
+def test_prompt_in_pieces_with_the_state_in_place():
+    d = inputs(2, 400, 24, 16, dtype="bf16")
+    want, wfin = fwd(d)
+    state = d["init"].clone()
+    parts = []
+    for t0, t1 in ((0, 1), (1, 18), (18, 200), (200, 400)):
+        p = {k: (d[k][:, t0:t1] if k in ("x", "dt", "B", "C", "z") else d[k]) for k in NAMES}
+        parts.append(ssd.selective_scan_fwd(p["x"], p["dt"], p["A"], p["B"], p["C"], p["D"], p["z"], p["dt_bias"],
+                                            state, final_out=state))
+    assert nerr(host(torch.cat(parts, 1)), host(want)) <= TOL and nerr(host(state), host(wfin)) <= TOL
+
+
+def test_same_call_same_bits():
+    d = inputs(2, 300, 70, 16, ragged=True)
+    first, again = bwd(d), bwd(d)
+    assert all(torch.equal(first[k], again[k]) for k in first)
+    assert all(torch.equal(p, q) for p, q in zip(fwd(d), fwd(d)))
+
+
+def test_optional_inputs_left_out():
+    d = inputs(2, 30, 12, 16)
+    y = ssd.selective_scan_fwd(d["x"], d["dt"], d["A"], d["B"], d["C"])
+    ref, _ = lo.scan(*[host(d[k]) for k in ("x", "dt", "A", "B", "C")])
+    assert nerr(host(y), ref) <= TOL
+    got = ssd.selective_scan_bwd(d["x"], d["dt"], d["A"], d["B"], d["C"], None, d["dy"], want_d_initial=False)
+    r = lo.scan_bwd(*[host(d[k]) for k in ("x", "dt", "A", "B", "C")], None, host(d["dy"]))
+    assert "d_initial_states" not in got and "dz" not in got
+    assert all(nerr(host(v), r[k]) <= TOL for k, v in got.items())
+
+
+def test_refusals_leave_the_outputs():
+    d = inputs(2, 8, 12, 16)
+    y = torch.full((2, 8, 12), 7.0, device="cuda")
+    with pytest.raises(ssd.SSDError, match="UNSUPPORTED"):
+        ssd.selective_scan_fwd(d["x"], d["dt"], -torch.ones(12, 65, device="cuda"), torch.ones(2, 8, 1, 65, device="cuda"),
+                               torch.ones(2, 8, 1, 65, device="cuda"), out=y)
+    with pytest.raises(ssd.SSDError, match="INVALID"):  # 12 channels in 5 groups
+        ssd.selective_scan_fwd(d["x"], d["dt"], d["A"], torch.ones(2, 8, 5, 16, device="cuda"),
+                               torch.ones(2, 8, 5, 16, device="cuda"), out=y)
+    with pytest.raises(ValueError, match="shape"):
+        ssd.selective_scan_fwd(d["x"], d["dt"][:, :7], d["A"], d["B"], d["C"], out=y)
+    with pytest.raises(TypeError):
+        ssd.selective_scan_fwd(d["x"], d["dt"].bfloat16(), d["A"], d["B"], d["C"], out=y)
+    with pytest.raises(ssd.SSDError, match="INVALID"):
+        ssd.selective_scan_fwd(d["x"], d["dt"], d["A"], d["B"], d["C"], out=d["dt"])
+    with pytest.raises(ssd.SSDError, match="WORKSPACE"):
+        bwd(d, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    assert bool((y == 7.0).all())
+
+
+def test_captured_call_replays():
+    d = inputs(2, 150, 20, 16, dtype="bf16", ragged=True)
+    fwd(d), bwd(d)
+    torch.cuda.synchronize()
+    state = d["init"].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, fin = fwd(d)
+        g = bwd(d)
+        ys = ssd.selective_scan_step(d["x"][:, 0], d["dt"][:, 0], d["A"], d["B"][:, 0], d["C"][:, 0], d["D"], state,
+                                     d["z"][:, 0], d["dt_bias"])
+    for k in range(3):
+        new = inputs(2, 150, 20, 16, dtype="bf16", seed=50 + k)
+        for n in ("x", "dt", "B", "C", "z"):
+            d[n].copy_(new[n])
+        state.copy_(d["init"])
+        graph.replay()
+        torch.cuda.synchronize()
+        ey, efin = fwd(d)
+        e = bwd(d)
+        assert torch.equal(y, ey) and torch.equal(fin, efin)
+        assert all(torch.equal(g[n], e[n]) for n in e)
+        s2 = d["init"].clone()
+        want = ssd.selective_scan_step(d["x"][:, 0], d["dt"][:, 0], d["A"], d["B"][:, 0], d["C"][:, 0], d["D"], s2,
+                                       d["z"][:, 0], d["dt_bias"])
+        assert torch.equal(ys, want) and torch.equal(state, s2)
+
+
+def test_a_given_stream_runs_the_call():
+    d = inputs(2, 300, 30, 16)
+    want = bwd(d)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = bwd(d, stream=side.cuda_stream)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(got[k], want[k]) for k in want)
+
+
+def test_layer_path_prompt_then_tokens():
+    # convolution and scan over a ragged prompt, then token by token from their states, against the oracle over
+    # prompt and tokens together
+    b, L, T, c, n = 3, 37, 5, 48, 16
+    d = inputs(b, L + T, c, n, ragged=False, state=False)
+    gen = torch.Generator().manual_seed(5)
+    w, bias = torch.randn((c, 4), generator=gen).cuda(), torch.randn(c, generator=gen).cuda()
+    lengths = torch.tensor([37, 9, 0], dtype=torch.int32, device="cuda")
+    cut = {k: d[k][:, :L].contiguous() for k in ("x", "dt", "B", "C", "z")}
+    u, cs = ssd.causal_conv_fwd(cut["x"], w, bias, return_final_states=True, lengths=lengths)
+    y, hs = ssd.selective_scan_fwd(u, cut["dt"], d["A"], cut["B"], cut["C"], d["D"], cut["z"], d["dt_bias"], None, True,
+                                   lengths=lengths)
+    outs = []
+    for t in range(L, L + T):
+        ut = ssd.causal_conv_step(d["x"][:, t], w, bias, cs)
+        outs.append(ssd.selective_scan_step(ut, d["dt"][:, t], d["A"], d["B"][:, t], d["C"][:, t], d["D"], hs,
+                                            d["z"][:, t], d["dt_bias"]))
+    got = torch.stack(outs, 1)
+    for i, end in enumerate([37, 9, 0]):
+        pick = list(range(end)) + list(range(L, L + T))
+        xi, dti, Bi, Ci, zi = (host(d[k][i:i + 1][:, pick]) for k in ("x", "dt", "B", "C", "z"))
+        ui, _ = lo.conv(xi, host(w), host(bias))
+        ref, rfin = lo.scan(ui, dti, host(d["A"]), Bi, Ci, host(d["D"]), zi, host(d["dt_bias"]))
+        assert nerr(host(got[i]), ref[0, end:]) <= TOL
+        assert nerr(host(y[i, :end]), ref[0, :end]) <= TOL
+        assert nerr(host(hs[i]), rfin[0]) <= TOL
+
+
+def test_convolution_before_the_chunked_scan():
+    # x, B and C cut from one projection, each through the convolution, then the chunked scan and its backward, the
+    # convolution's gradient taking the chunked scan's fp32 one
+    b, L, nh, p, g, n = 2, 100, 2, 32, 1, 16
+    gen = torch.Generator().manual_seed(8)
+    proj = torch.randn((b, L, nh * p + 2 * g * n + nh), generator=gen).cuda()
+    cuts = {"x": (0, nh * p), "B": (nh * p, nh * p + g * n), "C": (nh * p + g * n, nh * p + 2 * g * n)}
+    w = (0.5 * torch.randn((nh * p + 2 * g * n, 4), generator=gen)).cuda()
+    v = {k: ssd.causal_conv_fwd(proj[..., a:z], w[a:z]) for k, (a, z) in cuts.items()}
+    dt = torch.nn.functional.softplus(proj[..., -nh:]).contiguous()
+    A = -torch.exp(torch.randn(nh, generator=gen)).cuda()
+    x4, B4, C4 = v["x"].view(b, L, nh, p), v["B"].view(b, L, g, n), v["C"].view(b, L, g, n)
+    y, fin = ssd.chunk_scan_fwd(x4, dt, A, B4, C4, None, chunk_size=64, return_final_states=True)
+    ref = {k: lo.conv(host(proj[..., a:z]), host(w[a:z]))[0] for k, (a, z) in cuts.items()}
+    import oracle
+    yr, fr, _ = oracle.scan(ref["x"].reshape(b, L, nh, p), host(dt), host(A), ref["B"].reshape(b, L, g, n),
+                            ref["C"].reshape(b, L, g, n), None, None)
+    assert nerr(host(y), yr) <= TOL and nerr(host(fin), fr) <= TOL
+    dy = torch.randn((b, L, nh, p), generator=gen).cuda()
+    grads = ssd.chunk_scan_bwd(x4, dt, A, B4, C4, None, dy, chunk_size=64)
+    for k, name in (("x", "dx"), ("B", "dB"), ("C", "dC")):
+        a, z = cuts[k]
+        up = grads[name].view(b, L, z - a)
+        got = ssd.causal_conv_bwd(proj[..., a:z], w[a:z], None, up)
+        want = lo.conv_bwd(host(proj[..., a:z]), host(w[a:z]), None, host(up))
+        assert all(nerr(host(got[q]), want[q]) <= TOL for q in want)
