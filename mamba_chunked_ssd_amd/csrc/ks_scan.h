@@ -27,7 +27,7 @@
 
 namespace ssd {
 
-constexpr int kTT = kScanTile;  // tokens of one tile
+constexpr int kTT = 16;  // tokens of one tile (the backward pass's main kernel: kScanTile)
 
 // Kernel arguments with typed inputs.
 template <typename T>
@@ -47,7 +47,7 @@ template <int LPC>
 struct ScanPos {
     static constexpr int NP = 4 * LPC;
     static constexpr int CB = 256 / LPC;  // channels of a block
-    int j, cl, c, g, b, seg, blk;
+    int j, cl, c, c0, g, b, seg, blk;  // c0: the block's first channel
     bool ok;     // c exists (else it stands in for the group's first)
     int s0, s1;  // the segment's tokens
     int end;     // of them, those before `end` belong to the sequence
@@ -63,6 +63,7 @@ struct ScanPos {
         g = blk / a.gblocks;
         const int in_group = (blk % a.gblocks) * CB + cl;
         ok = in_group < a.cpg;
+        c0 = g * a.cpg + (blk % a.gblocks) * CB;
         c = g * a.cpg + (ok ? in_group : 0);
         const int len = a.lengths == nullptr ? a.L : min(max(a.lengths[b], 0), a.L);
         s0 = min(seg * a.seglen, a.L);
@@ -71,40 +72,175 @@ struct ScanPos {
     }
 };
 
-// One element of B or C per thread and tile: rows t .. t + kTT - 1 of the
-// group, padded states and tokens behind the end as 0.
-template <int NP, typename T>
+// Rows of one sequence seen from a tile of TT tokens: a raw buffer over the
+// tile's rows up to the segment's end, so that rows behind it read 0 and their
+// stores are dropped without a branch.  Offsets into the tile are 32-bit (the
+// entry points refuse row strides of 2^24 elements or more) and the same for
+// every tile; the scalar unit moves the base from tile to tile.
+constexpr uint32_t kNowhere = 0x7fffff00u;  // an offset behind any tile: lanes without a channel or state
+
+template <int TT, typename T>
+struct TileRows {
+    const T *at;   // the tile's first row
+    int64_t move;  // elements from tile to tile
+    uint32_t row;  // bytes of a row
+    __device__ __forceinline__ TileRows(const T *p, const Strides &s, int b, int t, bool forwards = true)
+        : at(p + b * s.batch + t * s.row), move(forwards ? TT * s.row : -TT * s.row),
+          row((uint32_t)(s.row * (int64_t)sizeof(T))) {}
+    __device__ __forceinline__ void next() { at += move; }
+    // left: rows from the tile's first to the end
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile(int left) const {
+        return buffer_rsrc(at, (uint32_t)min(max(left, 0), TT) * row);
+    }
+    __device__ __forceinline__ uint32_t offset(int token, int column) const {
+        return token * row + column * (uint32_t)sizeof(T);
+    }
+};
+
+__device__ __forceinline__ float raw_load(const float *, __amdgpu_buffer_rsrc_t r, uint32_t off) {
+    return buffer_load_f32(r, (int)off);
+}
+__device__ __forceinline__ float raw_load(const uint16_t *, __amdgpu_buffer_rsrc_t r, uint32_t off) {
+    return bf16_to_f32((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)off, 0, 0));
+}
+__device__ __forceinline__ void raw_store(float *, __amdgpu_buffer_rsrc_t r, uint32_t off, float v) {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, (int)off, 0, 0);
+}
+__device__ __forceinline__ void raw_store(uint16_t *, __amdgpu_buffer_rsrc_t r, uint32_t off, float v) {
+    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(pack_bf16(v, 0.f) & 0xffffu), r, (int)off, 0, 0);
+}
+
+// A lane's own tokens of a tile, i LPC + j, of one channel: one offset, and a
+// uniform step between the tokens.  HOLD keeps the offsets in registers over
+// the tiles; without, they are formed again at every tile.  Where a tile has
+// fewer tokens than a channel lanes, the lanes behind own none.
+template <int TT, int LPC>
+constexpr int own_tokens() { return TT >= LPC ? TT / LPC : 1; }
+template <int TT, int LPC, typename T, bool HOLD = true>
+struct OwnRows {
+    static constexpr int TPL = own_tokens<TT, LPC>();
+    TileRows<TT, T> rows;
+    uint32_t first;
+    __device__ __forceinline__ OwnRows(const T *p, const Strides &s, int b, int c, int j, bool ok, int t,
+                                       bool forwards = true)
+        : rows(p, s, b, t, forwards), first(ok && j < TT ? rows.offset(j, c) : kNowhere) {}
+    __device__ __forceinline__ void next() { rows.next(); }
+    __device__ __forceinline__ uint32_t base() const {
+        uint32_t o = first;
+        if constexpr (!HOLD) asm volatile("" : "+v"(o));
+        return o;
+    }
+    __device__ __forceinline__ void load(int left, float (&v)[TPL]) const {
+        const __amdgpu_buffer_rsrc_t r = rows.tile(left);
+        const uint32_t o = base();
+#pragma unroll
+        for (int i = 0; i < TPL; ++i) v[i] = raw_load((const T *)nullptr, r, o + i * LPC * rows.row);
+    }
+    __device__ __forceinline__ void store(int left, const float (&v)[TPL]) const {
+        const __amdgpu_buffer_rsrc_t r = rows.tile(left);
+        const uint32_t o = base();
+#pragma unroll
+        for (int i = 0; i < TPL; ++i) raw_store((T *)nullptr, r, o + i * LPC * rows.row, v[i]);
+    }
+};
+
+// One element of B or C per thread and tile: the group's rows, padded states
+// and tokens behind the end as 0.
+template <int TT, int NP, typename T>
 struct RowStage {
-    static constexpr int E = (kTT * NP + 255) / 256;
+    static constexpr int E = (TT * NP + 255) / 256;
+    TileRows<TT, T> rows;
+    uint32_t off[E];
     float v[E];
-    __device__ __forceinline__ void load(const T *p, const Strides &st, int b, int g, int N, int t, int end) {
+    __device__ __forceinline__ RowStage(const T *p, const Strides &s, int b, int g, int N, int t, bool forwards = true)
+        : rows(p, s, b, t, forwards) {
 #pragma unroll
         for (int k = 0; k < E; ++k) {
             const int e = threadIdx.x + 256 * k, tok = e / NP, n = e % NP;
-            v[k] = e < kTT * NP && n < N && t + tok < end && t + tok >= 0
-                       ? load_one(p + b * st.batch + (t + tok) * st.row + (int64_t)g * N, n)
-                       : 0.f;
+            off[k] = e < TT * NP && n < N ? rows.offset(tok, g * N + n) : kNowhere;
         }
+    }
+    __device__ __forceinline__ void next() { rows.next(); }
+    __device__ __forceinline__ void load(int left) {
+        const __amdgpu_buffer_rsrc_t r = rows.tile(left);
+#pragma unroll
+        for (int k = 0; k < E; ++k) v[k] = raw_load((const T *)nullptr, r, off[k]);
     }
     __device__ __forceinline__ void store(float *lds) const {
 #pragma unroll
         for (int k = 0; k < E; ++k) {
             const int e = threadIdx.x + 256 * k;
-            if (e < kTT * NP) lds[e] = v[k];
+            if (TT * NP >= 256 * (k + 1) || e < TT * NP) lds[e] = v[k];
         }
     }
 };
 
-// The values of a lane's own tokens of a tile, t + i LPC + j.
-template <int LPC, typename T>
-__device__ __forceinline__ void load_own(const T *p, const Strides &st, int b, int c, int t, int j, int end,
-                                         float (&v)[kTT / LPC]) {
+// Step sizes of a lane's own tokens; tokens behind the end take a step of 0,
+// so the state stays.
+template <int TT, int LPC>
+__device__ __forceinline__ void step_sizes(const float (&dt)[own_tokens<TT, LPC>()], float bias, bool sp, int left, int j,
+                                           float (&d)[own_tokens<TT, LPC>()]) {
+    constexpr int TPL = own_tokens<TT, LPC>();
 #pragma unroll
-    for (int i = 0; i < kTT / LPC; ++i) {
-        const int tt = t + i * LPC + j;
-        v[i] = tt < end ? load_one(p + b * st.batch + tt * st.row, c) : 0.f;
+    for (int i = 0; i < TPL; ++i) d[i] = dt[i] + bias;
+    if (sp) {
+#pragma unroll
+        for (int i = 0; i < TPL; ++i) d[i] = softplus(d[i]);
+    }
+    if (left < TT) {
+#pragma unroll
+        for (int i = 0; i < TPL; ++i) d[i] = i * LPC + j < left ? d[i] : 0.f;
     }
 }
+
+// p[t] of a tile's tokens summed over a channel's lanes: v[i] for a lane's own
+// token i LPC + j.
+template <int TT, int LPC>
+__device__ __forceinline__ float own_sum(const float (&p)[TT], int i, int j) {
+    if constexpr (TT >= LPC) {
+        float v[LPC];
+#pragma unroll
+        for (int k = 0; k < LPC; ++k) v[k] = p[i * LPC + k];
+        return lane_sums<LPC>(v, j);
+    } else {
+        static_assert(LPC == 2 * TT && LPC == 16, "two lanes a token");
+        float v[TT];
+#pragma unroll
+        for (int k = 0; k < TT; ++k) v[k] = p[k] + lane_swap<8>(p[k]);
+        return lane_sums<TT>(v, j % TT);
+    }
+}
+
+// A block's padded states and one number per channel, of a row of channels
+// kept in the workspace (16 bytes a thread): raw buffers again, from the
+// block's first channel on.
+template <int LPC>
+struct BlockRows {
+    uint32_t states, number;  // offsets; kNowhere for lanes without a channel
+    __device__ __forceinline__ BlockRows(bool ok, int j, int cl)
+        : states(ok ? 16 * threadIdx.x : kNowhere), number(ok ? 4 * cl : kNowhere) {}
+    static __device__ __forceinline__ __amdgpu_buffer_rsrc_t of(const float *first, int elements) {
+        return buffer_rsrc(first, 4 * elements);
+    }
+    __device__ __forceinline__ void load(const float *first, float (&h)[4]) const {
+        const u32x4 v = buffer_load_x4(of(first, 1024), (int)states);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) h[r] = __uint_as_float(v[r]);
+    }
+    __device__ __forceinline__ void store(float *first, const float (&h)[4]) const {
+        u32x4 v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = __float_as_uint(h[r]);
+        __builtin_amdgcn_raw_buffer_store_b128(v, of(first, 1024), (int)states, 0, 0);
+    }
+    __device__ __forceinline__ float load_number(const float *first) const {
+        return buffer_load_f32(of(first, 256 / LPC), (int)number);
+    }
+    // by every lane of the channel alike
+    __device__ __forceinline__ void store_number(float *first, float v) const {
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), of(first, 256 / LPC), (int)number, 0, 0);
+    }
+};
 
 // Four states of (row, channel) in padded fp32 storage.
 __device__ __forceinline__ void load_states(const float *p, float (&h)[4]) {

@@ -33,37 +33,49 @@ __global__ __launch_bounds__(256) void ks_scan(ScanIn<Tin> a, const float *init,
     const bool gate = !SUMMARY && a.z != nullptr;
     float steps = 0.f;
 
-    RowStage<NP, Tin> rB, rC;
+    OwnRows<kTT, LPC, Tin> dts(a.dt, a.dts, b, c, at.j, at.ok, at.s0), xs(a.x, a.xs, b, c, at.j, at.ok, at.s0),
+        zs(gate ? a.z : a.x, gate ? a.zs : a.xs, b, c, at.j, at.ok, at.s0);
+    OwnRows<kTT, LPC, Tout> ys(y, Strides{(int64_t)a.L * a.channels, a.channels}, b, c, at.j, at.ok, at.s0);
+    RowStage<kTT, NP, Tin> rB(a.B, a.Bs, b, at.g, a.N, at.s0), rC(a.C, a.Cs, b, at.g, a.N, at.s0);
     float dr[TPL], xr[TPL], zr[TPL];
-    auto fetch = [&](int t) {
-        load_own<LPC>(a.dt, a.dts, b, c, t, at.j, at.end, dr);
-        load_own<LPC>(a.x, a.xs, b, c, t, at.j, at.end, xr);
-        if (gate) load_own<LPC>(a.z, a.zs, b, c, t, at.j, at.end, zr);
-        rB.load(a.B, a.Bs, b, at.g, a.N, t, at.end);
-        if (!SUMMARY) rC.load(a.C, a.Cs, b, at.g, a.N, t, at.end);
+    auto fetch = [&](int left) {
+        dts.load(left, dr);
+        xs.load(left, xr);
+        if (gate) zs.load(left, zr);
+        rB.load(left);
+        if (!SUMMARY) rC.load(left);
+        dts.next();
+        xs.next();
+        zs.next();
+        rB.next();
+        rC.next();
     };
-    if (at.s0 < at.end) fetch(at.s0);
-    int buf = 0;
-    for (int t = at.s0; t < at.end; t += kTT, buf ^= 1) {
+    if (at.s0 < at.end) fetch(at.end - at.s0);
+    int buf = 0, t = at.s0;
+    for (; t < at.end; t += kTT, buf ^= 1) {
+        const int left = at.end - t;
         rB.store(sB[buf]);
         if (!SUMMARY) rC.store(sC[buf]);
-        float d[TPL], x[TPL], z[TPL];
+        float d[TPL], x[TPL], scale[TPL];
+        step_sizes<kTT, LPC>(dr, bias, a.softplus, left, at.j, d);
 #pragma unroll
         for (int i = 0; i < TPL; ++i) {
-            // tokens behind the end take a step of 0: the state stays
-            const float raw = dr[i] + bias;
-            d[i] = t + i * LPC + at.j < at.end ? (a.softplus ? softplus(raw) : raw) : 0.f;
             x[i] = xr[i];
-            z[i] = zr[i];
+            scale[i] = 1.f;
+        }
+        if (gate) {
+#pragma unroll
+            for (int i = 0; i < TPL; ++i) scale[i] = zr[i] * logistic(zr[i]);
         }
         __syncthreads();  // also: the buffer stored next was last read before this barrier
-        if (t + kTT < at.end) fetch(t + kTT);
+        if (left > kTT) fetch(left - kTT);
+        float o[TPL];
 #pragma unroll
         for (int i = 0; i < TPL; ++i) {
             const float u = d[i] * x[i];
             steps += d[i];
             float p[LPC];
-            auto token = [&](auto K) {
+            for_lanes<LPC>([&](auto K) {
                 constexpr int k = decltype(K)::value;
                 const float dk = lane_bcast<LPC, k>(d[i]), uk = lane_bcast<LPC, k>(u);
                 const int row = (i * LPC + k) * NP + n0;
@@ -77,15 +89,16 @@ __global__ __launch_bounds__(256) void ks_scan(ScanIn<Tin> a, const float *init,
                     for (int r = 1; r < 4; ++r) s = fmaf(Cv[r], h[r], s);
                     p[k] = s;
                 }
-            };
-            for_lanes<LPC>(token);
-            if constexpr (!SUMMARY) {
-                float o = fmaf(D, x[i], lane_sums<LPC>(p, at.j));
-                if (gate) o *= z[i] * logistic(z[i]);
-                const int tt = t + i * LPC + at.j;
-                float out[1] = {tt < at.end ? o : 0.f};
-                if (at.ok && tt < at.s1) store_n<1>(y + ((int64_t)b * a.L + tt) * a.channels + c, out);
+            });
+            if constexpr (!SUMMARY) o[i] = fmaf(D, x[i], lane_sums<LPC>(p, at.j)) * scale[i];
+        }
+        if constexpr (!SUMMARY) {
+            if (left < kTT) {
+#pragma unroll
+                for (int i = 0; i < TPL; ++i) o[i] = i * LPC + at.j < left ? o[i] : 0.f;
             }
+            ys.store(at.s1 - t, o);
+            ys.next();
         }
     }
     if constexpr (SUMMARY) {
@@ -96,10 +109,8 @@ __global__ __launch_bounds__(256) void ks_scan(ScanIn<Tin> a, const float *init,
         }
     } else {
         // tiles wholly behind the end
-        const int done = at.end > at.s0 ? at.s0 + (at.end - at.s0 + kTT - 1) / kTT * kTT : at.s0;
-        const float zero[1] = {0.f};
-        for (int tt = done + at.j; tt < at.s1; tt += LPC)
-            if (at.ok) store_n<1>(y + ((int64_t)b * a.L + tt) * a.channels + c, zero);
+        const float zero[TPL] = {};
+        for (; t < at.s1; t += kTT, ys.next()) ys.store(at.s1 - t, zero);
         if (a.nseg == 1 && final_state != nullptr && at.ok)
             store_states_n(final_state + bc * a.N, n0, a.N, h);
     }

@@ -10,37 +10,36 @@
 //   dz_t = dy_t (C_t . h_t + D x_t) silu'(z_t) ,  o_t = dy_t silu(z_t) .
 //
 // The states are not kept by the forward pass: one sweep stores the state
-// before every tile of 16 tokens (as many bytes as one fp32 tensor of x's
-// size), and the main kernel walks the tiles backwards, forming a tile's 16
-// states and decays again in registers.  Bound by vector instructions, as the
-// forward pass: about 30 issue slots per (token, channel, state) in all.
+// before every tile of 8 tokens (at 16 states as many bytes as two fp32 tensors
+// of x's size), and the main kernel walks the tiles backwards, forming a tile's
+// states and decays again in registers.  Where time is cut into segments the
+// sweep runs each from a zero state, leaving local tile states, the segment's
+// summary and its adjoint's together; the main kernel adds to a tile's local
+// state what the segment's start state has become by then (one exponential a
+// state and tile).  Bound by vector instructions, as the forward pass: about 35
+// issue slots per (token, channel, state) in all.
 //
-// dB and dC sum over channels, which lie across lanes.  That sum is left to
-// the matrix cores, idle otherwise: v_mfma_f32_16x16x4_f32 with the values as
-// A (row m = lane % 16, column k = lane / 16) and a column that is 1 for the
-// token and 0 elsewhere as B adds the four channels of one k to column
-// `token`, in fp32, so 16 tokens fill one accumulator; what is left (the
-// channels that share rows, and the block's waves) is added once per tile
-// from LDS.
+// dB and dC sum over channels, which lie across lanes and blocks: within a wave
+// by channel_sums, the rest of the block once per tile from LDS, and the
+// blocks' partial rows in ks_bwd_sums.
 #include "ks_scan.h"
 
 namespace ssd {
 namespace {
 
-// The output's gradient before the gate, and what the gate's own needs.
-__device__ __forceinline__ float ungate(float dy, float z, bool gate) { return gate ? dy * (z * logistic(z)) : dy; }
-
-// One sweep over a segment.  SUMMARY: its own end state from a zero start, its
-// own gradient at the start from a zero end, sum over t of
-// (e_first .. e_t) C_t o_t, and the sum of its step sizes.  Otherwise the
-// state before every tile, from the segment's start state.
-template <typename Tin, typename Tdy, int LPC, bool SUMMARY>
+// One sweep over a segment, storing the state before every tile.  SEGS (more
+// than one segment): the states are those from a zero start, and with each
+// goes the sum of the segment's steps before it; at the end the segment's own
+// end state, its own gradient at the start from a zero end,
+// sum over t of (e_first .. e_t) C_t o_t, and the sum of its steps.
+template <typename Tin, typename Tdy, int LPC, bool SEGS>
 __global__ __launch_bounds__(256) void ks_bwd_sweep(ScanIn<Tin> a, const Tdy *__restrict__ dy, Strides dys,
                                                     const float *__restrict__ init, float *__restrict__ seg_state,
                                                     float *__restrict__ seg_adj, float *__restrict__ seg_steps,
-                                                    float *__restrict__ tile_state, int64_t tiles) {
+                                                    float *__restrict__ tile_state, float *__restrict__ tile_steps,
+                                                    int64_t tiles) {
     constexpr int NP = 4 * LPC, TPL = kTT / LPC;
-    __shared__ float sB[2][kTT * NP], sC[2][SUMMARY ? kTT * NP : 1];
+    __shared__ float sB[2][kTT * NP], sC[2][SEGS ? kTT * NP : 1];
     const ScanPos<LPC> at(a);
     const int n0 = 4 * at.j, b = at.b, c = at.c;
     const int64_t slot = ((int64_t)b * a.nseg + at.seg) * a.channels + c;
@@ -51,68 +50,98 @@ __global__ __launch_bounds__(256) void ks_bwd_sweep(ScanIn<Tin> a, const Tdy *__
         h[r] = Gs[r] = 0.f;
         P[r] = 1.f;
     }
-    if (!SUMMARY) {
-        if (a.nseg > 1) load_states(seg_state + slot * NP + n0, h);
-        else load_states_n(init != nullptr ? init + ((int64_t)b * a.channels + c) * a.N : nullptr, n0, a.N, h);
-    }
+    if (!SEGS) load_states_n(init != nullptr ? init + ((int64_t)b * a.channels + c) * a.N : nullptr, n0, a.N, h);
     const float bias = a.bias != nullptr ? a.bias[c] : 0.f;
-    const bool gate = SUMMARY && a.z != nullptr;
+    const bool gate = SEGS && a.z != nullptr;
     float steps = 0.f;
-    RowStage<NP, Tin> rB, rC;
+    OwnRows<kTT, LPC, Tin> dts(a.dt, a.dts, b, c, at.j, at.ok, at.s0), xs(a.x, a.xs, b, c, at.j, at.ok, at.s0),
+        zs(gate ? a.z : a.x, gate ? a.zs : a.xs, b, c, at.j, at.ok, at.s0);
+    OwnRows<kTT, LPC, Tdy> gs(dy, dys, b, c, at.j, at.ok, at.s0);
+    RowStage<kTT, NP, Tin> rB(a.B, a.Bs, b, at.g, a.N, at.s0), rC(a.C, a.Cs, b, at.g, a.N, at.s0);
     float dr[TPL], xr[TPL], zr[TPL], gr[TPL];
-    auto fetch = [&](int t) {
-        load_own<LPC>(a.dt, a.dts, b, c, t, at.j, at.end, dr);
-        load_own<LPC>(a.x, a.xs, b, c, t, at.j, at.end, xr);
-        rB.load(a.B, a.Bs, b, at.g, a.N, t, at.end);
-        if constexpr (SUMMARY) {
-            if (gate) load_own<LPC>(a.z, a.zs, b, c, t, at.j, at.end, zr);
-            load_own<LPC>(dy, dys, b, c, t, at.j, at.end, gr);
-            rC.load(a.C, a.Cs, b, at.g, a.N, t, at.end);
+    auto fetch = [&](int left) {
+        dts.load(left, dr);
+        xs.load(left, xr);
+        rB.load(left);
+        dts.next();
+        xs.next();
+        rB.next();
+        if constexpr (SEGS) {
+            if (gate) zs.load(left, zr);
+            gs.load(left, gr);
+            rC.load(left);
+            zs.next();
+            gs.next();
+            rC.next();
         }
     };
-    if (at.s0 < at.end) fetch(at.s0);
+    if (at.s0 < at.end) fetch(at.end - at.s0);
     int buf = 0;
+    const BlockRows<LPC> mine(at.ok, at.j, at.cl);
+    int64_t tile = ((int64_t)b * tiles + at.s0 / kScanTile) * a.channels + at.c0;
     for (int t = at.s0; t < at.end; t += kTT, buf ^= 1) {
+        const int left = at.end - t;
         rB.store(sB[buf]);
-        if constexpr (SUMMARY) rC.store(sC[buf]);
-        else if (at.ok) store_states(tile_state + (((int64_t)b * tiles + t / kTT) * a.channels + c) * NP + n0, h);
+        if constexpr (SEGS) rC.store(sC[buf]);
         float d[TPL], u[TPL], o[TPL];
+        step_sizes<kTT, LPC>(dr, bias, a.softplus, left, at.j, d);
 #pragma unroll
-        for (int i = 0; i < TPL; ++i) {
-            const float raw = dr[i] + bias;
-            d[i] = t + i * LPC + at.j < at.end ? (a.softplus ? softplus(raw) : raw) : 0.f;
-            u[i] = d[i] * xr[i];
-            if constexpr (SUMMARY) o[i] = ungate(gr[i], zr[i], gate);
+        for (int i = 0; i < TPL; ++i) u[i] = d[i] * xr[i];
+        float first = 0.f, second = 0.f;  // sums of the steps of the two tiles
+        if constexpr (SEGS) {
+#pragma unroll
+            for (int i = 0; i < TPL; ++i) {
+                const bool early = i * LPC + at.j < kScanTile;
+                first += early ? d[i] : 0.f;
+                second += early ? 0.f : d[i];
+                o[i] = gr[i];
+            }
+            first = lane_total<LPC>(first);
+            second = lane_total<LPC>(second);
+            if (gate) {
+#pragma unroll
+                for (int i = 0; i < TPL; ++i) o[i] *= zr[i] * logistic(zr[i]);
+            }
         }
+        // the state before a tile
+        auto keep = [&] {
+            mine.store(tile_state + tile * NP, h);
+            if (SEGS) mine.store_number(tile_steps + tile, steps);
+            tile += a.channels;
+        };
         __syncthreads();
-        if (t + kTT < at.end) fetch(t + kTT);
+        if (left > kTT) fetch(left - kTT);
+        for_lanes<kTT>([&](auto T) {
+            constexpr int tk = decltype(T)::value, i = tk / LPC, k = tk % LPC;
+            if constexpr (tk == 0) {
+                keep();
+                steps += first;
+            }
+            if constexpr (tk == kScanTile) {
+                keep();
+                steps += second;
+            }
+            const float dk = lane_bcast<LPC, k>(d[i]), uk = lane_bcast<LPC, k>(u[i]);
+            const floatx4 Bv = *reinterpret_cast<const floatx4 *>(&sB[buf][tk * NP + n0]);
+            floatx4 Co;
+            if constexpr (SEGS) {
+                const float ok = lane_bcast<LPC, k>(o[i]);
+                Co = *reinterpret_cast<const floatx4 *>(&sC[buf][tk * NP + n0]);
 #pragma unroll
-        for (int i = 0; i < TPL; ++i) {
-            steps += d[i];
-            for_lanes<LPC>([&](auto K) {
-                constexpr int k = decltype(K)::value;
-                const float dk = lane_bcast<LPC, k>(d[i]), uk = lane_bcast<LPC, k>(u[i]);
-                const int row = (i * LPC + k) * NP + n0;
-                const floatx4 Bv = *reinterpret_cast<const floatx4 *>(&sB[buf][row]);
-                floatx4 Co;
-                if constexpr (SUMMARY) {
-                    const float ok = lane_bcast<LPC, k>(o[i]);
-                    Co = *reinterpret_cast<const floatx4 *>(&sC[buf][row]) * ok;
-                }
+                for (int r = 0; r < 4; ++r) Co[r] *= ok;
+            }
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float e = fast_exp2(dk * A2[r]);
-                    h[r] = fmaf(e, h[r], uk * Bv[r]);
-                    if constexpr (SUMMARY) {
-                        P[r] *= e;
-                        Gs[r] = fmaf(P[r], Co[r], Gs[r]);
-                    }
+            for (int r = 0; r < 4; ++r) {
+                const float e = fast_exp2(dk * A2[r]);
+                h[r] = fmaf(e, h[r], uk * Bv[r]);
+                if constexpr (SEGS) {
+                    P[r] *= e;
+                    Gs[r] = fmaf(P[r], Co[r], Gs[r]);
                 }
-            });
-        }
+            }
+        });
     }
-    if constexpr (SUMMARY) {
-        steps = lane_total<LPC>(steps);
+    if constexpr (SEGS) {
         if (at.ok) {
             store_states(seg_state + slot * NP + n0, h);
             store_states(seg_adj + slot * NP + n0, Gs);
@@ -156,40 +185,61 @@ struct BwdOut {
     float *dap, *ddp, *dbiasp;
 };
 
-constexpr int kRedStride = kTT + 1;       // LDS row of 16 tokens, padded
-constexpr int kRedWave = 64 * kRedStride;  // one wave's accumulator: 64 rows
+// LDS row of one lane's 8 + 8 sums of a tile, padded so that neither the
+// 16-byte writes nor the reads down a column meet in a bank.
+constexpr int kRedStride = 2 * kScanTile + 4;
 
+// One segment, its tiles from the last to the first.  Registers limit it: a
+// tile's states and decays take 8 a token, so tiles have 8 tokens.
 template <typename Tin, typename Tdy, int LPC>
 __global__ __launch_bounds__(256, 2) void ks_bwd_main(ScanIn<Tin> a, const Tdy *__restrict__ dy, Strides dys,
                                                       const float *__restrict__ dfinal,
+                                                      const float *__restrict__ seg_state,
                                                       const float *__restrict__ seg_adj,
-                                                      const float *__restrict__ tile_state, int64_t tiles, BwdOut out) {
-    constexpr int NP = 4 * LPC, TPL = kTT / LPC;
-    __shared__ float sB[kTT * NP], sC[kTT * NP], red[2][4][kRedWave];
+                                                      const float *__restrict__ tile_state,
+                                                      const float *__restrict__ tile_steps, int64_t tiles, BwdOut out) {
+    constexpr int TT = kScanTile, NP = 4 * LPC, TPL = own_tokens<TT, LPC>();
+    __shared__ float sB[TT * NP], sC[TT * NP], red[256 * kRedStride];
     const ScanPos<LPC> at(a);
     const int n0 = 4 * at.j, b = at.b, c = at.c;
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int lane = threadIdx.x % 64;
+    // LDS rows of sums: the parts of the waves, each of NP states
+    const int red_row = threadIdx.x / 64 * 64 + channel_sum_part<LPC>(lane) * NP + n0 + channel_sum_r<LPC>(lane);
     const int64_t slot = ((int64_t)b * a.nseg + at.seg) * a.channels + c;
     const int64_t bc = (int64_t)b * a.channels + c;
-    float A2[4], carry[4], dA[4];
+    const bool segs = a.nseg > 1;
+    float A2[4], carry[4], dA[4], hs[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         A2[r] = n0 + r < a.N ? kLog2e * a.A[(int64_t)c * a.N + n0 + r] : 0.f;
-        dA[r] = 0.f;
+        dA[r] = hs[r] = 0.f;
     }
-    if (a.nseg > 1) load_states(seg_adj + slot * NP + n0, carry);
-    else load_states_n(dfinal != nullptr ? dfinal + bc * a.N : nullptr, n0, a.N, carry);
+    if (segs) {
+        load_states(seg_adj + slot * NP + n0, carry);
+        load_states(seg_state + slot * NP + n0, hs);
+    } else {
+        load_states_n(dfinal != nullptr ? dfinal + bc * a.N : nullptr, n0, a.N, carry);
+    }
     const float bias = a.bias != nullptr ? a.bias[c] : 0.f;
     const float D = a.D != nullptr ? a.D[c] : 0.f;
     const bool gate = a.z != nullptr;
     float dD = 0.f, dbias = 0.f;
 
-    // a block's last channels may stand in for the group's first: they add nothing to the sums over channels
-    const float mine = at.ok ? 1.f : 0.f;
+    // lanes without a channel read zeros: they add nothing to the sums over channels
+    const int done = at.end > at.s0 ? at.s0 + (at.end - at.s0 + TT - 1) / TT * TT : at.s0;
+    const int last = done - TT;
+    OwnRows<TT, LPC, Tin, false> dts(a.dt, a.dts, b, c, at.j, at.ok, last, false),
+        xs(a.x, a.xs, b, c, at.j, at.ok, last, false),
+        zs(gate ? a.z : a.x, gate ? a.zs : a.xs, b, c, at.j, at.ok, last, false);
+    OwnRows<TT, LPC, Tdy, false> gs(dy, dys, b, c, at.j, at.ok, last, false);
+    const Strides dense{(int64_t)a.L * a.channels, a.channels};
+    OwnRows<TT, LPC, float, false> dxs(out.dx, dense, b, c, at.j, at.ok, last, false),
+        ddts(out.ddt, dense, b, c, at.j, at.ok, last, false),
+        dzs(gate ? out.dz : out.dx, dense, b, c, at.j, at.ok, last, false);
+    RowStage<TT, NP, Tin> rB(a.B, a.Bs, b, at.g, a.N, last, false), rC(a.C, a.Cs, b, at.g, a.N, last, false);
     float *db = out.db + at.blk * out.blk, *dc = out.dc + at.blk * out.blk;
 
     // rows behind the end
-    const int done = at.end > at.s0 ? at.s0 + (at.end - at.s0 + kTT - 1) / kTT * kTT : at.s0;
     for (int tt = done + at.j; tt < at.s1; tt += LPC)
         if (at.ok) {
             const int64_t i = ((int64_t)b * a.L + tt) * a.channels + c;
@@ -203,116 +253,133 @@ __global__ __launch_bounds__(256, 2) void ks_bwd_main(ScanIn<Tin> a, const Tdy *
         dc[p] = 0.f;
     }
 
-    for (int t = done - kTT; t >= at.s0; t -= kTT) {
-        RowStage<NP, Tin> rB, rC;
-        float d[TPL], x[TPL], z[TPL], g[TPL], sl[TPL], o[TPL], dt[TPL];
-        float h0[4];
-        load_own<LPC>(a.dt, a.dts, b, c, t, at.j, at.end, dt);
-        load_own<LPC>(a.x, a.xs, b, c, t, at.j, at.end, x);
-        if (gate) load_own<LPC>(a.z, a.zs, b, c, t, at.j, at.end, z);
-        load_own<LPC>(dy, dys, b, c, t, at.j, at.end, g);
-        rB.load(a.B, a.Bs, b, at.g, a.N, t, at.end);
-        rC.load(a.C, a.Cs, b, at.g, a.N, t, at.end);
-        load_states(tile_state + (((int64_t)b * tiles + t / kTT) * a.channels + c) * NP + n0, h0);
+    float dr[TPL], xr[TPL], zr[TPL], gr[TPL], hr[4], sr = 0.f;
+    const BlockRows<LPC> mine(at.ok, at.j, at.cl);
+    int64_t tile = ((int64_t)b * tiles + last / TT) * a.channels + at.c0;
+    auto fetch = [&](int left) {
+        dts.load(left, dr);
+        xs.load(left, xr);
+        if (gate) zs.load(left, zr);
+        gs.load(left, gr);
+        rB.load(left);
+        rC.load(left);
+        mine.load(tile_state + tile * NP, hr);
+        if (segs) sr = mine.load_number(tile_steps + tile);
+        tile -= a.channels;
+        dts.next();
+        xs.next();
+        zs.next();
+        gs.next();
+        rB.next();
+        rC.next();
+    };
+    if (at.s0 < at.end) fetch(at.end - last);
+    for (int t = last; t >= at.s0; t -= TT) {
+        const int left = at.end - t, room = at.s1 - t;
         rB.store(sB);
         rC.store(sC);
-        __syncthreads();
-
-        float e[kTT][4], h[kTT][4], tot[TPL];
+        float d[TPL], u[TPL], x[TPL], o[TPL], sl[TPL], zy[TPL], h0[4];
+        step_sizes<TT, LPC>(dr, bias, a.softplus, left, at.j, d);
 #pragma unroll
         for (int i = 0; i < TPL; ++i) {
-            const bool live = t + i * LPC + at.j < at.end;
-            const float raw = dt[i] + bias;
-            d[i] = live ? (a.softplus ? softplus(raw) : raw) : 0.f;
-            sl[i] = live ? (a.softplus ? logistic(raw) : 1.f) : 0.f;  // softplus', 0 behind the end
-            o[i] = ungate(g[i], z[i], gate);
-            const float u = d[i] * x[i];
-            float p[LPC];
-            for_lanes<LPC>([&](auto K) {
-                constexpr int k = decltype(K)::value;
-                const int tk = i * LPC + k;
-                const float dk = lane_bcast<LPC, k>(d[i]), uk = lane_bcast<LPC, k>(u);
-                const floatx4 Bv = *reinterpret_cast<const floatx4 *>(&sB[tk * NP + n0]);
-                const floatx4 Cv = *reinterpret_cast<const floatx4 *>(&sC[tk * NP + n0]);
-                p[k] = 0.f;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    e[tk][r] = fast_exp2(dk * A2[r]);
-                    h[tk][r] = fmaf(e[tk][r], tk == 0 ? h0[r] : h[tk > 0 ? tk - 1 : 0][r], uk * Bv[r]);
-                    p[k] = fmaf(Cv[r], h[tk][r], p[k]);
-                }
-            });
-            tot[i] = lane_sums<LPC>(p, at.j);
+            x[i] = xr[i];
+            u[i] = d[i] * x[i];
+            o[i] = gr[i];
+            sl[i] = a.softplus ? logistic(dr[i] + bias) : 1.f;  // softplus'
         }
-
-        floatx4 accB[4], accC[4];
+        if (gate) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) accB[r] = accC[r] = zero4();
-#pragma unroll
-        for (int ii = 0; ii < TPL; ++ii) {
-            const int i = TPL - 1 - ii;
-            const float u = d[i] * x[i];
-            float pB[LPC], pA[LPC];
-            for_lanes<LPC>([&](auto K) {
-                constexpr int k = LPC - 1 - decltype(K)::value;
-                const int tk = i * LPC + k;
-                const float dk = lane_bcast<LPC, k>(d[i]), uk = lane_bcast<LPC, k>(u) * mine;
-                const float ok = lane_bcast<LPC, k>(o[i]);
-                const float om = ok * mine;
-                const floatx4 Bv = *reinterpret_cast<const floatx4 *>(&sB[tk * NP + n0]);
-                const floatx4 Cv = *reinterpret_cast<const floatx4 *>(&sC[tk * NP + n0]);
-                const float column = lane % 16 == tk ? 1.f : 0.f;
-                pB[k] = pA[k] = 0.f;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float G = fmaf(Cv[r], ok, carry[r]);
-                    accC[r] = mfma_f32(om * h[tk][r], column, accC[r]);
-                    accB[r] = mfma_f32(uk * G, column, accB[r]);
-                    pB[k] = fmaf(G, Bv[r], pB[k]);
-                    carry[r] = e[tk][r] * G;
-                    const float q = carry[r] * (tk == 0 ? h0[r] : h[tk > 0 ? tk - 1 : 0][r]);
-                    pA[k] = fmaf(q, A2[r], pA[k]);
-                    dA[r] = fmaf(q, dk, dA[r]);
-                }
-            });
-            const float gB = lane_sums<LPC>(pB, at.j), gA = lane_sums<LPC>(pA, at.j);
-            const int tt = t + i * LPC + at.j;
-            // pA used log2(e) A
-            const float ddt = fmaf(0.6931471805599453f, gA, gB * x[i]) * sl[i];
-            dbias += ddt;
-            dD = fmaf(o[i], x[i], dD);
-            if (at.ok && tt < at.s1) {
-                const int64_t w = ((int64_t)b * a.L + tt) * a.channels + c;
-                out.dx[w] = fmaf(gB, d[i], D * o[i]);
-                out.ddt[w] = ddt;
-                if (gate) {
-                    const float s = logistic(z[i]);
-                    out.dz[w] = g[i] * fmaf(D, x[i], tot[i]) * (s * fmaf(z[i], 1.f - s, 1.f));
-                }
+            for (int i = 0; i < TPL; ++i) {
+                const float s = logistic(zr[i]);
+                zy[i] = o[i] * (s * fmaf(zr[i], 1.f - s, 1.f));  // dy silu'(z)
+                o[i] *= zr[i] * s;
             }
         }
-
-        // accumulator rows m = 4 (lane / 16) + q, columns the tokens; row (m, r) of the LDS tile is channel
-        // m / LPC of its k and state 4 (m % LPC) + r
+        if (left < TT || TT < LPC) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+            for (int i = 0; i < TPL; ++i) sl[i] = i * LPC + at.j < min(left, TT) ? sl[i] : 0.f;
+        }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int row = (4 * (lane / 16) + q) * 4 + r;
-                red[0][wave][row * kRedStride + lane % 16] = accB[r][q];
-                red[1][wave][row * kRedStride + lane % 16] = accC[r][q];
-            }
+        for (int r = 0; r < 4; ++r) h0[r] = hr[r];
+        if (segs) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) h0[r] = fmaf(fast_exp2(sr * A2[r]), hs[r], h0[r]);
+        }
         __syncthreads();
-        for (int i = threadIdx.x; i < 2 * kTT * NP; i += 256) {
-            const int n = i % NP, tok = i / NP % kTT, kind = i / (NP * kTT);
+        if (t - TT >= at.s0) fetch(TT);
+
+        // B's and C's rows are read from LDS again on the way back: kept, they would take 64 registers
+        auto Brow = [&](int tk) { return *reinterpret_cast<const floatx4 *>(&sB[tk * NP + n0]); };
+        auto Crow = [&](int tk) { return *reinterpret_cast<const floatx4 *>(&sC[tk * NP + n0]); };
+        float e[TT][4], h[TT][4], pY[TT], pA[TT], pB[TT], sums[2][TT], v[2][4];
+        for_lanes<TT>([&](auto T) {
+            constexpr int tk = decltype(T)::value, i = tk / LPC, k = tk % LPC;
+            const float dk = lane_bcast<LPC, k>(d[i]), uk = lane_bcast<LPC, k>(u[i]), ok = lane_bcast<LPC, k>(o[i]);
+            const floatx4 Bv = Brow(tk), Cv = Crow(tk);
+            pY[tk] = 0.f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                e[tk][r] = fast_exp2(dk * A2[r]);
+                h[tk][r] = fmaf(e[tk][r], tk == 0 ? h0[r] : h[tk > 0 ? tk - 1 : 0][r], uk * Bv[r]);
+                pY[tk] = fmaf(Cv[r], h[tk][r], pY[tk]);
+                v[tk % 2][r] = ok * h[tk][r];
+            }
+            if constexpr (tk % 2 == 1) channel_sums<LPC>(v, sums[1][tk - 1], sums[1][tk]);
+        });
+        if (gate) {
+#pragma unroll
+            for (int i = 0; i < TPL; ++i) zy[i] *= fmaf(D, x[i], own_sum<TT, LPC>(pY, i, at.j));
+            dzs.store(room, zy);
+        }
+        asm volatile("" ::: "memory");
+        for_lanes<TT>([&](auto K) {
+            constexpr int tk = TT - 1 - decltype(K)::value, i = tk / LPC, k = tk % LPC;
+            const float dk = lane_bcast<LPC, k>(d[i]), uk = lane_bcast<LPC, k>(u[i]), ok = lane_bcast<LPC, k>(o[i]);
+            const floatx4 Bv = Brow(tk), Cv = Crow(tk);
+            pB[tk] = pA[tk] = 0.f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float G = fmaf(Cv[r], ok, carry[r]);
+                v[tk % 2][r] = uk * G;
+                pB[tk] = fmaf(G, Bv[r], pB[tk]);
+                carry[r] = e[tk][r] * G;
+                const float q = carry[r] * (tk == 0 ? h0[r] : h[tk > 0 ? tk - 1 : 0][r]);
+                pA[tk] = fmaf(q, A2[r], pA[tk]);
+                dA[r] = fmaf(q, dk, dA[r]);
+            }
+            if constexpr (tk % 2 == 0) channel_sums<LPC>(v, sums[0][tk], sums[0][tk + 1]);
+        });
+
+        float dxv[TPL], ddtv[TPL];
+#pragma unroll
+        for (int i = 0; i < TPL; ++i) {
+            const float gB = own_sum<TT, LPC>(pB, i, at.j), gA = own_sum<TT, LPC>(pA, i, at.j);
+            ddtv[i] = fmaf(0.6931471805599453f, gA, gB * x[i]) * sl[i];  // pA used log2(e) A
+            dxv[i] = fmaf(gB, d[i], D * o[i]);
+            dbias += ddtv[i];
+            dD = fmaf(o[i], x[i], dD);
+        }
+        dxs.store(room, dxv);
+        ddts.store(room, ddtv);
+        dxs.next();
+        ddts.next();
+        dzs.next();
+
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int tk = 0; tk < TT; tk += 4)
+                *reinterpret_cast<floatx4 *>(&red[red_row * kRedStride + q * TT + tk]) =
+                    floatx4{sums[q][tk], sums[q][tk + 1], sums[q][tk + 2], sums[q][tk + 3]};
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2 * TT * NP; i += 256) {
+            const int n = i % NP, column = i / NP, tok = column % TT;
             float s = 0.f;
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
-#pragma unroll
-                for (int q = 0; q < 16 / LPC; ++q) s += red[kind][w][(q * NP + n) * kRedStride + tok];
-            if (n < a.N && t + tok < at.s1) {
+            for (int q = 0; q < 256 / NP; ++q) s += red[(q * NP + n) * kRedStride + column];
+            if (n < a.N && tok < room) {
                 const int64_t p = ((int64_t)b * a.L + t + tok) * out.tok + n;
-                (kind == 0 ? db : dc)[p] = s;
+                (column < TT ? db : dc)[p] = s;
             }
         }
     }
@@ -365,6 +432,7 @@ __global__ __launch_bounds__(256) void ks_bwd_sums(BwdSums s, int64_t nA, int64_
     const int64_t n = i % s.N, g = i / s.N % s.ngroups, row = i / ((int64_t)s.N * s.ngroups);
     const float *from = (first ? s.dbp : s.dcp) + (g * s.gblocks * s.rows + row) * s.N + n;
     double v = 0.0;
+#pragma unroll 8
     for (int k = 0; k < s.gblocks; ++k) v += (double)from[(int64_t)k * s.rows * s.N];
     (first ? s.dB : s.dC)[i] = (float)v;
 }
@@ -376,19 +444,17 @@ hipError_t bwd(const ScanArgs &a, const ScanPlan &plan, hipStream_t stream) {
     const dim3 grid((unsigned)(plan.nblk * plan.nseg), (unsigned)a.batch);
     hipError_t e = hipSuccess;
     if (a.batch > 0) {
-        if (plan.nseg > 1) {
-            e = launch_kernel(ks_bwd_sweep<Tin, Tdy, LPC, true>, grid, dim3(256), 0, stream, LaunchEvents{}, in, dy,
-                              a.dys, a.init, a.seg_state, a.seg_adj, a.seg_steps, a.tile_state, plan.tiles);
+        const auto sweep = plan.nseg > 1 ? ks_bwd_sweep<Tin, Tdy, LPC, true> : ks_bwd_sweep<Tin, Tdy, LPC, false>;
+        if (a.seqlen > 0) {
+            e = launch_kernel(sweep, grid, dim3(256), 0, stream, LaunchEvents{}, in, dy, a.dys, a.init, a.seg_state,
+                              a.seg_adj, a.seg_steps, a.tile_state, a.tile_steps, plan.tiles);
             if (e != hipSuccess) return e;
+        }
+        if (plan.nseg > 1) {
             const int64_t n = (int64_t)a.channels * plan.np;
             e = launch_kernel(ks_bwd_carry, dim3((unsigned)((n + 255) / 256), (unsigned)a.batch, 2), dim3(256), 0,
                               stream, LaunchEvents{}, a.A, a.init, a.dfinal, a.seg_state, a.seg_adj,
                               (const float *)a.seg_steps, a.dinit, a.channels, a.dstate, plan.np, plan.nseg);
-            if (e != hipSuccess) return e;
-        }
-        if (a.seqlen > 0) {
-            e = launch_kernel(ks_bwd_sweep<Tin, Tdy, LPC, false>, grid, dim3(256), 0, stream, LaunchEvents{}, in, dy,
-                              a.dys, a.init, a.seg_state, a.seg_adj, a.seg_steps, a.tile_state, plan.tiles);
             if (e != hipSuccess) return e;
         }
         BwdOut out{a.dx, a.ddt, a.dz, a.dinit, a.dbp, a.dcp, a.batch * a.seqlen * a.dstate, a.dstate,
@@ -400,7 +466,8 @@ hipError_t bwd(const ScanArgs &a, const ScanPlan &plan, hipStream_t stream) {
             out.tok = (int64_t)a.ngroups * a.dstate;
         }
         e = launch_kernel(ks_bwd_main<Tin, Tdy, LPC>, grid, dim3(256), 0, stream, LaunchEvents{}, in, dy, a.dys,
-                          a.dfinal, (const float *)a.seg_adj, (const float *)a.tile_state, plan.tiles, out);
+                          a.dfinal, (const float *)a.seg_state, (const float *)a.seg_adj,
+                          (const float *)a.tile_state, (const float *)a.tile_steps, plan.tiles, out);
         if (e != hipSuccess) return e;
     }
     const BwdSums s{a.dap, a.ddp, a.dbiasp, a.dbp, a.dcp, a.dA, a.dD, a.ddt_bias, a.dB, a.dC,
@@ -415,7 +482,6 @@ hipError_t bwd(const ScanArgs &a, const ScanPlan &plan, hipStream_t stream) {
 template <typename Tin, typename Tdy>
 hipError_t bwd_np(const ScanArgs &a, const ScanPlan &plan, hipStream_t s) {
     switch (plan.np) {
-        case 8: return bwd<Tin, Tdy, 2>(a, plan, s);
         case 16: return bwd<Tin, Tdy, 4>(a, plan, s);
         case 32: return bwd<Tin, Tdy, 8>(a, plan, s);
         case 64: return bwd<Tin, Tdy, 16>(a, plan, s);

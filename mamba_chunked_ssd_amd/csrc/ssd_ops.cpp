@@ -35,17 +35,17 @@ ConvBwdPlan conv_bwd_plan(int64_t batch, int64_t seqlen, int64_t channels) {
 // more than half of the 1024 SIMDs without a wave.
 ScanPlan scan_plan(int64_t batch, int64_t seqlen, int64_t channels, int64_t dstate, int64_t ngroups, bool backward) {
     ScanPlan p;
-    (void)backward;
-    const int64_t cpg = channels / ngroups, cb = scan_block_channels(dstate);
-    p.np = padded_states(dstate);
+    // the backward pass has no layout of two lanes a channel (its registers do not hold 8 tokens a lane)
+    p.np = backward ? std::max(16, padded_states(dstate)) : padded_states(dstate);
+    const int64_t cpg = channels / ngroups, cb = 1024 / p.np;
     p.gblocks = (int)((cpg + cb - 1) / cb);
     p.nblk = (int)(ngroups * p.gblocks);
-    p.tiles = (seqlen + kScanTile - 1) / kScanTile;
+    p.tiles = (seqlen + kScanSegment - 1) / kScanSegment * (kScanSegment / kScanTile);
     const int64_t waves = std::max<int64_t>(1, batch * p.nblk * 4);
     int64_t nseg = waves >= 1024 ? 1 : (2048 + waves - 1) / waves;
     nseg = std::max<int64_t>(1, std::min<int64_t>(nseg, seqlen / 64));
     int64_t len = (seqlen + nseg - 1) / nseg;
-    len = std::max<int64_t>(kScanTile, (len + kScanTile - 1) / kScanTile * kScanTile);
+    len = std::max<int64_t>(kScanSegment, (len + kScanSegment - 1) / kScanSegment * kScanSegment);
     p.seglen = (int)len;
     p.nseg = (int)std::max<int64_t>(1, (seqlen + len - 1) / len);
     return p;
@@ -54,6 +54,7 @@ ScanPlan scan_plan(int64_t batch, int64_t seqlen, int64_t channels, int64_t dsta
 namespace {
 
 constexpr int64_t kMaxLen = (int64_t)1 << 30;
+constexpr int64_t kMaxRow = (int64_t)1 << 24;
 
 bool product(std::initializer_list<int64_t> v, int64_t *out) {
     int64_t r = 1;
@@ -74,6 +75,7 @@ ssd_status rows_of(const ssd_stride &in, int64_t batch, int64_t seqlen, int64_t 
     if (!product({batch, seqlen, width}, &dense)) return SSD_ERROR_UNSUPPORTED;
     if (s.batch == 0 && s.row == 0) s = Strides{seqlen * width, width};
     if (s.batch < 0 || s.row < 0 || (seqlen > 1 && s.row < width)) return SSD_ERROR_INVALID_VALUE;
+    if (seqlen <= 1) s.row = width;  // plays no part
     *out = s;
     *bytes = 0;
     if (batch == 0 || seqlen == 0) return SSD_OK;
@@ -186,7 +188,7 @@ ssd_status check_scan(const ssd_selective_shape *s, ScanArgs *a, ScanBytes *n) {
     if (!dtype_ok(s->dtype) || (s->y_dtype != SSD_DTYPE_F32 && s->y_dtype != s->dtype)) return SSD_ERROR_INVALID_VALUE;
     if ((s->flags & ~(uint32_t)SSD_SCAN_DT_SOFTPLUS) != 0) return SSD_ERROR_INVALID_VALUE;
     if (s->dstate > 64) return SSD_ERROR_UNSUPPORTED;
-    if (s->batch > 65535 || s->seqlen > kMaxLen || s->channels > kMaxLen / 64) return SSD_ERROR_UNSUPPORTED;
+    if (s->batch > 65535 || s->seqlen > kMaxLen || s->channels >= kMaxRow) return SSD_ERROR_UNSUPPORTED;
     *a = ScanArgs{};
     *n = ScanBytes{};
     const size_t i = size_of(s->dtype), o = size_of(s->y_dtype);
@@ -203,6 +205,7 @@ ssd_status check_scan(const ssd_selective_shape *s, ScanArgs *a, ScanBytes *n) {
     for (const auto &r : rows) {
         const ssd_status st = rows_of(r.in, s->batch, s->seqlen, r.width, r.esz, r.out, r.bytes);
         if (st != SSD_OK) return st;
+        if (r.out->row >= kMaxRow) return SSD_ERROR_UNSUPPORTED;  // a tile's rows within 32-bit byte offsets
     }
     const ScanPlan p = scan_plan(s->batch, s->seqlen, s->channels, s->dstate, s->ngroups, true);
     int64_t t;
@@ -261,6 +264,7 @@ size_t scan_bwd_carve(ScanArgs *a, const ScanPlan &p, void *ws) {
         a->seg_state = w.take(segs * p.np);
         a->seg_adj = w.take(segs * p.np);
         a->seg_steps = w.take(segs);
+        a->tile_steps = w.take((size_t)a->batch * p.tiles * a->channels);
     }
     a->tile_state = w.take((size_t)a->batch * p.tiles * a->channels * p.np);
     const size_t bc = (size_t)p.nblk * a->batch * a->seqlen * a->dstate;

@@ -115,23 +115,16 @@ __device__ __forceinline__ float logistic(float v) {
     return __builtin_amdgcn_rcpf(1.f + fast_exp2(-kLog2e * v));
 }
 
-// log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1], and
-// log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3, by the odd series of atanh to
-// s^15 (the rest is below 1e-9 of the sum).  1 + e is never formed, so small e
-// keep their relative accuracy: step sizes near 1e-3 come from such e.
+// log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1].  u = 1 + e
+// drops low bits of e; e - (u - 1) is that loss exactly, and to first order
+// log1p(e) = log(u) + (e - (u - 1)) / u, where / u matters only once the loss
+// itself is below half a unit of log(u)'s last place.  So step sizes near
+// 1e-3, which come from small e, keep their relative accuracy.
 __device__ __forceinline__ float softplus(float v) {
     const float e = fast_exp2(-kLog2e * __builtin_fabsf(v));
-    const float s = e * __builtin_amdgcn_rcpf(2.f + e);
-    const float q = s * s;
-    float r = 1.f / 15.f;
-    r = fmaf(r, q, 1.f / 13.f);
-    r = fmaf(r, q, 1.f / 11.f);
-    r = fmaf(r, q, 1.f / 9.f);
-    r = fmaf(r, q, 1.f / 7.f);
-    r = fmaf(r, q, 1.f / 5.f);
-    r = fmaf(r, q, 1.f / 3.f);
-    r = fmaf(r, q, 1.f);
-    return fmaf(2.f * s, r, fmaxf(v, 0.f));
+    const float u = 1.f + e;
+    const float lost = e - (u - 1.f);
+    return fmaf(__builtin_amdgcn_logf(u), 0.6931471805599453f, lost) + fmaxf(v, 0.f);
 }
 
 // v moved by one DPP control (every lane of the controls used has a source).
@@ -200,6 +193,73 @@ __device__ __forceinline__ float lane_total(float v) {
     if constexpr (LPC >= 4) v += lane_swap<2>(v);
     v += lane_swap<1>(v);
     return v;
+}
+
+// Sums over the channels of a wave, each channel on LPC neighbouring lanes:
+// v[q][r], r < 4, is a lane's value number r of sum q.  Each step adds two
+// lanes' values and hands one half of the sums to each, so a lane ends with
+// one value a sum: that of r = channel_sum_r(lane), over the channels that lie
+// on lanes of the same 64 / (16 .. 64) part.  Rows of 16 lanes hold 16 / LPC
+// channels; within them a DPP add writes only the quads (bank_mask) that keep
+// its half, two instructions for a pair of values.  (The matrix units would
+// take the sum over lanes too, but fp32 products run on the vector units'
+// time: 41 cycles each beside 4.4 for a fused multiply-add, measured, with
+// nothing gained by interleaving.)
+template <int LPC>
+__device__ __forceinline__ int channel_sum_r(int lane) {
+    if constexpr (LPC == 4) return lane >> 2 & 3;
+    else if constexpr (LPC == 8) return (lane >> 4 & 1) + 2 * (lane >> 3 & 1);
+    else return (lane >> 4 & 1) + 2 * (lane >> 5 & 1);
+}
+// Which part a lane's sum covers, of 64 / (4 LPC).
+template <int LPC>
+__device__ __forceinline__ int channel_sum_part(int lane) {
+    return LPC == 4 ? lane >> 4 : LPC == 8 ? lane >> 5 : 0;
+}
+template <int LPC>
+__device__ __forceinline__ void channel_sums(const float (&v)[2][4], float &s0, float &s1) {
+    if constexpr (LPC == 4) {
+        float a, b, c, d;
+        // lanes 8-15 of a row keep r + 2, then odd quads r + 1.  A DPP operand must have been written two
+        // instructions before: the nop covers the values coming in, the order those within.
+        asm("s_nop 1\n\t"
+            "v_add_f32_dpp %2, %6, %6 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+            "v_add_f32_dpp %2, %8, %8 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+            "v_add_f32_dpp %3, %7, %7 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+            "v_add_f32_dpp %3, %9, %9 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+            "v_add_f32_dpp %4, %10, %10 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+            "v_add_f32_dpp %4, %12, %12 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+            "v_add_f32_dpp %5, %11, %11 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+            "v_add_f32_dpp %5, %13, %13 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+            "v_add_f32_dpp %0, %2, %2 row_shl:4 row_mask:0xf bank_mask:0x5\n\t"
+            "v_add_f32_dpp %0, %3, %3 row_shr:4 row_mask:0xf bank_mask:0xa\n\t"
+            "v_add_f32_dpp %1, %4, %4 row_shl:4 row_mask:0xf bank_mask:0x5\n\t"
+            "v_add_f32_dpp %1, %5, %5 row_shr:4 row_mask:0xf bank_mask:0xa"
+            : "=&v"(s0), "=&v"(s1), "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d)
+            : "v"(v[0][0]), "v"(v[0][1]), "v"(v[0][2]), "v"(v[0][3]), "v"(v[1][0]), "v"(v[1][1]), "v"(v[1][2]),
+              "v"(v[1][3]));
+    } else {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            float x, y;
+            if constexpr (LPC == 8) {
+                const bool upper = (threadIdx.x & 8) != 0;
+                const float a = v[q][0] + lane_swap<8>(v[q][0]), b = v[q][2] + lane_swap<8>(v[q][2]);
+                const float c = v[q][1] + lane_swap<8>(v[q][1]), d = v[q][3] + lane_swap<8>(v[q][3]);
+                x = upper ? b : a;
+                y = upper ? d : c;
+            } else {
+                // lanes 32-63 of the first and 0-31 of the second change places
+                const auto e = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[q][0]), __float_as_uint(v[q][2]), false, false);
+                const auto o = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[q][1]), __float_as_uint(v[q][3]), false, false);
+                x = __uint_as_float(e[0]) + __uint_as_float(e[1]);
+                y = __uint_as_float(o[0]) + __uint_as_float(o[1]);
+            }
+            // odd rows of the first and even rows of the second change places
+            const auto w = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+            (q == 0 ? s0 : s1) = __uint_as_float(w[0]) + __uint_as_float(w[1]);
+        }
+    }
 }
 
 // f(integral constant k) for k = 0 .. N - 1 (DPP controls are immediates).

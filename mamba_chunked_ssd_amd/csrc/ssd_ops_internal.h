@@ -56,19 +56,19 @@ hipError_t launch_conv_step(const ConvArgs &a, hipStream_t stream);
 // ---------------------------------------------------------------------------
 
 // Each channel's states are spread over 2, 4, 8 or 16 lanes, 4 states a lane;
-// a block of 256 threads holds 1024 / padded_states(dstate) channels.
+// a block of 256 threads holds 1024 / (padded states) channels.
 inline int padded_states(int64_t dstate) { return dstate <= 8 ? 8 : dstate <= 16 ? 16 : dstate <= 32 ? 32 : 64; }
-inline int scan_block_channels(int64_t dstate) { return 1024 / padded_states(dstate); }
 
-constexpr int kScanTile = 16;  // tokens between the states that the backward pass keeps
+constexpr int kScanTile = 8;    // tokens between the states that the backward pass keeps
+constexpr int kScanSegment = 16;  // segments start at multiples of this
 
 struct ScanPlan {
     int np;           // padded states
     int gblocks;      // blocks of one group
     int nblk;         // blocks of one batch entry: ngroups * gblocks
     int nseg;         // segments of the time axis
-    int seglen;       // tokens of one, a multiple of kScanTile
-    int64_t tiles;    // tiles of kScanTile tokens in seqlen
+    int seglen;       // tokens of one, a multiple of kScanSegment
+    int64_t tiles;    // tiles of kScanTile tokens in seqlen, rounded up to whole kScanSegments
 };
 ScanPlan scan_plan(int64_t batch, int64_t seqlen, int64_t channels, int64_t dstate, int64_t ngroups, bool backward);
 
@@ -93,6 +93,7 @@ struct ScanArgs {
     float *dx, *ddt, *dA, *dB, *dC, *dD, *dz, *ddt_bias, *dinit;
     float *seg_adj;     // as seg_state, for the gradient at each segment's end
     float *tile_state;  // state before each tile, (batch, tiles, channels, np)
+    float *tile_steps;  // sum of the segment's steps before each tile (nseg > 1)
     float *dbp, *dcp;   // partial dB, dC per block of a group, (nblk, batch, seqlen, dstate)
     float *dap;         // partial dA, (batch, nseg, channels, np)
     float *ddp, *dbiasp;  // partial dD and ddt_bias, (batch, nseg, channels)
