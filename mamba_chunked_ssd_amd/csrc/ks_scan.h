@@ -97,11 +97,18 @@ struct TileRows {
     }
 };
 
-__device__ __forceinline__ float raw_load(const float *, __amdgpu_buffer_rsrc_t r, uint32_t off) {
-    return buffer_load_f32(r, (int)off);
+// Loaded bits are widened only where they are used: a shift beside the load
+// would wait for it, and the loads of the next tile are to be in flight over
+// this one's work.
+__device__ __forceinline__ uint32_t raw_load(const float *, __amdgpu_buffer_rsrc_t r, uint32_t off) {
+    return __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0);
 }
-__device__ __forceinline__ float raw_load(const uint16_t *, __amdgpu_buffer_rsrc_t r, uint32_t off) {
-    return bf16_to_f32((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)off, 0, 0));
+__device__ __forceinline__ uint32_t raw_load(const uint16_t *, __amdgpu_buffer_rsrc_t r, uint32_t off) {
+    return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)off, 0, 0);
+}
+template <typename T>
+__device__ __forceinline__ float widen(uint32_t bits) {
+    return sizeof(T) == 2 ? bf16_to_f32(bits) : __uint_as_float(bits);
 }
 __device__ __forceinline__ void raw_store(float *, __amdgpu_buffer_rsrc_t r, uint32_t off, float v) {
     __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, (int)off, 0, 0);
@@ -130,7 +137,7 @@ struct OwnRows {
         if constexpr (!HOLD) asm volatile("" : "+v"(o));
         return o;
     }
-    __device__ __forceinline__ void load(int left, float (&v)[TPL]) const {
+    __device__ __forceinline__ void load(int left, uint32_t (&v)[TPL]) const {
         const __amdgpu_buffer_rsrc_t r = rows.tile(left);
         const uint32_t o = base();
 #pragma unroll
@@ -150,8 +157,7 @@ template <int TT, int NP, typename T>
 struct RowStage {
     static constexpr int E = (TT * NP + 255) / 256;
     TileRows<TT, T> rows;
-    uint32_t off[E];
-    float v[E];
+    uint32_t off[E], v[E];
     __device__ __forceinline__ RowStage(const T *p, const Strides &s, int b, int g, int N, int t, bool forwards = true)
         : rows(p, s, b, t, forwards) {
 #pragma unroll
@@ -170,19 +176,19 @@ struct RowStage {
 #pragma unroll
         for (int k = 0; k < E; ++k) {
             const int e = threadIdx.x + 256 * k;
-            if (TT * NP >= 256 * (k + 1) || e < TT * NP) lds[e] = v[k];
+            if (TT * NP >= 256 * (k + 1) || e < TT * NP) lds[e] = widen<T>(v[k]);
         }
     }
 };
 
 // Step sizes of a lane's own tokens; tokens behind the end take a step of 0,
 // so the state stays.
-template <int TT, int LPC>
-__device__ __forceinline__ void step_sizes(const float (&dt)[own_tokens<TT, LPC>()], float bias, bool sp, int left, int j,
+template <int TT, int LPC, typename T>
+__device__ __forceinline__ void step_sizes(const uint32_t (&dt)[own_tokens<TT, LPC>()], float bias, bool sp, int left, int j,
                                            float (&d)[own_tokens<TT, LPC>()]) {
     constexpr int TPL = own_tokens<TT, LPC>();
 #pragma unroll
-    for (int i = 0; i < TPL; ++i) d[i] = dt[i] + bias;
+    for (int i = 0; i < TPL; ++i) d[i] = widen<T>(dt[i]) + bias;
     if (sp) {
 #pragma unroll
         for (int i = 0; i < TPL; ++i) d[i] = softplus(d[i]);
@@ -260,6 +266,34 @@ __device__ __forceinline__ void store_states_n(float *p, int n0, int N, const fl
 #pragma unroll
     for (int r = 0; r < 4; ++r)
         if (n0 + r < N) p[n0 + r] = h[r];
+}
+
+// One state of one channel over the segments, in their order (or backwards,
+// for the gradient): each slot's own end value gives way to the value it
+// starts from, h <- exp2(A2 sum of steps) h + own.  Eight slots are loaded
+// before the first is overwritten, or every load would wait for the store
+// before it.
+__device__ __forceinline__ float carry_segments(float h, float A2, float *state, const float *steps, int64_t state_stride,
+                                                int64_t steps_stride, int nseg, bool backwards) {
+    constexpr int G = 8;
+    for (int q = 0; q < nseg; q += G) {
+        float own[G], d[G];
+#pragma unroll
+        for (int e = 0; e < G; ++e) {
+            const int k = backwards ? nseg - 1 - q - e : q + e;
+            own[e] = q + e < nseg ? state[k * state_stride] : 0.f;
+            d[e] = q + e < nseg ? steps[k * steps_stride] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < G; ++e) {
+            const int k = backwards ? nseg - 1 - q - e : q + e;
+            if (q + e < nseg) {
+                state[k * state_stride] = h;
+                h = fmaf(fast_exp2(A2 * d[e]), h, own[e]);
+            }
+        }
+    }
+    return h;
 }
 
 template <typename T>

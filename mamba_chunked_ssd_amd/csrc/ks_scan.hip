@@ -37,7 +37,7 @@ __global__ __launch_bounds__(256) void ks_scan(ScanIn<Tin> a, const float *init,
         zs(gate ? a.z : a.x, gate ? a.zs : a.xs, b, c, at.j, at.ok, at.s0);
     OwnRows<kTT, LPC, Tout> ys(y, Strides{(int64_t)a.L * a.channels, a.channels}, b, c, at.j, at.ok, at.s0);
     RowStage<kTT, NP, Tin> rB(a.B, a.Bs, b, at.g, a.N, at.s0), rC(a.C, a.Cs, b, at.g, a.N, at.s0);
-    float dr[TPL], xr[TPL], zr[TPL];
+    uint32_t dr[TPL], xr[TPL], zr[TPL];
     auto fetch = [&](int left) {
         dts.load(left, dr);
         xs.load(left, xr);
@@ -57,15 +57,18 @@ __global__ __launch_bounds__(256) void ks_scan(ScanIn<Tin> a, const float *init,
         rB.store(sB[buf]);
         if (!SUMMARY) rC.store(sC[buf]);
         float d[TPL], x[TPL], scale[TPL];
-        step_sizes<kTT, LPC>(dr, bias, a.softplus, left, at.j, d);
+        step_sizes<kTT, LPC, Tin>(dr, bias, a.softplus, left, at.j, d);
 #pragma unroll
         for (int i = 0; i < TPL; ++i) {
-            x[i] = xr[i];
+            x[i] = widen<Tin>(xr[i]);
             scale[i] = 1.f;
         }
         if (gate) {
 #pragma unroll
-            for (int i = 0; i < TPL; ++i) scale[i] = zr[i] * logistic(zr[i]);
+            for (int i = 0; i < TPL; ++i) {
+                const float z = widen<Tin>(zr[i]);
+                scale[i] = z * logistic(z);
+            }
         }
         __syncthreads();  // also: the buffer stored next was last read before this barrier
         if (left > kTT) fetch(left - kTT);
@@ -128,15 +131,10 @@ __global__ __launch_bounds__(256) void ks_carry(const float *__restrict__ A, con
     const bool ok = n < N;
     const int64_t bcn = ((int64_t)b * channels + c) * N + n;
     const float A2 = ok ? kLog2e * A[(int64_t)c * N + n] : 0.f;
-    float h = ok && init != nullptr ? init[bcn] : 0.f;
-    float *s = seg_state + (int64_t)b * nseg * channels * NP + i;
-    const float *sum = seg_steps + (int64_t)b * nseg * channels + c;
-#pragma unroll 4
-    for (int k = 0; k < nseg; ++k) {
-        const float own = s[(int64_t)k * channels * NP], d = sum[(int64_t)k * channels];
-        s[(int64_t)k * channels * NP] = h;
-        h = fmaf(fast_exp2(A2 * d), h, own);
-    }
+    const float h = carry_segments(ok && init != nullptr ? init[bcn] : 0.f, A2,
+                                   seg_state + (int64_t)b * nseg * channels * NP + i,
+                                   seg_steps + (int64_t)b * nseg * channels + c, (int64_t)channels * NP, channels, nseg,
+                                   false);
     if (ok && final_state != nullptr) final_state[bcn] = h;
 }
 

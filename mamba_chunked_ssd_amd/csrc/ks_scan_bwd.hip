@@ -58,7 +58,7 @@ __global__ __launch_bounds__(256) void ks_bwd_sweep(ScanIn<Tin> a, const Tdy *__
         zs(gate ? a.z : a.x, gate ? a.zs : a.xs, b, c, at.j, at.ok, at.s0);
     OwnRows<kTT, LPC, Tdy> gs(dy, dys, b, c, at.j, at.ok, at.s0);
     RowStage<kTT, NP, Tin> rB(a.B, a.Bs, b, at.g, a.N, at.s0), rC(a.C, a.Cs, b, at.g, a.N, at.s0);
-    float dr[TPL], xr[TPL], zr[TPL], gr[TPL];
+    uint32_t dr[TPL], xr[TPL], zr[TPL], gr[TPL];
     auto fetch = [&](int left) {
         dts.load(left, dr);
         xs.load(left, xr);
@@ -84,9 +84,9 @@ __global__ __launch_bounds__(256) void ks_bwd_sweep(ScanIn<Tin> a, const Tdy *__
         rB.store(sB[buf]);
         if constexpr (SEGS) rC.store(sC[buf]);
         float d[TPL], u[TPL], o[TPL];
-        step_sizes<kTT, LPC>(dr, bias, a.softplus, left, at.j, d);
+        step_sizes<kTT, LPC, Tin>(dr, bias, a.softplus, left, at.j, d);
 #pragma unroll
-        for (int i = 0; i < TPL; ++i) u[i] = d[i] * xr[i];
+        for (int i = 0; i < TPL; ++i) u[i] = d[i] * widen<Tin>(xr[i]);
         float first = 0.f, second = 0.f;  // sums of the steps of the two tiles
         if constexpr (SEGS) {
 #pragma unroll
@@ -94,13 +94,16 @@ __global__ __launch_bounds__(256) void ks_bwd_sweep(ScanIn<Tin> a, const Tdy *__
                 const bool early = i * LPC + at.j < kScanTile;
                 first += early ? d[i] : 0.f;
                 second += early ? 0.f : d[i];
-                o[i] = gr[i];
+                o[i] = widen<Tdy>(gr[i]);
             }
             first = lane_total<LPC>(first);
             second = lane_total<LPC>(second);
             if (gate) {
 #pragma unroll
-                for (int i = 0; i < TPL; ++i) o[i] *= zr[i] * logistic(zr[i]);
+                for (int i = 0; i < TPL; ++i) {
+                    const float z = widen<Tin>(zr[i]);
+                    o[i] *= z * logistic(z);
+                }
             }
         }
         // the state before a tile
@@ -165,16 +168,10 @@ __global__ __launch_bounds__(256) void ks_bwd_carry(const float *__restrict__ A,
     const int64_t bcn = ((int64_t)b * channels + c) * N + n;
     const float A2 = ok ? kLog2e * A[(int64_t)c * N + n] : 0.f;
     const float *from = adj ? dfinal : init;
-    float h = ok && from != nullptr ? from[bcn] : 0.f;
-    float *s = (adj ? seg_adj : seg_state) + (int64_t)b * nseg * channels * NP + i;
-    const float *sum = seg_steps + (int64_t)b * nseg * channels + c;
-#pragma unroll 4
-    for (int q = 0; q < nseg; ++q) {
-        const int k = adj ? nseg - 1 - q : q;
-        const float own = s[(int64_t)k * channels * NP], d = sum[(int64_t)k * channels];
-        s[(int64_t)k * channels * NP] = h;
-        h = fmaf(fast_exp2(A2 * d), h, own);
-    }
+    const float h = carry_segments(ok && from != nullptr ? from[bcn] : 0.f, A2,
+                                   (adj ? seg_adj : seg_state) + (int64_t)b * nseg * channels * NP + i,
+                                   seg_steps + (int64_t)b * nseg * channels + c, (int64_t)channels * NP, channels, nseg,
+                                   adj);
     if (adj && ok && dinit != nullptr) dinit[bcn] = h;
 }
 
@@ -253,7 +250,8 @@ __global__ __launch_bounds__(256, 2) void ks_bwd_main(ScanIn<Tin> a, const Tdy *
         dc[p] = 0.f;
     }
 
-    float dr[TPL], xr[TPL], zr[TPL], gr[TPL], hr[4], sr = 0.f;
+    uint32_t dr[TPL], xr[TPL], zr[TPL], gr[TPL];
+    float hr[4], sr = 0.f;
     const BlockRows<LPC> mine(at.ok, at.j, at.cl);
     int64_t tile = ((int64_t)b * tiles + last / TT) * a.channels + at.c0;
     auto fetch = [&](int left) {
@@ -279,20 +277,20 @@ __global__ __launch_bounds__(256, 2) void ks_bwd_main(ScanIn<Tin> a, const Tdy *
         rB.store(sB);
         rC.store(sC);
         float d[TPL], u[TPL], x[TPL], o[TPL], sl[TPL], zy[TPL], h0[4];
-        step_sizes<TT, LPC>(dr, bias, a.softplus, left, at.j, d);
+        step_sizes<TT, LPC, Tin>(dr, bias, a.softplus, left, at.j, d);
 #pragma unroll
         for (int i = 0; i < TPL; ++i) {
-            x[i] = xr[i];
+            x[i] = widen<Tin>(xr[i]);
             u[i] = d[i] * x[i];
-            o[i] = gr[i];
-            sl[i] = a.softplus ? logistic(dr[i] + bias) : 1.f;  // softplus'
+            o[i] = widen<Tdy>(gr[i]);
+            sl[i] = a.softplus ? logistic(widen<Tin>(dr[i]) + bias) : 1.f;  // softplus'
         }
         if (gate) {
 #pragma unroll
             for (int i = 0; i < TPL; ++i) {
-                const float s = logistic(zr[i]);
-                zy[i] = o[i] * (s * fmaf(zr[i], 1.f - s, 1.f));  // dy silu'(z)
-                o[i] *= zr[i] * s;
+                const float z = widen<Tin>(zr[i]), s = logistic(z);
+                zy[i] = o[i] * (s * fmaf(z, 1.f - s, 1.f));  // dy silu'(z)
+                o[i] *= z * s;
             }
         }
         if (left < TT || TT < LPC) {
@@ -396,7 +394,8 @@ __global__ __launch_bounds__(256, 2) void ks_bwd_main(ScanIn<Tin> a, const Tdy *
 
 // The last sums, in a fixed order and 64 bits: dA, dD and ddt_bias over batch
 // and segments; dB and dC over the blocks of each group (gblocks 1: written
-// in place already).
+// in place already).  Eight threads an output, each every eighth term, so that
+// few outputs of many terms still have their loads in flight together.
 struct BwdSums {
     const float *dap, *ddp, *dbiasp, *dbp, *dcp;
     float *dA, *dD, *ddt_bias, *dB, *dC;
@@ -404,37 +403,47 @@ struct BwdSums {
     int64_t rows;         // batch * seqlen
     int channels, N, NP, ngroups, gblocks;
 };
+constexpr int kSumSlices = 8;
 __global__ __launch_bounds__(256) void ks_bwd_sums(BwdSums s, int64_t nA, int64_t nBC) {
-    int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    constexpr int COLS = 256 / kSumSlices;
+    __shared__ double part[256];
+    const int slice = threadIdx.x / COLS;
+    int64_t i = (int64_t)blockIdx.x * COLS + threadIdx.x % COLS;
+    const float *from = nullptr;
+    float *to = nullptr;
+    int64_t terms = s.slots, stride = 0;
     if (i < nA) {
-        const int64_t c = i / s.N, n = i % s.N;
-        double v = 0.0;
-        for (int64_t k = 0; k < s.slots; ++k) v += (double)s.dap[(k * s.channels + c) * s.NP + n];
-        s.dA[i] = (float)v;
-        return;
-    }
-    i -= nA;
-    if (i < 2 * (int64_t)s.channels) {
+        from = s.dap + i / s.N * s.NP + i % s.N;
+        stride = (int64_t)s.channels * s.NP;
+        to = s.dA + i;
+    } else if ((i -= nA) < 2 * (int64_t)s.channels) {
         const bool first = i < s.channels;
         const int64_t c = first ? i : i - s.channels;
-        float *to = first ? s.dD : s.ddt_bias;
-        if (to == nullptr) return;
-        const float *from = first ? s.ddp : s.dbiasp;
-        double v = 0.0;
-        for (int64_t k = 0; k < s.slots; ++k) v += (double)from[k * s.channels + c];
-        to[c] = (float)v;
-        return;
+        from = (first ? s.ddp : s.dbiasp) + c;
+        stride = s.channels;
+        to = first ? s.dD : s.ddt_bias;
+        to = to != nullptr ? to + c : nullptr;
+    } else if ((i -= 2 * (int64_t)s.channels) < 2 * nBC) {
+        const bool first = i < nBC;
+        if (!first) i -= nBC;
+        const int64_t n = i % s.N, g = i / s.N % s.ngroups, row = i / ((int64_t)s.N * s.ngroups);
+        from = (first ? s.dbp : s.dcp) + (g * s.gblocks * s.rows + row) * s.N + n;
+        stride = s.rows * s.N;
+        terms = s.gblocks;
+        to = (first ? s.dB : s.dC) + i;
     }
-    i -= 2 * (int64_t)s.channels;
-    if (i >= 2 * nBC) return;
-    const bool first = i < nBC;
-    if (!first) i -= nBC;
-    const int64_t n = i % s.N, g = i / s.N % s.ngroups, row = i / ((int64_t)s.N * s.ngroups);
-    const float *from = (first ? s.dbp : s.dcp) + (g * s.gblocks * s.rows + row) * s.N + n;
     double v = 0.0;
+    if (to != nullptr) {
 #pragma unroll 8
-    for (int k = 0; k < s.gblocks; ++k) v += (double)from[(int64_t)k * s.rows * s.N];
-    (first ? s.dB : s.dC)[i] = (float)v;
+        for (int64_t k = slice; k < terms; k += kSumSlices) v += (double)from[k * stride];
+    }
+    part[threadIdx.x] = v;
+    __syncthreads();
+    if (slice == 0 && to != nullptr) {
+#pragma unroll
+        for (int q = 1; q < kSumSlices; ++q) v += part[q * COLS + threadIdx.x];
+        *to = (float)v;
+    }
 }
 
 template <typename Tin, typename Tdy, int LPC>
@@ -475,8 +484,8 @@ hipError_t bwd(const ScanArgs &a, const ScanPlan &plan, hipStream_t stream) {
     const int64_t nA = (int64_t)a.channels * a.dstate;
     const int64_t nBC = plan.gblocks == 1 ? 0 : a.batch * a.seqlen * a.ngroups * a.dstate;
     const int64_t n = nA + 2 * (int64_t)a.channels + 2 * nBC;
-    return launch_kernel(ks_bwd_sums, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, LaunchEvents{}, s, nA,
-                         nBC);
+    return launch_kernel(ks_bwd_sums, dim3((unsigned)((n + 256 / kSumSlices - 1) / (256 / kSumSlices))), dim3(256), 0,
+                         stream, LaunchEvents{}, s, nA, nBC);
 }
 
 template <typename Tin, typename Tdy>

@@ -30,9 +30,11 @@ ConvBwdPlan conv_bwd_plan(int64_t batch, int64_t seqlen, int64_t channels) {
     return p;
 }
 
-// Segments of the time axis.  A segment costs the summary pass (about 7/8 of
-// the output pass's work) once more, so it pays only where the channels leave
-// more than half of the 1024 SIMDs without a wave.
+// Segments of the time axis.  They cost the summary pass (two thirds of the
+// output pass's work; in the backward pass the sweep is there anyway) and a
+// carry whose time grows with their number, and pay by filling the SIMDs:
+// one wave alone runs at 45 % of a SIMD's rate, six at 80 %.
+constexpr int64_t kFwdWhole = 2048, kBwdWhole = 4096, kScanWaves = 16384;
 ScanPlan scan_plan(int64_t batch, int64_t seqlen, int64_t channels, int64_t dstate, int64_t ngroups, bool backward) {
     ScanPlan p;
     // the backward pass has no layout of two lanes a channel (its registers do not hold 8 tokens a lane)
@@ -42,8 +44,10 @@ ScanPlan scan_plan(int64_t batch, int64_t seqlen, int64_t channels, int64_t dsta
     p.nblk = (int)(ngroups * p.gblocks);
     p.tiles = (seqlen + kScanSegment - 1) / kScanSegment * (kScanSegment / kScanTile);
     const int64_t waves = std::max<int64_t>(1, batch * p.nblk * 4);
-    int64_t nseg = waves >= 1024 ? 1 : (2048 + waves - 1) / waves;
-    nseg = std::max<int64_t>(1, std::min<int64_t>(nseg, seqlen / 64));
+    int64_t root = 1;
+    while (root * root < seqlen) ++root;
+    int64_t nseg = waves >= (backward ? kBwdWhole : kFwdWhole) ? 1 : (kScanWaves + waves - 1) / waves;
+    nseg = std::max<int64_t>(1, std::min<int64_t>({nseg, seqlen / 32, root}));
     int64_t len = (seqlen + nseg - 1) / nseg;
     len = std::max<int64_t>(kScanSegment, (len + kScanSegment - 1) / kScanSegment * kScanSegment);
     p.seglen = (int)len;
