@@ -606,22 +606,20 @@ def tune(x, dt, A, B, C, D=None, chunk_size: int = 256, initial_states=None, *, 
 _ACTIVATIONS = {None: SSD_ACT_NONE, "silu": SSD_ACT_SILU}
 
 
-def _storage(t, name):
-    """dtype code of an operator's first input, which its other inputs share."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if t.device.type != "cuda":
-        raise ValueError("tensors must be on a ROCm device (got %s)" % t.device)
-    if t.dtype == torch.bfloat16:
+def _input_dtype(x, torch):
+    """ssd_dtype of an operator's first input, which its other inputs share."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if not x.is_cuda:
+        raise ValueError("tensors must be on a ROCm device (got %s)" % x.device)
+    if x.dtype == torch.bfloat16:
         return SSD_DTYPE_BF16
-    if t.dtype == torch.float32:
+    if x.dtype == torch.float32:
         return SSD_DTYPE_F32
-    raise TypeError("%s must be float32 or bfloat16" % name)
+    raise TypeError("x must be float32 or bfloat16")
 
 
-def _result_dtype(dtype, given, name):
-    torch = _torch()
+def _result_dtype(dtype, given, name, torch):
     if dtype is None or dtype == torch.float32:
         return torch.float32, SSD_DTYPE_F32
     if dtype != given:
@@ -629,57 +627,59 @@ def _result_dtype(dtype, given, name):
     return dtype, SSD_DTYPE_BF16
 
 
-def _rows(t, name, dtype, shape, device, tokens=True):
-    """Checks an input of one row per token (or, without ``tokens``, per batch
-    entry), whose rows may lie apart, and returns its ssd_stride."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if t.device != device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
-    if t.dtype != dtype:
-        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-    if t.shape != shape:
+def _dense(t, name, dtype, shape, device, tensor):
+    """As :func:`_check`, which words the error; one token's calls are as fast as their checks."""
+    if not (isinstance(t, tensor) and t.dtype == dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        _check(t, name, dtype, shape, device)
+
+
+def _rows(t, name, dtype, shape, device, tensor, lead):
+    """Checks an input of rows that may lie apart, one per token (``lead`` 2: batch and token) or per batch entry
+    (``lead`` 1), and returns its ssd_stride, None if it is dense."""
+    if isinstance(t, tensor) and t.dtype == dtype and t.shape == shape and t.device == device:
+        if t.is_contiguous():
+            return None
+        st = t.stride()
+        width = 1
+        for k in range(t.dim() - 1, lead - 1, -1):
+            if shape[k] != 1 and st[k] != width:
+                raise ValueError("%s: each row must be contiguous (strides %s)" % (name, st))
+            width *= shape[k]
+        tokens = shape[1] if lead == 2 else 1
+        row = st[1] if tokens > 1 else width
+        if row < width:
+            raise ValueError("%s: rows of different tokens overlap (strides %s)" % (name, st))
+        return Stride(st[0] if shape[0] > 1 else row * tokens, row)
+    if isinstance(t, tensor) and t.dtype == dtype and t.device == device:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if t.is_contiguous():
-        return 0, 0
-    st = t.stride()
-    lead = 2 if tokens else 1
-    width = 1
-    for k in range(t.dim() - 1, lead - 1, -1):
-        if shape[k] != 1 and st[k] != width:
-            raise ValueError("%s: each row must be contiguous (strides %s)" % (name, st))
-        width *= shape[k]
-    row = st[1] if tokens and shape[1] > 1 else width
-    if tokens and shape[1] > 1 and row < width:
-        raise ValueError("%s: rows of different tokens overlap (strides %s)" % (name, st))
-    return (st[0] if shape[0] > 1 else row * (shape[1] if tokens else 1)), row
+    return _check(t, name, dtype, shape, device)
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _call(where, device, stream, run):
-    """``run(stream handle)`` with ``device`` current; what it
-    allocates belongs to the stream that the kernels run on."""
-    torch = _torch()
-    if device.index != torch.cuda.current_device():
+def _call(where, device, stream, run, torch):
+    """``run(stream handle)`` with ``device`` current; what it allocates
+    belongs to the stream that the kernels run on."""
+    index = device.index
+    if index != torch.cuda.current_device():
         with torch.cuda.device(device):
-            return _call(where, device, stream, run)
+            return _call(where, device, stream, run, torch)
     if stream is None:
-        st, res = run(torch.cuda.current_stream(device).cuda_stream)
+        st, res = run(torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+        given = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+        with torch.cuda.stream(given):
             st, res = run(stream)
     if st != 0:
         raise SSDError(st, where)
     return res
 
 
-def _workspace(given, need, device):
-    """(address, bytes) of the caller's workspace or of a new one (kept by the third value)."""
-    torch = _torch()
+def _workspace(given, need, device, torch):
+    """(address, bytes, the tensor that holds them) of the caller's workspace or a new one."""
     if given is not None:
         if given.device != device or not given.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on %s" % device)
@@ -690,23 +690,25 @@ def _workspace(given, need, device):
     return ws.data_ptr(), need, ws
 
 
-def _conv_args(x, weight, bias, lengths, activation, tokens):
-    torch = _torch()
-    code = _storage(x, "x")
-    if x.dim() != (3 if tokens else 2) or weight.dim() != 2:
-        raise ValueError("x must be (batch, %schannels) and weight (channels, width)" % ("seqlen, " if tokens else ""))
+def _conv_args(x, weight, bias, lengths, activation, lead, torch):
+    tensor, f32 = torch.Tensor, torch.float32
+    code = _input_dtype(x, torch)
+    dims = x.shape
+    if len(dims) != lead + 1 or weight.dim() != 2:
+        raise ValueError("x must be (batch, %schannels) and weight (channels, width)" % ("seqlen, " if lead == 2 else ""))
     if activation not in _ACTIVATIONS:
         raise ValueError("activation must be None or 'silu'")
-    dev = x.device
-    b, c, w = x.shape[0], x.shape[-1], weight.shape[1]
-    L = x.shape[1] if tokens else 1
-    xs = _rows(x, "x", x.dtype, x.shape, dev, tokens)
-    _check(weight, "weight", torch.float32, (c, w), dev)
+    dev, b, c, w = x.device, dims[0], dims[-1], weight.shape[1]
+    L = dims[1] if lead == 2 else 1
+    shape = ConvShape(b, L, c, w, _ACTIVATIONS[activation], code)
+    st = _rows(x, "x", x.dtype, dims, dev, tensor, lead)
+    if st is not None:
+        shape.x = st
+    _dense(weight, "weight", f32, (c, w), dev, tensor)
     if bias is not None:
-        _check(bias, "bias", torch.float32, (c,), dev)
+        _dense(bias, "bias", f32, (c,), dev, tensor)
     if lengths is not None:
-        _check(lengths, "lengths", torch.int32, (b,), dev)
-    shape = ConvShape(b, L, c, w, _ACTIVATIONS[activation], code, 0, 0, 0, Stride(*xs), Stride(0, 0))
+        _dense(lengths, "lengths", torch.int32, (b,), dev, tensor)
     return shape, dev, b, L, c, w
 
 
@@ -724,14 +726,14 @@ def causal_conv_fwd(x, weight, bias=None, initial_states=None, return_final_stat
     ``final_out`` may be ``initial_states`` itself.
     """
     torch = _torch()
-    shape, dev, b, L, c, w = _conv_args(x, weight, bias, lengths, activation, True)
+    shape, dev, b, L, c, w = _conv_args(x, weight, bias, lengths, activation, 2, torch)
     if initial_states is not None:
-        _check(initial_states, "initial_states", x.dtype, (b, w - 1, c), dev)
-    ytype, shape.y_dtype = _result_dtype(y_dtype, x.dtype, "y_dtype")
+        _dense(initial_states, "initial_states", x.dtype, (b, w - 1, c), dev, torch.Tensor)
+    ytype, shape.y_dtype = _result_dtype(y_dtype, x.dtype, "y_dtype", torch)
     if out is not None:
-        _check(out, "out", ytype, (b, L, c), dev)
+        _dense(out, "out", ytype, (b, L, c), dev, torch.Tensor)
     if final_out is not None:
-        _check(final_out, "final_out", x.dtype, (b, w - 1, c), dev)
+        _dense(final_out, "final_out", x.dtype, (b, w - 1, c), dev, torch.Tensor)
 
     def run(handle):
         y = out if out is not None else torch.empty((b, L, c), dtype=ytype, device=dev)
@@ -743,7 +745,7 @@ def causal_conv_fwd(x, weight, bias=None, initial_states=None, return_final_stat
                                                 handle)
         return st, (y, fin) if return_final_states else y
 
-    return _call("ssd_causal_conv_fwd", dev, stream, run)
+    return _call("ssd_causal_conv_fwd", dev, stream, run, torch)
 
 
 def causal_conv_bwd(x, weight, bias, dy, initial_states=None, d_final_states=None, *, activation="silu",
@@ -758,14 +760,16 @@ def causal_conv_bwd(x, weight, bias, dy, initial_states=None, d_final_states=Non
     """
     torch = _torch()
     lib = load_library()
-    shape, dev, b, L, c, w = _conv_args(x, weight, bias, lengths, activation, True)
+    shape, dev, b, L, c, w = _conv_args(x, weight, bias, lengths, activation, 2, torch)
     if initial_states is not None:
-        _check(initial_states, "initial_states", x.dtype, (b, w - 1, c), dev)
+        _dense(initial_states, "initial_states", x.dtype, (b, w - 1, c), dev, torch.Tensor)
     if d_final_states is not None:
-        _check(d_final_states, "d_final_states", torch.float32, (b, w - 1, c), dev)
-    dytype, shape.y_dtype = _result_dtype(dy.dtype, x.dtype, "dy's dtype")
-    shape.dy = Stride(*_rows(dy, "dy", dytype, x.shape, dev))
-    dxtype, shape.dx_dtype = _result_dtype(dx_dtype, x.dtype, "dx_dtype")
+        _dense(d_final_states, "d_final_states", torch.float32, (b, w - 1, c), dev, torch.Tensor)
+    dytype, shape.y_dtype = _result_dtype(dy.dtype, x.dtype, "dy's dtype", torch)
+    st = _rows(dy, "dy", dytype, x.shape, dev, torch.Tensor, 2)
+    if st is not None:
+        shape.dy = st
+    dxtype, shape.dx_dtype = _result_dtype(dx_dtype, x.dtype, "dx_dtype", torch)
 
     def run(handle):
         f32 = dict(dtype=torch.float32, device=dev)
@@ -773,14 +777,14 @@ def causal_conv_bwd(x, weight, bias, dy, initial_states=None, d_final_states=Non
                "dbias": torch.empty((c,), **f32)}
         if want_d_initial:
             res["d_initial_states"] = torch.empty((b, max(w - 1, 0), c), **f32)
-        ws, size, _keep = _workspace(workspace, lib.ssd_causal_conv_bwd_workspace_size(ctypes.byref(shape)), dev)
+        ws, size, _keep = _workspace(workspace, lib.ssd_causal_conv_bwd_workspace_size(ctypes.byref(shape)), dev, torch)
         st = lib.ssd_causal_conv_bwd(ctypes.byref(shape), x.data_ptr(), weight.data_ptr(), _addr(bias),
                                      _addr(initial_states), _addr(lengths), dy.data_ptr(), _addr(d_final_states),
                                      res["dx"].data_ptr(), res["dweight"].data_ptr(), res["dbias"].data_ptr(),
                                      _addr(res.get("d_initial_states")), ws, size, handle)
         return st, res
 
-    return _call("ssd_causal_conv_bwd", dev, stream, run)
+    return _call("ssd_causal_conv_bwd", dev, stream, run, torch)
 
 
 def causal_conv_step(x, weight, bias, state, *, activation="silu", y_dtype=None, out=None, stream=None):
@@ -791,11 +795,11 @@ def causal_conv_step(x, weight, bias, state, *, activation="silu", y_dtype=None,
     x's dtype).
     """
     torch = _torch()
-    shape, dev, b, _, c, w = _conv_args(x, weight, bias, None, activation, False)
-    _check(state, "state", x.dtype, (b, w - 1, c), dev)
-    ytype, shape.y_dtype = _result_dtype(y_dtype, x.dtype, "y_dtype")
+    shape, dev, b, _, c, w = _conv_args(x, weight, bias, None, activation, 1, torch)
+    _dense(state, "state", x.dtype, (b, w - 1, c), dev, torch.Tensor)
+    ytype, shape.y_dtype = _result_dtype(y_dtype, x.dtype, "y_dtype", torch)
     if out is not None:
-        _check(out, "out", ytype, (b, c), dev)
+        _dense(out, "out", ytype, (b, c), dev, torch.Tensor)
 
     def run(handle):
         y = out if out is not None else torch.empty((b, c), dtype=ytype, device=dev)
@@ -803,32 +807,32 @@ def causal_conv_step(x, weight, bias, state, *, activation="silu", y_dtype=None,
                                                  state.data_ptr(), y.data_ptr(), handle)
         return st, y
 
-    return _call("ssd_causal_conv_step", dev, stream, run)
+    return _call("ssd_causal_conv_step", dev, stream, run, torch)
 
 
-def _scan_args(x, dt, A, B, C, D, z, dt_bias, lengths, dt_softplus, tokens):
-    torch = _torch()
-    code = _storage(x, "x")
-    lead = 2 if tokens else 1
-    if x.dim() != lead + 1 or B.dim() != lead + 2 or A.dim() != 2:
+def _scan_args(x, dt, A, B, C, D, z, dt_bias, lengths, dt_softplus, lead, torch):
+    tensor, f32 = torch.Tensor, torch.float32
+    code = _input_dtype(x, torch)
+    dims, of_b = x.shape, B.shape
+    if len(dims) != lead + 1 or len(of_b) != lead + 2 or A.dim() != 2:
         raise ValueError("x must be (batch, %schannels), B (batch, %sngroups, dstate) and A (channels, dstate)"
-                         % (("seqlen, ",) * 2 if tokens else ("", "")))
-    dev, dtype = x.device, x.dtype
-    b, c, g, n = x.shape[0], x.shape[-1], B.shape[-2], B.shape[-1]
-    L = x.shape[1] if tokens else 1
-    rows = torch.Size((b, L, g, n) if tokens else (b, g, n))
-    none = (0, 0)
-    shape = SelectiveShape(b, L, c, n, g, code, 0, SSD_SCAN_DT_SOFTPLUS if dt_softplus else 0, 0,
-                           _rows(x, "x", dtype, x.shape, dev, tokens), _rows(dt, "dt", dtype, x.shape, dev, tokens),
-                           _rows(B, "B", dtype, rows, dev, tokens), _rows(C, "C", dtype, rows, dev, tokens),
-                           none if z is None else _rows(z, "z", dtype, x.shape, dev, tokens), none)
-    _check(A, "A", torch.float32, (c, n), dev)
+                         % (("seqlen, ",) * 2 if lead == 2 else ("", "")))
+    dev, dtype, b, c, g, n = x.device, x.dtype, dims[0], dims[-1], of_b[-2], of_b[-1]
+    L = dims[1] if lead == 2 else 1
+    rows = (b, L, g, n) if lead == 2 else (b, g, n)
+    shape = SelectiveShape(b, L, c, n, g, code, 0, SSD_SCAN_DT_SOFTPLUS if dt_softplus else 0)
+    for name, t, want in (("x", x, dims), ("dt", dt, dims), ("B", B, rows), ("C", C, rows), ("z", z, dims)):
+        if t is not None or name != "z":
+            st = _rows(t, name, dtype, want, dev, tensor, lead)
+            if st is not None:
+                setattr(shape, name, st)
+    _dense(A, "A", f32, (c, n), dev, tensor)
     if D is not None:
-        _check(D, "D", torch.float32, (c,), dev)
+        _dense(D, "D", f32, (c,), dev, tensor)
     if dt_bias is not None:
-        _check(dt_bias, "dt_bias", torch.float32, (c,), dev)
+        _dense(dt_bias, "dt_bias", f32, (c,), dev, tensor)
     if lengths is not None:
-        _check(lengths, "lengths", torch.int32, (b,), dev)
+        _dense(lengths, "lengths", torch.int32, (b,), dev, tensor)
     return shape, dev, b, L, c, g, n
 
 
@@ -849,27 +853,27 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, initial_sta
     """
     torch = _torch()
     lib = load_library()
-    shape, dev, b, L, c, g, n = _scan_args(x, dt, A, B, C, D, z, dt_bias, lengths, dt_softplus, True)
+    shape, dev, b, L, c, g, n = _scan_args(x, dt, A, B, C, D, z, dt_bias, lengths, dt_softplus, 2, torch)
     if initial_states is not None:
-        _check(initial_states, "initial_states", torch.float32, (b, c, n), dev)
-    ytype, shape.y_dtype = _result_dtype(y_dtype, x.dtype, "y_dtype")
+        _dense(initial_states, "initial_states", torch.float32, (b, c, n), dev, torch.Tensor)
+    ytype, shape.y_dtype = _result_dtype(y_dtype, x.dtype, "y_dtype", torch)
     if out is not None:
-        _check(out, "out", ytype, (b, L, c), dev)
+        _dense(out, "out", ytype, (b, L, c), dev, torch.Tensor)
     if final_out is not None:
-        _check(final_out, "final_out", torch.float32, (b, c, n), dev)
+        _dense(final_out, "final_out", torch.float32, (b, c, n), dev, torch.Tensor)
 
     def run(handle):
         y = out if out is not None else torch.empty((b, L, c), dtype=ytype, device=dev)
         fin = final_out
         if fin is None and return_final_states:
             fin = torch.empty((b, c, n), dtype=torch.float32, device=dev)
-        ws, size, _keep = _workspace(workspace, lib.ssd_selective_scan_fwd_workspace_size(ctypes.byref(shape)), dev)
+        ws, size, _keep = _workspace(workspace, lib.ssd_selective_scan_fwd_workspace_size(ctypes.byref(shape)), dev, torch)
         st = lib.ssd_selective_scan_fwd(ctypes.byref(shape), x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(),
                                         C.data_ptr(), _addr(D), _addr(z), _addr(dt_bias), _addr(initial_states),
                                         _addr(lengths), y.data_ptr(), _addr(fin), ws, size, handle)
         return st, (y, fin) if return_final_states else y
 
-    return _call("ssd_selective_scan_fwd", dev, stream, run)
+    return _call("ssd_selective_scan_fwd", dev, stream, run, torch)
 
 
 def selective_scan_bwd(x, dt, A, B, C, D, dy, z=None, dt_bias=None, initial_states=None, d_final_states=None, *,
@@ -884,12 +888,14 @@ def selective_scan_bwd(x, dt, A, B, C, D, dy, z=None, dt_bias=None, initial_stat
     """
     torch = _torch()
     lib = load_library()
-    shape, dev, b, L, c, g, n = _scan_args(x, dt, A, B, C, D, z, dt_bias, lengths, dt_softplus, True)
+    shape, dev, b, L, c, g, n = _scan_args(x, dt, A, B, C, D, z, dt_bias, lengths, dt_softplus, 2, torch)
     for name, t in (("initial_states", initial_states), ("d_final_states", d_final_states)):
         if t is not None:
-            _check(t, name, torch.float32, (b, c, n), dev)
-    dytype, shape.y_dtype = _result_dtype(dy.dtype, x.dtype, "dy's dtype")
-    shape.dy = Stride(*_rows(dy, "dy", dytype, x.shape, dev))
+            _dense(t, name, torch.float32, (b, c, n), dev, torch.Tensor)
+    dytype, shape.y_dtype = _result_dtype(dy.dtype, x.dtype, "dy's dtype", torch)
+    st = _rows(dy, "dy", dytype, x.shape, dev, torch.Tensor, 2)
+    if st is not None:
+        shape.dy = st
 
     def run(handle):
         def new(*dims):
@@ -901,7 +907,7 @@ def selective_scan_bwd(x, dt, A, B, C, D, dy, z=None, dt_bias=None, initial_stat
             res["dz"] = new(b, L, c)
         if want_d_initial:
             res["d_initial_states"] = new(b, c, n)
-        ws, size, _keep = _workspace(workspace, lib.ssd_selective_scan_bwd_workspace_size(ctypes.byref(shape)), dev)
+        ws, size, _keep = _workspace(workspace, lib.ssd_selective_scan_bwd_workspace_size(ctypes.byref(shape)), dev, torch)
         st = lib.ssd_selective_scan_bwd(
             ctypes.byref(shape), x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _addr(D),
             _addr(z), _addr(dt_bias), _addr(initial_states), _addr(lengths), dy.data_ptr(), _addr(d_final_states),
@@ -910,7 +916,7 @@ def selective_scan_bwd(x, dt, A, B, C, D, dy, z=None, dt_bias=None, initial_stat
             _addr(res.get("d_initial_states")), ws, size, handle)
         return st, res
 
-    return _call("ssd_selective_scan_bwd", dev, stream, run)
+    return _call("ssd_selective_scan_bwd", dev, stream, run, torch)
 
 
 def selective_scan_step(x, dt, A, B, C, D, state, z=None, dt_bias=None, *, dt_softplus: bool = True, y_dtype=None,
@@ -922,11 +928,11 @@ def selective_scan_step(x, dt, A, B, C, D, state, z=None, dt_bias=None, *, dt_so
     dtype).
     """
     torch = _torch()
-    shape, dev, b, _, c, g, n = _scan_args(x, dt, A, B, C, D, z, dt_bias, None, dt_softplus, False)
-    _check(state, "state", torch.float32, (b, c, n), dev)
-    ytype, shape.y_dtype = _result_dtype(y_dtype, x.dtype, "y_dtype")
+    shape, dev, b, _, c, g, n = _scan_args(x, dt, A, B, C, D, z, dt_bias, None, dt_softplus, 1, torch)
+    _dense(state, "state", torch.float32, (b, c, n), dev, torch.Tensor)
+    ytype, shape.y_dtype = _result_dtype(y_dtype, x.dtype, "y_dtype", torch)
     if out is not None:
-        _check(out, "out", ytype, (b, c), dev)
+        _dense(out, "out", ytype, (b, c), dev, torch.Tensor)
 
     def run(handle):
         y = out if out is not None else torch.empty((b, c), dtype=ytype, device=dev)
@@ -935,4 +941,4 @@ def selective_scan_step(x, dt, A, B, C, D, state, z=None, dt_bias=None, *, dt_so
             _addr(z), _addr(dt_bias), state.data_ptr(), y.data_ptr(), handle)
         return st, y
 
-    return _call("ssd_selective_scan_step", dev, stream, run)
+    return _call("ssd_selective_scan_step", dev, stream, run, torch)
