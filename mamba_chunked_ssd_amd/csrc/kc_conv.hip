@@ -118,21 +118,30 @@ __global__ __launch_bounds__(256) void kc_conv_fwd(ConvIn<Tin> a, Tout *__restri
 
 // Backward: with d_t = dy_t act'(p_t) (0 behind the end),
 //   dx_s = sum_k w_k d_{s+W-1-k} ,  dw_k = sum_t d_t x_{t-W+1+k} ,  db = sum_t d_t .
-// A thread walks t over its strip and W - 1 tokens beyond it, whose d_t it
-// forms again: dx_{t-W+1} is complete at t.  dw and db stay in registers over
-// the strip, are joined over the block's strips in LDS and leave one row of
+// A wave walks t over its strip, four tokens at a time with the next four's
+// loads in flight, and over one group beyond it, whose d_t it forms again:
+// dx_{t-W+1} is complete at t.  Rows come through raw buffers over the group,
+// so ends need no branch in the loop.  dw and db stay in registers over the
+// strip, are joined over the block's four strips in LDS and leave one row of
 // partial sums per block, which kc_conv_sums adds in a fixed order.
+constexpr int kGroup = 4;  // tokens; at least W - 1
+
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t group_rows(const T *first, int64_t row, int rows) {
+    return buffer_rsrc(first, (uint32_t)min(max(rows, 0), kGroup) * (uint32_t)(row * (int64_t)sizeof(T)));
+}
+
 template <typename Tin, typename Tdy, typename Tdx, int W, int V>
 __global__ __launch_bounds__(256) void kc_conv_bwd(ConvIn<Tin> a, const Tdy *__restrict__ dy, int64_t dyb, int64_t dyr,
                                                    const float *__restrict__ dfinal, Tdx *__restrict__ dx,
                                                    float *__restrict__ dinit, float *__restrict__ partials, int strip,
                                                    int nstrips) {
-    extern __shared__ float red[];  // (blockDim.y, (W + 1) * V, blockDim.x)
-    const int vec = (int)(blockIdx.x % a.nvb) * blockDim.x + threadIdx.x;
-    const int sb = blockIdx.x / a.nvb;  // block of strips
-    const int st = sb * blockDim.y + threadIdx.y;
-    const int b = blockIdx.y, c0 = vec * V;
-    const bool work = vec < a.nvec && st < nstrips;
+    constexpr int U = kGroup, R = (W + 1) * V;
+    __shared__ float red[4 * R * 64];
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int vb = blockIdx.x % a.nvb, sb = blockIdx.x / a.nvb;
+    const int vec = vb * 64 + lane, st = sb * 4 + wave, b = blockIdx.y, c0 = vec * V;
+    const bool mine = vec < a.nvec;
     const int len = conv_length(a.lengths, b, a.L);
 
     float dw[W][V], db[V];
@@ -142,103 +151,124 @@ __global__ __launch_bounds__(256) void kc_conv_bwd(ConvIn<Tin> a, const Tdy *__r
 #pragma unroll
         for (int k = 0; k < W; ++k) dw[k][e] = 0.f;
     }
-    if (work) {
-        const int t0 = st * strip, t1 = min(t0 + strip, a.L);
+    if (st < nstrips) {
+        const int t0 = st * strip, t1 = min(t0 + strip, a.L), tend = min(t1 + W - 1, len);
+        const uint32_t xoff = mine ? c0 * (uint32_t)sizeof(Tin) : kNowhere;
+        const uint32_t yoff = mine ? c0 * (uint32_t)sizeof(Tdy) : kNowhere;
+        const uint32_t goff = mine ? c0 * (uint32_t)sizeof(Tdx) : kNowhere;
+        const uint32_t xrow = (uint32_t)(a.xr * (int64_t)sizeof(Tin)), yrow = (uint32_t)(dyr * (int64_t)sizeof(Tdy));
+        const uint32_t grow = (uint32_t)a.C * (uint32_t)sizeof(Tdx);
+        const Tin *xp = a.x + b * a.xb + t0 * a.xr;
+        const Tdy *yp = dy + b * dyb + t0 * dyr;
+        Tdx *gp = dx + ((int64_t)b * a.L + t0 - (W - 1)) * a.C;
+
         float w[W][V], bs[V], win[W][V], dp[W][V];  // dp[k]: d_{t - W + 1 + k}
-        load_filter<W, V>(a.weight, a.bias, c0, w, bs);
+        load_filter<W, V>(a.weight, a.bias, mine ? c0 : 0, w, bs);
 #pragma unroll
         for (int k = 0; k < W; ++k)
 #pragma unroll
             for (int e = 0; e < V; ++e) dp[k][e] = 0.f;
 #pragma unroll
-        for (int k = 1; k < W; ++k) conv_row<Tin, W, V>(a, b, t0 - W + k, len, c0).unpack(win[k]);
-        const int tend = t1 + W - 1;
-        for (int t = t0; t < tend; t += kUnroll) {
-            Raw<Tin, V> in[kUnroll];
-            Raw<Tdy, V> up[kUnroll];
+        for (int k = 1; k < W; ++k) conv_row<Tin, W, V>(a, b, t0 - W + k, len, mine ? c0 : 0).unpack(win[k]);
+
+        Raw<Tin, V> in[U];
+        Raw<Tdy, V> up[U];
+        auto fetch = [&](int t) {
+            const __amdgpu_buffer_rsrc_t rx = group_rows(xp, a.xr, tend - t), ry = group_rows(yp, dyr, tend - t);
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                in[u].zero();
-                up[u].zero();
-                if (t + u < min(len, tend)) {
-                    in[u].load(a.x + b * a.xb + (t + u) * a.xr + c0);
-                    up[u].load(dy + b * dyb + (t + u) * dyr + c0);
-                }
+            for (int u = 0; u < U; ++u) {
+                in[u].load(rx, xoff + u * xrow);
+                up[u].load(ry, yoff + u * yrow);
             }
+            xp += U * a.xr;
+            yp += U * dyr;
+        };
+        auto group = [&](int t, bool own) {
+            float x[U][V], d[U][V], g[U][V];
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                if (t + u >= tend) break;
+            for (int u = 0; u < U; ++u) {
+                in[u].unpack(x[u]);
+                up[u].unpack(d[u]);
+            }
+            fetch(t + U);
 #pragma unroll
-                for (int k = 0; k < W - 1; ++k)
+            for (int u = 0; u < U; ++u) {
 #pragma unroll
-                    for (int e = 0; e < V; ++e) {
+                for (int e = 0; e < V; ++e) {
+#pragma unroll
+                    for (int k = 0; k < W - 1; ++k) {
                         win[k][e] = win[k + 1][e];
                         dp[k][e] = dp[k + 1][e];
                     }
-                in[u].unpack(win[W - 1]);
-                up[u].unpack(dp[W - 1]);
-                if (a.silu) {
-#pragma unroll
-                    for (int e = 0; e < V; ++e) {
+                    win[W - 1][e] = x[u][e];
+                    float de = d[u][e];
+                    if (a.silu) {
                         float p = bs[e];
 #pragma unroll
                         for (int k = 0; k < W; ++k) p = fmaf(w[k][e], win[k][e], p);
                         const float sg = logistic(p);
                         // silu'(p) = s (1 + p (1 - s)); rows behind the end have dy = 0
-                        dp[W - 1][e] *= sg * fmaf(p, 1.f - sg, 1.f);
+                        de *= sg * fmaf(p, 1.f - sg, 1.f);
                     }
+                    dp[W - 1][e] = de;
+                    if (own) {
+                        db[e] += de;
+#pragma unroll
+                        for (int k = 0; k < W; ++k) dw[k][e] = fmaf(de, win[k][e], dw[k][e]);
+                    }
+                    g[u][e] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < W; ++k) g[u][e] = fmaf(w[k][e], dp[W - 1 - k][e], g[u][e]);
                 }
-                if (t + u < t1) {
+            }
+            const int s0 = t - (W - 1);  // the row of g[0]
+            if (dfinal != nullptr && s0 + U > len - (W - 1) && s0 < len && mine) {
 #pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        db[e] += dp[W - 1][e];
-#pragma unroll
-                        for (int k = 0; k < W; ++k) dw[k][e] = fmaf(dp[W - 1][e], win[k][e], dw[k][e]);
-                    }
-                }
-                const int s = t + u - (W - 1);
-                if (s >= t0 || st == 0) {
-                    float g[V];
-#pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        g[e] = 0.f;
-#pragma unroll
-                        for (int k = 0; k < W; ++k) g[e] = fmaf(w[k][e], dp[W - 1 - k][e], g[e]);
-                    }
-                    const int i = s - len + (W - 1);  // x_s's row in the final state
-                    if (dfinal != nullptr && i >= 0 && i < W - 1) {
+                for (int u = 0; u < U; ++u) {
+                    const int i = s0 + u - len + (W - 1);  // its row in the final state
+                    if (i >= 0 && i < W - 1) {
                         Raw<float, V> r;
                         float f[V];
                         r.load(dfinal + ((int64_t)b * (W - 1) + i) * a.C + c0);
                         r.unpack(f);
 #pragma unroll
-                        for (int e = 0; e < V; ++e) g[e] += f[e];
+                        for (int e = 0; e < V; ++e) g[u][e] += f[e];
                     }
-                    if (s >= 0) store_n<V>(dx + ((int64_t)b * a.L + s) * a.C + c0, g);
-                    else if (dinit != nullptr) store_n<V>(dinit + ((int64_t)b * (W - 1) + (W - 1) + s) * a.C + c0, g);
                 }
             }
-        }
+            // the strip's first rows have no place here: they end the strip before, or the initial state
+            const bool first = t == t0;
+            if (first && st == 0 && dinit != nullptr && mine) {
+#pragma unroll
+                for (int u = 0; u < W - 1; ++u) store_n<V>(dinit + ((int64_t)b * (W - 1) + u) * a.C + c0, g[u]);
+            }
+            const __amdgpu_buffer_rsrc_t rg = group_rows(gp, a.C, t1 - s0);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (u >= W - 1 || !first) store_n<V>((const Tdx *)nullptr, rg, goff + u * grow, g[u]);
+            gp += U * (int64_t)a.C;
+        };
+        fetch(t0);
+        int t = t0;
+        for (; t < t1; t += U) group(t, true);
+        group(t, false);
     }
 
-    constexpr int R = (W + 1) * V;
-    float *mine = red + (threadIdx.y * R) * blockDim.x + threadIdx.x;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
 #pragma unroll
-        for (int k = 0; k < W; ++k) mine[(k * V + e) * blockDim.x] = dw[k][e];
-        mine[(W * V + e) * blockDim.x] = db[e];
+        for (int k = 0; k < W; ++k) red[(wave * R + k * V + e) * 64 + lane] = dw[k][e];
+        red[(wave * R + W * V + e) * 64 + lane] = db[e];
     }
     __syncthreads();
-    const int nsb = (nstrips + blockDim.y - 1) / blockDim.y;
+    const int nsb = (nstrips + 3) / 4;
     float *out = partials + ((int64_t)b * nsb + sb) * (W + 1) * a.C;
-    const int tid = threadIdx.y * blockDim.x + threadIdx.x, n = R * blockDim.x;
-    for (int i = tid; i < n; i += 256) {
+    for (int i = threadIdx.x; i < R * 64; i += 256) {
         // consecutive threads take consecutive channels of one tap
-        const int k = i / (V * blockDim.x), cl = i % (V * blockDim.x), e = cl % V, xi = cl / V;
-        const int c = ((int)(blockIdx.x % a.nvb) * blockDim.x) * V + cl;
+        const int k = i / (V * 64), cl = i % (V * 64), c = vb * 64 * V + cl;
         float sum = 0.f;
-        for (int q = 0; q < (int)blockDim.y; ++q) sum += red[(q * R + k * V + e) * blockDim.x + xi];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sum += red[(q * R + k * V + cl % V) * 64 + cl / V];
         if (c < a.C) out[(int64_t)k * a.C + c] = sum;
     }
 }
@@ -337,15 +367,12 @@ hipError_t fwd(const ConvArgs &a, hipStream_t stream) {
 
 template <typename Tin, typename Tdy, typename Tdx, int W, int V>
 hipError_t bwd(const ConvArgs &a, const ConvBwdPlan &plan, hipStream_t stream) {
-    // the plan's blocks are for 4 channels a thread; with one, the same blocks take a quarter of the channels
-    const ConvIn<Tin> in = conv_in<Tin>(a, V, plan.bx);
-    const int nsb = (plan.nstrips + plan.by - 1) / plan.by;
-    const int64_t blocks = (int64_t)in.nvb * nsb;
+    const ConvIn<Tin> in = conv_in<Tin>(a, V, 64);
     if (a.batch > 0) {
-        const size_t lds = sizeof(float) * 256 * (W + 1) * V;
+        const int64_t blocks = (int64_t)in.nvb * ((plan.nstrips + 3) / 4);
         const hipError_t e = launch_kernel(
-            kc_conv_bwd<Tin, Tdy, Tdx, W, V>, dim3((unsigned)blocks, (unsigned)a.batch), dim3(plan.bx, plan.by), lds,
-            stream, LaunchEvents{}, in, static_cast<const Tdy *>(a.dy), a.dys.batch, a.dys.row, a.dfinal,
+            kc_conv_bwd<Tin, Tdy, Tdx, W, V>, dim3((unsigned)blocks, (unsigned)a.batch), dim3(256), 0, stream,
+            LaunchEvents{}, in, static_cast<const Tdy *>(a.dy), a.dys.batch, a.dys.row, a.dfinal,
             static_cast<Tdx *>(a.dx), a.dinit, a.partials, plan.strip, plan.nstrips);
         if (e != hipSuccess) return e;
     }
@@ -374,13 +401,15 @@ hipError_t fwd_w(const ConvArgs &a, hipStream_t s) {
     return v ? fwd<uint16_t, float, W, 8>(a, s) : fwd<uint16_t, float, W, 1>(a, s);
 }
 
-// four channels a thread: the sums of a wider one would halve the waves a CU holds
+// Four channels a lane (eight would take the registers of two waves) where
+// the waves that cover a row are at least three quarters full of them, else
+// one.
 template <typename Tin, typename Tdy, typename Tdx, int W>
 hipError_t bwd_v(const ConvArgs &a, const ConvBwdPlan &p, hipStream_t s) {
     const bool v = a.channels % 4 == 0 && a.xs.batch % 4 == 0 && a.xs.row % 4 == 0 && a.dys.batch % 4 == 0 &&
                    a.dys.row % 4 == 0 && vec_ok<Tin>(a.x, 4) && vec_ok<Tin>(a.init, 4) && vec_ok<Tdy>(a.dy, 4) &&
                    vec_ok<Tdx>(a.dx, 4) && vec_ok<float>(a.dfinal, 4) && vec_ok<float>(a.dinit, 4);
-    return v ? bwd<Tin, Tdy, Tdx, W, 4>(a, p, s) : bwd<Tin, Tdy, Tdx, W, 1>(a, p, s);
+    return v && p.four ? bwd<Tin, Tdy, Tdx, W, 4>(a, p, s) : bwd<Tin, Tdy, Tdx, W, 1>(a, p, s);
 }
 
 template <int W>

@@ -77,7 +77,6 @@ struct ScanPos {
 // stores are dropped without a branch.  Offsets into the tile are 32-bit (the
 // entry points refuse row strides of 2^24 elements or more) and the same for
 // every tile; the scalar unit moves the base from tile to tile.
-constexpr uint32_t kNowhere = 0x7fffff00u;  // an offset behind any tile: lanes without a channel or state
 
 template <int TT, typename T>
 struct TileRows {

@@ -15,18 +15,16 @@
 
 namespace ssd {
 
-// Strips long enough that the W - 1 tokens formed twice and the partial sums
-// stay small, short enough that every SIMD gets two waves.
+// Strips long enough that the group formed twice and the partial sums stay
+// small, short enough that every SIMD gets two waves.
 ConvBwdPlan conv_bwd_plan(int64_t batch, int64_t seqlen, int64_t channels) {
     ConvBwdPlan p;
-    const int64_t nvec = std::max<int64_t>(1, channels / 4);
-    p.bx = 1;
-    while (p.bx < 64 && p.bx < nvec) p.bx <<= 1;
-    p.by = 256 / p.bx;
+    p.four = 4 * channels >= 3 * ((channels + 255) / 256 * 256);
+    const int64_t waves = p.four ? (channels + 255) / 256 : (channels + 63) / 64;
     p.strip = 128;
-    while (p.strip > 16 && batch * nvec * ((seqlen + p.strip - 1) / p.strip) < 2 * 1024 * 64) p.strip /= 2;
+    while (p.strip > 16 && batch * waves * ((seqlen + p.strip - 1) / p.strip) < 2 * 1024) p.strip /= 2;
     p.nstrips = (int)std::max<int64_t>(1, (seqlen + p.strip - 1) / p.strip);
-    p.parts = batch * ((p.nstrips + p.by - 1) / p.by);
+    p.parts = batch * ((p.nstrips + 3) / 4);
     return p;
 }
 
@@ -148,6 +146,7 @@ ssd_status check_conv(const ssd_conv_shape *s, ConvArgs *a, ConvBytes *n) {
     ssd_status st = rows_of(s->x, s->batch, s->seqlen, s->channels, size_of(s->dtype), &a->xs, &n->x);
     if (st == SSD_OK) st = rows_of(s->dy, s->batch, s->seqlen, s->channels, size_of(s->y_dtype), &a->dys, &n->dy);
     if (st != SSD_OK) return st;
+    if (a->xs.row >= kMaxRow || a->dys.row >= kMaxRow) return SSD_ERROR_UNSUPPORTED;  // 32-bit offsets in a group
     // launch geometry: fewer than 2^24 blocks of 256 threads along x, with one channel and one run of 16 a thread
     int64_t work;
     if (!product({(s->channels + 63) / 64 + 1, s->seqlen / 16 + 256}, &work) || work >= (int64_t)1 << 24)

@@ -9,7 +9,10 @@
 
 namespace ssd {
 
-// V stored elements as one load; unpack widens them exactly.
+constexpr uint32_t kNowhere = 0x7fffff00u;  // an offset behind any raw buffer here: such loads read 0, stores are dropped
+
+// V stored elements as one load, from memory or a raw buffer; unpack widens
+// them exactly.
 template <typename T, int V>
 struct Raw;
 template <>
@@ -17,6 +20,7 @@ struct Raw<float, 1> {
     float v;
     __device__ void zero() { v = 0.f; }
     __device__ void load(const float *p) { v = *p; }
+    __device__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) { v = buffer_load_f32(r, (int)off); }
     __device__ void unpack(float (&f)[1]) const { f[0] = v; }
 };
 template <>
@@ -24,6 +28,9 @@ struct Raw<float, 4> {
     floatx4 v;
     __device__ void zero() { v = zero4(); }
     __device__ void load(const float *p) { v = *reinterpret_cast<const floatx4 *>(p); }
+    __device__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+        v = __builtin_bit_cast(floatx4, buffer_load_x4(r, (int)off));
+    }
     __device__ void unpack(float (&f)[4]) const {
 #pragma unroll
         for (int e = 0; e < 4; ++e) f[e] = v[e];
@@ -47,6 +54,9 @@ struct Raw<uint16_t, 1> {
     uint32_t v;
     __device__ void zero() { v = 0; }
     __device__ void load(const uint16_t *p) { v = *p; }
+    __device__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+        v = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)off, 0, 0);
+    }
     __device__ void unpack(float (&f)[1]) const { f[0] = bf16_to_f32(v); }
 };
 template <>
@@ -54,6 +64,9 @@ struct Raw<uint16_t, 4> {
     u32x2 v;
     __device__ void zero() { v = u32x2{0, 0}; }
     __device__ void load(const uint16_t *p) { v = *reinterpret_cast<const u32x2 *>(p); }
+    __device__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+        v = __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0);
+    }
     __device__ void unpack(float (&f)[4]) const {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -97,6 +110,27 @@ __device__ __forceinline__ void store_n(uint16_t *p, const float (&f)[V]) {
     } else {
         *reinterpret_cast<u32x4 *>(p) = u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
                                               pack_bf16(f[6], f[7])};
+    }
+}
+
+// The same into a raw buffer, which drops what falls outside.
+template <int V>
+__device__ __forceinline__ void store_n(const float *, __amdgpu_buffer_rsrc_t r, uint32_t off, const float (&f)[V]) {
+    if constexpr (V == 1) {
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f[0]), r, (int)off, 0, 0);
+    } else {
+        static_assert(V == 4, "16 bytes");
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, floatx4{f[0], f[1], f[2], f[3]}), r, (int)off, 0,
+                                               0);
+    }
+}
+template <int V>
+__device__ __forceinline__ void store_n(const uint16_t *, __amdgpu_buffer_rsrc_t r, uint32_t off, const float (&f)[V]) {
+    if constexpr (V == 1) {
+        __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(pack_bf16(f[0], 0.f) & 0xffffu), r, (int)off, 0, 0);
+    } else {
+        static_assert(V == 4, "8 bytes");
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])}, r, (int)off, 0, 0);
     }
 }
 

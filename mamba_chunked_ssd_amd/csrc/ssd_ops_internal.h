@@ -40,10 +40,10 @@ struct ConvArgs {
 // The strips of tokens the backward pass cuts each sequence into, and how many
 // rows of partial sums its blocks leave.
 struct ConvBwdPlan {
-    int strip;      // tokens of one thread
+    int strip;      // tokens of one wave, a multiple of 16
     int nstrips;    // strips of one sequence
-    int bx, by;     // block: channel vectors x strips
-    int64_t parts;  // batch * ceil(nstrips / by)
+    bool four;      // four channels a lane where alignment allows
+    int64_t parts;  // batch * ceil(nstrips / 4)
 };
 ConvBwdPlan conv_bwd_plan(int64_t batch, int64_t seqlen, int64_t channels);
 
