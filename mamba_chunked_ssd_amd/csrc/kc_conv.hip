@@ -128,7 +128,7 @@ constexpr int kGroup = 4;  // tokens; at least W - 1
 
 template <typename T>
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t group_rows(const T *first, int64_t row, int rows) {
-    return buffer_rsrc(first, (uint32_t)min(max(rows, 0), kGroup) * (uint32_t)(row * (int64_t)sizeof(T)));
+    return uniform_rsrc(first, (uint32_t)min(max(rows, 0), kGroup) * (uint32_t)(row * (int64_t)sizeof(T)));
 }
 
 template <typename Tin, typename Tdy, typename Tdx, int W, int V>

@@ -89,7 +89,7 @@ struct TileRows {
     __device__ __forceinline__ void next() { at += move; }
     // left: rows from the tile's first to the end
     __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile(int left) const {
-        return buffer_rsrc(at, (uint32_t)min(max(left, 0), TT) * row);
+        return uniform_rsrc(at, (uint32_t)min(max(left, 0), TT) * row);
     }
     __device__ __forceinline__ uint32_t offset(int token, int column) const {
         return token * row + column * (uint32_t)sizeof(T);
@@ -225,7 +225,7 @@ struct BlockRows {
     __device__ __forceinline__ BlockRows(bool ok, int j, int cl)
         : states(ok ? 16 * threadIdx.x : kNowhere), number(ok ? 4 * cl : kNowhere) {}
     static __device__ __forceinline__ __amdgpu_buffer_rsrc_t of(const float *first, int elements) {
-        return buffer_rsrc(first, 4 * elements);
+        return uniform_rsrc(first, 4 * elements);
     }
     __device__ __forceinline__ void load(const float *first, float (&h)[4]) const {
         const u32x4 v = buffer_load_x4(of(first, 1024), (int)states);

@@ -11,6 +11,15 @@ namespace ssd {
 
 constexpr uint32_t kNowhere = 0x7fffff00u;  // an offset behind any raw buffer here: such loads read 0, stores are dropped
 
+// A raw buffer whose base is the same in every lane.  Said so outright: where
+// the compiler cannot see it, it wraps every access in a loop over the lanes'
+// values.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void *base, uint32_t bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(base);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a), hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+    return buffer_rsrc(reinterpret_cast<const void *>((uint64_t)hi << 32 | lo), __builtin_amdgcn_readfirstlane(bytes));
+}
+
 // V stored elements as one load, from memory or a raw buffer; unpack widens
 // them exactly.
 template <typename T, int V>
