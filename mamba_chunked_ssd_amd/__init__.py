@@ -901,10 +901,11 @@ def selective_scan_bwd(x, dt, A, B, C, D, dy, z=None, dt_bias=None, initial_stat
         def new(*dims):
             return torch.empty(dims, dtype=torch.float32, device=dev)
 
-        res = {"dx": new(b, L, c), "ddt": new(b, L, c), "dA": new(c, n), "dB": new(b, L, g, n), "dC": new(b, L, g, n),
-               "dD": new(c), "ddt_bias": new(c)}
+        like = torch.empty_like
+        res = {"dx": new(b, L, c), "dB": new(b, L, g, n), "dA": like(A), "dD": new(c)}
+        res["ddt"], res["dC"], res["ddt_bias"] = like(res["dx"]), like(res["dB"]), like(res["dD"])
         if z is not None:
-            res["dz"] = new(b, L, c)
+            res["dz"] = like(res["dx"])
         if want_d_initial:
             res["d_initial_states"] = new(b, c, n)
         ws, size, _keep = _workspace(workspace, lib.ssd_selective_scan_bwd_workspace_size(ctypes.byref(shape)), dev, torch)

@@ -45,7 +45,7 @@ ScanPlan scan_plan(int64_t batch, int64_t seqlen, int64_t channels, int64_t dsta
     int64_t root = 1;
     while (root * root < seqlen) ++root;
     int64_t nseg = waves >= (backward ? kBwdWhole : kFwdWhole) ? 1 : (kScanWaves + waves - 1) / waves;
-    nseg = std::max<int64_t>(1, std::min<int64_t>({nseg, seqlen / 32, root}));
+    nseg = std::max<int64_t>(1, std::min<int64_t>({nseg, seqlen / 16, root * 3 / 2}));
     int64_t len = (seqlen + nseg - 1) / nseg;
     len = std::max<int64_t>(kScanSegment, (len + kScanSegment - 1) / kScanSegment * kScanSegment);
     p.seglen = (int)len;
