@@ -57,7 +57,7 @@ typedef enum {
     SSD_ERROR_INVALID_VALUE = 1, /* NULL required pointer, negative size, nheads % ngroups != 0, aliasing */
     SSD_ERROR_UNSUPPORTED = 2,   /* valid problem outside the sizes the kernels are built for */
     SSD_ERROR_MISALIGNED = 3,    /* a pointer below its required alignment */
-    SSD_ERROR_WORKSPACE = 4,     /* workspace NULL or smaller than ssd_chunk_scan_fwd_workspace_size */
+    SSD_ERROR_WORKSPACE = 4,     /* workspace NULL or smaller than the call's workspace_size query says */
     SSD_ERROR_LAUNCH = 5,        /* the HIP runtime refused a launch or an event record */
     SSD_ERROR_SCRATCH = 6        /* ssd_chunk_scan_fwd_noalloc: the problem needs more workspace
                                     than the library's scratch holds (SSD_NOALLOC_SCRATCH_BYTES) */
@@ -417,6 +417,10 @@ ssd_status ssd_chunk_scan_bwd_saved(const ssd_shape *shape,
  *   (its initial state when it has none).
  * - Sums over tokens and channels use fixed orders and no atomics: the same
  *   call gives the same bits.
+ * - SSD_ERROR_UNSUPPORTED also for batch > 65535, seqlen > 2^30, a row of
+ *   2^24 elements or more (as strided), or a launch of 2^24 blocks or more
+ *   (channels x seqlen of 2^36 at the least).
+ * - `stream` belongs to the device that is current.
  * ------------------------------------------------------------------------- */
 typedef struct {
     int64_t batch, row;

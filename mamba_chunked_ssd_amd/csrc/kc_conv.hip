@@ -4,20 +4,20 @@
 //   p_t = bias + sum_k w_k x_{t-W+1+k} ,  y_t = act(p_t)
 //
 // Bound by memory: each element of x is read and each of y written once,
-// against 2 W + about 10 vector operations.  A thread owns the channels of
-// one 16-byte load and walks a run of tokens with the last W - 1 inputs in
-// registers, so only the run's first W - 1 rows are read twice (from the L2).
-// Threads of a wave take consecutive channels: every access is one contiguous
-// piece of a row.
+// against 2 W + about 10 vector operations.  A lane owns the channels of one
+// load and walks a run of tokens with the last W - 1 inputs in registers, so
+// only the run's first W - 1 rows are read twice (from the L2).  The lanes of a
+// wave take consecutive channels, so every access is one contiguous piece of a
+// row, and rows come and go through raw buffers over a group of tokens, so
+// that the ends of sequences and rows need no branch.
+#include <algorithm>
+
 #include "ssd_launch.h"
 #include "ssd_ops_device.h"
 #include "ssd_ops_internal.h"
 
 namespace ssd {
 namespace {
-
-constexpr int kFwdRun = 16;  // tokens of one thread of the forward pass
-constexpr int kUnroll = 8;   // tokens whose loads are in flight together
 
 template <typename T>
 struct ConvIn {
@@ -57,24 +57,49 @@ __device__ __forceinline__ Raw<T, V> conv_row(const ConvIn<T> &a, int b, int t, 
     return r;
 }
 
-template <typename Tin, typename Tout, int W, int V>
-__global__ __launch_bounds__(256) void kc_conv_fwd(ConvIn<Tin> a, Tout *__restrict__ y, Tin *final_state) {
-    const int vec = (int)(blockIdx.x % a.nvb) * blockDim.x + threadIdx.x;
-    if (vec >= a.nvec) return;
-    const int run = (int)(blockIdx.x / a.nvb) * blockDim.y + threadIdx.y;
-    const int b = blockIdx.y, c0 = vec * V;
-    const int t0 = run * kFwdRun, t1 = min(t0 + kFwdRun, a.L);
-    if (run > 0 && t0 >= a.L) return;
-    const int len = conv_length(a.lengths, b, a.L);
+// Rows first .. of a group of U tokens, none behind `rows`.
+template <int U, typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t group_rows(const T *first, int64_t row, int rows) {
+    return uniform_rsrc(first, (uint32_t)min(max(rows, 0), U) * (uint32_t)(row * (int64_t)sizeof(T)));
+}
 
+// A wave takes a run of 16 tokens, eight at a time with the next eight's loads
+// in flight.  Longer runs read the filters less often, from the L2, and were
+// slower (4 x 4096 tokens of 5376 channels, fp32: 130 us with 16, 137 with 32,
+// 149 with 128).  8 x 4096 tokens of 5376 channels, bf16: 140 us, 5.0 TB/s,
+// 97 % of a copy's rate.
+constexpr int kFwdRun = 16;
+template <typename Tin, typename Tout, int W, int V>
+__global__ __launch_bounds__(256) void kc_conv_fwd(ConvIn<Tin> a, Tout *__restrict__ y, Tin *final_state, int nruns) {
+    constexpr int U = 8;
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int vec = (int)(blockIdx.x % a.nvb) * 64 + lane, rn = (int)(blockIdx.x / a.nvb) * 4 + wave;
+    if (rn >= nruns) return;
+    const bool mine = vec < a.nvec;
+    const int b = blockIdx.y, c0 = mine ? vec * V : 0;
+    const int t0 = rn * kFwdRun, t1 = min(t0 + kFwdRun, a.L);
+    const int len = conv_length(a.lengths, b, a.L), tend = min(t1, len);
+    const uint32_t xoff = mine ? c0 * (uint32_t)sizeof(Tin) : kNowhere, xrow = (uint32_t)(a.xr * (int64_t)sizeof(Tin));
+    const uint32_t yoff = mine ? c0 * (uint32_t)sizeof(Tout) : kNowhere, yrow = (uint32_t)a.C * (uint32_t)sizeof(Tout);
+    const Tin *xp = a.x + b * a.xb + t0 * a.xr;
+    Tout *yp = y + ((int64_t)b * a.L + t0) * a.C;
+
+    Raw<Tin, V> in[U], next[U];
+    auto fetch = [&](int t, Raw<Tin, V>(&to)[U]) {
+        const __amdgpu_buffer_rsrc_t r = group_rows<U>(xp, a.xr, tend - t);
+#pragma unroll
+        for (int u = 0; u < U; ++u) to[u].load(r, xoff + u * xrow);
+        xp += U * a.xr;
+    };
+    fetch(t0, in);
     float w[W][V], bs[V], win[W][V];  // win[k]: x_{t - W + 1 + k}
     load_filter<W, V>(a.weight, a.bias, c0, w, bs);
 #pragma unroll
     for (int k = 1; k < W; ++k) conv_row<Tin, W, V>(a, b, t0 - W + k, len, c0).unpack(win[k]);
 
-    // The first run's thread holds the initial state already when it writes
-    // the final one, so the two may be the same buffer.
-    if (run == 0 && final_state != nullptr) {
+    // The first run's lanes hold the initial state already when they write the
+    // final one, so the two may be the same buffer.
+    if (rn == 0 && final_state != nullptr && mine) {
         Raw<Tin, V> keep[W - 1];
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) keep[k] = conv_row<Tin, W, V>(a, b, len - (W - 1) + k, len, c0);
@@ -86,16 +111,11 @@ __global__ __launch_bounds__(256) void kc_conv_fwd(ConvIn<Tin> a, Tout *__restri
         }
     }
 
-    Tout *yp = y + ((int64_t)b * a.L + t0) * a.C + c0;
-    for (int t = t0; t < t1; t += kUnroll) {
-        Raw<Tin, V> in[kUnroll];
+    for (int t = t0; t < t1; t += U) {
+        fetch(t + U, next);
+        const __amdgpu_buffer_rsrc_t ry = group_rows<U>(yp, a.C, t1 - t);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            in[u].zero();
-            if (t + u < min(len, t1)) in[u].load(a.x + b * a.xb + (t + u) * a.xr + c0);
-        }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
+        for (int u = 0; u < U; ++u) {
 #pragma unroll
             for (int k = 0; k < W - 1; ++k)
 #pragma unroll
@@ -110,9 +130,10 @@ __global__ __launch_bounds__(256) void kc_conv_fwd(ConvIn<Tin> a, Tout *__restri
                 if (a.silu) p *= logistic(p);
                 out[e] = t + u < len ? p : 0.f;
             }
-            if (t + u < t1) store_n<V>(yp, out);
-            yp += a.C;
+            store_n<V>((const Tout *)nullptr, ry, yoff + u * yrow, out);
+            in[u] = next[u];
         }
+        yp += U * (int64_t)a.C;
     }
 }
 
@@ -125,11 +146,6 @@ __global__ __launch_bounds__(256) void kc_conv_fwd(ConvIn<Tin> a, Tout *__restri
 // strip, are joined over the block's four strips in LDS and leave one row of
 // partial sums per block, which kc_conv_sums adds in a fixed order.
 constexpr int kGroup = 4;  // tokens; at least W - 1
-
-template <typename T>
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t group_rows(const T *first, int64_t row, int rows) {
-    return uniform_rsrc(first, (uint32_t)min(max(rows, 0), kGroup) * (uint32_t)(row * (int64_t)sizeof(T)));
-}
 
 template <typename Tin, typename Tdy, typename Tdx, int W, int V>
 __global__ __launch_bounds__(256) void kc_conv_bwd(ConvIn<Tin> a, const Tdy *__restrict__ dy, int64_t dyb, int64_t dyr,
@@ -174,7 +190,7 @@ __global__ __launch_bounds__(256) void kc_conv_bwd(ConvIn<Tin> a, const Tdy *__r
         Raw<Tin, V> in[U];
         Raw<Tdy, V> up[U];
         auto fetch = [&](int t) {
-            const __amdgpu_buffer_rsrc_t rx = group_rows(xp, a.xr, tend - t), ry = group_rows(yp, dyr, tend - t);
+            const __amdgpu_buffer_rsrc_t rx = group_rows<U>(xp, a.xr, tend - t), ry = group_rows<U>(yp, dyr, tend - t);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 in[u].load(rx, xoff + u * xrow);
@@ -242,7 +258,7 @@ __global__ __launch_bounds__(256) void kc_conv_bwd(ConvIn<Tin> a, const Tdy *__r
 #pragma unroll
                 for (int u = 0; u < W - 1; ++u) store_n<V>(dinit + ((int64_t)b * (W - 1) + u) * a.C + c0, g[u]);
             }
-            const __amdgpu_buffer_rsrc_t rg = group_rows(gp, a.C, t1 - s0);
+            const __amdgpu_buffer_rsrc_t rg = group_rows<U>(gp, a.C, t1 - s0);
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (u >= W - 1 || !first) store_n<V>((const Tdx *)nullptr, rg, goff + u * grow, g[u]);
@@ -274,20 +290,25 @@ __global__ __launch_bounds__(256) void kc_conv_bwd(ConvIn<Tin> a, const Tdy *__r
 }
 
 // dweight and dbias: column (tap, channel) summed over the rows of partial
-// sums, four threads a column, in 64 bits (thousands of rows at long inputs;
-// free beside the reads).
+// sums in a fixed order and 64 bits, sixteen threads a column, each every
+// sixteenth row: few channels over long inputs leave hundreds of rows to few
+// columns.
 __global__ __launch_bounds__(256) void kc_conv_sums(const float *__restrict__ partials, int64_t parts, int C, int W,
                                                     float *__restrict__ dweight, float *__restrict__ dbias) {
+    constexpr int COLS = 16, SLICES = 16;
     __shared__ double part[256];
-    const int64_t cols = (int64_t)(W + 1) * C, col = (int64_t)blockIdx.x * 64 + threadIdx.x % 64;
-    const int q = threadIdx.x / 64;
+    const int64_t cols = (int64_t)(W + 1) * C, col = (int64_t)blockIdx.x * COLS + threadIdx.x % COLS;
+    const int q = threadIdx.x / COLS;
     double sum = 0.0;
-    if (col < cols)
-        for (int64_t p = q; p < parts; p += 4) sum += (double)partials[p * cols + col];
+    if (col < cols) {
+#pragma unroll 4
+        for (int64_t p = q; p < parts; p += SLICES) sum += (double)partials[p * cols + col];
+    }
     part[threadIdx.x] = sum;
     __syncthreads();
     if (q == 0 && col < cols) {
-        sum += part[threadIdx.x + 64] + part[threadIdx.x + 128] + part[threadIdx.x + 192];
+#pragma unroll
+        for (int k = 1; k < SLICES; ++k) sum += part[k * COLS + threadIdx.x];
         const int k = (int)(col / C), c = (int)(col % C);
         if (k < W) dweight[(int64_t)c * W + k] = (float)sum;
         else if (dbias != nullptr) dbias[c] = (float)sum;
@@ -347,22 +368,19 @@ ConvIn<Tin> conv_in(const ConvArgs &a, int V, int bx) {
     return in;
 }
 
-// Threads of a block along the channel vectors: a wave's worth where there
-// are that many, else the next power of two, the rest along the tokens.
-int conv_bx(int nvec) {
-    int bx = 1;
-    while (bx < 64 && bx < nvec) bx <<= 1;
-    return bx;
+// Lanes of whole waves that V channels a lane would leave idle, at most one in four.
+bool waves_full(int channels, int V) {
+    const int64_t waves = (channels + 64 * V - 1) / (64 * V);
+    return 4 * (int64_t)channels >= 3 * waves * 64 * V;
 }
 
 template <typename Tin, typename Tout, int W, int V>
 hipError_t fwd(const ConvArgs &a, hipStream_t stream) {
-    const int bx = conv_bx(a.channels / V), by = 256 / bx;
-    const ConvIn<Tin> in = conv_in<Tin>(a, V, bx);
-    const int runs = a.seqlen > 0 ? (a.seqlen + kFwdRun - 1) / kFwdRun : 1;
-    const int64_t blocks = (int64_t)in.nvb * ((runs + by - 1) / by);
-    return launch_kernel(kc_conv_fwd<Tin, Tout, W, V>, dim3((unsigned)blocks, (unsigned)a.batch), dim3(bx, by), 0,
-                         stream, LaunchEvents{}, in, static_cast<Tout *>(a.y), static_cast<Tin *>(a.final_state));
+    const ConvIn<Tin> in = conv_in<Tin>(a, V, 64);
+    const int nruns = a.seqlen > 0 ? (a.seqlen + kFwdRun - 1) / kFwdRun : 1;
+    const int64_t blocks = (int64_t)in.nvb * ((nruns + 3) / 4);
+    return launch_kernel(kc_conv_fwd<Tin, Tout, W, V>, dim3((unsigned)blocks, (unsigned)a.batch), dim3(256), 0, stream,
+                         LaunchEvents{}, in, static_cast<Tout *>(a.y), static_cast<Tin *>(a.final_state), nruns);
 }
 
 template <typename Tin, typename Tdy, typename Tdx, int W, int V>
@@ -377,7 +395,7 @@ hipError_t bwd(const ConvArgs &a, const ConvBwdPlan &plan, hipStream_t stream) {
         if (e != hipSuccess) return e;
     }
     const int64_t cols = (int64_t)(W + 1) * a.channels;
-    return launch_kernel(kc_conv_sums, dim3((unsigned)((cols + 63) / 64)), dim3(256), 0, stream, LaunchEvents{},
+    return launch_kernel(kc_conv_sums, dim3((unsigned)((cols + 15) / 16)), dim3(256), 0, stream, LaunchEvents{},
                          (const float *)a.partials, plan.parts, a.channels, W, a.dweight, a.dbias);
 }
 
@@ -388,28 +406,35 @@ hipError_t step(const ConvArgs &a, hipStream_t stream) {
                          LaunchEvents{}, in, static_cast<Tin *>(const_cast<void *>(a.init)), static_cast<Tout *>(a.y));
 }
 
+// Whether V channels a thread fit every operand of the forward pass.
+template <typename Tin, typename Tout>
+bool fwd_vec(const ConvArgs &a, int V) {
+    return a.channels % V == 0 && a.xs.batch % V == 0 && a.xs.row % V == 0 && vec_ok<Tin>(a.x, V) &&
+           vec_ok<Tin>(a.init, V) && (uintptr_t)a.y % std::min<size_t>(16, V * sizeof(Tout)) == 0 &&
+           vec_ok<Tin>(a.final_state, V);
+}
+// The widest loads that fit and leave few lanes idle.
+template <typename Tin, typename Tout, int W>
+hipError_t fwd_v(const ConvArgs &a, hipStream_t s) {
+    if constexpr (sizeof(Tin) == 2) {
+        if (fwd_vec<Tin, Tout>(a, 8) && waves_full(a.channels, 8)) return fwd<Tin, Tout, W, 8>(a, s);
+    }
+    if (fwd_vec<Tin, Tout>(a, 4) && waves_full(a.channels, 4)) return fwd<Tin, Tout, W, 4>(a, s);
+    return fwd<Tin, Tout, W, 1>(a, s);
+}
 template <int W>
 hipError_t fwd_w(const ConvArgs &a, hipStream_t s) {
-    if (!a.in_bf16) {
-        const bool v = a.channels % 4 == 0 && a.xs.batch % 4 == 0 && a.xs.row % 4 == 0 && vec_ok<float>(a.x, 4) &&
-                       vec_ok<float>(a.init, 4) && vec_ok<float>(a.y, 4) && vec_ok<float>(a.final_state, 4);
-        return v ? fwd<float, float, W, 4>(a, s) : fwd<float, float, W, 1>(a, s);
-    }
-    const bool v = a.channels % 8 == 0 && a.xs.batch % 8 == 0 && a.xs.row % 8 == 0 && vec_ok<uint16_t>(a.x, 8) &&
-                   vec_ok<uint16_t>(a.init, 8) && (uintptr_t)a.y % 16 == 0 && vec_ok<uint16_t>(a.final_state, 8);
-    if (a.y_bf16) return v ? fwd<uint16_t, uint16_t, W, 8>(a, s) : fwd<uint16_t, uint16_t, W, 1>(a, s);
-    return v ? fwd<uint16_t, float, W, 8>(a, s) : fwd<uint16_t, float, W, 1>(a, s);
+    if (!a.in_bf16) return fwd_v<float, float, W>(a, s);
+    return a.y_bf16 ? fwd_v<uint16_t, uint16_t, W>(a, s) : fwd_v<uint16_t, float, W>(a, s);
 }
 
-// Four channels a lane (eight would take the registers of two waves) where
-// the waves that cover a row are at least three quarters full of them, else
-// one.
+// Four channels a lane at most (eight would take the registers of two waves).
 template <typename Tin, typename Tdy, typename Tdx, int W>
 hipError_t bwd_v(const ConvArgs &a, const ConvBwdPlan &p, hipStream_t s) {
     const bool v = a.channels % 4 == 0 && a.xs.batch % 4 == 0 && a.xs.row % 4 == 0 && a.dys.batch % 4 == 0 &&
                    a.dys.row % 4 == 0 && vec_ok<Tin>(a.x, 4) && vec_ok<Tin>(a.init, 4) && vec_ok<Tdy>(a.dy, 4) &&
                    vec_ok<Tdx>(a.dx, 4) && vec_ok<float>(a.dfinal, 4) && vec_ok<float>(a.dinit, 4);
-    return v && p.four ? bwd<Tin, Tdy, Tdx, W, 4>(a, p, s) : bwd<Tin, Tdy, Tdx, W, 1>(a, p, s);
+    return v && waves_full(a.channels, 4) ? bwd<Tin, Tdy, Tdx, W, 4>(a, p, s) : bwd<Tin, Tdy, Tdx, W, 1>(a, p, s);
 }
 
 template <int W>

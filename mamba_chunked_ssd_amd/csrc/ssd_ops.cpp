@@ -19,8 +19,7 @@ namespace ssd {
 // small, short enough that every SIMD gets two waves.
 ConvBwdPlan conv_bwd_plan(int64_t batch, int64_t seqlen, int64_t channels) {
     ConvBwdPlan p;
-    p.four = 4 * channels >= 3 * ((channels + 255) / 256 * 256);
-    const int64_t waves = p.four ? (channels + 255) / 256 : (channels + 63) / 64;
+    const int64_t waves = (channels + 255) / 256;  // of four channels a lane; with one there are up to four times as many
     p.strip = 128;
     while (p.strip > 16 && batch * waves * ((seqlen + p.strip - 1) / p.strip) < 2 * 1024) p.strip /= 2;
     p.nstrips = (int)std::max<int64_t>(1, (seqlen + p.strip - 1) / p.strip);
@@ -147,9 +146,9 @@ ssd_status check_conv(const ssd_conv_shape *s, ConvArgs *a, ConvBytes *n) {
     if (st == SSD_OK) st = rows_of(s->dy, s->batch, s->seqlen, s->channels, size_of(s->y_dtype), &a->dys, &n->dy);
     if (st != SSD_OK) return st;
     if (a->xs.row >= kMaxRow || a->dys.row >= kMaxRow) return SSD_ERROR_UNSUPPORTED;  // 32-bit offsets in a group
-    // launch geometry: fewer than 2^24 blocks of 256 threads along x, with one channel and one run of 16 a thread
+    // launch geometry: fewer than 2^24 blocks, of 64 channels and 64 tokens at the least
     int64_t work;
-    if (!product({(s->channels + 63) / 64 + 1, s->seqlen / 16 + 256}, &work) || work >= (int64_t)1 << 24)
+    if (!product({(s->channels + 63) / 64, s->seqlen / 64 + 2}, &work) || work >= (int64_t)1 << 24)
         return SSD_ERROR_UNSUPPORTED;
     const size_t tok = (size_t)(s->batch * s->seqlen * s->channels), held = (size_t)(s->batch * (s->width - 1) * s->channels);
     a->batch = s->batch;

@@ -46,19 +46,6 @@ struct Raw<float, 4> {
     }
 };
 template <>
-struct Raw<float, 8> {
-    floatx4 v[2];
-    __device__ void zero() { v[0] = v[1] = zero4(); }
-    __device__ void load(const float *p) {
-        v[0] = *reinterpret_cast<const floatx4 *>(p);
-        v[1] = *reinterpret_cast<const floatx4 *>(p + 4);
-    }
-    __device__ void unpack(float (&f)[8]) const {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = v[e / 4][e % 4];
-    }
-};
-template <>
 struct Raw<uint16_t, 1> {
     uint32_t v;
     __device__ void zero() { v = 0; }
@@ -89,6 +76,7 @@ struct Raw<uint16_t, 8> {
     u32x4 v;
     __device__ void zero() { v = u32x4{0, 0, 0, 0}; }
     __device__ void load(const uint16_t *p) { v = *reinterpret_cast<const u32x4 *>(p); }
+    __device__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) { v = buffer_load_x4(r, (int)off); }
     __device__ void unpack(float (&f)[8]) const {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -128,18 +116,22 @@ __device__ __forceinline__ void store_n(const float *, __amdgpu_buffer_rsrc_t r,
     if constexpr (V == 1) {
         __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f[0]), r, (int)off, 0, 0);
     } else {
-        static_assert(V == 4, "16 bytes");
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, floatx4{f[0], f[1], f[2], f[3]}), r, (int)off, 0,
-                                               0);
+#pragma unroll
+        for (int e = 0; e < V; e += 4)
+            __builtin_amdgcn_raw_buffer_store_b128(
+                __builtin_bit_cast(u32x4, floatx4{f[e], f[e + 1], f[e + 2], f[e + 3]}), r, (int)(off + 4 * e), 0, 0);
     }
 }
 template <int V>
 __device__ __forceinline__ void store_n(const uint16_t *, __amdgpu_buffer_rsrc_t r, uint32_t off, const float (&f)[V]) {
     if constexpr (V == 1) {
         __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(pack_bf16(f[0], 0.f) & 0xffffu), r, (int)off, 0, 0);
-    } else {
-        static_assert(V == 4, "8 bytes");
+    } else if constexpr (V == 4) {
         __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])}, r, (int)off, 0, 0);
+    } else {
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                                                     pack_bf16(f[6], f[7])},
+                                               r, (int)off, 0, 0);
     }
 }
 

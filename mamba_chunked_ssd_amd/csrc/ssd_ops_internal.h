@@ -42,7 +42,6 @@ struct ConvArgs {
 struct ConvBwdPlan {
     int strip;      // tokens of one wave, a multiple of 16
     int nstrips;    // strips of one sequence
-    bool four;      // four channels a lane where alignment allows
     int64_t parts;  // batch * ceil(nstrips / 4)
 };
 ConvBwdPlan conv_bwd_plan(int64_t batch, int64_t seqlen, int64_t channels);
