@@ -5,6 +5,7 @@
 #include <hip/hip_runtime_api.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <initializer_list>
 #include <limits>
@@ -41,8 +42,7 @@ ScanPlan scan_plan(int64_t batch, int64_t seqlen, int64_t channels, int64_t dsta
     p.nblk = (int)(ngroups * p.gblocks);
     p.tiles = (seqlen + kScanSegment - 1) / kScanSegment * (kScanSegment / kScanTile);
     const int64_t waves = std::max<int64_t>(1, batch * p.nblk * 4);
-    int64_t root = 1;
-    while (root * root < seqlen) ++root;
+    const int64_t root = (int64_t)std::ceil(std::sqrt((double)seqlen));
     int64_t nseg = waves >= (backward ? kBwdWhole : kFwdWhole) ? 1 : (kScanWaves + waves - 1) / waves;
     nseg = std::max<int64_t>(1, std::min<int64_t>({nseg, seqlen / 16, root * 3 / 2}));
     int64_t len = (seqlen + nseg - 1) / nseg;

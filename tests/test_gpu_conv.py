@@ -247,3 +247,40 @@ def test_c_abi_events_free_call():
                                  y.data_ptr(), None, torch.cuda.current_stream().cuda_stream)
     assert st == 0
     assert torch.equal(y, ssd.causal_conv_fwd(d["x"], d["weight"], activation=None))
+
+
+def test_two_streams_at_once():
+    cases = [inputs(2, 300, 128, 4, "bf16", seed=70 + k) for k in range(2)]
+    call = lambda d: ssd.causal_conv_bwd(d["x"], d["weight"], d["bias"], d["dy"], d["init"], d["dfinal"])  # noqa: E731
+    want = [call(d) for d in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(3):
+        for k, (d, s) in enumerate(zip(cases, streams)):
+            with torch.cuda.stream(s):
+                got[k] = call(d)
+    torch.cuda.synchronize()
+    assert all(torch.equal(g[k], w[k]) for g, w in zip(got, want) for k in w)
+
+
+@pytest.mark.parametrize("c", [4096, 4099])
+def test_offsets_beyond_32_bits(c):
+    # 2.2e9 elements: the last rows against a call on them alone, continued from the inputs before them
+    L, tail = 540_000, 1000
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    piece = torch.randn((1000, c), generator=gen, device="cuda").bfloat16()
+    x = piece.repeat(L // 1000, 1)[None]
+    w, bias = torch.randn((c, 4), generator=gen, device="cuda"), torch.randn(c, generator=gen, device="cuda")
+    y, fin = ssd.causal_conv_fwd(x, w, bias, None, True, y_dtype=torch.bfloat16)
+    before = x[:, L - tail - 3:L - tail].contiguous()
+    y1, fin1 = ssd.causal_conv_fwd(x[:, -tail:], w, bias, before, True, y_dtype=torch.bfloat16)
+    assert torch.equal(y[:, -tail:], y1) and torch.equal(fin, fin1)
+    g = ssd.causal_conv_bwd(x, w, bias, y, dx_dtype=torch.bfloat16)
+    g1 = ssd.causal_conv_bwd(x[:, -tail:], w, bias, y[:, -tail:], before, dx_dtype=torch.bfloat16)
+    assert torch.equal(g["dx"][:, -tail:], g1["dx"])
+    # the sums: all pieces of 1000 rows but the first are alike
+    mid = ssd.causal_conv_bwd(x[:, 1000:2000], w, bias, y[:, 1000:2000], x[:, 997:1000].contiguous())
+    want = mid["dweight"].double() * (L // 1000 - 1)
+    first = ssd.causal_conv_bwd(x[:, :1000], w, bias, y[:, :1000])["dweight"].double()
+    assert float((g["dweight"].double() - want - first).norm() / want.norm()) < 1e-5

@@ -324,3 +324,68 @@ def test_convolution_before_the_chunked_scan():
         got = ssd.causal_conv_bwd(proj[..., a:z], w[a:z], None, up)
         want = lo.conv_bwd(host(proj[..., a:z]), host(w[a:z]), None, host(up))
         assert all(nerr(host(got[q]), want[q]) <= TOL for q in want)
+
+
+def test_interleaved_and_broadcast_rows():
+    # (seqlen, batch, channels) storage; B and C of one sequence read by the whole batch; one tensor as two inputs
+    d = inputs(3, 45, 20, 16, g=2)
+    want, gwant = fwd(d), bwd(d)
+    turned = dict(d)
+    for k in ("x", "dt", "z", "B", "C", "dy"):
+        turned[k] = d[k].transpose(0, 1).contiguous().transpose(0, 1)
+        assert not turned[k].is_contiguous()
+    got, ggot = fwd(turned), bwd(turned)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    assert all(torch.equal(ggot[k], gwant[k]) for k in gwant)
+    one = dict(d)
+    one["B"] = one["C"] = d["B"][:1].expand(3, 45, 2, 16)
+    plain = dict(d)
+    plain["B"] = plain["C"] = one["B"].contiguous()
+    assert all(torch.equal(p, q) for p, q in zip(fwd(one), fwd(plain)))
+    g1, g2 = bwd(one), bwd(plain)
+    assert all(torch.equal(g1[k], g2[k]) for k in g1)
+
+
+def test_two_streams_at_once():
+    cases = [inputs(2, 500, 64, 16, seed=60 + k) for k in range(2)]
+    want = [(fwd(d), bwd(d)) for d in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(3):
+        for k, (d, s) in enumerate(zip(cases, streams)):
+            with torch.cuda.stream(s):
+                got[k] = (fwd(d), bwd(d))
+    torch.cuda.synchronize()
+    for (f, g), (wf, wg) in zip(got, want):
+        assert all(torch.equal(p, q) for p, q in zip(f, wf)) and all(torch.equal(g[k], wg[k]) for k in wg)
+
+
+def test_offsets_beyond_32_bits():
+    # two sequences of 1.15e9 elements each: the second one's results against a call on it alone
+    b, L, c, n = 2, 140_000, 8192, 16
+    gen = torch.Generator(device="cuda").manual_seed(3)
+
+    def rows(width):
+        t = torch.empty((b, L, width), dtype=torch.bfloat16, device="cuda")
+        piece = torch.randn((b, 1000, width), generator=gen, device="cuda").bfloat16()
+        for t0 in range(0, L, 1000):
+            t[:, t0:t0 + 1000] = piece[:, :L - t0]
+        return t
+
+    x, dt = rows(c), rows(c)
+    B, C = rows(n)[:, :, None], rows(n)[:, :, None]
+    A = -torch.arange(1, n + 1, device="cuda").float().expand(c, n).contiguous()
+    bias = torch.full((c,), -3.0, device="cuda")
+    kw = dict(y_dtype=torch.bfloat16)
+    y, fin = ssd.selective_scan_fwd(x, dt, A, B, C, None, None, bias, None, True, **kw)
+    y1, fin1 = ssd.selective_scan_fwd(x[1:], dt[1:], A, B[1:], C[1:], None, None, bias, None, True, **kw)
+    assert float((y[1:, -4096:].float() - y1[:, -4096:].float()).abs().max()) <= 2.0 ** -7 * float(y1.abs().max())
+    assert float((fin[1:] - fin1).norm() / fin1.norm()) < TOL
+    del y1
+    g = ssd.selective_scan_bwd(x, dt, A, B, C, None, y, None, bias, want_d_initial=True)
+    g1 = ssd.selective_scan_bwd(x[1:], dt[1:], A, B[1:], C[1:], None, y[1:], None, bias, want_d_initial=True)
+    for k in ("dx", "ddt", "dB", "dC"):
+        a, r = g[k][1:, -4096:], g1[k][:, -4096:]
+        assert float((a - r).norm() / r.norm()) < TOL, k
+    assert float((g["d_initial_states"][1:] - g1["d_initial_states"]).norm() / g1["d_initial_states"].norm()) < TOL
