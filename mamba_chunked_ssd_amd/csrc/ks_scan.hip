@@ -114,28 +114,28 @@ __global__ __launch_bounds__(256) void ks_scan(ScanIn<Tin> a, const float *init,
         // tiles wholly behind the end
         const float zero[TPL] = {};
         for (; t < at.s1; t += kTT, ys.next()) ys.store(at.s1 - t, zero);
-        if (a.nseg == 1 && final_state != nullptr && at.ok)
+        if (at.seg == a.nseg - 1 && final_state != nullptr && at.ok)
             store_states_n(final_state + bc * a.N, n0, a.N, h);
     }
 }
 
 // The state at each segment's start, written over the segments' own end
-// states, and the final state: h <- exp(A sum of steps) h + own.
-__global__ __launch_bounds__(256) void ks_carry(const float *__restrict__ A, const float *init, float *seg_state,
-                                                const float *__restrict__ seg_steps, float *final_state, int channels,
-                                                int N, int NP, int nseg) {
+// states: h <- exp(A sum of steps) h + own.  The last segment has no own end
+// state: no segment starts from it.
+__global__ __launch_bounds__(256) void ks_carry(const float *__restrict__ A, const float *__restrict__ init,
+                                                float *__restrict__ seg_state, const float *__restrict__ seg_steps,
+                                                int channels, int N, int NP, int nseg) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int b = blockIdx.y;
     if (i >= (int64_t)channels * NP) return;
     const int c = (int)(i / NP), n = (int)(i % NP);
     const bool ok = n < N;
-    const int64_t bcn = ((int64_t)b * channels + c) * N + n;
     const float A2 = ok ? kLog2e * A[(int64_t)c * N + n] : 0.f;
-    const float h = carry_segments(ok && init != nullptr ? init[bcn] : 0.f, A2,
-                                   seg_state + (int64_t)b * nseg * channels * NP + i,
-                                   seg_steps + (int64_t)b * nseg * channels + c, (int64_t)channels * NP, channels, nseg,
-                                   false);
-    if (ok && final_state != nullptr) final_state[bcn] = h;
+    float *state = seg_state + (int64_t)b * nseg * channels * NP + i;
+    const float h = carry_segments(ok && init != nullptr ? init[((int64_t)b * channels + c) * N + n] : 0.f, A2, state,
+                                   seg_steps + (int64_t)b * nseg * channels + c, (int64_t)channels * NP, channels,
+                                   nseg - 1, false);
+    state[(int64_t)(nseg - 1) * channels * NP] = h;
 }
 
 // What one token of one channel brings beside its states.
@@ -254,13 +254,14 @@ hipError_t fwd(const ScanArgs &a, const ScanPlan &plan, hipStream_t stream) {
     const ScanIn<Tin> in = scan_in<Tin>(a, plan);
     const dim3 grid((unsigned)(plan.nblk * plan.nseg), (unsigned)a.batch);
     if (plan.nseg > 1) {
-        hipError_t e = launch_kernel(ks_scan<Tin, Tout, LPC, true>, grid, dim3(256), 0, stream, LaunchEvents{}, in,
-                                     a.init, a.seg_state, a.seg_steps, (Tout *)nullptr, (float *)nullptr);
+        const dim3 all_but_last((unsigned)(plan.nblk * (plan.nseg - 1)), (unsigned)a.batch);
+        hipError_t e = launch_kernel(ks_scan<Tin, Tout, LPC, true>, all_but_last, dim3(256), 0, stream, LaunchEvents{},
+                                     in, a.init, a.seg_state, a.seg_steps, (Tout *)nullptr, (float *)nullptr);
         if (e != hipSuccess) return e;
         const int64_t n = (int64_t)a.channels * plan.np;
         e = launch_kernel(ks_carry, dim3((unsigned)((n + 255) / 256), (unsigned)a.batch), dim3(256), 0, stream,
-                          LaunchEvents{}, a.A, a.init, a.seg_state, (const float *)a.seg_steps, a.final_state,
-                          a.channels, a.dstate, plan.np, plan.nseg);
+                          LaunchEvents{}, a.A, a.init, a.seg_state, (const float *)a.seg_steps, a.channels, a.dstate,
+                          plan.np, plan.nseg);
         if (e != hipSuccess) return e;
     }
     return launch_kernel(ks_scan<Tin, Tout, LPC, false>, grid, dim3(256), 0, stream, LaunchEvents{}, in, a.init,
