@@ -8,6 +8,11 @@ CPU fallback: if the library is missing, importing works but any call raises.
     y = chunk_scan_fwd(x, dt, A, B, C, D, chunk_size=256)
     y, final = chunk_scan_fwd(..., initial_states=h0, return_final_states=True)
 
+Beside it stand the operators of the layers around it: the short causal
+convolution (``causal_conv_fwd``, ``_bwd``, ``_step``) and the selective scan
+with a decay per channel and state (``selective_scan_fwd``, ``_bwd``,
+``_step``).
+
 The operation is the selective state-space recurrence of "Accelerating Mamba-2
 with High-Performance Forward Pass Kernels in NVIDIA CUDA Tile" (section
 "Mamba-2 architecture"): h_t = exp(A dt_t) h_{t-1} + dt_t B_t x_t^T,

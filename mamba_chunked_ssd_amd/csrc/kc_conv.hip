@@ -66,8 +66,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t group_rows(const T *first, int
 // A wave takes a run of 16 tokens, eight at a time with the next eight's loads
 // in flight.  Longer runs read the filters less often, from the L2, and were
 // slower (4 x 4096 tokens of 5376 channels, fp32: 130 us with 16, 137 with 32,
-// 149 with 128).  8 x 4096 tokens of 5376 channels, bf16: 140 us, 5.0 TB/s,
-// 97 % of a copy's rate.
+// 149 with 128).  8 x 4096 tokens of 5376 channels, bf16: 139 us, 5.1 TB/s,
+// 98 % of a copy's rate.
 constexpr int kFwdRun = 16;
 template <typename Tin, typename Tout, int W, int V>
 __global__ __launch_bounds__(256) void kc_conv_fwd(ConvIn<Tin> a, Tout *__restrict__ y, Tin *final_state, int nruns) {
@@ -144,7 +144,9 @@ __global__ __launch_bounds__(256) void kc_conv_fwd(ConvIn<Tin> a, Tout *__restri
 // dx_{t-W+1} is complete at t.  Rows come through raw buffers over the group,
 // so ends need no branch in the loop.  dw and db stay in registers over the
 // strip, are joined over the block's four strips in LDS and leave one row of
-// partial sums per block, which kc_conv_sums adds in a fixed order.
+// partial sums per block, which kc_conv_sums adds in a fixed order.  Bound by
+// memory: 2 x 2048 tokens of 5376 channels, bf16 with dy in fp32, 34 us of
+// which the 176 MB that must move take 34 at a copy's rate (sums 4 us more).
 constexpr int kGroup = 4;  // tokens; at least W - 1
 
 template <typename Tin, typename Tdy, typename Tdx, int W, int V>
@@ -368,11 +370,8 @@ ConvIn<Tin> conv_in(const ConvArgs &a, int V, int bx) {
     return in;
 }
 
-// Lanes of whole waves that V channels a lane would leave idle, at most one in four.
-bool waves_full(int channels, int V) {
-    const int64_t waves = (channels + 64 * V - 1) / (64 * V);
-    return 4 * (int64_t)channels >= 3 * waves * 64 * V;
-}
+// Whether four channels a lane leave at most one lane in four of their waves idle.
+bool waves_full(int channels) { return 4 * (int64_t)channels >= 3 * ((channels + 255) / 256 * (int64_t)256); }
 
 template <typename Tin, typename Tout, int W, int V>
 hipError_t fwd(const ConvArgs &a, hipStream_t stream) {
@@ -406,21 +405,17 @@ hipError_t step(const ConvArgs &a, hipStream_t stream) {
                          LaunchEvents{}, in, static_cast<Tin *>(const_cast<void *>(a.init)), static_cast<Tout *>(a.y));
 }
 
-// Whether V channels a thread fit every operand of the forward pass.
-template <typename Tin, typename Tout>
-bool fwd_vec(const ConvArgs &a, int V) {
-    return a.channels % V == 0 && a.xs.batch % V == 0 && a.xs.row % V == 0 && vec_ok<Tin>(a.x, V) &&
-           vec_ok<Tin>(a.init, V) && (uintptr_t)a.y % std::min<size_t>(16, V * sizeof(Tout)) == 0 &&
-           vec_ok<Tin>(a.final_state, V);
-}
-// The widest loads that fit and leave few lanes idle.
+// Four channels a lane where every operand's rows are whole pieces of four and
+// the waves they fill are nearly full, else one.  Measured (forward, 4 x 4096
+// tokens): 5376 channels fp32 135 us with four, 147 with one; bf16 75 with
+// four, 80 with eight, 81 with one.  264 channels, which fill half of two
+// waves of fours: fp32 8 x 4096 tokens 21.8 us with four, 19.8 with one, and
+// backward 35.5 and 32.5.
 template <typename Tin, typename Tout, int W>
 hipError_t fwd_v(const ConvArgs &a, hipStream_t s) {
-    if constexpr (sizeof(Tin) == 2) {
-        if (fwd_vec<Tin, Tout>(a, 8) && waves_full(a.channels, 8)) return fwd<Tin, Tout, W, 8>(a, s);
-    }
-    if (fwd_vec<Tin, Tout>(a, 4) && waves_full(a.channels, 4)) return fwd<Tin, Tout, W, 4>(a, s);
-    return fwd<Tin, Tout, W, 1>(a, s);
+    const bool v = a.channels % 4 == 0 && a.xs.batch % 4 == 0 && a.xs.row % 4 == 0 && vec_ok<Tin>(a.x, 4) &&
+                   vec_ok<Tin>(a.init, 4) && vec_ok<Tout>(a.y, 4) && vec_ok<Tin>(a.final_state, 4);
+    return v && waves_full(a.channels) ? fwd<Tin, Tout, W, 4>(a, s) : fwd<Tin, Tout, W, 1>(a, s);
 }
 template <int W>
 hipError_t fwd_w(const ConvArgs &a, hipStream_t s) {
@@ -428,13 +423,12 @@ hipError_t fwd_w(const ConvArgs &a, hipStream_t s) {
     return a.y_bf16 ? fwd_v<uint16_t, uint16_t, W>(a, s) : fwd_v<uint16_t, float, W>(a, s);
 }
 
-// Four channels a lane at most (eight would take the registers of two waves).
 template <typename Tin, typename Tdy, typename Tdx, int W>
 hipError_t bwd_v(const ConvArgs &a, const ConvBwdPlan &p, hipStream_t s) {
     const bool v = a.channels % 4 == 0 && a.xs.batch % 4 == 0 && a.xs.row % 4 == 0 && a.dys.batch % 4 == 0 &&
                    a.dys.row % 4 == 0 && vec_ok<Tin>(a.x, 4) && vec_ok<Tin>(a.init, 4) && vec_ok<Tdy>(a.dy, 4) &&
                    vec_ok<Tdx>(a.dx, 4) && vec_ok<float>(a.dfinal, 4) && vec_ok<float>(a.dinit, 4);
-    return v && waves_full(a.channels, 4) ? bwd<Tin, Tdy, Tdx, W, 4>(a, p, s) : bwd<Tin, Tdy, Tdx, W, 1>(a, p, s);
+    return v && waves_full(a.channels) ? bwd<Tin, Tdy, Tdx, W, 4>(a, p, s) : bwd<Tin, Tdy, Tdx, W, 1>(a, p, s);
 }
 
 template <int W>

@@ -16,8 +16,10 @@
 // sweep runs each from a zero state, leaving local tile states, the segment's
 // summary and its adjoint's together; the main kernel adds to a tile's local
 // state what the segment's start state has become by then (one exponential a
-// state and tile).  Bound by vector instructions, as the forward pass: about 35
-// issue slots per (token, channel, state) in all.
+// state and tile).  Bound by vector instructions, as the forward pass: 11 issue
+// slots per (token, channel, state) in the sweep, 26 in the main kernel (2 x
+// 2048 tokens of 5120 channels and 16 states: sweep 132 us at VALUBusy 71 %,
+// main kernel 300 at 79 %, carry 14, sums 16).
 //
 // dB and dC sum over channels, which lie across lanes and blocks: within a wave
 // by channel_sums, the rest of the block once per tile from LDS, and the
@@ -187,7 +189,8 @@ struct BwdOut {
 constexpr int kRedStride = 2 * kScanTile + 4;
 
 // One segment, its tiles from the last to the first.  Registers limit it: a
-// tile's states and decays take 8 a token, so tiles have 8 tokens.
+// tile's states and decays take 8 a token, so tiles have 8 tokens (167
+// registers at 16 states: three waves a SIMD; 16 tokens would leave one).
 template <typename Tin, typename Tdy, int LPC>
 __global__ __launch_bounds__(256, 2) void ks_bwd_main(ScanIn<Tin> a, const Tdy *__restrict__ dy, Strides dys,
                                                       const float *__restrict__ dfinal,

@@ -71,68 +71,33 @@ struct Raw<uint16_t, 4> {
         }
     }
 };
-template <>
-struct Raw<uint16_t, 8> {
-    u32x4 v;
-    __device__ void zero() { v = u32x4{0, 0, 0, 0}; }
-    __device__ void load(const uint16_t *p) { v = *reinterpret_cast<const u32x4 *>(p); }
-    __device__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) { v = buffer_load_x4(r, (int)off); }
-    __device__ void unpack(float (&f)[8]) const {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            f[2 * e] = bf16lo(v[e]);
-            f[2 * e + 1] = bf16hi(v[e]);
-        }
-    }
-};
-
 // V values stored as T (bf16: one rounding to nearest even, the output's own
-// type; sums before it are fp32).
+// type; sums before it are fp32), to memory or to a raw buffer, which drops
+// what falls outside.
 template <int V>
 __device__ __forceinline__ void store_n(float *p, const float (&f)[V]) {
-    if constexpr (V == 1) {
-        *p = f[0];
-    } else {
-#pragma unroll
-        for (int e = 0; e < V; e += 4)
-            *reinterpret_cast<floatx4 *>(p + e) = floatx4{f[e], f[e + 1], f[e + 2], f[e + 3]};
-    }
+    if constexpr (V == 1) *p = f[0];
+    else *reinterpret_cast<floatx4 *>(p) = floatx4{f[0], f[1], f[2], f[3]};
 }
 template <int V>
 __device__ __forceinline__ void store_n(uint16_t *p, const float (&f)[V]) {
-    if constexpr (V == 1) {
-        *p = (uint16_t)(pack_bf16(f[0], 0.f) & 0xffffu);
-    } else if constexpr (V == 4) {
-        *reinterpret_cast<u32x2 *>(p) = u32x2{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])};
-    } else {
-        *reinterpret_cast<u32x4 *>(p) = u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                                              pack_bf16(f[6], f[7])};
-    }
+    if constexpr (V == 1) *p = (uint16_t)(pack_bf16(f[0], 0.f) & 0xffffu);
+    else *reinterpret_cast<u32x2 *>(p) = u32x2{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])};
 }
-
-// The same into a raw buffer, which drops what falls outside.
 template <int V>
 __device__ __forceinline__ void store_n(const float *, __amdgpu_buffer_rsrc_t r, uint32_t off, const float (&f)[V]) {
-    if constexpr (V == 1) {
+    if constexpr (V == 1)
         __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f[0]), r, (int)off, 0, 0);
-    } else {
-#pragma unroll
-        for (int e = 0; e < V; e += 4)
-            __builtin_amdgcn_raw_buffer_store_b128(
-                __builtin_bit_cast(u32x4, floatx4{f[e], f[e + 1], f[e + 2], f[e + 3]}), r, (int)(off + 4 * e), 0, 0);
-    }
+    else
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, floatx4{f[0], f[1], f[2], f[3]}), r, (int)off, 0,
+                                               0);
 }
 template <int V>
 __device__ __forceinline__ void store_n(const uint16_t *, __amdgpu_buffer_rsrc_t r, uint32_t off, const float (&f)[V]) {
-    if constexpr (V == 1) {
+    if constexpr (V == 1)
         __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(pack_bf16(f[0], 0.f) & 0xffffu), r, (int)off, 0, 0);
-    } else if constexpr (V == 4) {
+    else
         __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])}, r, (int)off, 0, 0);
-    } else {
-        __builtin_amdgcn_raw_buffer_store_b128(u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                                                     pack_bf16(f[6], f[7])},
-                                               r, (int)off, 0, 0);
-    }
 }
 
 template <typename T>
