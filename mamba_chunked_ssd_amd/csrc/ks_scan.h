@@ -80,15 +80,16 @@ struct ScanPos {
 // entry points refuse row strides of 2^24 elements or more) and the same for
 // every tile; the scalar unit moves the base from tile to tile.
 
-template <int TT, typename T>
+template <int TT, typename T, bool FORTH = true>
 struct TileRows {
     const T *at;   // the tile's first row
-    int64_t move;  // elements from tile to tile
-    uint32_t row;  // bytes of a row
-    __device__ __forceinline__ TileRows(const T *p, const Strides &s, int b, int t, bool forwards = true)
-        : at(p + b * s.batch + t * s.row), move(forwards ? TT * s.row : -TT * s.row),
-          row((uint32_t)(s.row * (int64_t)sizeof(T))) {}
-    __device__ __forceinline__ void next() { at += move; }
+    uint32_t row;  // bytes of a row (a tile's are below 2^30: one scalar register each, of which the streams take many)
+    __device__ __forceinline__ TileRows(const T *p, const Strides &s, int b, int t)
+        : at(p + b * s.batch + t * s.row), row((uint32_t)(s.row * (int64_t)sizeof(T))) {}
+    __device__ __forceinline__ void next() {
+        const int64_t move = (uint32_t)TT * row;
+        at = reinterpret_cast<const T *>(reinterpret_cast<uintptr_t>(at) + (FORTH ? move : -move));
+    }
     // left: rows from the tile's first to the end
     __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile(int left) const {
         return uniform_rsrc(at, (uint32_t)min(max(left, 0), TT) * row);
@@ -124,14 +125,13 @@ __device__ __forceinline__ void raw_store(uint16_t *, __amdgpu_buffer_rsrc_t r, 
 // fewer tokens than a channel lanes, the lanes behind own none.
 template <int TT, int LPC>
 constexpr int own_tokens() { return TT >= LPC ? TT / LPC : 1; }
-template <int TT, int LPC, typename T, bool HOLD = true>
+template <int TT, int LPC, typename T, bool HOLD = true, bool FORTH = true>
 struct OwnRows {
     static constexpr int TPL = own_tokens<TT, LPC>();
-    TileRows<TT, T> rows;
+    TileRows<TT, T, FORTH> rows;
     uint32_t first;
-    __device__ __forceinline__ OwnRows(const T *p, const Strides &s, int b, int c, int j, bool ok, int t,
-                                       bool forwards = true)
-        : rows(p, s, b, t, forwards), first(ok && j < TT ? rows.offset(j, c) : kNowhere) {}
+    __device__ __forceinline__ OwnRows(const T *p, const Strides &s, int b, int c, int j, bool ok, int t)
+        : rows(p, s, b, t), first(ok && j < TT ? rows.offset(j, c) : kNowhere) {}
     __device__ __forceinline__ void next() { rows.next(); }
     __device__ __forceinline__ uint32_t base() const {
         uint32_t o = first;
@@ -154,13 +154,12 @@ struct OwnRows {
 
 // One element of B or C per thread and tile: the group's rows, padded states
 // and tokens behind the end as 0.
-template <int TT, int NP, typename T>
+template <int TT, int NP, typename T, bool FORTH = true>
 struct RowStage {
     static constexpr int E = (TT * NP + 255) / 256;
-    TileRows<TT, T> rows;
+    TileRows<TT, T, FORTH> rows;
     uint32_t off[E], v[E];
-    __device__ __forceinline__ RowStage(const T *p, const Strides &s, int b, int g, int N, int t, bool forwards = true)
-        : rows(p, s, b, t, forwards) {
+    __device__ __forceinline__ RowStage(const T *p, const Strides &s, int b, int g, int N, int t) : rows(p, s, b, t) {
 #pragma unroll
         for (int k = 0; k < E; ++k) {
             const int e = threadIdx.x + 256 * k, tok = e / NP, n = e % NP;

@@ -192,7 +192,7 @@ constexpr int kRedStride = 2 * kScanTile + 4;
 // tile's states and decays take 8 a token, so tiles have 8 tokens (167
 // registers at 16 states: three waves a SIMD; 16 tokens would leave one).
 template <typename Tin, typename Tdy, int LPC>
-__global__ __launch_bounds__(256, 2) void ks_bwd_main(ScanIn<Tin> a, const Tdy *__restrict__ dy, Strides dys,
+__global__ __launch_bounds__(256, LPC == 4 ? 3 : 2) void ks_bwd_main(ScanIn<Tin> a, const Tdy *__restrict__ dy, Strides dys,
                                                       const float *__restrict__ dfinal,
                                                       const float *__restrict__ seg_state,
                                                       const float *__restrict__ seg_adj,
@@ -228,15 +228,16 @@ __global__ __launch_bounds__(256, 2) void ks_bwd_main(ScanIn<Tin> a, const Tdy *
     // lanes without a channel read zeros: they add nothing to the sums over channels
     const int done = at.end > at.s0 ? at.s0 + (at.end - at.s0 + TT - 1) / TT * TT : at.s0;
     const int last = done - TT;
-    OwnRows<TT, LPC, Tin, false> dts(a.dt, a.dts, b, c, at.j, at.ok, last, false),
-        xs(a.x, a.xs, b, c, at.j, at.ok, last, false),
-        zs(gate ? a.z : a.x, gate ? a.zs : a.xs, b, c, at.j, at.ok, last, false);
-    OwnRows<TT, LPC, Tdy, false> gs(dy, dys, b, c, at.j, at.ok, last, false);
+    // backwards through the tiles, offsets formed again at each (registers)
+    using InRows = OwnRows<TT, LPC, Tin, false, false>;
+    using OutRows = OwnRows<TT, LPC, float, false, false>;
+    InRows dts(a.dt, a.dts, b, c, at.j, at.ok, last), xs(a.x, a.xs, b, c, at.j, at.ok, last),
+        zs(gate ? a.z : a.x, gate ? a.zs : a.xs, b, c, at.j, at.ok, last);
+    OwnRows<TT, LPC, Tdy, false, false> gs(dy, dys, b, c, at.j, at.ok, last);
     const Strides dense{(int64_t)a.L * a.channels, a.channels};
-    OwnRows<TT, LPC, float, false> dxs(out.dx, dense, b, c, at.j, at.ok, last, false),
-        ddts(out.ddt, dense, b, c, at.j, at.ok, last, false),
-        dzs(gate ? out.dz : out.dx, dense, b, c, at.j, at.ok, last, false);
-    RowStage<TT, NP, Tin> rB(a.B, a.Bs, b, at.g, a.N, last, false), rC(a.C, a.Cs, b, at.g, a.N, last, false);
+    OutRows dxs(out.dx, dense, b, c, at.j, at.ok, last), ddts(out.ddt, dense, b, c, at.j, at.ok, last),
+        dzs(gate ? out.dz : out.dx, dense, b, c, at.j, at.ok, last);
+    RowStage<TT, NP, Tin, false> rB(a.B, a.Bs, b, at.g, a.N, last), rC(a.C, a.Cs, b, at.g, a.N, last);
     float *db = out.db + at.blk * out.blk, *dc = out.dc + at.blk * out.blk;
 
     // rows behind the end
