@@ -634,7 +634,7 @@ def _result_dtype(dtype, given, name, torch):
 
 def _dense(t, name, dtype, shape, device, tensor):
     """As :func:`_check`, which words the error; one token's calls are as fast as their checks."""
-    if not (isinstance(t, tensor) and t.dtype == dtype and t.shape == shape and t.device == device
+    if not (isinstance(t, tensor) and t.dtype == dtype and t.shape == shape and t.get_device() == device.index
             and t.is_contiguous()):
         _check(t, name, dtype, shape, device)
 
@@ -642,7 +642,7 @@ def _dense(t, name, dtype, shape, device, tensor):
 def _rows(t, name, dtype, shape, device, tensor, lead):
     """Checks an input of rows that may lie apart, one per token (``lead`` 2: batch and token) or per batch entry
     (``lead`` 1), and returns its ssd_stride, None if it is dense."""
-    if isinstance(t, tensor) and t.dtype == dtype and t.shape == shape and t.device == device:
+    if isinstance(t, tensor) and t.dtype == dtype and t.shape == shape and t.get_device() == device.index:
         if t.is_contiguous():
             return None
         st = t.stride()
@@ -663,6 +663,13 @@ def _rows(t, name, dtype, shape, device, tensor, lead):
 
 def _addr(t):
     return None if t is None else t.data_ptr()
+
+
+def _rows_like(x, stride, shape, dtype, device, torch):
+    """A new dense tensor; ``empty_like`` is the cheaper call where x has that shape, type and layout."""
+    if dtype == x.dtype and stride.row == 0:
+        return torch.empty_like(x)
+    return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _call(where, device, stream, run, torch):
@@ -741,7 +748,7 @@ def causal_conv_fwd(x, weight, bias=None, initial_states=None, return_final_stat
         _dense(final_out, "final_out", x.dtype, (b, w - 1, c), dev, torch.Tensor)
 
     def run(handle):
-        y = out if out is not None else torch.empty((b, L, c), dtype=ytype, device=dev)
+        y = out if out is not None else _rows_like(x, shape.x, (b, L, c), ytype, dev, torch)
         fin = final_out
         if fin is None and return_final_states:
             fin = torch.empty((b, max(w - 1, 0), c), dtype=x.dtype, device=dev)
@@ -778,8 +785,8 @@ def causal_conv_bwd(x, weight, bias, dy, initial_states=None, d_final_states=Non
 
     def run(handle):
         f32 = dict(dtype=torch.float32, device=dev)
-        res = {"dx": torch.empty((b, L, c), dtype=dxtype, device=dev), "dweight": torch.empty((c, w), **f32),
-               "dbias": torch.empty((c,), **f32)}
+        res = {"dx": _rows_like(x, shape.x, (b, L, c), dxtype, dev, torch), "dweight": torch.empty_like(weight),
+               "dbias": torch.empty((c,), **f32) if bias is None else torch.empty_like(bias)}
         if want_d_initial:
             res["d_initial_states"] = torch.empty((b, max(w - 1, 0), c), **f32)
         ws, size, _keep = _workspace(workspace, lib.ssd_causal_conv_bwd_workspace_size(ctypes.byref(shape)), dev, torch)
@@ -807,7 +814,7 @@ def causal_conv_step(x, weight, bias, state, *, activation="silu", y_dtype=None,
         _dense(out, "out", ytype, (b, c), dev, torch.Tensor)
 
     def run(handle):
-        y = out if out is not None else torch.empty((b, c), dtype=ytype, device=dev)
+        y = out if out is not None else _rows_like(x, shape.x, (b, c), ytype, dev, torch)
         st = load_library().ssd_causal_conv_step(ctypes.byref(shape), x.data_ptr(), weight.data_ptr(), _addr(bias),
                                                  state.data_ptr(), y.data_ptr(), handle)
         return st, y
@@ -868,7 +875,7 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, initial_sta
         _dense(final_out, "final_out", torch.float32, (b, c, n), dev, torch.Tensor)
 
     def run(handle):
-        y = out if out is not None else torch.empty((b, L, c), dtype=ytype, device=dev)
+        y = out if out is not None else _rows_like(x, shape.x, (b, L, c), ytype, dev, torch)
         fin = final_out
         if fin is None and return_final_states:
             fin = torch.empty((b, c, n), dtype=torch.float32, device=dev)
@@ -941,7 +948,7 @@ def selective_scan_step(x, dt, A, B, C, D, state, z=None, dt_bias=None, *, dt_so
         _dense(out, "out", ytype, (b, c), dev, torch.Tensor)
 
     def run(handle):
-        y = out if out is not None else torch.empty((b, c), dtype=ytype, device=dev)
+        y = out if out is not None else _rows_like(x, shape.x, (b, c), ytype, dev, torch)
         st = load_library().ssd_selective_scan_step(
             ctypes.byref(shape), x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _addr(D),
             _addr(z), _addr(dt_bias), state.data_ptr(), y.data_ptr(), handle)
