@@ -158,7 +158,8 @@ struct StepToken {
 // One token: a stream of the state (bound by memory, 8 bytes a state), a
 // thread four neighbouring entries as one 16-byte piece (5120 channels of 16,
 // batch 128: 5.2 TB/s, the rate of a copy).
-template <typename Tin, typename Tout, int LPC>
+// FULL: no lane without states (a branch around the loads costs 7 % there).
+template <typename Tin, typename Tout, int LPC, bool FULL>
 __global__ __launch_bounds__(256) void ks_step(ScanIn<Tin> a, float *state, Tout *__restrict__ y) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int b = blockIdx.y, n0 = 4 * (int)(i % LPC);
@@ -166,7 +167,7 @@ __global__ __launch_bounds__(256) void ks_step(ScanIn<Tin> a, float *state, Tout
     const int c = (int)(i / LPC), g = c / a.cpg;
     const int64_t bc = (int64_t)b * a.channels + c;
     float h[4] = {}, A[4] = {}, Bv[4] = {}, Cv[4] = {};
-    if (n0 < a.N) {
+    if (FULL || n0 < a.N) {
         load_states(state + bc * a.N + n0, h);
         load_states(a.A + (int64_t)c * a.N + n0, A);
         const Tin *Bp = a.B + b * a.Bs.batch + (int64_t)g * a.N, *Cp = a.C + b * a.Cs.batch + (int64_t)g * a.N;
@@ -184,7 +185,7 @@ __global__ __launch_bounds__(256) void ks_step(ScanIn<Tin> a, float *state, Tout
         h[r] = fmaf(fast_exp2(kLog2e * A[r] * tok.d), h[r], u * Bv[r]);
         s = fmaf(Cv[r], h[r], s);
     }
-    if (n0 < a.N) store_states(state + bc * a.N + n0, h);
+    if (FULL || n0 < a.N) store_states(state + bc * a.N + n0, h);
     s = lane_total<LPC>(s);
     if (n0 == 0) {
         const float o[1] = {tok.output(s, a.z != nullptr)};
@@ -278,7 +279,8 @@ ScanIn<Tin> step_in(const ScanArgs &a) {
 template <typename Tin, typename Tout, int LPC>
 hipError_t step(const ScanArgs &a, hipStream_t stream) {
     const dim3 grid((unsigned)(((int64_t)a.channels * LPC + 255) / 256), (unsigned)a.batch);
-    return launch_kernel(ks_step<Tin, Tout, LPC>, grid, dim3(256), 0, stream, LaunchEvents{}, step_in<Tin>(a),
+    const auto kernel = a.dstate == 4 * LPC ? ks_step<Tin, Tout, LPC, true> : ks_step<Tin, Tout, LPC, false>;
+    return launch_kernel(kernel, grid, dim3(256), 0, stream, LaunchEvents{}, step_in<Tin>(a),
                          const_cast<float *>(a.init), static_cast<Tout *>(a.y));
 }
 
