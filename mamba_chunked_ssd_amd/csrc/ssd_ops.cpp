@@ -33,14 +33,25 @@ ConvBwdPlan conv_bwd_plan(int64_t batch, int64_t seqlen, int64_t channels) {
 // Segments of the time axis.  They cost the summary pass (two thirds of the
 // output pass's work; the backward sweep is there anyway) and a carry whose
 // time grows with their number, and pay by filling the SIMDs: one wave alone
-// runs at 45 % of a SIMD's rate, six at 80 %.  Measured with 5120 channels of
-// 16 states, 2048 tokens: batch 8 (2560 waves) 500 us whole, 558 cut; batch 4
-// (1280) 375 whole, 281 cut; batch 2 286 whole, 153 cut; backward at batch 8
-// 1752 whole, 1641 cut.  16 384 waves rather than 8192: batch 4 287 against
-// 306 us.  The carry bounds the number by the square root of the length:
-// 65 536 tokens of 64 channels 88 us with that many segments, 259 with four
-// times as many, 127 with half.
-constexpr int64_t kFwdWhole = 2048, kBwdWhole = 4096, kScanWaves = 16384;
+// runs at 45 % of a SIMD's rate, six at 80 %.
+//
+// Whole or cut, forward: whole, the time goes in steps with the waves on the
+// fullest of the 1024 SIMDs, cut, with the waves.  Measured per 2048 tokens of
+// 16 states (5120 channels are 320 waves a sequence), whole and cut:
+//   1280 waves 376 and 295 us, 1600 378 and 345, 1920 380 and 413,
+//   2240 500 and 470, 2560 503 and 528, 3200 593 and 652,
+// which 180 + 105 steps and 25 + 0.203 waves follow.  Backward: 2560 waves
+// 1654 and 1581 us, 3840 2349 and 2300, 5120 2768 and 3020.
+//
+// How many, when cut: enough for 16 384 waves (4 x 2048 tokens 281 us, with
+// 8192 waves 306), but no more than 1.5 times the square root of the length,
+// or the carry weighs (65 536 tokens of 64 channels: 88 us with the root, 259
+// with four times as many, 127 with half).
+constexpr int64_t kBwdWhole = 4096, kScanWaves = 16384;
+bool scan_whole(int64_t waves, bool backward) {
+    if (backward) return waves >= kBwdWhole;
+    return 180 + 105 * ((waves + 1023) / 1024) <= 25 + waves * 203 / 1000;
+}
 ScanPlan scan_plan(int64_t batch, int64_t seqlen, int64_t channels, int64_t dstate, int64_t ngroups, bool backward) {
     ScanPlan p;
     // the backward pass has no layout of two lanes a channel (its registers do not hold 8 tokens a lane)
@@ -51,7 +62,7 @@ ScanPlan scan_plan(int64_t batch, int64_t seqlen, int64_t channels, int64_t dsta
     p.tiles = (seqlen + kScanSegment - 1) / kScanSegment * (kScanSegment / kScanTile);
     const int64_t waves = std::max<int64_t>(1, batch * p.nblk * 4);
     const int64_t root = (int64_t)std::ceil(std::sqrt((double)seqlen));
-    int64_t nseg = waves >= (backward ? kBwdWhole : kFwdWhole) ? 1 : (kScanWaves + waves - 1) / waves;
+    int64_t nseg = scan_whole(waves, backward) ? 1 : (kScanWaves + waves - 1) / waves;
     nseg = std::max<int64_t>(1, std::min<int64_t>({nseg, seqlen / 16, root * 3 / 2}));
     int64_t len = (seqlen + nseg - 1) / nseg;
     len = std::max<int64_t>(kScanSegment, (len + kScanSegment - 1) / kScanSegment * kScanSegment);
