@@ -66,7 +66,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t group_rows(const T *first, int
 // A wave takes a run of 16 tokens, eight at a time with the next eight's loads
 // in flight.  Longer runs read the filters less often, from the L2, and were
 // slower (4 x 4096 tokens of 5376 channels, fp32: 130 us with 16, 137 with 32,
-// 149 with 128).  8 x 4096 tokens of 5376 channels, bf16: 139 us, 5.1 TB/s,
+// 149 with 128).  8 x 4096 tokens of 5376 channels, bf16: 134 us, 5.25 TB/s,
 // 98 % of a copy's rate.
 constexpr int kFwdRun = 16;
 template <typename Tin, typename Tout, int W, int V>
@@ -145,7 +145,7 @@ __global__ __launch_bounds__(256) void kc_conv_fwd(ConvIn<Tin> a, Tout *__restri
 // so ends need no branch in the loop.  dw and db stay in registers over the
 // strip, are joined over the block's four strips in LDS and leave one row of
 // partial sums per block, which kc_conv_sums adds in a fixed order.  Bound by
-// memory: 2 x 2048 tokens of 5376 channels, bf16 with dy in fp32, 34 us of
+// memory: 2 x 2048 tokens of 5376 channels, bf16 with dy in fp32, 35 us of
 // which the 176 MB that must move take 34 at a copy's rate (sums 4 us more).
 constexpr int kGroup = 4;  // tokens; at least W - 1
 

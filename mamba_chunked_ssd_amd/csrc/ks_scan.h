@@ -10,7 +10,7 @@
 // product and two fused multiply-adds per token, and the scan is bound by
 // vector instructions, not by memory.  2 x 2048 tokens of 5120 channels and 16
 // states, bf16: six slots a state are 53 us at the measured 4.17 cycles a slot
-// on 1024 SIMDs; the output pass takes 91 (8.3 slots a state, VALUBusy 85 %),
+// on 1024 SIMDs; the output pass takes 91 (8.3 slots a state, VALUBusy 87 %),
 // the summary pass before it 66; their bytes at a copy's rate 32.
 //
 // Layout: a channel's NP padded states lie on LPC = NP / 4 neighbouring lanes,
@@ -79,7 +79,6 @@ struct ScanPos {
 // stores are dropped without a branch.  Offsets into the tile are 32-bit (the
 // entry points refuse row strides of 2^24 elements or more) and the same for
 // every tile; the scalar unit moves the base from tile to tile.
-
 template <int TT, typename T, bool FORTH = true>
 struct TileRows {
     const T *at;   // the tile's first row

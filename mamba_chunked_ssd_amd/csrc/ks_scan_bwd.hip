@@ -17,9 +17,9 @@
 // summary and its adjoint's together; the main kernel adds to a tile's local
 // state what the segment's start state has become by then (one exponential a
 // state and tile).  Bound by vector instructions, as the forward pass: 11 issue
-// slots per (token, channel, state) in the sweep, 26 in the main kernel (2 x
-// 2048 tokens of 5120 channels and 16 states: sweep 132 us at VALUBusy 71 %,
-// main kernel 300 at 79 %, carry 14, sums 16).
+// slots per (token, channel, state) in the sweep, 25 in the main kernel (2 x
+// 2048 tokens of 5120 channels and 16 states: sweep 132 us at VALUBusy 74 %,
+// main kernel 300 at 79 %, carry 15, sums 16).
 //
 // dB and dC sum over channels, which lie across lanes and blocks: within a wave
 // by channel_sums, the rest of the block once per tile from LDS, and the
@@ -192,12 +192,13 @@ constexpr int kRedStride = 2 * kScanTile + 4;
 // tile's states and decays take 8 a token, so tiles have 8 tokens (167
 // registers at 16 states: three waves a SIMD; 16 tokens would leave one).
 template <typename Tin, typename Tdy, int LPC>
-__global__ __launch_bounds__(256, LPC == 4 ? 3 : 2) void ks_bwd_main(ScanIn<Tin> a, const Tdy *__restrict__ dy, Strides dys,
-                                                      const float *__restrict__ dfinal,
-                                                      const float *__restrict__ seg_state,
-                                                      const float *__restrict__ seg_adj,
-                                                      const float *__restrict__ tile_state,
-                                                      const float *__restrict__ tile_steps, int64_t tiles, BwdOut out) {
+__global__ __launch_bounds__(256, LPC == 4 ? 3 : 2)
+void ks_bwd_main(ScanIn<Tin> a, const Tdy *__restrict__ dy, Strides dys,
+                 const float *__restrict__ dfinal,
+                 const float *__restrict__ seg_state,
+                 const float *__restrict__ seg_adj,
+                 const float *__restrict__ tile_state,
+                 const float *__restrict__ tile_steps, int64_t tiles, BwdOut out) {
     constexpr int TT = kScanTile, NP = 4 * LPC, TPL = own_tokens<TT, LPC>();
     __shared__ float sB[TT * NP], sC[TT * NP], red[256 * kRedStride];
     const ScanPos<LPC> at(a);
@@ -225,10 +226,10 @@ __global__ __launch_bounds__(256, LPC == 4 ? 3 : 2) void ks_bwd_main(ScanIn<Tin>
     const bool gate = a.z != nullptr;
     float dD = 0.f, dbias = 0.f;
 
-    // lanes without a channel read zeros: they add nothing to the sums over channels
     const int done = at.end > at.s0 ? at.s0 + (at.end - at.s0 + TT - 1) / TT * TT : at.s0;
     const int last = done - TT;
-    // backwards through the tiles, offsets formed again at each (registers)
+    // backwards through the tiles, offsets formed again at each (registers);
+    // lanes without a channel read zeros: they add nothing to the sums over channels
     using InRows = OwnRows<TT, LPC, Tin, false, false>;
     using OutRows = OwnRows<TT, LPC, float, false, false>;
     InRows dts(a.dt, a.dts, b, c, at.j, at.ok, last), xs(a.x, a.xs, b, c, at.j, at.ok, last),

@@ -22,7 +22,8 @@ namespace ssd {
 // of 264: 23 us with 16).
 ConvBwdPlan conv_bwd_plan(int64_t batch, int64_t seqlen, int64_t channels) {
     ConvBwdPlan p;
-    const int64_t waves = (channels + 255) / 256;  // of four channels a lane; with one there are up to four times as many
+    // of four channels a lane; with one there are up to four times as many
+    const int64_t waves = (channels + 255) / 256;
     p.strip = 128;
     while (p.strip > 16 && batch * waves * ((seqlen + p.strip - 1) / p.strip) < 2 * 1024) p.strip /= 2;
     p.nstrips = (int)std::max<int64_t>(1, (seqlen + p.strip - 1) / p.strip);
@@ -169,7 +170,8 @@ ssd_status check_conv(const ssd_conv_shape *s, ConvArgs *a, ConvBytes *n) {
     int64_t work;
     if (!product({(s->channels + 63) / 64, s->seqlen / 64 + 2}, &work) || work >= (int64_t)1 << 24)
         return SSD_ERROR_UNSUPPORTED;
-    const size_t tok = (size_t)(s->batch * s->seqlen * s->channels), held = (size_t)(s->batch * (s->width - 1) * s->channels);
+    const size_t tok = (size_t)(s->batch * s->seqlen * s->channels);
+    const size_t held = (size_t)(s->batch * (s->width - 1) * s->channels);
     a->batch = s->batch;
     a->seqlen = (int)s->seqlen;
     a->channels = (int)s->channels;

@@ -16,7 +16,8 @@ constexpr uint32_t kNowhere = 0x7fffff00u;  // an offset behind any raw buffer h
 // values.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void *base, uint32_t bytes) {
     const uint64_t a = reinterpret_cast<uint64_t>(base);
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a), hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
     return buffer_rsrc(reinterpret_cast<const void *>((uint64_t)hi << 32 | lo), __builtin_amdgcn_readfirstlane(bytes));
 }
 
@@ -250,8 +251,10 @@ __device__ __forceinline__ void channel_sums(const float (&v)[2][4], float &s0, 
                 y = upper ? d : c;
             } else {
                 // lanes 32-63 of the first and 0-31 of the second change places
-                const auto e = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[q][0]), __float_as_uint(v[q][2]), false, false);
-                const auto o = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[q][1]), __float_as_uint(v[q][3]), false, false);
+                const auto e = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[q][0]), __float_as_uint(v[q][2]),
+                                                                false, false);
+                const auto o = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[q][1]), __float_as_uint(v[q][3]),
+                                                                false, false);
                 x = __uint_as_float(e[0]) + __uint_as_float(e[1]);
                 y = __uint_as_float(o[0]) + __uint_as_float(o[1]);
             }
