@@ -507,7 +507,7 @@ typedef struct {
 
 /* Forward pass over prompts.
  *   x, dt, z         (batch, seqlen, channels) dtype; z NULL => no gate
- *   A                (channels, dstate) fp32, <= 0
+ *   A                (channels, dstate) fp32, <= 0; -infinity: that state keeps nothing
  *   B, C             (batch, seqlen, ngroups, dstate) dtype
  *   D, dt_bias       (channels) fp32, NULL => 0
  *   initial_states   (batch, channels, dstate) fp32, NULL => 0

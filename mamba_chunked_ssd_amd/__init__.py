@@ -705,6 +705,8 @@ def _workspace(given, need, device, torch):
 def _conv_args(x, weight, bias, lengths, activation, lead, torch):
     tensor, f32 = torch.Tensor, torch.float32
     code = _input_dtype(x, torch)
+    if not isinstance(weight, tensor):
+        raise TypeError("weight must be a torch.Tensor")
     dims = x.shape
     if len(dims) != lead + 1 or weight.dim() != 2:
         raise ValueError("x must be (batch, %schannels) and weight (channels, width)" % ("seqlen, " if lead == 2 else ""))
@@ -777,6 +779,8 @@ def causal_conv_bwd(x, weight, bias, dy, initial_states=None, d_final_states=Non
         _dense(initial_states, "initial_states", x.dtype, (b, w - 1, c), dev, torch.Tensor)
     if d_final_states is not None:
         _dense(d_final_states, "d_final_states", torch.float32, (b, w - 1, c), dev, torch.Tensor)
+    if not isinstance(dy, torch.Tensor):
+        raise TypeError("dy must be a torch.Tensor")
     dytype, shape.y_dtype = _result_dtype(dy.dtype, x.dtype, "dy's dtype", torch)
     st = _rows(dy, "dy", dytype, x.shape, dev, torch.Tensor, 2)
     if st is not None:
@@ -825,6 +829,8 @@ def causal_conv_step(x, weight, bias, state, *, activation="silu", y_dtype=None,
 def _scan_args(x, dt, A, B, C, D, z, dt_bias, lengths, dt_softplus, lead, torch):
     tensor, f32 = torch.Tensor, torch.float32
     code = _input_dtype(x, torch)
+    if not (isinstance(A, tensor) and isinstance(B, tensor)):
+        raise TypeError("A and B must be torch.Tensor")
     dims, of_b = x.shape, B.shape
     if len(dims) != lead + 1 or len(of_b) != lead + 2 or A.dim() != 2:
         raise ValueError("x must be (batch, %schannels), B (batch, %sngroups, dstate) and A (channels, dstate)"
@@ -904,6 +910,8 @@ def selective_scan_bwd(x, dt, A, B, C, D, dy, z=None, dt_bias=None, initial_stat
     for name, t in (("initial_states", initial_states), ("d_final_states", d_final_states)):
         if t is not None:
             _dense(t, name, torch.float32, (b, c, n), dev, torch.Tensor)
+    if not isinstance(dy, torch.Tensor):
+        raise TypeError("dy must be a torch.Tensor")
     dytype, shape.y_dtype = _result_dtype(dy.dtype, x.dtype, "dy's dtype", torch)
     st = _rows(dy, "dy", dytype, x.shape, dev, torch.Tensor, 2)
     if st is not None:

@@ -267,6 +267,15 @@ __device__ __forceinline__ void store_states_n(float *p, int n0, int N, const fl
         if (n0 + r < N) p[n0 + r] = h[r];
 }
 
+// The decay's rate in base 2, exp(d A) = exp2(d rate(A)), held finite: rows
+// behind an end take steps of 0, and 0 times the infinite A of a state that
+// keeps nothing would be NaN.  A NaN stays one.
+__device__ __forceinline__ float rate(float A) {
+    constexpr float most = __FLT_MAX__;
+    const float v = kLog2e * A;
+    return v < -most ? -most : v > most ? most : v;
+}
+
 // One state of one channel over the segments, in their order (or backwards,
 // for the gradient): each slot's own end value gives way to the value it
 // starts from, h <- exp2(A2 sum of steps) h + own.  Eight slots are loaded

@@ -21,7 +21,7 @@ __global__ __launch_bounds__(256) void ks_scan(ScanIn<Tin> a, const float *init,
     float A2[4], h[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        A2[r] = n0 + r < a.N ? kLog2e * a.A[(int64_t)c * a.N + n0 + r] : 0.f;
+        A2[r] = n0 + r < a.N ? rate(a.A[(int64_t)c * a.N + n0 + r]) : 0.f;
         h[r] = 0.f;
     }
     if (!SUMMARY) {
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(256) void ks_carry(const float *__restrict__ A, con
     if (i >= (int64_t)channels * NP) return;
     const int c = (int)(i / NP), n = (int)(i % NP);
     const bool ok = n < N;
-    const float A2 = ok ? kLog2e * A[(int64_t)c * N + n] : 0.f;
+    const float A2 = ok ? rate(A[(int64_t)c * N + n]) : 0.f;
     float *state = seg_state + (int64_t)b * nseg * channels * NP + i;
     const float h = carry_segments(ok && init != nullptr ? init[((int64_t)b * channels + c) * N + n] : 0.f, A2, state,
                                    seg_steps + (int64_t)b * nseg * channels + c, (int64_t)channels * NP, channels,

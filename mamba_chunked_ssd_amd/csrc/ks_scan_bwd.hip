@@ -48,7 +48,7 @@ __global__ __launch_bounds__(256) void ks_bwd_sweep(ScanIn<Tin> a, const Tdy *__
     float A2[4], h[4], P[4], Gs[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        A2[r] = n0 + r < a.N ? kLog2e * a.A[(int64_t)c * a.N + n0 + r] : 0.f;
+        A2[r] = n0 + r < a.N ? rate(a.A[(int64_t)c * a.N + n0 + r]) : 0.f;
         h[r] = Gs[r] = 0.f;
         P[r] = 1.f;
     }
@@ -168,7 +168,7 @@ __global__ __launch_bounds__(256) void ks_bwd_carry(const float *__restrict__ A,
     const int c = (int)(i / NP), n = (int)(i % NP);
     const bool ok = n < N;
     const int64_t bcn = ((int64_t)b * channels + c) * N + n;
-    const float A2 = ok ? kLog2e * A[(int64_t)c * N + n] : 0.f;
+    const float A2 = ok ? rate(A[(int64_t)c * N + n]) : 0.f;
     const float *from = adj ? dfinal : init;
     const float h = carry_segments(ok && from != nullptr ? from[bcn] : 0.f, A2,
                                    (adj ? seg_adj : seg_state) + (int64_t)b * nseg * channels * NP + i,
@@ -212,7 +212,7 @@ void ks_bwd_main(ScanIn<Tin> a, const Tdy *__restrict__ dy, Strides dys,
     float A2[4], carry[4], dA[4], hs[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        A2[r] = n0 + r < a.N ? kLog2e * a.A[(int64_t)c * a.N + n0 + r] : 0.f;
+        A2[r] = n0 + r < a.N ? rate(a.A[(int64_t)c * a.N + n0 + r]) : 0.f;
         dA[r] = hs[r] = 0.f;
     }
     if (segs) {
@@ -298,10 +298,6 @@ void ks_bwd_main(ScanIn<Tin> a, const Tdy *__restrict__ dy, Strides dys,
                 o[i] *= z * s;
             }
         }
-        if (left < TT || TT < LPC) {
-#pragma unroll
-            for (int i = 0; i < TPL; ++i) sl[i] = i * LPC + at.j < min(left, TT) ? sl[i] : 0.f;
-        }
 #pragma unroll
         for (int r = 0; r < 4; ++r) h0[r] = hr[r];
         if (segs) {
@@ -359,9 +355,15 @@ void ks_bwd_main(ScanIn<Tin> a, const Tdy *__restrict__ dy, Strides dys,
             const float gB = own_sum<TT, LPC>(pB, i, at.j), gA = own_sum<TT, LPC>(pA, i, at.j);
             ddtv[i] = fmaf(0.6931471805599453f, gA, gB * x[i]) * sl[i];  // pA used log2(e) A
             dxv[i] = fmaf(gB, d[i], D * o[i]);
-            dbias += ddtv[i];
             dD = fmaf(o[i], x[i], dD);
         }
+        // rows that take no step, where the states' part may be anything
+        if (left < TT || TT < LPC) {
+#pragma unroll
+            for (int i = 0; i < TPL; ++i) ddtv[i] = i * LPC + at.j < min(left, TT) ? ddtv[i] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < TPL; ++i) dbias += ddtv[i];
         dxs.store(room, dxv);
         ddts.store(room, ddtv);
         dxs.next();

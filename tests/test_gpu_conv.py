@@ -174,6 +174,15 @@ def test_interleaved_and_broadcast_rows():
     assert all(torch.equal(got[i], want[0]) for i in range(3))
 
 
+def test_arguments_that_are_no_tensors():
+    d = inputs(2, 8, 16, 4, "f32")
+    for x, weight, bias in ((3.0, d["weight"], d["bias"]), (d["x"], None, d["bias"]), (d["x"], d["weight"], 3.0)):
+        with pytest.raises(TypeError):
+            ssd.causal_conv_fwd(x, weight, bias)
+    with pytest.raises(TypeError):
+        ssd.causal_conv_bwd(d["x"], d["weight"], d["bias"], None)
+
+
 def test_refusals_leave_the_outputs():
     d = inputs(2, 8, 16, 4, "f32")
     y = torch.full((2, 8, 16), 7.0, device="cuda")

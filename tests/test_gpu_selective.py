@@ -181,6 +181,30 @@ def test_extreme_steps():
     assert all(bool(torch.isfinite(v).all()) for v in got.values())
 
 
+@pytest.mark.parametrize("b,L,c,n", [(2, 5, 8, 16), (1, 301, 40, 16), (2, 37, 12, 6), (1, 20, 9, 40)])
+def test_states_that_keep_nothing(b, L, c, n):
+    # A of -infinity: exp(d A) = 0 at every token, also where tiles and segments end in rows that take no step
+    d = inputs(b, L, c, n, ragged=b > 1, seed=5)
+    d["A"][:, ::3] = -float("inf")
+    d["A"][0] = -float("inf")
+    a = {k: host(d[k]) for k in NAMES}
+    a["A"] = np.maximum(a["A"], -1e30)  # as good as infinite, and 0 times it is 0
+    y, fin = fwd(d)
+    ref, rfin = lo.scan(*[a[k] for k in NAMES])
+    assert nerr(host(y), ref) <= TOL and nerr(host(fin), rfin) <= TOL
+    got = bwd(d)
+    want = lo.scan_bwd(a["x"], a["dt"], a["A"], a["B"], a["C"], a["D"], host(d["dy"]), a["z"], a["dt_bias"], a["init"],
+                       host(d["dfinal"]), a["lengths"])
+    errs = {k: nerr(host(got[k]), r) for k, r in want.items()}
+    assert all(e <= TOL for e in errs.values()), errs
+    state = d["init"].clone()
+    row = {k: d[k][:, 0].contiguous() for k in ("x", "dt", "B", "C", "z")}
+    y1 = ssd.selective_scan_step(row["x"], row["dt"], d["A"], row["B"], row["C"], d["D"], state, row["z"], d["dt_bias"])
+    a1 = dict(a, **{k: a[k][:, :1] for k in ("x", "dt", "B", "C", "z")}, lengths=None)
+    ref, rfin = lo.scan(*[a1[k] for k in NAMES])
+    assert nerr(host(y1), ref[:, 0]) <= TOL and nerr(host(state), rfin) <= TOL
+
+
 def test_prompt_in_pieces_with_the_state_in_place():
     d = inputs(2, 400, 24, 16, dtype="bf16")
     want, wfin = fwd(d)
@@ -230,6 +254,15 @@ def test_refusals_leave_the_outputs():
         bwd(d, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     torch.cuda.synchronize()
     assert bool((y == 7.0).all())
+
+
+def test_arguments_that_are_no_tensors():
+    d = inputs(1, 4, 8, 16)
+    for k in ("x", "dt", "A", "B", "C", "z", "dt_bias", "init", "lengths"):
+        with pytest.raises(TypeError):
+            fwd(dict(d, **{k: 3.0}))
+    with pytest.raises(TypeError):
+        bwd(d, dy=3.0)
 
 
 def test_captured_call_replays():
