@@ -225,8 +225,10 @@ __global__ __launch_bounds__(256) void kc_conv_bwd(ConvIn<Tin> a, const Tdy *__r
 #pragma unroll
                         for (int k = 0; k < W; ++k) p = fmaf(w[k][e], win[k][e], p);
                         const float sg = logistic(p);
-                        // silu'(p) = s (1 + p (1 - s)); rows behind the end have dy = 0
+                        // silu'(p) = s (1 + p (1 - s))
                         de *= sg * fmaf(p, 1.f - sg, 1.f);
+                        // the first rows behind the end still see the last inputs, and 0 times their slope may be NaN
+                        de = t + u < len ? de : 0.f;
                     }
                     dp[W - 1][e] = de;
                     if (own) {
@@ -253,6 +255,12 @@ __global__ __launch_bounds__(256) void kc_conv_bwd(ConvIn<Tin> a, const Tdy *__r
                         for (int e = 0; e < V; ++e) g[u][e] += f[e];
                     }
                 }
+            }
+            if (s0 + U > len) {  // whatever the filter
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) g[u][e] = s0 + u < len ? g[u][e] : 0.f;
             }
             // the strip's first rows have no place here: they end the strip before, or the initial state
             const bool first = t == t0;

@@ -293,3 +293,39 @@ def test_offsets_beyond_32_bits(c):
     want = mid["dweight"].double() * (L // 1000 - 1)
     first = ssd.causal_conv_bwd(x[:, :1000], w, bias, y[:, :1000])["dweight"].double()
     assert float((g["dweight"].double() - want - first).norm() / want.norm()) < 1e-5
+
+
+@pytest.mark.parametrize("c", [24, 512])  # one channel a lane, and four
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+def test_last_inputs_not_finite_leave_the_rows_behind_them_zero(c, value):
+    # the first W - 1 rows behind an end have the last inputs in their windows
+    L, W = 40, 4
+    d = inputs(4, L, c, W, "f32", seed=6)
+    d["lengths"] = torch.tensor([L, 18, 2, 0], dtype=torch.int32, device="cuda")
+    for i, end in enumerate(d["lengths"].tolist()):
+        if end > 0:
+            d["x"][i, end - 1, ::2] = value
+        else:
+            d["init"][i, -1, ::2] = value
+    d["weight"][5, 1] = value
+    g = ssd.causal_conv_bwd(d["x"], d["weight"], d["bias"], d["dy"], d["init"], d["dfinal"], lengths=d["lengths"])
+    y = ssd.causal_conv_fwd(d["x"], d["weight"], d["bias"], d["init"], lengths=d["lengths"])
+    for i, end in enumerate(d["lengths"].tolist()):
+        assert bool((g["dx"][i, end:] == 0).all()) and bool((y[i, end:] == 0).all())
+
+
+@pytest.mark.parametrize("c", [24, 512])
+def test_rows_behind_the_end_add_nothing_to_the_sums(c):
+    # a filter whose oldest tap overflows on the last input: no live row meets the two, a padded one does
+    d = inputs(2, 30, c, 4, "f32", state=False, seed=7)
+    end = 18
+    d["lengths"] = torch.full((2,), end, dtype=torch.int32, device="cuda")
+    d["x"][:, end - 1] = 1e30
+    d["weight"][:, 0] = 1e30
+    d["weight"][:, 3] = 1e-30
+    d["x"][:, :end - 1] *= 1e-30
+    got = ssd.causal_conv_bwd(d["x"], d["weight"], d["bias"], d["dy"], lengths=d["lengths"])
+    cut = ssd.causal_conv_bwd(d["x"][:, :end].contiguous(), d["weight"], d["bias"], d["dy"][:, :end].contiguous())
+    assert all(bool(torch.isfinite(v).all()) for v in cut.values())
+    assert torch.equal(got["dx"][:, :end], cut["dx"])
+    assert all(torch.equal(got[k], cut[k]) for k in ("dweight", "dbias"))
