@@ -328,7 +328,18 @@ void ks_bwd_main(ScanIn<Tin> a, const Tdy *__restrict__ dy, Strides dys,
         if (gate) {
 #pragma unroll
             for (int i = 0; i < TPL; ++i) zy[i] *= fmaf(D, x[i], own_sum<TT, LPC>(pY, i, at.j));
+            if (left < TT) {
+#pragma unroll
+                for (int i = 0; i < TPL; ++i) zy[i] = i * LPC + at.j < left ? zy[i] : 0.f;
+            }
             dzs.store(room, zy);
+        }
+        // rows behind the end: the last state, should it not be finite, stays out of their products
+        if (left < TT) {
+#pragma unroll
+            for (int tk = 0; tk < TT; ++tk)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) h[tk][r] = tk + 1 < left ? h[tk][r] : 0.f;
         }
         asm volatile("" ::: "memory");
         for_lanes<TT>([&](auto K) {
@@ -357,10 +368,14 @@ void ks_bwd_main(ScanIn<Tin> a, const Tdy *__restrict__ dy, Strides dys,
             dxv[i] = fmaf(gB, d[i], D * o[i]);
             dD = fmaf(o[i], x[i], dD);
         }
-        // rows that take no step, where the states' part may be anything
+        // rows behind the end, where the states' part may be anything
         if (left < TT || TT < LPC) {
 #pragma unroll
-            for (int i = 0; i < TPL; ++i) ddtv[i] = i * LPC + at.j < min(left, TT) ? ddtv[i] : 0.f;
+            for (int i = 0; i < TPL; ++i) {
+                const bool live = i * LPC + at.j < min(left, TT);
+                ddtv[i] = live ? ddtv[i] : 0.f;
+                dxv[i] = live ? dxv[i] : 0.f;
+            }
         }
 #pragma unroll
         for (int i = 0; i < TPL; ++i) dbias += ddtv[i];
@@ -384,7 +399,7 @@ void ks_bwd_main(ScanIn<Tin> a, const Tdy *__restrict__ dy, Strides dys,
             for (int q = 0; q < 256 / NP; ++q) s += red[(q * NP + n) * kRedStride + column];
             if (n < a.N && tok < room) {
                 const int64_t p = ((int64_t)b * a.L + t + tok) * out.tok + n;
-                (column < TT ? db : dc)[p] = s;
+                (column < TT ? db : dc)[p] = tok < left ? s : 0.f;
             }
         }
     }

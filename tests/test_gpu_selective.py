@@ -422,3 +422,38 @@ def test_offsets_beyond_32_bits():
         a, r = g[k][1:, -4096:], g1[k][:, -4096:]
         assert float((a - r).norm() / r.norm()) < TOL, k
     assert float((g["d_initial_states"][1:] - g1["d_initial_states"]).norm() / g1["d_initial_states"].norm()) < TOL
+
+
+@pytest.mark.parametrize("c,n", [(24, 16), (9, 30), (5, 64)])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_last_state_not_finite_leaves_the_rows_behind_it_zero(c, n, value):
+    # an overflow at a sequence's last token, or in its final state's gradient
+    d = inputs(4, 45, c, n, seed=9)
+    d["lengths"] = torch.tensor([45, 19, 3, 0], dtype=torch.int32, device="cuda")
+    for i, end in enumerate(d["lengths"].tolist()):
+        if end > 0:
+            d["x"][i, end - 1, ::2] = value
+    d["dfinal"][:, 1::2] = value
+    y, got = fwd(d)[0], bwd(d)
+    for i, end in enumerate(d["lengths"].tolist()):
+        assert bool((y[i, end:] == 0).all())
+        assert all(bool((got[k][i, end:] == 0).all()) for k in ("dx", "ddt", "dz", "dB", "dC"))
+
+
+@pytest.mark.parametrize("c,n", [(24, 16), (9, 30), (5, 64)])
+def test_rows_behind_the_end_add_nothing_to_the_sums(c, n):
+    # the last token's input overflows the last state, which no gradient of A or of an earlier token contains
+    d = inputs(2, 45, c, n, gate=False, seed=10)
+    end = 19
+    d["dfinal"] = None
+    d["x"][:, end - 1] = float("inf")
+    d["lengths"] = torch.full((2,), end, dtype=torch.int32, device="cuda")
+    got = bwd(d)
+    a = {k: host(d[k]) for k in NAMES}
+    a["x"][:, end - 1] = 0.0
+    want = lo.scan_bwd(a["x"], a["dt"], a["A"], a["B"], a["C"], a["D"], host(d["dy"]), a["z"], a["dt_bias"], a["init"],
+                       None, a["lengths"])
+    assert nerr(host(got["dA"]), want["dA"]) <= TOL
+    for k in ("dx", "ddt", "dB"):
+        assert nerr(host(got[k][:, :end - 1]), want[k][:, :end - 1]) <= TOL, k
+    assert nerr(host(got["d_initial_states"]), want["d_initial_states"]) <= TOL
