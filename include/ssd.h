@@ -507,7 +507,9 @@ typedef struct {
 
 /* Forward pass over prompts.
  *   x, dt, z         (batch, seqlen, channels) dtype; z NULL => no gate
- *   A                (channels, dstate) fp32, <= 0; -infinity: that state keeps nothing
+ *   A                (channels, dstate) fp32, <= 0; -infinity: that state keeps
+ *                    nothing from one token to the next, whatever d_t (rows
+ *                    behind a sequence's end are no tokens and leave it)
  *   B, C             (batch, seqlen, ngroups, dstate) dtype
  *   D, dt_bias       (channels) fp32, NULL => 0
  *   initial_states   (batch, channels, dstate) fp32, NULL => 0
@@ -518,7 +520,8 @@ typedef struct {
  *   workspace        256-byte aligned, at least
  *                    ssd_selective_scan_fwd_workspace_size(shape) bytes (which
  *                    may be 0; also 0 for an invalid shape)
- * Without the softplus flag d_t >= 0 is the caller's part, as A <= 0 is.
+ * Without the softplus flag d_t >= 0 is the caller's part, as A <= 0 is.  A
+ * d_t below 2^-144 counts as 0.
  * Time is cut into segments run beside each other where batch and channels
  * alone would leave compute units idle. */
 size_t ssd_selective_scan_fwd_workspace_size(const ssd_selective_shape *shape);

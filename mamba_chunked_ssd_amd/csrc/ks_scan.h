@@ -180,8 +180,16 @@ struct RowStage {
     }
 };
 
-// Step sizes of a lane's own tokens; tokens behind the end take a step of 0,
-// so the state stays.
+// A token's step size as its decay takes it: never 0, which an infinite rate
+// would leave undefined (0 times infinity) where it is to keep nothing.  What is
+// added changes no step of 2^-96 or more, and brings the exponent to -256 at
+// that rate and to 0 at any below 2^95; other products take the step without it.
+constexpr float kLeastStep = 0x1p-120f;
+__device__ __forceinline__ float held_step(float d) { return d + kLeastStep; }
+__device__ __forceinline__ float taken(float held) { return held - kLeastStep; }
+
+// Step sizes of a lane's own tokens; rows behind the end take a step of 0, so
+// the state stays.
 template <int TT, int LPC, typename T>
 __device__ __forceinline__ void step_sizes(const uint32_t (&dt)[own_tokens<TT, LPC>()], float bias, bool sp, int left, int j,
                                            float (&d)[own_tokens<TT, LPC>()]) {
@@ -192,6 +200,8 @@ __device__ __forceinline__ void step_sizes(const uint32_t (&dt)[own_tokens<TT, L
 #pragma unroll
         for (int i = 0; i < TPL; ++i) d[i] = softplus(d[i]);
     }
+#pragma unroll
+    for (int i = 0; i < TPL; ++i) d[i] = held_step(d[i]);
     if (left < TT) {
 #pragma unroll
         for (int i = 0; i < TPL; ++i) d[i] = i * LPC + j < left ? d[i] : 0.f;
@@ -269,7 +279,8 @@ __device__ __forceinline__ void store_states_n(float *p, int n0, int N, const fl
 
 // The decay's rate in base 2, exp(d A) = exp2(d rate(A)), held finite: rows
 // behind an end take steps of 0, and 0 times the infinite A of a state that
-// keeps nothing would be NaN.  A NaN stays one.
+// keeps nothing would be NaN.  (The one-token step has no such rows and takes A
+// as it is.)  A NaN stays one.
 __device__ __forceinline__ float rate(float A) {
     constexpr float most = __FLT_MAX__;
     const float v = kLog2e * A;

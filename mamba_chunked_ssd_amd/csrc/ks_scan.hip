@@ -75,7 +75,7 @@ __global__ __launch_bounds__(256) void ks_scan(ScanIn<Tin> a, const float *init,
         float o[TPL];
 #pragma unroll
         for (int i = 0; i < TPL; ++i) {
-            const float u = d[i] * x[i];
+            const float u = taken(d[i]) * x[i];
             steps += d[i];
             float p[LPC];
             for_lanes<LPC>([&](auto K) {
@@ -147,7 +147,7 @@ struct StepToken {
         const float raw = load_one(a.dt + b * a.dts.batch, c) + (a.bias != nullptr ? a.bias[c] : 0.f);
         z = a.z != nullptr ? load_one(a.z + b * a.zs.batch, c) : 0.f;
         D = a.D != nullptr ? a.D[c] : 0.f;
-        d = a.softplus ? softplus(raw) : raw;
+        d = held_step(a.softplus ? softplus(raw) : raw);
     }
     __device__ __forceinline__ float output(float s, bool gate) const {
         const float o = fmaf(D, x, s);
@@ -178,7 +178,7 @@ __global__ __launch_bounds__(256) void ks_step(ScanIn<Tin> a, float *state, Tout
         }
     }
     const StepToken<Tin> tok(a, b, c);
-    const float u = tok.d * tok.x;
+    const float u = taken(tok.d) * tok.x;
     float s = 0.f;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -234,7 +234,7 @@ __global__ __launch_bounds__(256) void ks_step_any(ScanIn<Tin> a, float *state, 
         }
         const int64_t bc = (int64_t)b * a.channels + c;
         const StepToken<Tin> tok(a, b, c);
-        const float u = tok.d * tok.x;
+        const float u = taken(tok.d) * tok.x;
         float s = 0.f;
 #pragma unroll
         for (int r = 0; r < R; ++r) {

@@ -88,7 +88,7 @@ __global__ __launch_bounds__(256) void ks_bwd_sweep(ScanIn<Tin> a, const Tdy *__
         float d[TPL], u[TPL], o[TPL];
         step_sizes<kTT, LPC, Tin>(dr, bias, a.softplus, left, at.j, d);
 #pragma unroll
-        for (int i = 0; i < TPL; ++i) u[i] = d[i] * widen<Tin>(xr[i]);
+        for (int i = 0; i < TPL; ++i) u[i] = taken(d[i]) * widen<Tin>(xr[i]);
         float first = 0.f, second = 0.f;  // sums of the steps of the two tiles
         if constexpr (SEGS) {
 #pragma unroll
@@ -286,7 +286,7 @@ void ks_bwd_main(ScanIn<Tin> a, const Tdy *__restrict__ dy, Strides dys,
 #pragma unroll
         for (int i = 0; i < TPL; ++i) {
             x[i] = widen<Tin>(xr[i]);
-            u[i] = d[i] * x[i];
+            u[i] = taken(d[i]) * x[i];
             o[i] = widen<Tdy>(gr[i]);
             sl[i] = a.softplus ? logistic(widen<Tin>(dr[i]) + bias) : 1.f;  // softplus'
         }
@@ -365,7 +365,7 @@ void ks_bwd_main(ScanIn<Tin> a, const Tdy *__restrict__ dy, Strides dys,
         for (int i = 0; i < TPL; ++i) {
             const float gB = own_sum<TT, LPC>(pB, i, at.j), gA = own_sum<TT, LPC>(pA, i, at.j);
             ddtv[i] = fmaf(0.6931471805599453f, gA, gB * x[i]) * sl[i];  // pA used log2(e) A
-            dxv[i] = fmaf(gB, d[i], D * o[i]);
+            dxv[i] = fmaf(gB, taken(d[i]), D * o[i]);
             dD = fmaf(o[i], x[i], dD);
         }
         // rows behind the end, where the states' part may be anything

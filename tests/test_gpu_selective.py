@@ -457,3 +457,38 @@ def test_rows_behind_the_end_add_nothing_to_the_sums(c, n):
     for k in ("dx", "ddt", "dB"):
         assert nerr(host(got[k][:, :end - 1]), want[k][:, :end - 1]) <= TOL, k
     assert nerr(host(got["d_initial_states"]), want["d_initial_states"]) <= TOL
+
+
+@pytest.mark.parametrize("softplus", [True, False])
+@pytest.mark.parametrize("b,L,c,n", [(2, 5, 8, 16), (1, 301, 40, 16), (2, 37, 12, 6), (1, 20, 9, 40), (2, 19, 20, 8)])
+def test_tokens_without_a_step(b, L, c, n, softplus):
+    # d_t = 0, by a dt so low that softplus is 0 or by dt = 0 without it: finite rates keep their state, infinite ones
+    # keep nothing, in the prompt, the gradients and the one-token step alike
+    d = inputs(b, L, c, n, ragged=b > 1, seed=11, softplus=softplus)
+    d["A"][:, ::3] = -float("inf")
+    d["A"][0] = -float("inf")
+    d["dt_bias"] = None
+    none = torch.zeros(L, dtype=torch.bool, device="cuda")
+    none[1::3] = none[-1] = True
+    low = torch.where(torch.arange(c, device="cuda") % 2 == 0, -200.0, -float("inf")) if softplus else torch.zeros(c, device="cuda")
+    d["dt"] = torch.where(none[:, None], low, d["dt"] - 2 if softplus else d["dt"])
+    a = {k: host(d[k]) for k in NAMES}
+    # the definition's limit: a step too small for anything but an infinite rate
+    a["A"] = np.maximum(a["A"], -1e300)
+    a["dt"] = np.where(host(none)[:, None], -100.0 if softplus else 1e-60, a["dt"])
+    y, fin = fwd(d, dt_softplus=softplus)
+    ref, rfin = lo.scan(*[a[k] for k in NAMES], use_softplus=softplus)
+    assert nerr(host(y), ref) <= TOL and nerr(host(fin), rfin) <= TOL
+    got = bwd(d, dt_softplus=softplus)
+    want = lo.scan_bwd(a["x"], a["dt"], a["A"], a["B"], a["C"], a["D"], host(d["dy"]), a["z"], a["dt_bias"], a["init"],
+                       host(d["dfinal"]), a["lengths"], use_softplus=softplus)
+    errs = {k: nerr(host(got[k]), r) for k, r in want.items()}
+    assert all(e <= TOL for e in errs.values()), errs
+    state = d["init"].clone()
+    every, _ = lo.scan(*[a[k] for k in NAMES[:9]], use_softplus=softplus)
+    rms = np.sqrt(np.mean(every ** 2))
+    for t in range(min(L, 20)):
+        yt = ssd.selective_scan_step(d["x"][:, t], d["dt"][:, t], d["A"], d["B"][:, t], d["C"][:, t], d["D"], state,
+                                     d["z"][:, t], None, dt_softplus=softplus)
+        assert float(np.max(np.abs(host(yt) - every[:, t]))) <= TOL * rms
+    assert bool(torch.isfinite(state).all())
