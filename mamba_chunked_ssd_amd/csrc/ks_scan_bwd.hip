@@ -425,46 +425,48 @@ struct BwdSums {
     int64_t rows;         // batch * seqlen
     int channels, N, NP, ngroups, gblocks;
 };
-constexpr int kSumSlices = 8;
-__global__ __launch_bounds__(256) void ks_bwd_sums(BwdSums s, int64_t nA, int64_t nBC) {
-    constexpr int COLS = 256 / kSumSlices;
+__global__ __launch_bounds__(256) void ks_bwd_sums(BwdSums s, ScanSums plan) {
+    constexpr int COLS = kSumOutputs;
     __shared__ double part[256];
     const int slice = threadIdx.x / COLS;
-    int64_t i = (int64_t)blockIdx.x * COLS + threadIdx.x % COLS;
-    const float *from = nullptr;
-    float *to = nullptr;
-    int64_t terms = s.slots, stride = 0;
-    if (i < nA) {
-        from = s.dap + i / s.N * s.NP + i % s.N;
-        stride = (int64_t)s.channels * s.NP;
-        to = s.dA + i;
-    } else if ((i -= nA) < 2 * (int64_t)s.channels) {
-        const bool first = i < s.channels;
-        const int64_t c = first ? i : i - s.channels;
-        from = (first ? s.ddp : s.dbiasp) + c;
-        stride = s.channels;
-        to = first ? s.dD : s.ddt_bias;
-        to = to != nullptr ? to + c : nullptr;
-    } else if ((i -= 2 * (int64_t)s.channels) < 2 * nBC) {
-        const bool first = i < nBC;
-        if (!first) i -= nBC;
-        const int64_t n = i % s.N, g = i / s.N % s.ngroups, row = i / ((int64_t)s.N * s.ngroups);
-        from = (first ? s.dbp : s.dcp) + (g * s.gblocks * s.rows + row) * s.N + n;
-        stride = s.rows * s.N;
-        terms = s.gblocks;
-        to = (first ? s.dB : s.dC) + i;
-    }
-    double v = 0.0;
-    if (to != nullptr) {
+    for (int64_t group = blockIdx.x; group < plan.groups; group += plan.blocks) {
+        int64_t i = group * COLS + threadIdx.x % COLS;
+        const float *from = nullptr;
+        float *to = nullptr;
+        int64_t terms = s.slots, stride = 0;
+        if (i < plan.rates) {
+            from = s.dap + i / s.N * s.NP + i % s.N;
+            stride = (int64_t)s.channels * s.NP;
+            to = s.dA + i;
+        } else if ((i -= plan.rates) < 2 * (int64_t)s.channels) {
+            const bool first = i < s.channels;
+            const int64_t c = first ? i : i - s.channels;
+            from = (first ? s.ddp : s.dbiasp) + c;
+            stride = s.channels;
+            to = first ? s.dD : s.ddt_bias;
+            to = to != nullptr ? to + c : nullptr;
+        } else if ((i -= 2 * (int64_t)s.channels) < 2 * plan.rows) {
+            const bool first = i < plan.rows;
+            if (!first) i -= plan.rows;
+            const int64_t n = i % s.N, g = i / s.N % s.ngroups, row = i / ((int64_t)s.N * s.ngroups);
+            from = (first ? s.dbp : s.dcp) + (g * s.gblocks * s.rows + row) * s.N + n;
+            stride = s.rows * s.N;
+            terms = s.gblocks;
+            to = (first ? s.dB : s.dC) + i;
+        }
+        double v = 0.0;
+        if (to != nullptr) {
 #pragma unroll 8
-        for (int64_t k = slice; k < terms; k += kSumSlices) v += (double)from[k * stride];
-    }
-    part[threadIdx.x] = v;
-    __syncthreads();
-    if (slice == 0 && to != nullptr) {
+            for (int64_t k = slice; k < terms; k += kSumSlices) v += (double)from[k * stride];
+        }
+        part[threadIdx.x] = v;
+        __syncthreads();
+        if (slice == 0 && to != nullptr) {
 #pragma unroll
-        for (int q = 1; q < kSumSlices; ++q) v += part[q * COLS + threadIdx.x];
-        *to = (float)v;
+            for (int q = 1; q < kSumSlices; ++q) v += part[q * COLS + threadIdx.x];
+            *to = (float)v;
+        }
+        __syncthreads();  // the next group's partial sums take this one's place
     }
 }
 
@@ -503,11 +505,8 @@ hipError_t bwd(const ScanArgs &a, const ScanPlan &plan, hipStream_t stream) {
     }
     const BwdSums s{a.dap, a.ddp, a.dbiasp, a.dbp, a.dcp, a.dA, a.dD, a.ddt_bias, a.dB, a.dC,
                     a.batch * plan.nseg, a.batch * a.seqlen, a.channels, a.dstate, plan.np, a.ngroups, plan.gblocks};
-    const int64_t nA = (int64_t)a.channels * a.dstate;
-    const int64_t nBC = plan.gblocks == 1 ? 0 : a.batch * a.seqlen * a.ngroups * a.dstate;
-    const int64_t n = nA + 2 * (int64_t)a.channels + 2 * nBC;
-    return launch_kernel(ks_bwd_sums, dim3((unsigned)((n + 256 / kSumSlices - 1) / (256 / kSumSlices))), dim3(256), 0,
-                         stream, LaunchEvents{}, s, nA, nBC);
+    const ScanSums sums = scan_sums(a.batch, a.seqlen, a.channels, a.dstate, a.ngroups, plan.gblocks);
+    return launch_kernel(ks_bwd_sums, dim3(sums.blocks), dim3(256), 0, stream, LaunchEvents{}, s, sums);
 }
 
 template <typename Tin, typename Tdy>

@@ -98,6 +98,25 @@ struct ScanArgs {
     float *ddp, *dbiasp;  // partial dD and ddt_bias, (batch, nseg, channels)
 };
 
+// The backward pass's last sums: eight threads an output.  A launch has fewer
+// than 2^24 blocks of 256 threads (32 bits of threads); its blocks take groups
+// of outputs in turn.
+constexpr int kSumSlices = 8, kSumOutputs = 256 / kSumSlices;
+struct ScanSums {
+    int64_t rates;   // outputs of dA
+    int64_t rows;    // of dB, of dC; 0 where one block a group wrote them in place
+    int64_t groups;  // of kSumOutputs outputs
+    unsigned blocks;
+};
+inline ScanSums scan_sums(int64_t batch, int64_t seqlen, int64_t channels, int64_t dstate, int64_t ngroups, int gblocks) {
+    ScanSums s;
+    s.rates = channels * dstate;
+    s.rows = gblocks == 1 ? 0 : batch * seqlen * ngroups * dstate;
+    s.groups = (s.rates + 2 * channels + 2 * s.rows + kSumOutputs - 1) / kSumOutputs;
+    s.blocks = (unsigned)(s.groups < (int64_t)1 << 20 ? s.groups : (int64_t)1 << 20);
+    return s;
+}
+
 hipError_t launch_scan_fwd(const ScanArgs &a, const ScanPlan &plan, hipStream_t stream);
 hipError_t launch_scan_bwd(const ScanArgs &a, const ScanPlan &plan, hipStream_t stream);
 hipError_t launch_scan_step(const ScanArgs &a, hipStream_t stream);

@@ -492,3 +492,25 @@ def test_tokens_without_a_step(b, L, c, n, softplus):
                                      d["z"][:, t], None, dt_softplus=softplus)
         assert float(np.max(np.abs(host(yt) - every[:, t]))) <= TOL * rms
     assert bool(torch.isfinite(state).all())
+
+
+def test_more_gradient_rows_than_a_launch_has_threads():
+    # dB and dC of 2^28 numbers each, 17 channels on two blocks: the last sequence against a call on it alone
+    b, L, c, n = 64, 65536, 17, 64
+    gen = torch.Generator(device="cuda").manual_seed(12)
+
+    def rows(width):
+        return torch.randn((b, L, width), generator=gen, device="cuda").bfloat16()
+
+    x, dt, dy = rows(c), rows(c), rows(c)
+    B, C = rows(n)[:, :, None], rows(n)[:, :, None]
+    A = -torch.arange(1, n + 1, device="cuda").float().expand(c, n).contiguous()
+    bias = torch.full((c,), -3.0, device="cuda")
+    g = ssd.selective_scan_bwd(x, dt, A, B, C, None, dy, None, bias)
+    one = [t[-1:] for t in (x, dt, B, C, dy)]
+    g1 = ssd.selective_scan_bwd(one[0], one[1], A, one[2], one[3], None, one[4], None, bias)
+    for k in ("dx", "ddt", "dB", "dC"):
+        assert float((g[k][-1:] - g1[k]).norm() / g1[k].norm()) < TOL, k
+    # dD is a plain sum: over all sequences in 64 bits
+    want = (dy.double() * x.double()).sum((0, 1))
+    assert float((g["dD"].double() - want).norm() / want.norm()) < TOL
