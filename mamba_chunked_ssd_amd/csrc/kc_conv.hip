@@ -144,9 +144,15 @@ __global__ __launch_bounds__(256) void kc_conv_fwd(ConvIn<Tin> a, Tout *__restri
 // dx_{t-W+1} is complete at t.  Rows come through raw buffers over the group,
 // so ends need no branch in the loop.  dw and db stay in registers over the
 // strip, are joined over the block's four strips in LDS and leave one row of
-// partial sums per block, which kc_conv_sums adds in a fixed order.  Bound by
-// memory: 2 x 2048 tokens of 5376 channels, bf16 with dy in fp32, 35 us of
-// which the 176 MB that must move take 34 at a copy's rate (sums 4 us more).
+// partial sums per block, which kc_conv_sums adds in a fixed order.  They are
+// held in 64 bits, where a product of two fp32 numbers is exact, and rounded to
+// fp32 three times, as a strip's, a block's and the whole sum, however time is
+// cut.  Bound by memory: 2 x 2048 tokens of 5376 channels, bf16 with dy in fp32,
+// 38 us of which the 176 MB that must move take 34 at a copy's rate (sums 4 us
+// more); 4 x 4096 tokens fp32 228 us, its bytes 204.  The 64 bits cost 5 % of
+// the first (44 registers more leave two waves a SIMD) and nothing of the second.
+// Measured and no faster: partial sums as two floats (47 us for both kernels
+// against 46), 64-bit sums in LDS, added to every four tokens (44, but 231 fp32).
 constexpr int kGroup = 4;  // tokens; at least W - 1
 
 template <typename Tin, typename Tdy, typename Tdx, int W, int V>
@@ -162,12 +168,12 @@ __global__ __launch_bounds__(256) void kc_conv_bwd(ConvIn<Tin> a, const Tdy *__r
     const bool mine = vec < a.nvec;
     const int len = conv_length(a.lengths, b, a.L);
 
-    float dw[W][V], db[V];
+    double dw[W][V], db[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        db[e] = 0.f;
+        db[e] = 0.0;
 #pragma unroll
-        for (int k = 0; k < W; ++k) dw[k][e] = 0.f;
+        for (int k = 0; k < W; ++k) dw[k][e] = 0.0;
     }
     if (st < nstrips) {
         const int t0 = st * strip, t1 = min(t0 + strip, a.L), tend = min(t1 + W - 1, len);
@@ -234,7 +240,7 @@ __global__ __launch_bounds__(256) void kc_conv_bwd(ConvIn<Tin> a, const Tdy *__r
                     if (own) {
                         db[e] += de;
 #pragma unroll
-                        for (int k = 0; k < W; ++k) dw[k][e] = fmaf(de, win[k][e], dw[k][e]);
+                        for (int k = 0; k < W; ++k) dw[k][e] = fma((double)de, (double)win[k][e], dw[k][e]);
                     }
                     g[u][e] = 0.f;
 #pragma unroll
@@ -283,8 +289,8 @@ __global__ __launch_bounds__(256) void kc_conv_bwd(ConvIn<Tin> a, const Tdy *__r
 #pragma unroll
     for (int e = 0; e < V; ++e) {
 #pragma unroll
-        for (int k = 0; k < W; ++k) red[(wave * R + k * V + e) * 64 + lane] = dw[k][e];
-        red[(wave * R + W * V + e) * 64 + lane] = db[e];
+        for (int k = 0; k < W; ++k) red[(wave * R + k * V + e) * 64 + lane] = (float)dw[k][e];
+        red[(wave * R + W * V + e) * 64 + lane] = (float)db[e];
     }
     __syncthreads();
     const int nsb = (nstrips + 3) / 4;
@@ -292,10 +298,10 @@ __global__ __launch_bounds__(256) void kc_conv_bwd(ConvIn<Tin> a, const Tdy *__r
     for (int i = threadIdx.x; i < R * 64; i += 256) {
         // consecutive threads take consecutive channels of one tap
         const int k = i / (V * 64), cl = i % (V * 64), c = vb * 64 * V + cl;
-        float sum = 0.f;
+        double sum = 0.0;
 #pragma unroll
         for (int q = 0; q < 4; ++q) sum += red[(q * R + k * V + cl % V) * 64 + cl / V];
-        if (c < a.C) out[(int64_t)k * a.C + c] = sum;
+        if (c < a.C) out[(int64_t)k * a.C + c] = (float)sum;
     }
 }
 

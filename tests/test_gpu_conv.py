@@ -329,3 +329,32 @@ def test_rows_behind_the_end_add_nothing_to_the_sums(c):
     assert all(bool(torch.isfinite(v).all()) for v in cut.values())
     assert torch.equal(got["dx"][:, :end], cut["dx"])
     assert all(torch.equal(got[k], cut[k]) for k in ("dweight", "dbias"))
+
+
+@pytest.mark.parametrize("kind", ["random", "drift"])
+@pytest.mark.parametrize("b,L,c,W,dtype", [(2, 3001, 24, 4, "f32"), (1, 5000, 512, 3, "f32"), (3, 2048, 771, 2, "bf16"),
+                                           (1, 300_000, 40, 4, "f32")])
+def test_sums_over_tokens_are_held_in_64_bits(b, L, c, W, dtype, kind):
+    # Without an activation the terms of dweight and dbias are products of two inputs, and inputs, exact in 64 bits.
+    # They are rounded to fp32, by half a step of 2^-24, as the sums of strips of a multiple of 16 tokens, as those
+    # of blocks of four strips and at the end; before that (terms + 4) roundings of 2^-53 of the terms' magnitudes.
+    # "drift": terms of 1 + 2^-18 + 2^-23, each just above half a step of a sum between 64 and 128, so that a sum
+    # in fp32 runs away from 128 of them by 2^-19.
+    d = inputs(b, L, c, W, dtype, ragged=b > 1, seed=13)
+    if kind == "drift":
+        d["dy"][:] = 1 + 2.0 ** -18 + 2.0 ** -23
+        d["x"][:] = 1.0
+        d["init"][:] = 1.0
+    got = ssd.causal_conv_bwd(d["x"], d["weight"], d["bias"], d["dy"], d["init"], activation=None, lengths=d["lengths"])
+    x = torch.cat([d["init"].double(), d["x"].double()], 1)
+    dy = d["dy"].double()
+    if d["lengths"] is not None:
+        dy = dy * (torch.arange(L, device="cuda")[None, :] < d["lengths"][:, None])[..., None]
+    pad = (0, 0, 0, -L % 16)
+    for k in range(W + 1):
+        terms = dy * x[:, k:k + L] if k < W else dy
+        have = got["dweight"][:, k] if k < W else got["dbias"]
+        want = terms.sum((0, 1))
+        pieces = torch.nn.functional.pad(terms, pad).view(b, -1, 16, c).sum(2).abs().sum((0, 1))
+        bound = 2.0 ** -24 * (want.abs() + 2.001 * pieces) + 2 * (b * L + 4) * 2.0 ** -53 * terms.abs().sum((0, 1))
+        assert bool(((have.double() - want).abs() <= bound).all()), k
