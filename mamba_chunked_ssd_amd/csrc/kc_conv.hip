@@ -150,7 +150,7 @@ __global__ __launch_bounds__(256) void kc_conv_fwd(ConvIn<Tin> a, Tout *__restri
 // cut.  Bound by memory: 2 x 2048 tokens of 5376 channels, bf16 with dy in fp32,
 // 38 us of which the 176 MB that must move take 34 at a copy's rate (sums 4 us
 // more); 4 x 4096 tokens fp32 228 us, its bytes 204.  The 64 bits cost 5 % of
-// the first (44 registers more leave two waves a SIMD) and nothing of the second.
+// the first, whose registers then leave two waves a SIMD, and 1 % of the second.
 // Measured and no faster: partial sums as two floats (47 us for both kernels
 // against 46), 64-bit sums in LDS, added to every four tokens (44, but 231 fp32).
 constexpr int kGroup = 4;  // tokens; at least W - 1

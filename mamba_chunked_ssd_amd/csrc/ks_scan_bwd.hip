@@ -182,6 +182,7 @@ struct BwdOut {
     float *db, *dc;         // dB and dC, or a block's partial rows of them
     int64_t blk, tok;       // elements between blocks and between tokens there
     float *dap, *ddp, *dbiasp;
+    int runs;
 };
 
 // LDS row of one lane's 8 + 8 sums of a tile, padded so that neither the
@@ -241,6 +242,21 @@ void ks_bwd_main(ScanIn<Tin> a, const Tdy *__restrict__ dy, Strides dys,
     RowStage<TT, NP, Tin, false> rB(a.B, a.Bs, b, at.g, a.N, last), rC(a.C, a.Cs, b, at.g, a.N, last);
     float *db = out.db + at.blk * out.blk, *dc = out.dc + at.blk * out.blk;
 
+    // The sums over tokens leave a row for every kScanRun tokens of the segment, so that a sum in fp32 has no more
+    // terms than that however time is cut, and start again.
+    const BlockRows<LPC> mine(at.ok, at.j, at.cl);
+    const int64_t run0 = ((int64_t)b * a.nseg + at.seg) * out.runs;
+    auto leave_sums = [&](int run) {
+        const int64_t row = (run0 + run) * a.channels + at.c0;
+        mine.store(out.dap + row * NP, dA);
+        mine.store_number(out.ddp + row, lane_total<LPC>(dD));
+        mine.store_number(out.dbiasp + row, lane_total<LPC>(dbias));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) dA[r] = 0.f;
+        dD = dbias = 0.f;
+    };
+    for (int run = (done - at.s0 + kScanRun - 1) / kScanRun; run < out.runs; ++run) leave_sums(run);
+
     // rows behind the end
     for (int tt = done + at.j; tt < at.s1; tt += LPC)
         if (at.ok) {
@@ -257,7 +273,6 @@ void ks_bwd_main(ScanIn<Tin> a, const Tdy *__restrict__ dy, Strides dys,
 
     uint32_t dr[TPL], xr[TPL], zr[TPL], gr[TPL];
     float hr[4], sr = 0.f;
-    const BlockRows<LPC> mine(at.ok, at.j, at.cl);
     int64_t tile = ((int64_t)b * tiles + last / TT) * a.channels + at.c0;
     auto fetch = [&](int left) {
         dts.load(left, dr);
@@ -402,26 +417,20 @@ void ks_bwd_main(ScanIn<Tin> a, const Tdy *__restrict__ dy, Strides dys,
                 (column < TT ? db : dc)[p] = tok < left ? s : 0.f;
             }
         }
+        if ((t - at.s0) % kScanRun == 0) leave_sums((t - at.s0) / kScanRun);
     }
 
-    if (at.ok) store_states(out.dap + slot * NP + n0, dA);
-    dD = lane_total<LPC>(dD);
-    dbias = lane_total<LPC>(dbias);
-    if (at.ok && at.j == 0) {
-        out.ddp[slot] = dD;
-        out.dbiasp[slot] = dbias;
-    }
     if (a.nseg == 1 && out.dinit != nullptr && at.ok) store_states_n(out.dinit + bc * a.N, n0, a.N, carry);
 }
 
-// The last sums, in a fixed order and 64 bits: dA, dD and ddt_bias over batch
-// and segments; dB and dC over the blocks of each group (gblocks 1: written
+// The last sums, in a fixed order and 64 bits: dA, dD and ddt_bias over batch,
+// segments and runs; dB and dC over the blocks of each group (gblocks 1: written
 // in place already).  Eight threads an output, each every eighth term, so that
 // few outputs of many terms still have their loads in flight together.
 struct BwdSums {
     const float *dap, *ddp, *dbiasp, *dbp, *dcp;
     float *dA, *dD, *ddt_bias, *dB, *dC;
-    int64_t slots;        // batch * nseg
+    int64_t slots;        // batch * nseg * runs
     int64_t rows;         // batch * seqlen
     int channels, N, NP, ngroups, gblocks;
 };
@@ -491,7 +500,7 @@ hipError_t bwd(const ScanArgs &a, const ScanPlan &plan, hipStream_t stream) {
             if (e != hipSuccess) return e;
         }
         BwdOut out{a.dx, a.ddt, a.dz, a.dinit, a.dbp, a.dcp, a.batch * a.seqlen * a.dstate, a.dstate,
-                   a.dap, a.ddp, a.dbiasp};
+                   a.dap, a.ddp, a.dbiasp, plan.runs};
         if (plan.gblocks == 1) {  // one block a group: its rows are the outputs'
             out.db = a.dB;
             out.dc = a.dC;
@@ -504,7 +513,7 @@ hipError_t bwd(const ScanArgs &a, const ScanPlan &plan, hipStream_t stream) {
         if (e != hipSuccess) return e;
     }
     const BwdSums s{a.dap, a.ddp, a.dbiasp, a.dbp, a.dcp, a.dA, a.dD, a.ddt_bias, a.dB, a.dC,
-                    a.batch * plan.nseg, a.batch * a.seqlen, a.channels, a.dstate, plan.np, a.ngroups, plan.gblocks};
+                    a.batch * plan.nseg * plan.runs, a.batch * a.seqlen, a.channels, a.dstate, plan.np, a.ngroups, plan.gblocks};
     const ScanSums sums = scan_sums(a.batch, a.seqlen, a.channels, a.dstate, a.ngroups, plan.gblocks);
     return launch_kernel(ks_bwd_sums, dim3(sums.blocks), dim3(256), 0, stream, LaunchEvents{}, s, sums);
 }

@@ -69,6 +69,7 @@ ScanPlan scan_plan(int64_t batch, int64_t seqlen, int64_t channels, int64_t dsta
     len = std::max<int64_t>(kScanSegment, (len + kScanSegment - 1) / kScanSegment * kScanSegment);
     p.seglen = (int)len;
     p.nseg = (int)std::max<int64_t>(1, (seqlen + len - 1) / len);
+    p.runs = (int)((len + kScanRun - 1) / kScanRun);
     return p;
 }
 
@@ -293,9 +294,9 @@ size_t scan_bwd_carve(ScanArgs *a, const ScanPlan &p, void *ws) {
     const size_t bc = (size_t)p.nblk * a->batch * a->seqlen * a->dstate;
     a->dbp = w.take(bc);
     a->dcp = w.take(bc);
-    a->dap = w.take(segs * p.np);
-    a->ddp = w.take(segs);
-    a->dbiasp = w.take(segs);
+    a->dap = w.take(segs * p.runs * p.np);
+    a->ddp = w.take(segs * p.runs);
+    a->dbiasp = w.take(segs * p.runs);
     return w.off;
 }
 

@@ -60,6 +60,7 @@ inline int padded_states(int64_t dstate) { return dstate <= 8 ? 8 : dstate <= 16
 
 constexpr int kScanTile = 8;    // tokens between the states that the backward pass keeps
 constexpr int kScanSegment = 16;  // segments start at multiples of this
+constexpr int kScanRun = 256;     // most tokens that a sum in fp32 takes; those sums are added in 64 bits
 
 struct ScanPlan {
     int np;           // padded states
@@ -67,6 +68,7 @@ struct ScanPlan {
     int nblk;         // blocks of one batch entry: ngroups * gblocks
     int nseg;         // segments of the time axis
     int seglen;       // tokens of one, a multiple of kScanSegment
+    int runs;         // backward: sums over tokens that a segment leaves, one per kScanRun tokens
     int64_t tiles;    // tiles of kScanTile tokens in seqlen, rounded up to whole kScanSegments
 };
 ScanPlan scan_plan(int64_t batch, int64_t seqlen, int64_t channels, int64_t dstate, int64_t ngroups, bool backward);
@@ -94,8 +96,8 @@ struct ScanArgs {
     float *tile_state;  // state before each tile, (batch, tiles, channels, np)
     float *tile_steps;  // sum of the segment's steps before each tile (nseg > 1)
     float *dbp, *dcp;   // partial dB, dC per block of a group, (nblk, batch, seqlen, dstate)
-    float *dap;         // partial dA, (batch, nseg, channels, np)
-    float *ddp, *dbiasp;  // partial dD and ddt_bias, (batch, nseg, channels)
+    float *dap;         // partial dA, (batch, nseg, runs, channels, np)
+    float *ddp, *dbiasp;  // partial dD and ddt_bias, (batch, nseg, runs, channels)
 };
 
 // The backward pass's last sums: eight threads an output.  A launch has fewer

@@ -514,3 +514,19 @@ def test_more_gradient_rows_than_a_launch_has_threads():
     # dD is a plain sum: over all sequences in 64 bits
     want = (dy.double() * x.double()).sum((0, 1))
     assert float((g["dD"].double() - want).norm() / want.norm()) < TOL
+
+
+@pytest.mark.parametrize("b,L,c,n", [(1024, 4096, 16, 64), (256, 4096, 260, 16)])
+def test_sums_over_long_sequences_do_not_run_off(b, L, c, n):
+    # Sequences walked whole, with q = 1 and d constant: dA sums L of 1 + 2^-14 - 2^-20 a sequence, each just below
+    # half a step of a sum between 1024 and 2048, and dD as many of 1 + 2^-16 - 2^-22, over the lanes of a channel.
+    # A sum in fp32 may take 256 tokens: 256 roundings, by half a step of 2^-24; two a lane step and one at the end.
+    one = lambda *shape: torch.ones(shape, device="cuda")  # noqa: E731
+    step, grad = 1 + 2.0 ** -14 - 2.0 ** -20, 1 + 2.0 ** -16 - 2.0 ** -22
+    none = torch.zeros((1, L, 1, n), device="cuda").expand(b, L, 1, n)
+    got = ssd.selective_scan_bwd(one(b, L, c), one(b, L, c) * step, torch.zeros((c, n), device="cuda"), none, none,
+                                 None, one(b, L, c) * grad, None, None, one(b, c, n), one(b, c, n), dt_softplus=False)
+    for k, want, roundings in (("dA", b * L * step, 256), ("dD", b * L * grad, 256 // (n // 8) + 4)):
+        bound = (roundings + 1) * 2.0 ** -24 * want
+        assert float((got[k].double() - want).abs().max()) <= bound, k
+    assert torch.equal(got["d_initial_states"], one(b, c, n))
