@@ -111,7 +111,11 @@ __device__ __forceinline__ float load_one(const T *p, int64_t i) {
 }
 
 // 1 / (1 + exp(-v)); exp2 overflows to infinity for very negative v, whose
-// reciprocal is the limit 0.
+// reciprocal is the limit 0.  The exponent is rounded to fp32, and by |v| 2^-24
+// the exponential is off: no more than 0.54 2^-24 of v logistic(v), which is
+// what all uses take, but a relative error that grows for negative v.
+// Corrected as in softplus, the convolution's backward pass took 11 % more
+// (4 x 4096 tokens of 5376 channels, bf16), the scan's 2 %.
 __device__ __forceinline__ float logistic(float v) {
     return __builtin_amdgcn_rcpf(1.f + fast_exp2(-kLog2e * v));
 }
@@ -122,7 +126,11 @@ __device__ __forceinline__ float logistic(float v) {
 // itself is below half a unit of log(u)'s last place.  So step sizes near
 // 1e-3, which come from small e, keep their relative accuracy.
 __device__ __forceinline__ float softplus(float v) {
-    const float e = fast_exp2(-kLog2e * __builtin_fabsf(v));
+    // exp(-|v|) = 2^t exp(-|v| - t log(2)): the exponent t rounded to fp32 would leave a relative error of |v| 2^-24,
+    // to first order the second factor takes it back (held finite where v is infinite; a NaN stays one)
+    const float t = -kLog2e * __builtin_fabsf(v);
+    const float rest = __builtin_amdgcn_fmed3f(fmaf(t, -0.6931471805599453f, -__builtin_fabsf(v)), -1.f, 1.f);
+    const float raw = fast_exp2(t), e = fmaf(raw, rest, raw);
     const float u = 1.f + e;
     const float lost = e - (u - 1.f);
     return fmaf(__builtin_amdgcn_logf(u), 0.6931471805599453f, lost) + fmaxf(v, 0.f);

@@ -530,3 +530,31 @@ def test_sums_over_long_sequences_do_not_run_off(b, L, c, n):
         bound = (roundings + 1) * 2.0 ** -24 * want
         assert float((got[k].double() - want).abs().max()) <= bound, k
     assert torch.equal(got["d_initial_states"], one(b, c, n))
+
+
+def test_softplus_keeps_its_relative_accuracy():
+    # one token from a zero state, x = B = C = 1: y is the step size itself.  Roundings of 2^-24: two each for the
+    # instructions of the exponential and the logarithm, one each for the exponential's correction, the product with
+    # log(2), the bits added back (to first order) and the sum; and 0.05 |v| for log(2) rounded in the correction
+    c = 50_000
+    dt = torch.linspace(-60, 60, c, device="cuda").view(1, 1, c)
+    one, A = torch.ones((1, 1, c), device="cuda"), -torch.ones((c, 1), device="cuda")
+    B = torch.ones((1, 1, 1, 1), device="cuda")
+    v = dt.double()
+    want = v.clamp(min=0) + torch.log1p(torch.exp(-v.abs()))
+    bound = (8 + 0.05 * v.abs()) * 2.0 ** -24 * want
+    y = ssd.selective_scan_fwd(one, dt, A, B, B)
+    assert bool(((y.double() - want).abs() <= bound).all())
+    state = torch.zeros((1, c, 1), device="cuda")
+    y = ssd.selective_scan_step(one[0], dt[0], A, B[0], B[0], None, state)
+    assert bool(((y.double() - want[0]).abs() <= bound[0]).all())
+
+
+def test_softplus_of_numbers_far_out():
+    far = torch.tensor([float("inf"), 1e30, -200.0, -1e30, -float("inf"), float("nan")], device="cuda").view(1, 1, 6)
+    one, A = torch.ones((1, 1, 6), device="cuda"), -torch.ones((6, 8), device="cuda")
+    B = torch.ones((1, 1, 1, 8), device="cuda")
+    for y in (ssd.selective_scan_fwd(one, far, A, B, B)[0, 0],
+              ssd.selective_scan_step(one[0], far[0], A, B[0], B[0], None, torch.zeros((1, 6, 8), device="cuda"))[0]):
+        y = (y / 8).tolist()  # of eight equal states
+        assert y[:5] == [float("inf"), far[0, 0, 1].item(), 0.0, 0.0, 0.0] and np.isnan(y[5])
