@@ -467,8 +467,8 @@ const char *ssd_status_string(ssd_status s) {
         case SSD_OK: return "ok";
         case SSD_ERROR_INVALID_VALUE: return "invalid argument (NULL pointer, bad size, or aliasing)";
         case SSD_ERROR_UNSUPPORTED: return "unsupported size (chunked scan: chunk_size 64/128/256, headdim 32/64/128, dstate 16..256 step 16; convolution: width 2..4; selective scan: dstate 1..64)";
-        case SSD_ERROR_MISALIGNED: return "misaligned pointer (the call's documentation gives each alignment; 256 B for workspace)";
-        case SSD_ERROR_WORKSPACE: return "workspace missing or smaller than the call's _workspace_size()";
+        case SSD_ERROR_MISALIGNED: return "misaligned pointer (chunked scan: 16 B for x/B/C/y/states; convolution and selective scan: the element size; 256 B for workspace)";
+        case SSD_ERROR_WORKSPACE: return "workspace missing or smaller than the call's query says (ssd_chunk_scan_fwd_workspace_size(), or that named after the call)";
         case SSD_ERROR_LAUNCH: return "the HIP runtime refused a kernel launch or event record";
         case SSD_ERROR_SCRATCH: return "problem needs more workspace than the no-allocation entry point's 128 MiB scratch";
     }

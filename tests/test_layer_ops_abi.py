@@ -205,3 +205,9 @@ def test_host_code_under_sanitizers(tmp_path, sanitize):
     assert r.returncode == 0, r.stderr[-4000:]
     r = subprocess.run([exe], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "ok", (r.stdout[-2000:], r.stderr[-4000:])
+
+
+def test_status_strings_name_every_calls_limits(lib):
+    text = lib.ssd_status_string(MISALIGNED)
+    assert b"16 B for x/B/C/y/states" in text and b"element size" in text and b"256 B for workspace" in text
+    assert b"ssd_chunk_scan_fwd_workspace_size()" in lib.ssd_status_string(WORKSPACE)
