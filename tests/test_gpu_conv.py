@@ -358,3 +358,76 @@ def test_sums_over_tokens_are_held_in_64_bits(b, L, c, W, dtype, kind):
         pieces = torch.nn.functional.pad(terms, pad).view(b, -1, 16, c).sum(2).abs().sum((0, 1))
         bound = 2.0 ** -24 * (want.abs() + 2.001 * pieces) + 2 * (b * L + 4) * 2.0 ** -53 * terms.abs().sum((0, 1))
         assert bool(((have.double() - want).abs() <= bound).all()), k
+
+
+# Four channels a lane, which take rows of whole aligned pieces that fill three quarters of their waves (192, 256,
+# 512, 1028 channels), and the same sizes where one operand lies an element off.  b, L, c, W, x, dy, dx (and y), act,
+# layout, state; lengths of L, 0, 1, 2 and what is left of the taps; one of several strips of 32 tokens
+WIDE = [
+    (5, 50, 192, 2, "f32", "f32", "f32", "silu", "dense", True),
+    (5, 33, 256, 3, "f32", "f32", "f32", "silu", "sliced", True),
+    (4, 17, 512, 4, "f32", "f32", "f32", None, "dense", True),
+    (2, 7000, 1028, 4, "f32", "f32", "f32", "silu", "dense", True),
+    (5, 47, 1028, 4, "bf16", "bf16", "bf16", "silu", "sliced", True),
+    (4, 64, 256, 4, "bf16", "f32", "bf16", "silu", "dense", True),
+    (3, 30, 512, 3, "bf16", "bf16", "f32", "silu", "sliced", False),
+    (5, 21, 192, 2, "bf16", "f32", "f32", None, "sliced", True),
+    (5, 50, 192, 4, "f32", "f32", "f32", "silu", "odd", True),
+    (4, 40, 512, 4, "bf16", "f32", "bf16", "silu", "odd", True),
+]
+
+
+def wide_inputs(case):
+    b, L, c, W, x, dy, _, _, layout, state = case
+    d = inputs(b, L, c, W, x, layout == "sliced", state, seed=17)
+    d["lengths"] = torch.tensor([L, 0, 1, 2, L - W + 1][:b], dtype=torch.int32, device="cuda")
+    d["dy"] = d["dy"].to(TYPES[dy])
+    if layout != "dense":
+        off = 8 if layout == "sliced" else 1
+        for k in ("x", "dy"):
+            wide = torch.zeros((b, L, c + 24), dtype=d[k].dtype, device="cuda")
+            wide[..., off:off + c] = d[k]
+            d[k] = wide[..., off:off + c]
+    return d
+
+
+@pytest.mark.parametrize("case", WIDE, ids=lambda c: "b%d_L%d_c%d_w%d_%s_%s_%s_%s_%s%s" % (c[:9] + ("_state" * c[9],)))
+def test_four_channels_a_lane(case):
+    b, L, c, W, dtype, dyt, dxt, act, layout, state = case
+    d = wide_inputs(case)
+    got = ssd.causal_conv_bwd(d["x"], d["weight"], d["bias"], d["dy"], d["init"], d["dfinal"], activation=act,
+                              lengths=d["lengths"], dx_dtype=TYPES[dxt])
+    y, fin = ssd.causal_conv_fwd(d["x"], d["weight"], d["bias"], d["init"], True, activation=act,
+                                 lengths=d["lengths"], y_dtype=TYPES[dxt])
+    fargs = [host(d[k]) for k in ("x", "weight", "bias", "init", "lengths")]
+    ref, rfin = lo.conv(*fargs, act=act is not None)
+    mag = lo.conv_magnitude(*fargs)
+    assert np.all(np.abs(host(y) - ref) <= 16 * EPS * (mag + 1) * (ref != 0) + half_step(dxt, ref))
+    assert np.array_equal(host(fin), rfin)
+    args = [host(d[k]) for k in ("x", "weight", "bias", "dy", "init", "dfinal", "lengths")]
+    ref = lo.conv_bwd(*args, act=act is not None)
+    mag = lo.conv_bwd(*[None if a is None else np.abs(a) for a in args], act=False)
+    scale = 1 + max(1.0, float(np.max(np.abs(args[0]))) * float(np.max(np.abs(args[1]).sum(1))))
+    assert set(got) == set(ref)
+    for k, r in ref.items():
+        bound = 400 * EPS * scale * mag[k] + half_step(dxt if k == "dx" else "f32", r)
+        assert np.all(np.abs(host(got[k]) - r) <= bound), k
+    for i, end in enumerate(host(d["lengths"])):
+        assert not got["dx"][i, end:].any() and not y[i, end:].any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_four_channels_a_lane_agree_with_one(dtype):
+    # the same numbers an element off, one channel a lane: every result is made of the same sums in the same order
+    b, L, c, W = 3, 100, 512, 4
+    d = inputs(b, L, c, W, dtype, ragged=True, seed=18)
+    odd = dict(d)
+    wide = torch.zeros((b, L, c + 1), dtype=TYPES[dtype], device="cuda")
+    wide[..., 1:] = d["x"]
+    odd["x"] = wide[..., 1:]
+    results = []
+    for q in (d, odd):
+        g = ssd.causal_conv_bwd(q["x"], q["weight"], q["bias"], q["dy"], q["init"], q["dfinal"], lengths=q["lengths"])
+        y, fin = ssd.causal_conv_fwd(q["x"], q["weight"], q["bias"], q["init"], True, lengths=q["lengths"])
+        results.append(dict(g, y=y, fin=fin))
+    assert all(torch.equal(results[0][k], results[1][k]) for k in results[0])
