@@ -11,6 +11,8 @@ a step, 2^-8 |y|.
 """
 from __future__ import annotations
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -558,3 +560,85 @@ def test_softplus_of_numbers_far_out():
               ssd.selective_scan_step(one[0], far[0], A, B[0], B[0], None, torch.zeros((1, 6, 8), device="cuda"))[0]):
         y = (y / 8).tolist()  # of eight equal states
         assert y[:5] == [float("inf"), far[0, 0, 1].item(), 0.0, 0.0, 0.0] and np.isnan(y[5])
+
+
+def in_64_bits(d, softplus=True, dy=None):
+    """y, the final state and every gradient: the definition in 64 bits, a token of all sequences at a time, and
+    differentiated by torch."""
+    v = {k: None if d[k] is None else d[k].double().requires_grad_() for k in NAMES[:9]}
+    b, L, c = v["x"].shape
+    per = c // v["B"].shape[2]
+    h = v["init"] if v["init"] is not None else torch.zeros((b, c, v["A"].shape[1]), dtype=torch.float64, device="cuda")
+    raw = v["dt"] if v["dt_bias"] is None else v["dt"] + v["dt_bias"]
+    step = raw.clamp(min=0) + torch.log1p(torch.exp(-raw.abs())) if softplus else raw
+    live = torch.ones((b, L, 1), dtype=torch.float64, device="cuda")
+    if d["lengths"] is not None:
+        live = (torch.arange(L, device="cuda")[None, :] < d["lengths"][:, None]).double()[..., None]
+    step = step * live
+    ys = []
+    for t in range(L):
+        dt = step[:, t, :, None]
+        h = torch.exp(dt * v["A"]) * h + dt * v["x"][:, t, :, None] * v["B"][:, t].repeat_interleave(per, 1)
+        ys.append((v["C"][:, t].repeat_interleave(per, 1) * h).sum(2))
+    y = torch.stack(ys, 1) + (0 if v["D"] is None else v["D"] * v["x"])
+    if v["z"] is not None:
+        y = y * v["z"] * torch.sigmoid(v["z"])
+    y = y * live
+    loss = (y * (d["dy"] if dy is None else dy).double()).sum()
+    if d["dfinal"] is not None:
+        loss = loss + (h * d["dfinal"].double()).sum()
+    loss.backward()
+    names = {"init": "d_initial_states", "dt": "ddt", "dt_bias": "ddt_bias"}
+    return y.detach(), h.detach(), {names.get(k, "d" + k): t.grad for k, t in v.items() if t is not None}
+
+
+# b, L, c, n, g, dtype: batch and channels enough for the waves of the uncut passes (forward from about 1800, backward
+# from 4096; batch x blocks of 1024 / (padded states) channels x 4), in every lane layout, with a last block that is
+# not full, several tiles, and more tokens than one sum in fp32 takes
+UNCUT = [
+    (1024, 300, 16, 64, 1, "f32"),
+    (64, 100, 1040, 16, 1, "bf16"),
+    (64, 41, 1040, 14, 1, "f32"),
+    (128, 70, 520, 30, 2, "f32"),
+    (64, 50, 2052, 8, 1, "f32"),
+]
+
+
+@pytest.mark.parametrize("case", UNCUT, ids=lambda c: "b%d_L%d_c%d_n%d_g%d_%s" % c)
+@pytest.mark.parametrize("full", [True, False])
+def test_sequences_walked_whole(case, full):
+    b, L, c, n, g, dtype = case
+    d = inputs(b, L, c, n, g, dtype, gate=full, state=full, ragged=full, seed=21)
+    shape = ssd.SelectiveShape(b, L, c, n, g, ssd.SSD_DTYPE_F32, 0, 1)
+    lib = ssd.load_library()
+    assert lib.ssd_selective_scan_fwd_workspace_size(ctypes.byref(shape)) == 0  # no segments
+    y, fin = fwd(d)
+    got = bwd(d)
+    ref, rfin, want = in_64_bits(d)
+
+    def err(a, r):
+        assert bool(torch.isfinite(a).all())
+        rms = r.square().mean().sqrt()
+        return float((a.double() - r).abs().max() / rms) if float(rms) > 0 else float(a.abs().max())
+
+    assert err(y, ref) <= TOL and err(fin, rfin) <= TOL
+    errs = {k: err(got[k], r) for k, r in want.items()}
+    assert all(e <= TOL for e in errs.values()), errs
+
+
+@pytest.mark.parametrize("b,c,n,g,off", [(3, 130, 21, 2, 0), (2, 96, 35, 3, 0), (2, 70, 61, 2, 0), (3, 12, 7, 4, 0),
+                                         (2, 260, 5, 65, 0), (2, 70, 16, 1, 1), (2, 35, 64, 5, 1), (2, 40, 44, 2, 3)])
+def test_one_token_of_any_number_of_states(b, c, n, g, off):
+    # state counts that are no multiple of four, or states that lie off a 16-byte boundary; groups that end between
+    # the channels of one thread
+    d = inputs(b, 4, c, n, g, "bf16" if n % 2 else "f32", seed=22)
+    room = torch.empty(b * c * n + off, device="cuda")
+    state = room[off:].view(b, c, n)
+    state.copy_(d["init"])
+    ref, rfin = lo.scan(*[host(d[k]) for k in NAMES])
+    rms = np.sqrt(np.mean(ref ** 2))
+    for t in range(4):
+        y = ssd.selective_scan_step(d["x"][:, t], d["dt"][:, t], d["A"], d["B"][:, t], d["C"][:, t], d["D"], state,
+                                    d["z"][:, t], d["dt_bias"])
+        assert float(np.max(np.abs(host(y) - ref[:, t]))) <= TOL * rms
+    assert nerr(host(state), rfin) <= TOL
