@@ -45,9 +45,11 @@ ConvBwdPlan conv_bwd_plan(int64_t batch, int64_t seqlen, int64_t channels) {
 // 1654 and 1581 us, 3840 2349 and 2300, 5120 2768 and 3020.
 //
 // How many, when cut: enough for 16 384 waves (4 x 2048 tokens 281 us, with
-// 8192 waves 306), but no more than 1.5 times the square root of the length,
-// or the carry weighs (65 536 tokens of 64 channels: 88 us with the root, 259
-// with four times as many, 127 with half).
+// 8192 waves 306), but no more than the square root of the length, or the carry
+// weighs.  With half the root, the root, 1.5, 2 and 4 times it: 65 536 tokens of
+// 64 channels forward 132, 94, 102, 103 and 148 us, backward 288, 180, 186, 174
+// and 234; 8191 of 771 forward 92, 84, 85, 87 and 95, backward 204, 181, 183,
+// 181 and 192.
 constexpr int64_t kBwdWhole = 4096, kScanWaves = 16384;
 bool scan_whole(int64_t waves, bool backward) {
     if (backward) return waves >= kBwdWhole;
@@ -64,7 +66,7 @@ ScanPlan scan_plan(int64_t batch, int64_t seqlen, int64_t channels, int64_t dsta
     const int64_t waves = std::max<int64_t>(1, batch * p.nblk * 4);
     const int64_t root = (int64_t)std::ceil(std::sqrt((double)seqlen));
     int64_t nseg = scan_whole(waves, backward) ? 1 : (kScanWaves + waves - 1) / waves;
-    nseg = std::max<int64_t>(1, std::min<int64_t>({nseg, seqlen / 16, root * 3 / 2}));
+    nseg = std::max<int64_t>(1, std::min<int64_t>({nseg, seqlen / 16, root}));
     int64_t len = (seqlen + nseg - 1) / nseg;
     len = std::max<int64_t>(kScanSegment, (len + kScanSegment - 1) / kScanSegment * kScanSegment);
     p.seglen = (int)len;

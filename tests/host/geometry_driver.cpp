@@ -30,7 +30,18 @@ static void sums(int64_t b, int64_t L, int64_t c, int64_t n, int64_t g) {
     CHECK(q.groups * ssd::kSumOutputs >= outputs && (q.groups - 1) * ssd::kSumOutputs < outputs);
 }
 
+// Segments that the carry walks one after the other: the square root of the
+// length at most.
+static void segments(int64_t b, int64_t L, int64_t c, int64_t n) {
+    for (bool bwd : {false, true}) {
+        const ssd::ScanPlan p = ssd::scan_plan(b, L, c, n, 1, bwd);
+        CHECK((int64_t)(p.nseg - 1) * (p.nseg - 1) < L && (int64_t)p.nseg * p.seglen >= L);
+    }
+}
+
 int main() {
+    for (int64_t L : {1, 15, 16, 300, 2048, 8191, 65536, 1 << 20})
+        for (int64_t c : {1, 64, 771, 5120}) segments(1, L, c, 16), segments(2, L, c, 64);
     sums(1, 1, 1, 1, 1);
     sums(2, 2048, 5120, 16, 1);
     sums(16, 4096, 1088, 64, 64);      // 2^29 outputs and some
