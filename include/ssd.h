@@ -407,9 +407,12 @@ ssd_status ssd_chunk_scan_bwd_saved(const ssd_shape *shape,
  *   row the elements are contiguous.  row must be at least the row's length
  *   when seqlen > 1; batch may be anything >= 0 (0 with a nonzero row: one
  *   sequence read by the whole batch).  Outputs and states are dense.
- * - Pointers need their element type's alignment only; 16-byte aligned
- *   operands whose channels and strides are multiples of 16 bytes run on
- *   wider loads.
+ * - Pointers need their element type's alignment only.  The convolution runs
+ *   four channels a load where channels and strides are multiples of four, all
+ *   operands are aligned to four of their elements and, over prompts, channels
+ *   fill at least three quarters of a multiple of 256; the one-token scan four
+ *   states a load where dstate is a multiple of four and state and A are
+ *   16-byte aligned; both one element otherwise.
  * - lengths: device int32 (batch) or NULL.  Sequence b has
  *   min(max(lengths[b], 0), seqlen) tokens (NULL: seqlen).  Rows behind a
  *   sequence's end are not read; they are written as 0 in y and in the

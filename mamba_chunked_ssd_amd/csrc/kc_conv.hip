@@ -148,7 +148,7 @@ __global__ __launch_bounds__(256) void kc_conv_fwd(ConvIn<Tin> a, Tout *__restri
 // held in 64 bits, where a product of two fp32 numbers is exact, and rounded to
 // fp32 three times, as a strip's, a block's and the whole sum, however time is
 // cut.  Bound by memory: 2 x 2048 tokens of 5376 channels, bf16 with dy in fp32,
-// 38 us of which the 176 MB that must move take 34 at a copy's rate (sums 4 us
+// 37 us of which the 176 MB that must move take 34 at a copy's rate (sums 4 us
 // more); 4 x 4096 tokens fp32 228 us, its bytes 204.  The 64 bits cost 5 % of
 // the first, whose registers then leave two waves a SIMD, and 1 % of the second.
 // Measured and no faster: partial sums as two floats (47 us for both kernels
@@ -420,11 +420,11 @@ hipError_t step(const ConvArgs &a, hipStream_t stream) {
 }
 
 // Four channels a lane where every operand's rows are whole pieces of four and
-// the waves they fill are nearly full, else one.  Measured (forward, 4 x 4096
-// tokens): 5376 channels fp32 135 us with four, 147 with one; bf16 75 with
-// four, 80 with eight, 81 with one.  264 channels, which fill half of two
-// waves of fours: fp32 8 x 4096 tokens 21.8 us with four, 19.8 with one, and
-// backward 35.5 and 32.5.
+// the waves they fill are nearly full, else one.  Measured (4 x 4096 tokens of
+// 5376 channels): forward fp32 136 us with four, 148 with one, bf16 78 and 84,
+// backward fp32 227 and 234.  264 channels, which fill half of two waves of
+// fours: fp32 8 x 4096 tokens 22.1 us with four, 19.9 with one, and backward
+// 35.6 and 33.0.
 template <typename Tin, typename Tout, int W>
 hipError_t fwd_v(const ConvArgs &a, hipStream_t s) {
     const bool v = a.channels % 4 == 0 && a.xs.batch % 4 == 0 && a.xs.row % 4 == 0 && vec_ok<Tin>(a.x, 4) &&

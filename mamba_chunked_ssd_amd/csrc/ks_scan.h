@@ -10,8 +10,8 @@
 // product and two fused multiply-adds per token, and the scan is bound by
 // vector instructions, not by memory.  2 x 2048 tokens of 5120 channels and 16
 // states, bf16: six slots a state are 53 us at the measured 4.17 cycles a slot
-// on 1024 SIMDs; the output pass takes 91 (8.3 slots a state, VALUBusy 87 %),
-// the summary pass before it 66; their bytes at a copy's rate 32.
+// on 1024 SIMDs; the output pass takes 91 (9 slots a state, VALUBusy 90 %), the
+// summary pass before it 67; their bytes at a copy's rate 32.
 //
 // Layout: a channel's NP padded states lie on LPC = NP / 4 neighbouring lanes,
 // four states a lane in registers, walking the tokens in order.  B_t and C_t,

@@ -16,10 +16,10 @@
 // sweep runs each from a zero state, leaving local tile states, the segment's
 // summary and its adjoint's together; the main kernel adds to a tile's local
 // state what the segment's start state has become by then (one exponential a
-// state and tile).  Bound by vector instructions, as the forward pass: 11 issue
-// slots per (token, channel, state) in the sweep, 25 in the main kernel (2 x
-// 2048 tokens of 5120 channels and 16 states: sweep 132 us at VALUBusy 74 %,
-// main kernel 300 at 79 %, carry 15, sums 16).
+// state and tile).  Bound by vector instructions, as the forward pass: 11
+// issue slots per (token, channel, state) in the sweep, 26 in the main kernel (2 x
+// 2048 tokens of 5120 channels and 16 states: sweep 132 us at VALUBusy 77 %,
+// main kernel 296 at 74 %, carry 14, sums 17).
 //
 // dB and dC sum over channels, which lie across lanes and blocks: within a wave
 // by channel_sums, the rest of the block once per tile from LDS, and the
@@ -185,8 +185,12 @@ struct BwdOut {
     int runs;
 };
 
-// LDS row of one lane's 8 + 8 sums of a tile, padded so that neither the
-// 16-byte writes nor the reads down a column meet in a bank.
+// LDS row of one lane's 8 + 8 sums of a tile, padded by four words: the first
+// words of 16 neighbouring rows lie on 16 different multiples of four modulo 64.
+// So the 64 words that a wave reads of four columns differ modulo 64 at 16
+// states; at 32 states two of them coincide, and at 64 four.  (Counted at 16
+// states, 2 x 2048 tokens of 5120 channels: 1e7 conflict cycles over 7.5e6 LDS
+// instructions of every kind, 16 us on each of 256 CUs.)
 constexpr int kRedStride = 2 * kScanTile + 4;
 
 // One segment, its tiles from the last to the first.  Registers limit it: a

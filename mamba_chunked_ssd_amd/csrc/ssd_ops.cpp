@@ -18,8 +18,8 @@ namespace ssd {
 
 // Strips long enough that the group formed twice and the partial sums stay
 // small, short enough that every SIMD gets two waves (2 x 2048 tokens of 5376
-// channels: 41 us with the 32 tokens this gives, 47 with 128; 3 x 1021 tokens
-// of 264: 23 us with 16).
+// channels: 46 us with the 32 tokens this gives, 50 with 16, 47 with 64, 54 with
+// 128; 3 x 1021 tokens of 264: 17 us with its 16, 27 with 128).
 ConvBwdPlan conv_bwd_plan(int64_t batch, int64_t seqlen, int64_t channels) {
     ConvBwdPlan p;
     // of four channels a lane; with one there are up to four times as many
@@ -39,10 +39,10 @@ ConvBwdPlan conv_bwd_plan(int64_t batch, int64_t seqlen, int64_t channels) {
 // Whole or cut, forward: whole, the time goes in steps with the waves on the
 // fullest of the 1024 SIMDs, cut, with the waves.  Measured per 2048 tokens of
 // 16 states (5120 channels are 320 waves a sequence), whole and cut:
-//   1280 waves 376 and 295 us, 1600 378 and 345, 1920 380 and 413,
-//   2240 500 and 470, 2560 503 and 528, 3200 593 and 652,
-// which 180 + 105 steps and 25 + 0.203 waves follow.  Backward: 2560 waves
-// 1654 and 1581 us, 3840 2349 and 2300, 5120 2768 and 3020.
+//   1280 waves 387 and 284 us, 1600 388 and 355, 1920 390 and 424,
+//   2240 512 and 483, 2560 513 and 544, 3200 607 and 670,
+// which 180 + 105 steps and 25 + 0.203 waves follow within 4 %.  Backward: 2560
+// waves 1691 and 1602 us, 3840 2366 and 2327, 5120 2812 and 3050.
 //
 // How many, when cut: enough for 16 384 waves (4 x 2048 tokens 281 us, with
 // 8192 waves 306), but no more than the square root of the length, or the carry

@@ -111,11 +111,12 @@ __device__ __forceinline__ float load_one(const T *p, int64_t i) {
 }
 
 // 1 / (1 + exp(-v)); exp2 overflows to infinity for very negative v, whose
-// reciprocal is the limit 0.  The exponent is rounded to fp32, and by |v| 2^-24
-// the exponential is off: no more than 0.54 2^-24 of v logistic(v), which is
-// what all uses take, but a relative error that grows for negative v.
-// Corrected as in softplus, the convolution's backward pass took 11 % more
-// (4 x 4096 tokens of 5376 channels, bf16), the scan's 2 %.
+// reciprocal is the limit 0.  The exponent is rounded to fp32, which puts the
+// exponential off by |v| 2^-24 or so: an absolute error of 0.54 2^-24 at most in
+// v logistic(v), of 0.27 2^-24 in logistic(v), though relative to the small
+// values of negative v it grows with |v|.  Corrected as in softplus, the
+// convolution's backward pass took 11 % more (4 x 4096 tokens of 5376 channels,
+// bf16), the scan's 2 %.
 __device__ __forceinline__ float logistic(float v) {
     return __builtin_amdgcn_rcpf(1.f + fast_exp2(-kLog2e * v));
 }

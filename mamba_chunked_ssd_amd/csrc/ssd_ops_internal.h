@@ -34,7 +34,7 @@ struct ConvArgs {
     const float *dfinal;
     void *dx;
     float *dweight, *dbias, *dinit;
-    float *partials;  // (conv_bwd_parts, width + 1, channels)
+    float *partials;  // (ConvBwdPlan::parts, width + 1, channels)
 };
 
 // The strips of tokens the backward pass cuts each sequence into, and how many
@@ -51,7 +51,7 @@ hipError_t launch_conv_bwd(const ConvArgs &a, const ConvBwdPlan &plan, hipStream
 hipError_t launch_conv_step(const ConvArgs &a, hipStream_t stream);
 
 // ---------------------------------------------------------------------------
-// Selective scan (ks_scan.hip, ks_scan_bwd.hip, ks_step.hip)
+// Selective scan (ks_scan.hip, ks_scan_bwd.hip)
 // ---------------------------------------------------------------------------
 
 // Each channel's states are spread over 2, 4, 8 or 16 lanes, 4 states a lane;
@@ -95,7 +95,9 @@ struct ScanArgs {
     float *seg_adj;     // as seg_state, for the gradient at each segment's end
     float *tile_state;  // state before each tile, (batch, tiles, channels, np)
     float *tile_steps;  // sum of the segment's steps before each tile (nseg > 1)
-    float *dbp, *dcp;   // partial dB, dC per block of a group, (nblk, batch, seqlen, dstate)
+    // partial dB, dC per block of a group, (nblk, batch, seqlen, dstate); reserved but not used where one block a
+    // group writes dB and dC themselves
+    float *dbp, *dcp;
     float *dap;         // partial dA, (batch, nseg, runs, channels, np)
     float *ddp, *dbiasp;  // partial dD and ddt_bias, (batch, nseg, runs, channels)
 };
