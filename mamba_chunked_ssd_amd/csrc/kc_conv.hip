@@ -153,10 +153,13 @@ __global__ __launch_bounds__(256) void kc_conv_fwd(ConvIn<Tin> a, Tout *__restri
 // the first, whose registers then leave two waves a SIMD, and 1 % of the second.
 // Measured and no faster: partial sums as two floats (47 us for both kernels
 // against 46), 64-bit sums in LDS, added to every four tokens (44, but 231 fp32).
+// Registers for three waves a SIMD are asked for where x, dy and dx are all bf16
+// (4 x 4096 tokens: 125 us, 132 with the two that the compiler leaves by itself);
+// with any of them in fp32 they spill (the first case 50 us against 45).
 constexpr int kGroup = 4;  // tokens; at least W - 1
 
 template <typename Tin, typename Tdy, typename Tdx, int W, int V>
-__global__ __launch_bounds__(256) void kc_conv_bwd(ConvIn<Tin> a, const Tdy *__restrict__ dy, int64_t dyb, int64_t dyr,
+__global__ __launch_bounds__(256, sizeof(Tin) + sizeof(Tdy) + sizeof(Tdx) == 6 ? 3 : 1) void kc_conv_bwd(ConvIn<Tin> a, const Tdy *__restrict__ dy, int64_t dyb, int64_t dyr,
                                                    const float *__restrict__ dfinal, Tdx *__restrict__ dx,
                                                    float *__restrict__ dinit, float *__restrict__ partials, int strip,
                                                    int nstrips) {
@@ -207,7 +210,11 @@ __global__ __launch_bounds__(256) void kc_conv_bwd(ConvIn<Tin> a, const Tdy *__r
             xp += U * a.xr;
             yp += U * dyr;
         };
-        auto group = [&](int t, bool own) {
+        const int live = min(t1, len);  // the strip's own tokens end here
+        // ENDS: a group that reaches behind them.  Rows behind a sequence's end get 0 by selection and add nothing: the
+        // windows of the first still hold the last inputs, and 0 times one that is not finite would be NaN.
+        auto group = [&](int t, auto ENDS) {
+            constexpr bool ends = decltype(ENDS)::value;
             float x[U][V], d[U][V], g[U][V];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -233,11 +240,10 @@ __global__ __launch_bounds__(256) void kc_conv_bwd(ConvIn<Tin> a, const Tdy *__r
                         const float sg = logistic(p);
                         // silu'(p) = s (1 + p (1 - s))
                         de *= sg * fmaf(p, 1.f - sg, 1.f);
-                        // the first rows behind the end still see the last inputs, and 0 times their slope may be NaN
-                        de = t + u < len ? de : 0.f;
+                        if constexpr (ends) de = t + u < len ? de : 0.f;
                     }
                     dp[W - 1][e] = de;
-                    if (own) {
+                    if (!ends || t + u < live) {
                         db[e] += de;
 #pragma unroll
                         for (int k = 0; k < W; ++k) dw[k][e] = fma((double)de, (double)win[k][e], dw[k][e]);
@@ -248,7 +254,7 @@ __global__ __launch_bounds__(256) void kc_conv_bwd(ConvIn<Tin> a, const Tdy *__r
                 }
             }
             const int s0 = t - (W - 1);  // the row of g[0]
-            if (dfinal != nullptr && s0 + U > len - (W - 1) && s0 < len && mine) {
+            if (ends && dfinal != nullptr && s0 + U > len - (W - 1) && s0 < len && mine) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int i = s0 + u - len + (W - 1);  // its row in the final state
@@ -262,7 +268,7 @@ __global__ __launch_bounds__(256) void kc_conv_bwd(ConvIn<Tin> a, const Tdy *__r
                     }
                 }
             }
-            if (s0 + U > len) {  // whatever the filter
+            if (ends && s0 + U > len) {  // whatever the filter
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -282,8 +288,8 @@ __global__ __launch_bounds__(256) void kc_conv_bwd(ConvIn<Tin> a, const Tdy *__r
         };
         fetch(t0);
         int t = t0;
-        for (; t < t1; t += U) group(t, true);
-        group(t, false);
+        for (; t + U <= live; t += U) group(t, std::false_type{});
+        for (; t < t1 + U; t += U) group(t, std::true_type{});
     }
 
 #pragma unroll

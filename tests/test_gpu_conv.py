@@ -431,3 +431,25 @@ def test_four_channels_a_lane_agree_with_one(dtype):
         y, fin = ssd.causal_conv_fwd(q["x"], q["weight"], q["bias"], q["init"], True, lengths=q["lengths"])
         results.append(dict(g, y=y, fin=fin))
     assert all(torch.equal(results[0][k], results[1][k]) for k in results[0])
+
+
+@pytest.mark.parametrize("L", [30, 64])
+@pytest.mark.parametrize("c", [24, 512])
+def test_last_inputs_not_finite_enter_only_their_own_taps(c, L):
+    # no live row meets the last input with another tap than the newest: those gradients of the filter stay finite,
+    # also where a sequence fills its rows but not the kernel's groups of tokens
+    d = inputs(3, L, c, 4, "f32", seed=23)
+    d["lengths"] = torch.tensor([L, 18, 1], dtype=torch.int32, device="cuda")
+    ends = d["lengths"].tolist()
+    args = {k: host(d[k]) for k in ("x", "weight", "bias", "dy", "init", "dfinal", "lengths")}
+    for i, end in enumerate(ends):
+        d["x"][i, end - 1] = float("inf")
+        args["x"][i, end - 1] = 0.0
+    got = ssd.causal_conv_bwd(d["x"], d["weight"], d["bias"], d["dy"], d["init"], d["dfinal"], activation=None,
+                              lengths=d["lengths"])
+    ref = lo.conv_bwd(*args.values(), act=False)
+    mag = lo.conv_bwd(*[np.abs(a) for a in args.values()], act=False)
+    for k in ("dx", "dbias", "d_initial_states"):
+        assert np.all(np.abs(host(got[k]) - ref[k]) <= 8 * EPS * mag[k]), k
+    assert np.all(np.abs(host(got["dweight"][:, :3]) - ref["dweight"][:, :3]) <= 8 * EPS * mag["dweight"][:, :3])
+    assert not bool(torch.isfinite(got["dweight"][:, 3]).any())
