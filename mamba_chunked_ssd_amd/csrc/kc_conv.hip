@@ -148,7 +148,7 @@ __global__ __launch_bounds__(256) void kc_conv_fwd(ConvIn<Tin> a, Tout *__restri
 // held in 64 bits, where a product of two fp32 numbers is exact, and rounded to
 // fp32 three times, as a strip's, a block's and the whole sum, however time is
 // cut.  Bound by memory: 2 x 2048 tokens of 5376 channels, bf16 with dy in fp32,
-// 37 us of which the 176 MB that must move take 34 at a copy's rate (sums 4 us
+// 38 us of which the 176 MB that must move take 34 at a copy's rate (sums 4 us
 // more); 4 x 4096 tokens fp32 228 us, its bytes 204.  The 64 bits cost 5 % of
 // the first, whose registers then leave two waves a SIMD, and 1 % of the second.
 // Measured and no faster: partial sums as two floats (47 us for both kernels

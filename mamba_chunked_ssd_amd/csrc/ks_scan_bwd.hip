@@ -194,8 +194,9 @@ struct BwdOut {
 constexpr int kRedStride = 2 * kScanTile + 4;
 
 // One segment, its tiles from the last to the first.  Registers limit it: a
-// tile's states and decays take 8 a token, so tiles have 8 tokens (167
-// registers at 16 states: three waves a SIMD; 16 tokens would leave one).
+// tile's states and decays take 8 a token, so tiles have 8 tokens (168
+// registers at 16 states, two more spilled: three waves a SIMD; 16 tokens would
+// leave one).
 template <typename Tin, typename Tdy, int LPC>
 __global__ __launch_bounds__(256, LPC == 4 ? 3 : 2)
 void ks_bwd_main(ScanIn<Tin> a, const Tdy *__restrict__ dy, Strides dys,
