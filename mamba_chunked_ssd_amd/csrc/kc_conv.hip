@@ -141,8 +141,8 @@ __global__ __launch_bounds__(256) void kc_conv_fwd(ConvIn<Tin> a, Tout *__restri
 //   dx_s = sum_k w_k d_{s+W-1-k} ,  dw_k = sum_t d_t x_{t-W+1+k} ,  db = sum_t d_t .
 // A wave walks t over its strip, four tokens at a time with the next four's
 // loads in flight, and over one group beyond it, whose d_t it forms again:
-// dx_{t-W+1} is complete at t.  Rows come through raw buffers over the group,
-// so ends need no branch in the loop.  dw and db stay in registers over the
+// dx_{t-W+1} is complete at t.  Rows come and go through raw buffers over the
+// group; what a sequence's end changes is a path of its own.  dw and db stay in registers over the
 // strip, are joined over the block's four strips in LDS and leave one row of
 // partial sums per block, which kc_conv_sums adds in a fixed order.  They are
 // held in 64 bits, where a product of two fp32 numbers is exact, and rounded to
@@ -151,7 +151,7 @@ __global__ __launch_bounds__(256) void kc_conv_fwd(ConvIn<Tin> a, Tout *__restri
 // 38 us of which the 176 MB that must move take 34 at a copy's rate (sums 4 us
 // more); 4 x 4096 tokens fp32 228 us, its bytes 204.  The 64 bits cost 5 % of
 // the first, whose registers then leave two waves a SIMD, and 1 % of the second.
-// Measured and no faster: partial sums as two floats (47 us for both kernels
+// Measured and not kept: partial sums as two floats (47 us for both kernels
 // against 46), 64-bit sums in LDS, added to every four tokens (44, but 231 fp32).
 // Registers for three waves a SIMD are asked for where x, dy and dx are all bf16
 // (4 x 4096 tokens: 125 us, 132 with the two that the compiler leaves by itself);
@@ -159,10 +159,9 @@ __global__ __launch_bounds__(256) void kc_conv_fwd(ConvIn<Tin> a, Tout *__restri
 constexpr int kGroup = 4;  // tokens; at least W - 1
 
 template <typename Tin, typename Tdy, typename Tdx, int W, int V>
-__global__ __launch_bounds__(256, sizeof(Tin) + sizeof(Tdy) + sizeof(Tdx) == 6 ? 3 : 1) void kc_conv_bwd(ConvIn<Tin> a, const Tdy *__restrict__ dy, int64_t dyb, int64_t dyr,
-                                                   const float *__restrict__ dfinal, Tdx *__restrict__ dx,
-                                                   float *__restrict__ dinit, float *__restrict__ partials, int strip,
-                                                   int nstrips) {
+__global__ __launch_bounds__(256, sizeof(Tin) + sizeof(Tdy) + sizeof(Tdx) == 6 ? 3 : 1)
+void kc_conv_bwd(ConvIn<Tin> a, const Tdy *__restrict__ dy, int64_t dyb, int64_t dyr, const float *__restrict__ dfinal,
+                 Tdx *__restrict__ dx, float *__restrict__ dinit, float *__restrict__ partials, int strip, int nstrips) {
     constexpr int U = kGroup, R = (W + 1) * V;
     __shared__ float red[4 * R * 64];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
