@@ -50,7 +50,11 @@
 extern "C" {
 #endif
 
-typedef enum { SSD_DTYPE_F32 = 0, SSD_DTYPE_BF16 = 1 } ssd_dtype;
+typedef enum {
+    SSD_DTYPE_F32 = 0,
+    SSD_DTYPE_BF16 = 1,
+    SSD_DTYPE_E4M3 = 2 /* y of ssd_rms_norm_fwd only: 4 exponent and 3 mantissa bits, largest 448, no infinities */
+} ssd_dtype;
 
 typedef enum {
     SSD_OK = 0,
@@ -563,6 +567,158 @@ ssd_status ssd_selective_scan_bwd(const ssd_selective_shape *shape, const void *
 ssd_status ssd_selective_scan_step(const ssd_selective_shape *shape, const void *x, const void *dt, const float *A,
                                    const void *B, const void *C, const float *D, const void *z, const float *dt_bias,
                                    float *state, void *y, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Sliding-window attention with sinks
+ *
+ * The sequence mixer that models put between the scans.  For query head h, of
+ * key and value head g = h / (nheads / nkvheads), and tokens t (the query's)
+ * and j (a key's), counted from the sequence's first token,
+ *     t sees j  <=>  j <= t  and  (t - j < window  or  j < sinks)
+ *     s_tj = scale q_t . k_j ,  p_tj = exp(s_tj - lse_t) for the j that t sees,
+ *     lse_t = log sum_j exp(s_tj) ,  y_t = sum_j p_tj v_j
+ * The first `sinks` tokens stay visible for ever.  A token that t does not see
+ * has no influence on row t, whatever it holds (infinities and NaN included).
+ *
+ * The state is a cache of constant size, k_cache and v_cache (batch, nkvheads,
+ * sinks + window, headdim) in dtype, 16-byte aligned, and the number of tokens
+ * each sequence has behind it, `positions`, device int32 (batch), at most 2^29.
+ * Token j lies in slot j if j < sinks, else in slot sinks + (j - sinks) mod
+ * window.  Positions are an input that one count of a model serves for all its
+ * layers: the caller adds the tokens of a call once all layers have had them.
+ *
+ * The conventions of the operators above hold (lengths, dense outputs, rows
+ * behind a sequence's end not read and written as 0, fixed orders of summation,
+ * limits), but for the strides of inputs: an ssd_head_stride gives the elements
+ * between batch entries, tokens and heads ({0, 0, 0}: dense), so that heads may
+ * lie outside tokens too; a head's elements are contiguous, row is at least
+ * headdim where seqlen > 1 and below 2^22, all are >= 0 and multiples of 16 bytes
+ * where there is more than one of their kind.  Inputs, outputs and caches are
+ * 16-byte aligned (lse, positions, lengths 4).  Products of bf16
+ * inputs run on the matrix cores with fp32 sums; the weights p and the
+ * gradients of the scores are rounded to bf16 as operands of the next product,
+ * never the softmax's maxima and sums.  Products of fp32 inputs are fp32.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int64_t batch, row, head;
+} ssd_head_stride;
+
+typedef struct {
+    int64_t batch, seqlen; /* >= 0 */
+    int64_t nheads;        /* of q and y, >= 1 */
+    int64_t nkvheads;      /* of k and v, >= 1, divides nheads; heads share them contiguously */
+    int64_t headdim;       /* supported 32, 64, 128 */
+    int64_t window;        /* >= 1; seqlen or more without a cache: every earlier token */
+    int64_t sinks;         /* >= 0 */
+    float scale;           /* > 0 and finite, usually headdim^-1/2 */
+    int32_t dtype;         /* ssd_dtype of q, k, v, y, their gradients and the cache */
+    int32_t reserved[2];   /* must be 0 */
+    ssd_head_stride q, k, v, y, dy; /* (y, dy: inputs of the backward pass) */
+} ssd_attn_shape;
+
+/* Forward pass over prompts.
+ *   q                (batch, seqlen, nheads, headdim) dtype, shape->q strides
+ *   k, v             (batch, seqlen, nkvheads, headdim)
+ *   positions        NULL => every sequence begins here; else needs the cache,
+ *                    whose tokens are read too (negative: taken as 0)
+ *   lengths          as above
+ *   k_cache, v_cache both or none; the new tokens are put in, whether or not
+ *                    positions is given.  Slots that no token of the sequence
+ *                    has reached are not read, and left as they are.
+ *   y                (batch, seqlen, nheads, headdim) dtype, out
+ *   lse              (batch, nheads, seqlen) fp32, out, NULL => not written
+ * Outputs and caches must not overlap an input or each other. */
+ssd_status ssd_window_attn_fwd(const ssd_attn_shape *shape, const void *q, const void *k, const void *v,
+                               const int32_t *positions, const int32_t *lengths, void *k_cache, void *v_cache,
+                               void *y, float *lse, void *stream);
+/* Gradients through ssd_window_attn_fwd without positions; q, k, v and lengths
+ * as passed there.
+ *   y, lse           as it wrote them (y by shape->y strides)
+ *   dy               (batch, seqlen, nheads, headdim) dtype, shape->dy strides
+ *   dq               (batch, seqlen, nheads, headdim) dtype, out
+ *   dk, dv           (batch, seqlen, nkvheads, headdim) dtype, out, summed over
+ *                    the heads that share them
+ *   workspace        256-byte aligned, at least
+ *                    ssd_window_attn_bwd_workspace_size(shape) bytes
+ * No output may overlap an input, the workspace or another output. */
+size_t ssd_window_attn_bwd_workspace_size(const ssd_attn_shape *shape);
+ssd_status ssd_window_attn_bwd(const ssd_attn_shape *shape, const void *q, const void *k, const void *v,
+                               const void *y, const float *lse, const void *dy, const int32_t *lengths, void *dq,
+                               void *dk, void *dv, void *workspace, size_t workspace_bytes, void *stream);
+/* One token per sequence (shape->seqlen must be 1; rows by the strides' batch):
+ * k and v are put into the cache, then q attends to all that it holds.
+ *   q            (batch, nheads, headdim) dtype
+ *   k, v         (batch, nkvheads, headdim) dtype
+ *   positions    the new token's own, required; negative: an empty place of the
+ *                batch, whose y is 0 and whose cache is left as it is
+ *   k_cache, v_cache  read and updated in place
+ *   y            (batch, nheads, headdim) dtype, out
+ *   workspace    256-byte aligned, at least
+ *                ssd_window_attn_step_workspace_size(shape) bytes (may be 0)
+ * y and the caches must not overlap each other or an input. */
+size_t ssd_window_attn_step_workspace_size(const ssd_attn_shape *shape);
+ssd_status ssd_window_attn_step(const ssd_attn_shape *shape, const void *q, const void *k, const void *v,
+                                const int32_t *positions, void *k_cache, void *v_cache, void *y, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Root-mean-square norm with the residual's addition
+ *
+ * What stands before a layer's input projection: for every token
+ *     u = x + residual ,  r = (mean_c u_c^2 + eps)^-1/2 ,  y_c = u_c r weight_c
+ * with u formed and used in fp32, also where it is stored in fewer bits.  y may
+ * come in 8 bits for a product that takes them: with m the largest |y_c| of a
+ * row, or of each scale_block consecutive columns of it (the last may be
+ * shorter), scale = max(m / 448, 2^-126) and the code e4m3(y_c / scale), rounded
+ * to nearest even.  A NaN among them makes the scale NaN.  Sums of squares that
+ * leave fp32's range (|u| from about 1e18) give r = 0.
+ * The conventions of the operators above hold; pointers need their element
+ * type's alignment only.  batch x seqlen must stay below 2^31.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int64_t batch, seqlen; /* >= 0 */
+    int64_t channels;      /* >= 1 */
+    float eps;             /* >= 0, finite */
+    int32_t dtype;         /* ssd_dtype of x and dx */
+    int32_t res_dtype;     /* ssd_dtype of the residual stream: residual, residual_out, u and their gradients */
+    int32_t y_dtype;       /* ssd_dtype of y and dy; SSD_DTYPE_E4M3 forward only */
+    int32_t scale_block;   /* SSD_DTYPE_E4M3: columns to a scale, 32, 64 or 128, or 0: the row; else 0 */
+    int32_t reserved;      /* must be 0 */
+    ssd_stride x, residual, dy, dres; /* (residual: also u backwards; dy, dres: backward only) */
+} ssd_norm_shape;
+
+/* Forward pass.
+ *   x             (batch, seqlen, channels) dtype, shape->x strides
+ *   residual      (batch, seqlen, channels) res_dtype, shape->residual strides;
+ *                 NULL => u = x
+ *   weight        (channels) fp32, NULL => 1
+ *   lengths       as above
+ *   y             (batch, seqlen, channels) y_dtype, out
+ *   scales        (batch, seqlen, ceil(channels / scale_block), or 1) fp32, out;
+ *                 with SSD_DTYPE_E4M3 required, else NULL
+ *   residual_out  u, (batch, seqlen, channels) res_dtype, out, NULL => not
+ *                 written; may be the very buffer of a dense residual
+ * Outputs must not overlap an input or each other otherwise. */
+ssd_status ssd_rms_norm_fwd(const ssd_norm_shape *shape, const void *x, const void *residual, const float *weight,
+                            const int32_t *lengths, void *y, float *scales, void *residual_out, void *stream);
+/* Gradients through ssd_rms_norm_fwd (of an 8-bit y, those of the y it rounds):
+ *     du_c = r weight_c dy_c - u_c r^3 mean(weight dy u) + d_residual_out_c
+ *     dweight_c = sum over tokens of dy_c u_c r
+ *   dy              (batch, seqlen, channels) y_dtype, shape->dy strides
+ *   u               x + residual (what residual_out holds, or x), res_dtype,
+ *                   shape->residual strides
+ *   d_residual_out  res_dtype, shape->dres strides; NULL => 0
+ *   dx              du, (batch, seqlen, channels) dtype, out
+ *   d_residual      du, res_dtype, out, NULL => not written; may be the very
+ *                   buffer of a dense d_residual_out
+ *   dweight         (channels) fp32, out, NULL => not written
+ *   workspace       256-byte aligned, at least
+ *                   ssd_rms_norm_bwd_workspace_size(shape) bytes
+ * No output may overlap an input, the workspace or another output otherwise. */
+size_t ssd_rms_norm_bwd_workspace_size(const ssd_norm_shape *shape);
+ssd_status ssd_rms_norm_bwd(const ssd_norm_shape *shape, const void *dy, const void *u, const float *weight,
+                            const void *d_residual_out, const int32_t *lengths, void *dx, void *d_residual,
+                            float *dweight, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Static, human-readable description of a status code. */
 const char *ssd_status_string(ssd_status status);

@@ -9,9 +9,11 @@ CPU fallback: if the library is missing, importing works but any call raises.
     y, final = chunk_scan_fwd(..., initial_states=h0, return_final_states=True)
 
 Beside it stand the operators of the layers around it: the short causal
-convolution (``causal_conv_fwd``, ``_bwd``, ``_step``) and the selective scan
+convolution (``causal_conv_fwd``, ``_bwd``, ``_step``), the selective scan
 with a decay per channel and state (``selective_scan_fwd``, ``_bwd``,
-``_step``).
+``_step``), sliding-window attention with sinks (``window_attention_fwd``,
+``_bwd``, ``_step``) and the RMS norm with the residual's addition
+(``rms_norm_fwd``, ``_bwd``).
 
 The operation is the selective state-space recurrence of "Accelerating Mamba-2
 with High-Performance Forward Pass Kernels in NVIDIA CUDA Tile" (section
@@ -29,6 +31,7 @@ LIB_PATH = os.path.join(HERE, "libssd.so")
 
 SSD_DTYPE_F32 = 0
 SSD_DTYPE_BF16 = 1
+SSD_DTYPE_E4M3 = 2
 SSD_FLAG_KEEP_INTERMEDIATES = 1
 
 STATUS = {
@@ -67,6 +70,14 @@ EXPORTS = [
     "ssd_selective_scan_bwd_workspace_size",
     "ssd_selective_scan_bwd",
     "ssd_selective_scan_step",
+    "ssd_window_attn_fwd",
+    "ssd_window_attn_bwd_workspace_size",
+    "ssd_window_attn_bwd",
+    "ssd_window_attn_step_workspace_size",
+    "ssd_window_attn_step",
+    "ssd_rms_norm_fwd",
+    "ssd_rms_norm_bwd_workspace_size",
+    "ssd_rms_norm_bwd",
     "ssd_status_string",
     "ssd_version",
 ]
@@ -154,6 +165,49 @@ class SelectiveShape(ctypes.Structure):
         ("C", Stride),
         ("z", Stride),
         ("dy", Stride),
+    ]
+
+
+class HeadStride(ctypes.Structure):
+    """ssd_head_stride: elements between batch entries, tokens and heads ({0, 0, 0}: dense)."""
+    _fields_ = [("batch", ctypes.c_int64), ("row", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class AttnShape(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("seqlen", ctypes.c_int64),
+        ("nheads", ctypes.c_int64),
+        ("nkvheads", ctypes.c_int64),
+        ("headdim", ctypes.c_int64),
+        ("window", ctypes.c_int64),
+        ("sinks", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32 * 2),
+        ("q", HeadStride),
+        ("k", HeadStride),
+        ("v", HeadStride),
+        ("y", HeadStride),
+        ("dy", HeadStride),
+    ]
+
+
+class NormShape(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("seqlen", ctypes.c_int64),
+        ("channels", ctypes.c_int64),
+        ("eps", ctypes.c_float),
+        ("dtype", ctypes.c_int32),
+        ("res_dtype", ctypes.c_int32),
+        ("y_dtype", ctypes.c_int32),
+        ("scale_block", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("x", Stride),
+        ("residual", Stride),
+        ("dy", Stride),
+        ("dres", Stride),
     ]
 
 
@@ -246,10 +300,21 @@ def load_library(path: str | None = None):
         lib.ssd_selective_scan_bwd_workspace_size.argtypes = [xp]
         lib.ssd_selective_scan_bwd.argtypes = [xp] + [vp] * 22 + [sz, vp]
         lib.ssd_selective_scan_step.argtypes = [xp] + [vp] * 11
-        for name in ("causal_conv_bwd", "selective_scan_fwd", "selective_scan_bwd"):
+        ap, np_ = ctypes.POINTER(AttnShape), ctypes.POINTER(NormShape)
+        lib.ssd_window_attn_fwd.argtypes = [ap] + [vp] * 10
+        lib.ssd_window_attn_bwd_workspace_size.argtypes = [ap]
+        lib.ssd_window_attn_bwd.argtypes = [ap] + [vp] * 11 + [sz, vp]
+        lib.ssd_window_attn_step_workspace_size.argtypes = [ap]
+        lib.ssd_window_attn_step.argtypes = [ap] + [vp] * 8 + [sz, vp]
+        lib.ssd_rms_norm_fwd.argtypes = [np_] + [vp] * 8
+        lib.ssd_rms_norm_bwd_workspace_size.argtypes = [np_]
+        lib.ssd_rms_norm_bwd.argtypes = [np_] + [vp] * 9 + [sz, vp]
+        for name in ("causal_conv_bwd", "selective_scan_fwd", "selective_scan_bwd", "window_attn_bwd",
+                     "window_attn_step", "rms_norm_bwd"):
             getattr(lib, "ssd_%s_workspace_size" % name).restype = sz
         for name in ("causal_conv_fwd", "causal_conv_bwd", "causal_conv_step", "selective_scan_fwd",
-                     "selective_scan_bwd", "selective_scan_step"):
+                     "selective_scan_bwd", "selective_scan_step", "window_attn_fwd", "window_attn_bwd",
+                     "window_attn_step", "rms_norm_fwd", "rms_norm_bwd"):
             getattr(lib, "ssd_" + name).restype = ctypes.c_int
         lib.ssd_status_string.argtypes = [ctypes.c_int]
         lib.ssd_status_string.restype = ctypes.c_char_p
@@ -611,17 +676,17 @@ def tune(x, dt, A, B, C, D=None, chunk_size: int = 256, initial_states=None, *, 
 _ACTIVATIONS = {None: SSD_ACT_NONE, "silu": SSD_ACT_SILU}
 
 
-def _input_dtype(x, torch):
+def _input_dtype(x, torch, name="x"):
     """ssd_dtype of an operator's first input, which its other inputs share."""
     if not isinstance(x, torch.Tensor):
-        raise TypeError("x must be a torch.Tensor")
+        raise TypeError("%s must be a torch.Tensor" % name)
     if not x.is_cuda:
         raise ValueError("tensors must be on a ROCm device (got %s)" % x.device)
     if x.dtype == torch.bfloat16:
         return SSD_DTYPE_BF16
     if x.dtype == torch.float32:
         return SSD_DTYPE_F32
-    raise TypeError("x must be float32 or bfloat16")
+    raise TypeError("%s must be float32 or bfloat16" % name)
 
 
 def _result_dtype(dtype, given, name, torch):
@@ -963,3 +1028,293 @@ def selective_scan_step(x, dt, A, B, C, D, state, z=None, dt_bias=None, *, dt_so
         return st, y
 
     return _call("ssd_selective_scan_step", dev, stream, run, torch)
+
+
+# ---------------------------------------------------------------------------
+# Sliding-window attention with sinks, and the RMS norm with the residual's addition
+# ---------------------------------------------------------------------------
+
+def _heads(t, name, dtype, shape, device, tensor, lead):
+    """Checks an input of heads that may lie apart, (batch, seqlen, heads, headdim) or without seqlen (``lead`` 1), and
+    returns its ssd_head_stride, None if it is dense."""
+    if isinstance(t, tensor) and t.dtype == dtype and t.shape == shape and t.get_device() == device.index:
+        if t.is_contiguous():
+            return None
+        st = t.stride()
+        if st[-1] != 1 and shape[-1] != 1:
+            raise ValueError("%s: each head must be contiguous (strides %s)" % (name, st))
+        row = st[1] if lead == 2 and shape[1] > 1 else shape[-1]
+        if row < shape[-1]:
+            raise ValueError("%s: rows of different tokens overlap (strides %s)" % (name, st))
+        return HeadStride(st[0] if shape[0] > 1 else 0, row, st[-2] if shape[-2] > 1 else shape[-1])
+    if isinstance(t, tensor) and t.dtype == dtype and t.device == device:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    return _check(t, name, dtype, shape, device)
+
+
+def _attn_args(q, k, v, window, sinks, scale, lead, torch):
+    tensor = torch.Tensor
+    code = _input_dtype(q, torch, "q")
+    if not isinstance(k, tensor):
+        raise TypeError("k must be a torch.Tensor")
+    dims, of_k = q.shape, k.shape
+    if len(dims) != lead + 2 or len(of_k) != lead + 2:
+        raise ValueError("q must be (batch, %snheads, headdim) and k (batch, %snkvheads, headdim)"
+                         % (("seqlen, ",) * 2 if lead == 2 else ("", "")))
+    dev, dtype, b, h, d, kv = q.device, q.dtype, dims[0], dims[-2], dims[-1], of_k[-2]
+    L = dims[1] if lead == 2 else 1
+    shape = AttnShape(b, L, h, kv, d, max(L, 1) if window is None else window, sinks, d ** -0.5 if scale is None else scale,
+                      code)
+    kdims = dims[:lead] + (kv, d)
+    for name, t, want in (("q", q, dims), ("k", k, kdims), ("v", v, kdims)):
+        st = _heads(t, name, dtype, want, dev, tensor, lead)
+        if st is not None:
+            setattr(shape, name, st)
+    return shape, dev, dtype, b, L, h, kv, d
+
+
+def _cache(k_cache, v_cache, dtype, shape, dev, torch):
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _dense(t, name, dtype, (shape.batch, shape.nkvheads, shape.sinks + shape.window, shape.headdim), dev,
+               torch.Tensor)
+
+
+def window_attention_fwd(q, k, v, window=None, sinks: int = 0, *, scale=None, lengths=None, positions=None,
+                         k_cache=None, v_cache=None, return_lse: bool = False, out=None, stream=None):
+    """Causal attention over prompts in which a token sees the last ``window``
+    tokens, itself among them, and the sequence's first ``sinks``
+    (``ssd_window_attn_fwd``).
+
+    q (b, L, h, d) and k, v (b, L, kv, d), h a multiple of kv, d 32, 64 or 128:
+    float32 or bfloat16, all the same dtype, heads may lie apart (column slices
+    of a wider projection, heads outside tokens).  ``window`` None: every earlier token of the call.
+    ``scale``: d ** -0.5 if None.  ``lengths``: int32 (b,) device tensor, tokens
+    of each padded sequence; rows behind are 0.  ``k_cache`` and ``v_cache``
+    (b, kv, sinks + window, d) are brought up to date; with ``positions``, int32
+    (b,), the tokens each sequence has behind it, the tokens in them are read
+    too.  Returns y (b, L, h, d) in q's dtype, or (y, lse) with lse (b, h, L)
+    float32, which :func:`window_attention_bwd` takes.
+    """
+    torch = _torch()
+    shape, dev, dtype, b, L, h, kv, d = _attn_args(q, k, v, window, sinks, scale, 2, torch)
+    if lengths is not None:
+        _dense(lengths, "lengths", torch.int32, (b,), dev, torch.Tensor)
+    if positions is not None:
+        _dense(positions, "positions", torch.int32, (b,), dev, torch.Tensor)
+    if k_cache is not None or v_cache is not None or positions is not None:
+        if window is None:
+            raise ValueError("a cache needs a window")
+        _cache(k_cache, v_cache, dtype, shape, dev, torch)
+    if out is not None:
+        _dense(out, "out", dtype, (b, L, h, d), dev, torch.Tensor)
+
+    def run(handle):
+        y = out if out is not None else torch.empty((b, L, h, d), dtype=dtype, device=dev)
+        lse = torch.empty((b, h, L), dtype=torch.float32, device=dev) if return_lse else None
+        st = load_library().ssd_window_attn_fwd(ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                                _addr(positions), _addr(lengths), _addr(k_cache), _addr(v_cache),
+                                                y.data_ptr(), _addr(lse), handle)
+        return st, (y, lse) if return_lse else y
+
+    return _call("ssd_window_attn_fwd", dev, stream, run, torch)
+
+
+def window_attention_bwd(q, k, v, y, lse, dy, window=None, sinks: int = 0, *, scale=None, lengths=None, workspace=None,
+                         stream=None):
+    """Gradients through :func:`window_attention_fwd` without positions (``ssd_window_attn_bwd``).
+
+    Inputs as passed there, ``y`` and ``lse`` as it returned them, and ``dy``
+    (b, L, h, d) in q's dtype, heads may lie apart.  Returns a dict of ``dq``,
+    ``dk`` and ``dv`` in q's dtype.
+    """
+    torch = _torch()
+    lib = load_library()
+    shape, dev, dtype, b, L, h, kv, d = _attn_args(q, k, v, window, sinks, scale, 2, torch)
+    _dense(lse, "lse", torch.float32, (b, h, L), dev, torch.Tensor)
+    for name, t in (("y", y), ("dy", dy)):
+        st = _heads(t, name, dtype, q.shape, dev, torch.Tensor, 2)
+        if st is not None:
+            setattr(shape, name, st)
+    if lengths is not None:
+        _dense(lengths, "lengths", torch.int32, (b,), dev, torch.Tensor)
+
+    def run(handle):
+        res = {"dq": torch.empty((b, L, h, d), dtype=dtype, device=dev), "dk": torch.empty((b, L, kv, d), dtype=dtype, device=dev)}
+        res["dv"] = torch.empty_like(res["dk"])
+        ws, size, _keep = _workspace(workspace, lib.ssd_window_attn_bwd_workspace_size(ctypes.byref(shape)), dev, torch)
+        st = lib.ssd_window_attn_bwd(ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(), y.data_ptr(),
+                                     lse.data_ptr(), dy.data_ptr(), _addr(lengths), res["dq"].data_ptr(),
+                                     res["dk"].data_ptr(), res["dv"].data_ptr(), ws, size, handle)
+        return st, res
+
+    return _call("ssd_window_attn_bwd", dev, stream, run, torch)
+
+
+def window_attention_step(q, k, v, k_cache, v_cache, positions, window, sinks: int = 0, *, scale=None, out=None,
+                          workspace=None, stream=None):
+    """The attention for one new token per sequence (``ssd_window_attn_step``).
+
+    q (b, h, d), k and v (b, kv, d); ``k_cache`` and ``v_cache`` (b, kv, sinks +
+    window, d) take the new token's and are read whole.  ``positions``: int32
+    (b,) device tensor, the new token's own (the tokens before it); negative
+    for an empty place of the batch, whose row is 0.  It is not changed: the
+    layers of a model share it.  Returns y (b, h, d) in q's dtype.
+    """
+    torch = _torch()
+    lib = load_library()
+    if window is None:
+        raise ValueError("a cache needs a window")
+    shape, dev, dtype, b, _, h, kv, d = _attn_args(q, k, v, window, sinks, scale, 1, torch)
+    _dense(positions, "positions", torch.int32, (b,), dev, torch.Tensor)
+    _cache(k_cache, v_cache, dtype, shape, dev, torch)
+    if out is not None:
+        _dense(out, "out", dtype, (b, h, d), dev, torch.Tensor)
+
+    def run(handle):
+        y = out if out is not None else torch.empty((b, h, d), dtype=dtype, device=dev)
+        ws, size, _keep = _workspace(workspace, lib.ssd_window_attn_step_workspace_size(ctypes.byref(shape)), dev, torch)
+        st = lib.ssd_window_attn_step(ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                      positions.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), y.data_ptr(), ws,
+                                      size, handle)
+        return st, y
+
+    return _call("ssd_window_attn_step", dev, stream, run, torch)
+
+
+def _stored(t, name, torch):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype == torch.bfloat16:
+        return SSD_DTYPE_BF16
+    if t.dtype == torch.float32:
+        return SSD_DTYPE_F32
+    raise TypeError("%s must be float32 or bfloat16" % name)
+
+
+def _norm_args(x, name, weight, eps, lengths, torch):
+    code = _input_dtype(x, torch, name)
+    dims, dev = x.shape, x.device
+    if len(dims) == 3:
+        shape = NormShape(dims[0], dims[1], dims[2], eps, code, code, code)
+    elif len(dims) == 2:
+        shape = NormShape(1, dims[0], dims[1], eps, code, code, code)
+    else:
+        raise ValueError("%s must be (tokens, channels) or (batch, seqlen, channels)" % name)
+    if weight is not None:
+        _dense(weight, "weight", torch.float32, (dims[-1],), dev, torch.Tensor)
+    if lengths is not None:
+        if len(dims) == 2:
+            raise ValueError("lengths belong to (batch, seqlen, channels)")
+        _dense(lengths, "lengths", torch.int32, (dims[0],), dev, torch.Tensor)
+    return shape, dev, dims
+
+
+def _norm_rows(t, name, dtype, shape, device, torch):
+    """:func:`_rows` of tokens in one or two dimensions."""
+    if len(shape) == 2 and isinstance(t, torch.Tensor) and t.dim() == 2:
+        return _rows(t[None], name, dtype, (1, *shape), device, torch.Tensor, 2)
+    return _rows(t, name, dtype, shape, device, torch.Tensor, 2)
+
+
+def rms_norm_fwd(x, weight=None, residual=None, *, eps: float = 1e-5, lengths=None, y_dtype=None, scale_block: int = 0,
+                 return_residual: bool = False, residual_dtype=None, out=None, scales_out=None, residual_out=None,
+                 stream=None):
+    """Root-mean-square norm over the last dimension of x + residual
+    (``ssd_rms_norm_fwd``): u = x + residual, y = u (mean(u^2) + eps)^-1/2 weight.
+
+    x and ``residual`` (b, L, c) or (tokens, c): float32 or bfloat16 each, rows may
+    lie apart; weight (c,) float32, None: 1.  ``y_dtype``: float32, the default,
+    x's dtype, or torch.float8_e4m3fn with a float32 scale for each row
+    (``scale_block`` 0) or each 32, 64 or 128 columns of it, y being code times
+    scale.  ``lengths``: int32 (b,) device tensor, tokens of each padded
+    sequence; rows behind are 0.  Returns y, followed by the scales (b, L,
+    blocks) of an 8-bit y and, if asked for, u in the residual's dtype
+    (``residual_dtype``, float32 if None, where there is no residual);
+    ``residual_out`` may be ``residual`` itself.
+    """
+    torch = _torch()
+    shape, dev, dims = _norm_args(x, "x", weight, eps, lengths, torch)
+    st = _norm_rows(x, "x", x.dtype, dims, dev, torch)
+    if st is not None:
+        shape.x = st
+    rtype = torch.float32 if residual_dtype is None else residual_dtype
+    if residual is not None:
+        shape.res_dtype, rtype = _stored(residual, "residual", torch), residual.dtype
+        st = _norm_rows(residual, "residual", rtype, dims, dev, torch)
+        if st is not None:
+            shape.residual = st
+    elif rtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("residual_dtype must be float32 or bfloat16")
+    else:
+        shape.res_dtype = SSD_DTYPE_F32 if rtype == torch.float32 else SSD_DTYPE_BF16
+    codes = y_dtype == torch.float8_e4m3fn
+    if codes:
+        ytype, shape.y_dtype, shape.scale_block = y_dtype, SSD_DTYPE_E4M3, scale_block
+        if scale_block not in (0, 32, 64, 128):
+            raise ValueError("scale_block must be 0 (the row), 32, 64 or 128")
+        sdims = dims[:-1] + (-(-dims[-1] // scale_block) if scale_block else 1,)
+        if scales_out is not None:
+            _dense(scales_out, "scales_out", torch.float32, sdims, dev, torch.Tensor)
+    else:
+        ytype, shape.y_dtype = _result_dtype(y_dtype, x.dtype, "y_dtype", torch)
+        if scale_block != 0 or scales_out is not None:
+            raise ValueError("scales belong to an 8-bit y")
+    if out is not None:
+        _dense(out, "out", ytype, dims, dev, torch.Tensor)
+    if residual_out is not None:
+        _dense(residual_out, "residual_out", rtype, dims, dev, torch.Tensor)
+
+    def run(handle):
+        y = out if out is not None else torch.empty(dims, dtype=ytype, device=dev)
+        scales, u = scales_out, residual_out
+        if codes and scales is None:
+            scales = torch.empty(sdims, dtype=torch.float32, device=dev)
+        if u is None and return_residual:
+            u = torch.empty(dims, dtype=rtype, device=dev)
+        st = load_library().ssd_rms_norm_fwd(ctypes.byref(shape), x.data_ptr(), _addr(residual), _addr(weight),
+                                             _addr(lengths), y.data_ptr(), _addr(scales), _addr(u), handle)
+        got = (y,) + ((scales,) if codes else ()) + ((u,) if return_residual else ())
+        return st, got if len(got) > 1 else y
+
+    return _call("ssd_rms_norm_fwd", dev, stream, run, torch)
+
+
+def rms_norm_bwd(dy, u, weight=None, d_residual=None, *, eps: float = 1e-5, lengths=None, dx_dtype=None,
+                 want_dresidual: bool = False, want_dweight: bool = True, workspace=None, stream=None):
+    """Gradients through :func:`rms_norm_fwd` (``ssd_rms_norm_bwd``).
+
+    ``dy`` and ``u`` (b, L, c) or (tokens, c), u being x + residual as the forward
+    pass returns it (or x): float32 or bfloat16 each, rows may lie apart;
+    ``d_residual`` in u's dtype, what reaches u by way of the residual stream.
+    Returns a dict of ``dx`` (``dx_dtype``: float32, the default, or bfloat16)
+    and, when requested, ``dresidual``, the same gradient in u's dtype, and
+    ``dweight`` (float32).
+    """
+    torch = _torch()
+    lib = load_library()
+    shape, dev, dims = _norm_args(u, "u", weight, eps, lengths, torch)
+    shape.y_dtype = _stored(dy, "dy", torch)
+    for name, t, dtype, field in (("u", u, u.dtype, "residual"), ("dy", dy, dy.dtype, "dy"),
+                                  ("d_residual", d_residual, u.dtype, "dres")):
+        if t is not None:
+            st = _norm_rows(t, name, dtype, dims, dev, torch)
+            if st is not None:
+                setattr(shape, field, st)
+    xtype = torch.float32 if dx_dtype is None else dx_dtype
+    if xtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("dx_dtype must be float32 or bfloat16")
+    shape.dtype = SSD_DTYPE_F32 if xtype == torch.float32 else SSD_DTYPE_BF16
+
+    def run(handle):
+        res = {"dx": torch.empty(dims, dtype=xtype, device=dev)}
+        if want_dresidual:
+            res["dresidual"] = torch.empty(dims, dtype=u.dtype, device=dev)
+        if want_dweight:
+            res["dweight"] = torch.empty((dims[-1],), dtype=torch.float32, device=dev)
+        ws, size, _keep = _workspace(workspace, lib.ssd_rms_norm_bwd_workspace_size(ctypes.byref(shape)), dev, torch)
+        st = lib.ssd_rms_norm_bwd(ctypes.byref(shape), dy.data_ptr(), u.data_ptr(), _addr(weight), _addr(d_residual),
+                                  _addr(lengths), res["dx"].data_ptr(), _addr(res.get("dresidual")),
+                                  _addr(res.get("dweight")), ws, size, handle)
+        return st, res
+
+    return _call("ssd_rms_norm_bwd", dev, stream, run, torch)

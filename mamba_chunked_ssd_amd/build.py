@@ -21,9 +21,11 @@ LIB_PATH = os.path.join(HERE, "libssd.so")
 SOURCES = ["ssd_api.cpp", "ssd_tune.cpp", "ssd_bwd.cpp", "k1_cumsum.hip", "k2_chunk_state.hip", "k3_state_pass.hip",
            "k23_state_fused.hip", "k5_decode_step.hip", "k4_out_bf16_f32.hip", "k4_out_bf16_bf16.hip",
            "k4_out_f32.hip", "ssd_noalloc.hip", "kb_aux.hip", "kb_pass_q.hip", "kb_pass_b.hip", "kb_pass_c.hip",
-           "ssd_ops.cpp", "kc_conv.hip", "ks_scan.hip", "ks_scan_bwd.hip"]
+           "ssd_ops.cpp", "kc_conv.hip", "ks_scan.hip", "ks_scan_bwd.hip", "ssd_mixer_ops.cpp",
+           "kn_norm.hip", "kn_norm_bwd.hip", "ka_attn_fwd.hip", "ka_attn_bwd.hip", "ka_attn_step.hip"]
 HEADERS = ["ssd_device.h", "ssd_internal.h", "ssd_host.h", "ssd_launch.h", "k_cb_tiles.h", "k4_chunk_out.h",
-           "kb_pass.h", "kb_pass_inst.h", "ssd_ops_device.h", "ssd_ops_internal.h", "ks_scan.h"]
+           "kb_pass.h", "kb_pass_inst.h", "ssd_ops_device.h", "ssd_ops_internal.h", "ssd_ops_host.h",
+           "ks_scan.h", "ka_attn.h", "kn_norm.h"]
 ARCH = "gfx950"
 
 

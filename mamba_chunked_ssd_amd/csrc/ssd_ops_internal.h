@@ -1,6 +1,7 @@
-// ssd_ops_internal.h -- interface between the host code of the short causal
-// convolution and the selective scan (ssd_ops.cpp) and their kernels.  Host
-// declarations only; not part of the ABI.
+// ssd_ops_internal.h -- interface between the host code of the layer operators
+// (ssd_ops.cpp: the short causal convolution and the selective scan;
+// ssd_mixer_ops.cpp: sliding-window attention and the RMS norm) and their
+// kernels.  Host declarations only; not part of the ABI.
 #pragma once
 
 #include <hip/hip_runtime_api.h>
@@ -124,5 +125,88 @@ inline ScanSums scan_sums(int64_t batch, int64_t seqlen, int64_t channels, int64
 hipError_t launch_scan_fwd(const ScanArgs &a, const ScanPlan &plan, hipStream_t stream);
 hipError_t launch_scan_bwd(const ScanArgs &a, const ScanPlan &plan, hipStream_t stream);
 hipError_t launch_scan_step(const ScanArgs &a, hipStream_t stream);
+
+// ---------------------------------------------------------------------------
+// Sliding-window attention with sinks (ka_attn_*.hip)
+// ---------------------------------------------------------------------------
+
+// Elements between batch entries, tokens and heads.
+struct HeadStrides {
+    int64_t batch, row, head;
+};
+
+struct AttnArgs {
+    int64_t batch;
+    int seqlen, heads, kvheads, headdim;
+    int window, sinks;  // window at most kAttnFar without a cache
+    float scale;
+    bool bf16;
+    HeadStrides qs, ks, vs, ys, dys;  // ys: y as an input of the backward pass
+    const void *q, *k, *v;
+    const int32_t *positions, *lengths;  // null: all 0; all seqlen
+    void *kc, *vc;                       // (batch, kvheads, sinks + window, headdim)
+    void *y;
+    float *lse;
+    // backward
+    const void *dy;
+    void *dq, *dk, *dv;
+    float *delta;     // (batch, heads, seqlen): sum_d dy y
+    float *partials;  // (batch, kvheads, AttnBwdPlan::parts, 2, AttnBwdPlan::rows, headdim)
+    // one token
+    float *part_y, *part_ml;  // (batch, heads, splits, headdim), (batch, heads, splits, 2)
+};
+constexpr int kAttnFar = 1 << 30;   // farther than any token sees
+constexpr int kAttnLast = 1 << 29;  // the largest position that a call begins at: tokens and what is added to them fit 32 bits
+
+// Keys of the backward pass's blocks and how the sinks' far queries (those that
+// see them as sinks only) are cut: chunks of `chunk` queries beside each other.
+struct AttnBwdPlan {
+    int sink_tiles;  // tiles of kAttnKeys keys that hold sinks with far queries
+    int chunk, nchunks;
+    int parts;       // partial sums of a sink tile's rows: its own block's, then the chunks'
+    int64_t rows;    // sink_tiles * kAttnKeys
+};
+constexpr int kAttnKeys = 128;
+AttnBwdPlan attn_bwd_plan(const AttnArgs &a);
+
+// Blocks that share the slots of one sequence and head of keys, and the slots of each.
+struct AttnStepPlan {
+    int splits, run;
+};
+AttnStepPlan attn_step_plan(const AttnArgs &a);
+
+hipError_t launch_attn_fwd(const AttnArgs &a, hipStream_t stream);
+hipError_t launch_attn_bwd(const AttnArgs &a, const AttnBwdPlan &plan, hipStream_t stream);
+hipError_t launch_attn_step(const AttnArgs &a, const AttnStepPlan &plan, hipStream_t stream);
+
+// ---------------------------------------------------------------------------
+// RMS norm with the residual's addition (kn_norm.hip)
+// ---------------------------------------------------------------------------
+
+enum class Stored { none, f32, bf16, e4m3 };
+
+struct NormArgs {
+    int64_t batch;
+    int seqlen, channels, scale_block;
+    float eps;
+    Stored x, res, y;  // x and dx; residual stream; y and dy
+    Strides xs, rs, dys, drs;
+    const int32_t *lengths;
+    const void *in, *residual;  // backward: dy, u
+    const float *weight;
+    void *out, *residual_out;  // backward: dx, d_residual
+    float *scales;
+    // backward
+    const void *dres;
+    float *dweight, *partials;  // (NormBwdPlan::parts, channels)
+};
+constexpr int kNormWaveRow = 4096, kNormBlockRow = 16384;  // channels that a wave's, a block's registers hold
+struct NormBwdPlan {
+    int parts;  // blocks, each of which leaves a row of partial sums
+};
+NormBwdPlan norm_bwd_plan(const NormArgs &a);
+
+hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t stream);
+hipError_t launch_norm_bwd(const NormArgs &a, const NormBwdPlan &plan, hipStream_t stream);
 
 }  // namespace ssd
