@@ -8,6 +8,10 @@
 // Two kernels, each of which owns what it writes, so that no sum depends on an
 // order of arrival: over the queries as the forward pass is laid out (dq, and
 // delta on the way), and over the keys (dk, dv), which forms the scores again.
+// A query that sees itself alone (token 0, or every one where window is 1 and
+// there are no sinks) has no gradient through its scores: dP - delta is 0 there,
+// which delta, a sum over the rounded y, would miss by its rounding.
+//
 // A key's block takes the queries that see it through the window.  Sinks are
 // seen by every later query of the sequence too: those are cut into chunks, a
 // block each, and their sums added by a third kernel.
@@ -108,6 +112,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnBwdIn<T> a) {
 #pragma unroll
     for (int db = 0; db < DB; ++db) o[db] = zero16();
     const int w0 = q0 + 32 * wave, w1 = min(w0 + 31, len - 1);
+    const bool alone = t == 0 || (a.window == 1 && a.sinks == 0);  // (such a row's tile is never whole)
     stage(0);
     for (int n = 0; n < ntiles; ++n) {
         lds_dma_wait();
@@ -137,7 +142,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnBwdIn<T> a) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const int j = j0 + 32 * kb + 8 * (r / 4) + 4 * h + r % 4;
-                    ds[r] = (n < nsink ? j < sunk : sees(t, j, a.window, a.sinks)) ? ds[r] : 0.f;
+                    ds[r] = (n < nsink ? j < sunk : sees(t, j, a.window, a.sinks)) && !alone ? ds[r] : 0.f;
                 }
             }
 #pragma unroll
@@ -182,7 +187,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnBwdIn<T> a) {
         for (int base = 0; base < seen; base += 64) {
             const int at = base + lane, j = at < far ? at : near + at - far;
             float ds = 0.f;
-            if (at < seen)
+            if (at < seen && seen > 1)
                 ds = fast_exp2(fmaf(row_dot<T, D>(qr, kh + (int64_t)j * a.ks.row), a.c, -rl)) *
                      (row_dot<T, D>(dr, vh + (int64_t)j * a.vs.row) - rd);
             for (int u = 0; u < min(64, seen - base); ++u) {
@@ -255,6 +260,7 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_kernel(const AttnBwdIn<T> a) 
         }
     };
 
+    const bool lone = a.window == 1 && a.sinks == 0;
     floatx16 dk[DB], dv[DB];
 #pragma unroll
     for (int db = 0; db < DB; ++db) dk[db] = dv[db] = zero16();
@@ -290,7 +296,7 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_kernel(const AttnBwdIn<T> a) 
                 const int t = t0 + 8 * (r / 4) + 4 * h + r % 4;
                 const bool on = t < hi && (sunk ? j < a.sinks && t - j >= a.window : j <= t && t - j < a.window);
                 p[r] = on ? p[r] : 0.f;
-                ds[r] = on ? ds[r] : 0.f;
+                ds[r] = on && t > 0 && !lone ? ds[r] : 0.f;
             }
         }
 #pragma unroll
@@ -349,7 +355,8 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_kernel(const AttnBwdIn<T> a) 
                 if (t < t_hi) {
                     const int64_t at = ((int64_t)b * a.heads + head) * a.L + t;
                     p = fast_exp2(fmaf(row_dot<T, D>(qb + (int64_t)t * a.qs.row + head * a.qs.head, kr), a.c, -a.lse[at] * kLog2e));
-                    ds = p * (row_dot<T, D>(db_ + (int64_t)t * a.dys.row + head * a.dys.head, vr) - a.delta[at]);
+                    if (t > 0 && !lone)
+                        ds = p * (row_dot<T, D>(db_ + (int64_t)t * a.dys.row + head * a.dys.head, vr) - a.delta[at]);
                 }
                 for (int u = 0; u < min(64, t_hi - base); ++u) {
                     const float pu = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(p), u));

@@ -172,6 +172,22 @@ def test_larger_sizes(case):
         assert off <= (4 * r if r else 2e-6), (name, off)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_queries_that_see_one_token_alone(dtype):
+    # their weight is 1 whatever the score: dq of token 0 is 0, and with a window of one and no sinks all of dq and dk
+    for d in (32, 64, 128):
+        s = inputs(2, 150, 4, 2, d, dtype, lengths=[150, 40], seed=12)
+        for w, n in ((1, 0), (1, 1), (30, 0)):
+            y, lse = ssd.window_attention_fwd(s["q"], s["k"], s["v"], w, n, lengths=s["lengths"], return_lse=True)
+            g = ssd.window_attention_bwd(s["q"], s["k"], s["v"], y, lse, s["dy"], w, n, lengths=s["lengths"])
+            assert not bool(g["dq"][:, 0].any())
+            if (w, n) == (1, 0):
+                assert not bool(g["dq"].any()) and not bool(g["dk"].any())
+                # (the exponential of a score less its own rounded product is 1 within E)
+                v, (e, _) = s["v"][0].repeat_interleave(2, 1).double(), spread(s, d ** -0.5, w, n, d)
+                assert bool(((y[0].double() - v).abs() <= (e + 2 * ROUND[dtype]) * v.abs()).all())
+
+
 def test_gradients_against_differences():
     # the oracle's own, in fp64: the error of central differences with h = 1e-5 is below 1e-8 here
     rng = np.random.default_rng(2)
