@@ -145,42 +145,45 @@ struct Tile {
             f.v[j] = *reinterpret_cast<const float *>(lds + at(r0 + 4 * h + (j & 3) + 8 * (j >> 2), c / 4) + 4 * (c & 3));
     }
 
-    // Rows 0 .. rows - 1 of a matrix copied in by THREADS threads without passing through registers; those behind
-    // them become 0.  stride: bytes between rows.
-    template <int THREADS>
-    __device__ static void copy(uint32_t lds, const unsigned char *base, int64_t stride, int rows) {
-        const i32x4 desc = buffer_desc(base, rows > 0 ? (uint32_t)((rows - 1) * stride + kRow) : 0u);
-        constexpr int kWavePieces = 64;
-        const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-#pragma unroll
-        for (int k = 0; k < (kBytes / 16 + THREADS - 1) / THREADS; ++k) {
-            const int first = (k * (THREADS / 64) + wave) * kWavePieces;
-            if (kBytes / 16 % THREADS != 0 && first >= kBytes / 16) break;  // (a tile of fewer pieces than threads)
-            const int n = first + (threadIdx.x & 63), r = n / kPieces, piece = (n % kPieces) ^ turn(r);
-            lds_dma_x4(desc, lds + first * 16, r * (int)stride + piece * 16);
-        }
-    }
-    // By one wave, rows that follow one another without a gap.
-    __device__ static void copy_wave(uint32_t lds, const unsigned char *base, int rows, int lane) {
-        const i32x4 desc = buffer_desc(base, rows > 0 ? (uint32_t)(rows * kRow) : 0u);
-#pragma unroll
-        for (int k = 0; k < kBytes / 1024; ++k) {
-            const int n = k * 64 + lane, r = n / kPieces, piece = (n % kPieces) ^ turn(r);
-            lds_dma_x4(desc, lds + k * 1024, r * kRow + piece * 16);
-        }
-    }
-    // The same through registers, row r from row(r), null: 0.
+    // Filled through registers, row r from row(r), null: 0.
     template <int THREADS, typename F>
     __device__ static void gather(unsigned char *lds, F &&row) {
         static_assert(kBytes / 16 % THREADS == 0, "every thread takes as many pieces");
 #pragma unroll 2
         for (int k = 0; k < kBytes / 16 / THREADS; ++k) {
-            const int n = k * THREADS + threadIdx.x, r = n / kPieces, piece = n % kPieces;
+            const int n = k * THREADS + (int)threadIdx.x % THREADS, r = n / kPieces, piece = n % kPieces;
             const T *p = row(r);
             u32x4 v = {0, 0, 0, 0};
             if (p != nullptr) v = *reinterpret_cast<const u32x4 *>(p + piece * kPer);
             *reinterpret_cast<u32x4 *>(lds + at(r, piece)) = v;
         }
+    }
+};
+
+// Copies into a Tile by WAVES waves, asynchronous and not through registers.
+// The offsets of a lane's pieces are the same for every tile of a matrix.
+template <typename Tl, int WAVES>
+struct Copier {
+    static constexpr int kAll = Tl::kBytes / 1024;  // pieces of a wave's instruction
+    static constexpr int kEach = (kAll + WAVES - 1) / WAVES;
+    int off[kEach];
+    uint32_t stride, to;
+    // stride: bytes between rows; wave: this one's number among the WAVES
+    __device__ void init(int64_t bytes, int wave, int lane) {
+        stride = (uint32_t)bytes;
+        to = (uint32_t)wave * 1024;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int n = (k * WAVES + wave) * 64 + lane, r = n / Tl::kPieces;
+            off[k] = r * (int)stride + ((n % Tl::kPieces) ^ Tl::turn(r)) * 16;
+        }
+    }
+    // Rows 0 .. rows - 1 from base on; those behind them become 0.
+    __device__ void copy(uint32_t lds, const void *base, int rows) const {
+        const i32x4 desc = buffer_desc(base, rows > 0 ? (uint32_t)(rows - 1) * stride + Tl::kRow : 0u);
+#pragma unroll
+        for (int k = 0; k < kEach; ++k)
+            if (kAll % WAVES == 0 || to + k * WAVES * 1024 < Tl::kBytes) lds_dma_x4(desc, lds + to + k * WAVES * 1024, off[k]);
     }
 };
 
@@ -190,10 +193,148 @@ __device__ __forceinline__ void lds_dma_wait_but() {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// Does token t see token j?
-__device__ __forceinline__ bool sees(int t, int j, int window, int sinks) {
-    return j <= t && (t - j < window || j < sinks);
-}
+// The mask of a block of keys whose first is token j0, for the lane's query t:
+// register r of block kb is key j0 + 4 h + place(kb, r), which t sees if seen().
+// Without branches: three comparisons, and the rest on scalar registers.
+__device__ constexpr int place(int kb, int r) { return 32 * kb + 8 * (r / 4) + r % 4; }
+struct Mask {
+    int last, before, sunk;
+    __device__ Mask(int t, int j0, int h, int window, int sinks)
+        : last(t - j0 - 4 * h), before(last - window), sunk(sinks - j0 - 4 * h) {}
+    __device__ bool seen(int at) const { return (at <= last) & ((at > before) | (at < sunk)); }
+};
+
+// Which tiles of KT keys a run of queries from token t0 to t1 takes: those of
+// the window from token `from`, on a grid that `first` lies on, and before them
+// the sinks below `from`.
+template <int KT>
+struct Walk {
+    int from, lo, sunk, nsink, ntiles;
+    __device__ Walk(int t0, int t1, int first, int window, int sinks) {
+        lo = max(t0 - window + 1, 0);
+        from = lo >= first ? first + (lo - first) / KT * KT : first - (first - lo + KT - 1) / KT * KT;
+        sunk = min(sinks, max(from, 0));
+        nsink = (sunk + KT - 1) / KT;
+        ntiles = nsink + (t1 - from) / KT + 1;
+    }
+    __device__ int start(int n) const { return n < nsink ? n * KT : from + (n - nsink) * KT; }
+    // Does a query of this run see a token of tile n that the cache may hold?  (No older one is there.)
+    __device__ bool held(int n, int j, int sinks, int end) const {
+        return n < nsink ? j < sunk : j >= 0 && j < end && (j >= lo || j < sinks);
+    }
+};
+
+constexpr float kInf = __builtin_inff();
+
+// The running softmax of a lane's query (column) and its sum of values, o^T =
+// V^T P^T: m the reference of the exponentials and l this lane's half of their
+// sum, in units of log(2).
+template <typename T, int D>
+struct Running {
+    static constexpr int DB = D / 32;
+    float m = -kInf, l = 0.f;
+    floatx16 o[DB];
+    __device__ void init() {
+#pragma unroll
+        for (int db = 0; db < DB; ++db) o[db] = zero16();
+    }
+    __device__ float ref() const { return m == -kInf ? 0.f : m; }
+    // Scores of 32 KB keys (-infinity: not seen), whose values are rows r0 .. of the tile at v.
+    template <typename Tl, int KB>
+    __device__ void take(const floatx16 (&s)[KB], float c, const unsigned char *v, int r0, int lane) {
+        float top = s[0][0];
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, s[kb][r]);
+        top = fmaxf(top, other_half(top)) * c;
+        // The reference follows the maximum only where it has fallen 2^8 behind: p stays below 2^8, which costs no
+        // precision, and most tiles rescale nothing.
+        if (__any(top > m + 8.f)) {
+            const float next = fmaxf(m, top);
+            const float by = next == -kInf ? 1.f : fast_exp2(m - next);
+            l *= by;
+#pragma unroll
+            for (int db = 0; db < DB; ++db)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[db][r] *= by;
+            m = next;
+        }
+        const float from = ref();
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+            float p[16];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                p[r] = fast_exp2(fmaf(s[kb][r], c, -from));
+                l += p[r];
+            }
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                Frag<T> pf;
+                to_frag(p, ks, pf);
+#pragma unroll
+                for (int db = 0; db < DB; ++db) {
+                    Frag<T> vf;
+                    Tl::across(v, r0 + 32 * kb + 16 * ks, 32 * db, lane, vf);
+                    o[db] = mma(vf, pf, o[db]);
+                }
+            }
+        }
+    }
+};
+
+// Results of NW waves over the same 32 columns joined through LDS: (wave,
+// column, m and l), then (wave, column, D values).  write(column, element,
+// value, m, l) gets the joined sums, not yet divided, of the first `columns`.
+template <typename T, int D, int NW>
+struct Join {
+    static constexpr int kPad = D + 4, kBytes = NW * 32 * (2 + kPad) * (int)sizeof(float);
+    template <typename F>
+    __device__ static void run(unsigned char *lds, const Running<T, D> &a, int wave, int lane, int columns, F &&write) {
+        float *ml = reinterpret_cast<float *>(lds), *os = ml + NW * 32 * 2;
+        const int col = lane & 31, h = lane >> 5;
+        const float l = both_halves(a.l);
+        __syncthreads();
+        if (col < columns) {
+            if (h == 0) {
+                ml[(wave * 32 + col) * 2] = a.m;
+                ml[(wave * 32 + col) * 2 + 1] = l;
+            }
+            float *row = os + (wave * 32 + col) * kPad;
+#pragma unroll
+            for (int db = 0; db < D / 32; ++db)
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    *reinterpret_cast<floatx4 *>(row + 32 * db + 8 * g + 4 * h) =
+                        floatx4{a.o[db][4 * g], a.o[db][4 * g + 1], a.o[db][4 * g + 2], a.o[db][4 * g + 3]};
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < columns * D; e += 64 * NW) {
+            const int c = e / D, d = e % D;
+            float most = -kInf, sum = 0.f, y = 0.f;
+#pragma unroll
+            for (int k = 0; k < NW; ++k) most = fmaxf(most, ml[(k * 32 + c) * 2]);
+            const float from = most == -kInf ? 0.f : most;
+#pragma unroll
+            for (int k = 0; k < NW; ++k) {
+                const float w = fast_exp2(ml[(k * 32 + c) * 2] - from);
+                sum = fmaf(ml[(k * 32 + c) * 2 + 1], w, sum);
+                y = fmaf(os[(k * 32 + c) * kPad + d], w, y);
+            }
+            write(c, d, y, most, sum);
+        }
+    }
+};
+
+// A wave's two stages of 32 keys and values; four waves to a block where they
+// fit its 128 KB (fp32 rows of 128 elements: two).
+template <typename T, int D>
+struct WaveLds {
+    static constexpr int kStage = 2 * Tile<T, D, 32>::kBytes, kWaves = 8 * kStage <= 131072 ? 4 : 2;
+    static constexpr int kResults = Join<T, D, kWaves>::kBytes, kCopies = kWaves * 2 * kStage;
+    static constexpr int kBytes = kCopies > kResults ? kCopies : kResults;
+};
 
 // A result whose columns are rows of memory: lane l's column is row l % 32, its
 // values the elements 32 b + 8 (r / 4) + 4 (l / 32) + r % 4 of it.  Lanes l and l

@@ -30,11 +30,12 @@ struct AttnBwdIn {
     const float *lse;
     const int32_t *lengths;
     T *dq, *dk, *dv;
-    float *delta, *partials;
+    float2 *stats;  // (batch, heads, seqlen): lse in units of log(2), delta
+    float *partials;
     HeadStrides qs, ks, vs, ys, dys;
-    int L, heads, kvheads, tiles;
+    int L, heads, kvheads;
     int window, sinks;
-    int sink_tiles, chunk, nchunks;
+    int sink_tiles, chunk, nchunks;  // of kSinkKeys keys; queries
     int64_t rows;  // of partial sums
     float scale, c;
 };
@@ -51,17 +52,18 @@ __device__ __forceinline__ float row_dot(const T *a, const T *b) {
 }
 
 template <typename T, int D>
-__global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnBwdIn<T> a) {
+__global__ __launch_bounds__(256, (D * sizeof(T) <= 256 ? 2 : 1)) void attn_dq_kernel(const AttnBwdIn<T> a) {
     constexpr int KT = sizeof(T) == 2 ? 64 : 32, KB = KT / 32, NS = D / 16, DB = D / 32;
     typedef Tile<T, D, KT> Tl;
     extern __shared__ __align__(16) unsigned char lds[];
 
     const int group = a.heads / a.kvheads;
+    const int tiles = (a.L + kQueries - 1) / kQueries;
     int n = xcd_remap((int)blockIdx.x, (int)gridDim.x);
     const int gh = n % group;
     n /= group;
-    const int q0 = (a.tiles - 1 - n % a.tiles) * kQueries;
-    n /= a.tiles;
+    const int q0 = (tiles - 1 - n % tiles) * kQueries;
+    n /= tiles;
     const int kvh = n % a.kvheads, b = n / a.kvheads, head = kvh * group + gh;
     const int len = length_of(a.lengths, b, a.L);
     const int lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
@@ -93,19 +95,19 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnBwdIn<T> a) {
         delta = dot_frag(df[s], yf, delta);
     }
     delta = both_halves(delta);
-    if (live && h == 0) a.delta[stat] = delta;
     const float lse = live ? a.lse[stat] * kLog2e : 0.f;
+    if (live && h == 0) a.stats[stat] = float2{lse, delta};
 
-    const int t1 = min(q0 + kQueries, len) - 1;
-    const int from = max(q0 - a.window + 1, 0) / KT * KT, sunk = min(a.sinks, from);
-    const int nsink = (sunk + KT - 1) / KT, ntiles = nsink + (t1 - from) / KT + 1;
+    const Walk<KT> walk(q0, min(q0 + kQueries, len) - 1, 0, a.window, a.sinks);
     const T *kh = a.k + (int64_t)b * a.ks.batch + kvh * a.ks.head, *vh = a.v + (int64_t)b * a.vs.batch + kvh * a.vs.head;
-    const auto start_of = [&](int n) { return n < nsink ? n * KT : from + (n - nsink) * KT; };
+    Copier<Tl, 4> kcopy, vcopy;
+    kcopy.init(a.ks.row * (int64_t)sizeof(T), wave, lane);
+    vcopy.init(a.vs.row * (int64_t)sizeof(T), wave, lane);
     const auto stage = [&](int n) {
-        const int j0 = start_of(n), rows = min((n < nsink ? sunk : len) - j0, KT);
+        const int j0 = walk.start(n), rows = min((n < walk.nsink ? walk.sunk : len) - j0, KT);
         const uint32_t kl = lds_addr(lds + (n & 1) * 2 * Tl::kBytes);
-        Tl::template copy<256>(kl, (const unsigned char *)(kh + (int64_t)j0 * a.ks.row), a.ks.row * (int64_t)sizeof(T), rows);
-        Tl::template copy<256>(kl + Tl::kBytes, (const unsigned char *)(vh + (int64_t)j0 * a.vs.row), a.vs.row * (int64_t)sizeof(T), rows);
+        kcopy.copy(kl, kh + (int64_t)j0 * a.ks.row, rows);
+        vcopy.copy(kl + Tl::kBytes, vh + (int64_t)j0 * a.vs.row, rows);
     };
 
     floatx16 o[DB];
@@ -113,17 +115,18 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnBwdIn<T> a) {
     for (int db = 0; db < DB; ++db) o[db] = zero16();
     const int w0 = q0 + 32 * wave, w1 = min(w0 + 31, len - 1);
     const bool alone = t == 0 || (a.window == 1 && a.sinks == 0);  // (such a row's tile is never whole)
-    stage(0);
-    for (int n = 0; n < ntiles; ++n) {
-        lds_dma_wait();
-        __syncthreads();
-        if (n + 1 < ntiles) stage(n + 1);
-        const int j0 = start_of(n);
-        if (w0 >= len || j0 > w1) continue;
-        if (n >= nsink && j0 + KT <= w0 - a.window + 1 && j0 >= a.sinks) continue;
+    for (int n = -1; n < walk.ntiles; ++n) {
+        if (n >= 0) {
+            lds_dma_wait();
+            __syncthreads();
+        }
+        if (n + 1 < walk.ntiles) stage(n + 1);
+        const int j0 = walk.start(n);
+        if (n < 0 || w0 >= len || j0 > w1) continue;
+        if (n >= walk.nsink && j0 + KT <= w0 - a.window + 1 && j0 >= a.sinks) continue;
         const unsigned char *kl = lds + (n & 1) * 2 * Tl::kBytes, *vl = kl + Tl::kBytes;
-        const bool whole = n < nsink ? j0 + KT <= sunk
-                                     : j0 + KT - 1 <= w0 && (w0 + 31 - j0 < a.window || j0 + KT <= a.sinks);
+        const bool whole = n < walk.nsink ? j0 + KT <= walk.sunk
+                                          : j0 + KT - 1 <= w0 && (w0 + 31 - j0 < a.window || j0 + KT <= a.sinks);
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
             floatx16 s = zero16(), g = zero16();
@@ -139,11 +142,10 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnBwdIn<T> a) {
 #pragma unroll
             for (int r = 0; r < 16; ++r) ds[r] = fast_exp2(fmaf(s[r], a.c, -lse)) * (g[r] - delta);
             if (!whole) {
+                // (a tile of sinks: all of them, up to its end)
+                const Mask mask(n < walk.nsink ? walk.sunk - 1 : t, j0, h, n < walk.nsink ? kAttnFar : a.window, a.sinks);
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int j = j0 + 32 * kb + 8 * (r / 4) + 4 * h + r % 4;
-                    ds[r] = (n < nsink ? j < sunk : sees(t, j, a.window, a.sinks)) && !alone ? ds[r] : 0.f;
-                }
+                for (int r = 0; r < 16; ++r) ds[r] = (mask.seen(place(kb, r)) & !alone) ? ds[r] : 0.f;
             }
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
@@ -205,37 +207,43 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnBwdIn<T> a) {
     }
 }
 
-// 128 keys, 32 a wave in registers (columns of the products S = Q K^T, dP = dY
-// V^T), against tiles of 32 queries; dv^T += dY^T P and dk^T += Q^T dS take the
-// same tiles across.
-template <typename T, int D>
-__global__ __launch_bounds__(256, 1) void attn_dkv_kernel(const AttnBwdIn<T> a) {
-    constexpr int NS = D / 16, DB = D / 32;
-    typedef Tile<T, D, 32> Tl;
-    extern __shared__ __align__(16) unsigned char lds[];  // (2 stages, queries and dy), then (2 stages, lse and delta)
-    float *stats = reinterpret_cast<float *>(lds + 4 * Tl::kBytes);
+// KW waves of 32 keys each, which they hold in registers (columns of the
+// products S = Q K^T, dP = dY V^T), G times over: against tiles of 32 G QB
+// queries, of which each group of waves takes its own blocks of 32, one tile on
+// the way while another is in use.  dv^T += dY^T P and dk^T += Q^T dS take the
+// same tiles across.  The groups' sums are added at the end, in order.
+//
+// SINKS: the queries are a chunk of those that see the block's keys as sinks
+// alone; else all those that see them through the window.
+template <typename T, int D, int KW, int G, int QB>
+struct KeyLds {
+    typedef Tile<T, D, 32 * G * QB> Tl;
+    static constexpr int kStats = Tl::kBytes * 2, kStage = kStats + 32 * G * QB * (int)sizeof(float2);
+    static constexpr int kSums = G > 1 ? KW * D * 256 : 0;  // of one group
+    static constexpr int kBytes = 2 * kStage > kSums ? 2 * kStage : kSums;
+};
 
-    const int group = a.heads / a.kvheads, ntiles = (a.L + kAttnKeys - 1) / kAttnKeys;
-    const int items = ntiles + a.sink_tiles * a.nchunks;
+template <typename T, int D, int KW, int G, int QB, bool SINKS>
+__global__ __launch_bounds__((64 * KW * G), 1) void attn_dkv_kernel(const AttnBwdIn<T> a) {
+    constexpr int NS = D / 16, DB = D / 32, NW = KW * G, QT = 32 * G * QB;
+    typedef KeyLds<T, D, KW, G, QB> Lds;
+    typedef typename Lds::Tl Tl;
+    extern __shared__ __align__(16) unsigned char lds[];  // (2 stages: queries, dy, stats); then a group's sums
+
+    const int group = a.heads / a.kvheads, tiles = SINKS ? a.sink_tiles * a.nchunks : (a.L + 32 * KW - 1) / (32 * KW);
     int n = xcd_remap((int)blockIdx.x, (int)gridDim.x);
-    const int item = n % items;
-    n /= items;
+    const int item = n % tiles;
+    n /= tiles;
     const int kvh = n % a.kvheads, b = n / a.kvheads;
     const int len = length_of(a.lengths, b, a.L);
-    // a tile's queries through the window, or a chunk of those that see its sinks from farther
-    const bool sunk = item >= ntiles;
-    const int tile = sunk ? (item - ntiles) / a.nchunks : item, part = sunk ? 1 + (item - ntiles) % a.nchunks : 0;
-    const int j0 = tile * kAttnKeys;
-    int lo = j0, hi = (int)min((int64_t)len, (int64_t)j0 + kAttnKeys - 1 + a.window);
-    if (sunk) {
-        lo = max(a.window + (part - 1) * a.chunk, a.window + j0);
-        hi = min(len, a.window + part * a.chunk);
-    }
-    const int nq = hi > lo ? (hi - lo + 31) / 32 : 0, turns = nq * group;
+    const int part = SINKS ? 1 + item % a.nchunks : 0, j0 = (SINKS ? item / a.nchunks : item) * 32 * KW;
+    const int lo = SINKS ? max(a.window + (part - 1) * a.chunk, a.window + j0) : j0;
+    const int hi = SINKS ? min(len, a.window + part * a.chunk) : (int)min((int64_t)len, (int64_t)j0 + 32 * KW - 1 + a.window);
+    const int turns = hi > lo ? (hi - lo + QT - 1) / QT * group : 0;
 
     const int lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int w0 = j0 + 32 * wave, j = w0 + col;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), part_of = wave / KW;  // which group
+    const int w0 = j0 + 32 * (wave % KW), j = w0 + col;
     const bool live = j < len;
     const T *kh = a.k + (int64_t)b * a.ks.batch + kvh * a.ks.head, *vh = a.v + (int64_t)b * a.vs.batch + kvh * a.vs.head;
     const T *qb = a.q + (int64_t)b * a.qs.batch, *db_ = a.dy + (int64_t)b * a.dys.batch;
@@ -246,17 +254,23 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_kernel(const AttnBwdIn<T> a) 
         load_frag(vf[s], vh + (int64_t)j * a.vs.row + 16 * s + 8 * h, live);
     }
 
-    const auto stage = [&](int n) {
-        const int head = kvh * group + n / nq, t0 = lo + n % nq * 32, rows = min(hi - t0, 32);
-        const uint32_t ql = lds_addr(lds + (n & 1) * 2 * Tl::kBytes);
-        Tl::template copy<256>(ql, (const unsigned char *)(qb + (int64_t)t0 * a.qs.row + head * a.qs.head), a.qs.row * (int64_t)sizeof(T), rows);
-        Tl::template copy<256>(ql + Tl::kBytes, (const unsigned char *)(db_ + (int64_t)t0 * a.dys.row + head * a.dys.head),
-                               a.dys.row * (int64_t)sizeof(T), rows);
-        if (threadIdx.x < 64) {
-            const int64_t at = ((int64_t)b * a.heads + head) * a.L + t0 + col;
-            float s = 0.f;
-            if (col < rows) s = h == 0 ? a.lse[at] * kLog2e : a.delta[at];
-            stats[(n & 1) * 64 + h * 32 + col] = s;
+    Copier<Tl, NW> qcopy, dcopy;
+    qcopy.init(a.qs.row * (int64_t)sizeof(T), wave, lane);
+    dcopy.init(a.dys.row * (int64_t)sizeof(T), wave, lane);
+    int head = kvh * group, next = lo;  // of the tile to stage
+    const auto stage = [&](int buf) {
+        const int rows = min(hi - next, QT);
+        const uint32_t to = lds_addr(lds + buf * Lds::kStage);
+        qcopy.copy(to, qb + (int64_t)next * a.qs.row + head * a.qs.head, rows);
+        dcopy.copy(to + Tl::kBytes, db_ + (int64_t)next * a.dys.row + head * a.dys.head, rows);
+        if (wave < QT / 32) {
+            const i32x4 desc = buffer_desc(a.stats + ((int64_t)b * a.heads + head) * a.L + next, (uint32_t)rows * (uint32_t)sizeof(float2));
+            lds_dma_x1(desc, to + Lds::kStats + 256 * wave, 256 * wave + 4 * lane);
+        }
+        next += QT;
+        if (next >= hi) {
+            next = lo;
+            ++head;
         }
     };
 
@@ -264,58 +278,102 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_kernel(const AttnBwdIn<T> a) 
     floatx16 dk[DB], dv[DB];
 #pragma unroll
     for (int db = 0; db < DB; ++db) dk[db] = dv[db] = zero16();
-    if (turns > 0) stage(0);
-    for (int n = 0; n < turns; ++n) {
-        lds_dma_wait();
-        __syncthreads();
-        if (n + 1 < turns) stage(n + 1);
-        const int t0 = lo + n % nq * 32;
-        if (sunk ? w0 >= a.sinks || t0 + 31 - w0 < a.window : t0 + 31 < w0 || t0 - w0 - 31 >= a.window) continue;
-        const bool whole = sunk ? w0 + 32 <= a.sinks && t0 - w0 - 31 >= 0 && t0 - w0 - 31 >= a.window
-                                : t0 >= w0 + 31 && t0 + 31 - w0 < a.window;
-        const unsigned char *ql = lds + (n & 1) * 2 * Tl::kBytes, *dl = ql + Tl::kBytes;
-        floatx16 s = zero16(), g = zero16();
-#pragma unroll
-        for (int ks = 0; ks < NS; ++ks) {
-            Frag<T> f;
-            Tl::down(ql, 0, ks, lane, f);
-            s = mma(f, kf[ks], s);
-            Tl::down(dl, 0, ks, lane, f);
-            g = mma(f, vf[ks], g);
+    int tile = lo;
+    for (int n = -1; n < turns; ++n) {
+        if (n >= 0) {
+            lds_dma_wait();
+            __syncthreads();
         }
-        float p[16], ds[16];
+        if (n + 1 < turns) stage((n + 1) & 1);
+        if (n < 0) continue;
+        const unsigned char *ql = lds + (n & 1) * Lds::kStage, *dl = ql + Tl::kBytes;
+        const float2 *stats = reinterpret_cast<const float2 *>(ql + Lds::kStats);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int row = 8 * (r / 4) + 4 * h + r % 4;
-            p[r] = fast_exp2(fmaf(s[r], a.c, -stats[(n & 1) * 64 + row]));
-            ds[r] = p[r] * (g[r] - stats[(n & 1) * 64 + 32 + row]);
-        }
-        if (!whole) {
+        for (int qi = 0; qi < QB; ++qi) {
+            const int q0 = 32 * (part_of * QB + qi), t0 = tile + q0;
+            if (SINKS ? w0 >= a.sinks || t0 + 31 - w0 < a.window : t0 + 31 < w0 || t0 - w0 - 31 >= a.window) continue;
+            if (t0 >= hi) continue;
+            const bool whole = SINKS ? w0 + 32 <= a.sinks && t0 - w0 - 31 >= a.window : t0 >= w0 + 31 && t0 + 31 - w0 < a.window;
+            floatx16 s = zero16(), g = zero16();
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int t = t0 + 8 * (r / 4) + 4 * h + r % 4;
-                const bool on = t < hi && (sunk ? j < a.sinks && t - j >= a.window : j <= t && t - j < a.window);
-                p[r] = on ? p[r] : 0.f;
-                ds[r] = on && t > 0 && !lone ? ds[r] : 0.f;
-            }
-        }
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            Frag<T> pf, sf;
-            to_frag(p, ks, pf);
-            to_frag(ds, ks, sf);
-#pragma unroll
-            for (int db = 0; db < DB; ++db) {
+            for (int ks = 0; ks < NS; ++ks) {
                 Frag<T> f;
-                Tl::across(dl, 16 * ks, 32 * db, lane, f);
-                dv[db] = mma(f, pf, dv[db]);
-                Tl::across(ql, 16 * ks, 32 * db, lane, f);
-                dk[db] = mma(f, sf, dk[db]);
+                Tl::down(ql, q0, ks, lane, f);
+                s = mma(f, kf[ks], s);
+                Tl::down(dl, q0, ks, lane, f);
+                g = mma(f, vf[ks], g);
             }
+            float p[16], ds[16];
+#pragma unroll
+            for (int r = 0; r < 16; r += 2) {
+                const floatx4 st = *reinterpret_cast<const floatx4 *>(stats + q0 + place(0, r) + 4 * h);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    p[r + e] = fast_exp2(fmaf(s[r + e], a.c, -st[2 * e]));
+                    ds[r + e] = p[r + e] * (g[r + e] - st[2 * e + 1]);
+                }
+            }
+            if (!whole) {
+                // rows are queries here: t - j within a window of the key's
+                const int back = t0 + 4 * h - j, left = hi - t0 - 4 * h, sunk = j < a.sinks ? 0 : kAttnFar;
+                const int first = t0 == 0 ? -4 * h : -1;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int at = place(0, r), d = at + back;
+                    const bool on = SINKS ? (at < left) & (d >= a.window + sunk) : (at < left) & (d >= 0) & (d < a.window);
+                    p[r] = on ? p[r] : 0.f;
+                    ds[r] = (on & (at != first) & !lone) ? ds[r] : 0.f;
+                }
+            }
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                Frag<T> pf, sf;
+                to_frag(p, ks, pf);
+                to_frag(ds, ks, sf);
+#pragma unroll
+                for (int db = 0; db < DB; ++db) {
+                    Frag<T> f;
+                    Tl::across(dl, q0 + 16 * ks, 32 * db, lane, f);
+                    dv[db] = mma(f, pf, dv[db]);
+                    Tl::across(ql, q0 + 16 * ks, 32 * db, lane, f);
+                    dk[db] = mma(f, sf, dk[db]);
+                }
+            }
+        }
+        tile += QT;
+        if (tile >= hi) tile = lo;
+    }
+#pragma unroll
+    for (int of = 1; of < G; ++of) {
+        floatx4 *sums = reinterpret_cast<floatx4 *>(lds) + (wave % KW) * D * 16 + lane;  // (register quad, lane)
+        __syncthreads();
+        if (part_of == of) {
+#pragma unroll
+            for (int db = 0; db < DB; ++db)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    sums[(db * 8 + i) * 64] = floatx4{dk[db][4 * i], dk[db][4 * i + 1], dk[db][4 * i + 2], dk[db][4 * i + 3]};
+                    sums[(db * 8 + 4 + i) * 64] = floatx4{dv[db][4 * i], dv[db][4 * i + 1], dv[db][4 * i + 2], dv[db][4 * i + 3]};
+                }
+        }
+        __syncthreads();
+        if (part_of == 0) {
+#pragma unroll
+            for (int db = 0; db < DB; ++db)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const floatx4 x = sums[(db * 8 + i) * 64], y = sums[(db * 8 + 4 + i) * 64];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        dk[db][4 * i + e] += x[e];
+                        dv[db][4 * i + e] += y[e];
+                    }
+                }
         }
     }
+    if (part_of != 0 || w0 >= a.L) return;  // (no barrier follows)
 
-    const bool partial = tile < a.sink_tiles;
+    const bool partial = SINKS || w0 < a.rows;
     const int64_t dense = ((int64_t)b * a.L + j) * a.kvheads * D + (int64_t)kvh * D;
     float *pk = a.partials + ((((int64_t)b * a.kvheads + kvh) * (1 + a.nchunks) + part) * 2 * a.rows + j) * D;
     float *pv = pk + a.rows * D;
@@ -345,29 +403,27 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_kernel(const AttnBwdIn<T> a) 
         again &= again - 1;
         const int jj = w0 + c;
         const T *kr = kh + (int64_t)jj * a.ks.row, *vr = vh + (int64_t)jj * a.vs.row;
-        const int t_lo = sunk ? max(lo, jj + a.window) : jj, t_hi = sunk ? (jj < a.sinks ? hi : t_lo) : (int)min((int64_t)hi, (int64_t)jj + a.window);
+        const int t_lo = SINKS ? max(lo, jj + a.window) : jj, t_hi = SINKS ? (jj < a.sinks ? hi : t_lo) : (int)min((int64_t)hi, (int64_t)jj + a.window);
         float acc[2][(D + 63) / 64] = {};
         for (int gh = 0; gh < group; ++gh) {
-            const int head = kvh * group + gh;
+            const int of = kvh * group + gh;
+            const T *qr = qb + of * a.qs.head, *dr = db_ + of * a.dys.head;
             for (int base = t_lo; base < t_hi; base += 64) {
                 const int t = base + lane;
                 float p = 0.f, ds = 0.f;
                 if (t < t_hi) {
-                    const int64_t at = ((int64_t)b * a.heads + head) * a.L + t;
-                    p = fast_exp2(fmaf(row_dot<T, D>(qb + (int64_t)t * a.qs.row + head * a.qs.head, kr), a.c, -a.lse[at] * kLog2e));
-                    if (t > 0 && !lone)
-                        ds = p * (row_dot<T, D>(db_ + (int64_t)t * a.dys.row + head * a.dys.head, vr) - a.delta[at]);
+                    const float2 st = a.stats[((int64_t)b * a.heads + of) * a.L + t];
+                    p = fast_exp2(fmaf(row_dot<T, D>(qr + (int64_t)t * a.qs.row, kr), a.c, -st.x));
+                    if (t > 0 && !lone) ds = p * (row_dot<T, D>(dr + (int64_t)t * a.dys.row, vr) - st.y);
                 }
                 for (int u = 0; u < min(64, t_hi - base); ++u) {
                     const float pu = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(p), u));
                     const float su = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ds), u));
-                    const T *qr = qb + (int64_t)(base + u) * a.qs.row + head * a.qs.head;
-                    const T *dr = db_ + (int64_t)(base + u) * a.dys.row + head * a.dys.head;
 #pragma unroll
                     for (int k = 0; k < (D + 63) / 64; ++k)
                         if (lane + 64 * k < D) {
-                            acc[0][k] = fmaf(su, widen(qr[lane + 64 * k]), acc[0][k]);
-                            acc[1][k] = fmaf(pu, widen(dr[lane + 64 * k]), acc[1][k]);
+                            acc[0][k] = fmaf(su, widen(qr[(int64_t)(base + u) * a.qs.row + lane + 64 * k]), acc[0][k]);
+                            acc[1][k] = fmaf(pu, widen(dr[(int64_t)(base + u) * a.dys.row + lane + 64 * k]), acc[1][k]);
                         }
                 }
             }
@@ -407,18 +463,31 @@ __global__ __launch_bounds__(256) void attn_sinks_kernel(const AttnBwdIn<T> a, i
     }
 }
 
+template <typename T, int D, int KW, int G, int QB, bool SINKS>
+hipError_t attn_dkv_launch(const AttnBwdIn<T> &in, int64_t blocks, hipStream_t stream) {
+    constexpr int kLds = KeyLds<T, D, KW, G, QB>::kBytes;
+    const hipError_t e = allow_lds<attn_dkv_kernel<T, D, KW, G, QB, SINKS>>(kLds);
+    if (e != hipSuccess) return e;
+    attn_dkv_kernel<T, D, KW, G, QB, SINKS><<<dim3((uint32_t)blocks), dim3(64 * KW * G), kLds, stream>>>(in);
+    return hipGetLastError();
+}
+
 template <typename T, int D>
 hipError_t attn_bwd_sized(const AttnBwdIn<T> &in, int64_t batch, hipStream_t stream) {
-    constexpr int kLdsQ = 2 * 2 * Tile<T, D, sizeof(T) == 2 ? 64 : 32>::kBytes, kLdsK = 2 * 2 * Tile<T, D, 32>::kBytes + 2 * 2 * 32 * (int)sizeof(float);
-    hipError_t e = allow_lds<attn_dq_kernel<T, D>>(kLdsQ);
-    if (e == hipSuccess) e = allow_lds<attn_dkv_kernel<T, D>>(kLdsK);
+    constexpr int kLds = 2 * 2 * Tile<T, D, sizeof(T) == 2 ? 64 : 32>::kBytes;
+    // two groups of waves where a wave's registers (keys, values, their gradients) leave room for two on a SIMD
+    constexpr bool kSmall = D * sizeof(T) <= 128;
+    constexpr int G = kSmall ? 2 : 1, QB = sizeof(T) == 2 && !kSmall ? 2 : 1, GS = D * sizeof(T) <= 256 ? 4 : 2;
+    hipError_t e = allow_lds<attn_dq_kernel<T, D>>(kLds);
     if (e != hipSuccess) return e;
-    attn_dq_kernel<T, D><<<dim3((uint32_t)(batch * in.heads * in.tiles)), dim3(256), kLdsQ, stream>>>(in);
+    attn_dq_kernel<T, D><<<dim3((uint32_t)(batch * in.heads * ((in.L + kQueries - 1) / kQueries))), dim3(256), kLds, stream>>>(in);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    const int64_t items = (in.L + kAttnKeys - 1) / kAttnKeys + (int64_t)in.sink_tiles * in.nchunks;
-    attn_dkv_kernel<T, D><<<dim3((uint32_t)(batch * in.kvheads * items)), dim3(256), kLdsK, stream>>>(in);
-    if ((e = hipGetLastError()) != hipSuccess || in.sink_tiles == 0) return e;
-    const int64_t heads = batch * in.kvheads, n = 2 * heads * std::min<int64_t>(in.L, in.rows) * D;
+    const int64_t heads = batch * in.kvheads;
+    e = attn_dkv_launch<T, D, 4, G, QB, false>(in, heads * ((in.L + 127) / 128), stream);
+    if (e != hipSuccess || in.sink_tiles == 0) return e;
+    e = attn_dkv_launch<T, D, 1, GS, 1, true>(in, heads * in.sink_tiles * in.nchunks, stream);
+    if (e != hipSuccess) return e;
+    const int64_t n = 2 * heads * std::min<int64_t>(in.L, in.rows) * D;
     attn_sinks_kernel<T><<<dim3((uint32_t)std::min<int64_t>((n + 255) / 256, 1 << 16)), dim3(256), 0, stream>>>(in, heads, D);
     return hipGetLastError();
 }
@@ -427,8 +496,8 @@ template <typename T>
 hipError_t attn_bwd_typed(const AttnArgs &a, const AttnBwdPlan &p, hipStream_t stream) {
     const AttnBwdIn<T> in{static_cast<const T *>(a.q), static_cast<const T *>(a.k), static_cast<const T *>(a.v),
                           static_cast<const T *>(a.y), static_cast<const T *>(a.dy), a.lse, a.lengths,
-                          static_cast<T *>(a.dq), static_cast<T *>(a.dk), static_cast<T *>(a.dv), a.delta, a.partials,
-                          a.qs, a.ks, a.vs, a.ys, a.dys, a.seqlen, a.heads, a.kvheads, (a.seqlen + kQueries - 1) / kQueries,
+                          static_cast<T *>(a.dq), static_cast<T *>(a.dk), static_cast<T *>(a.dv), reinterpret_cast<float2 *>(a.stats), a.partials,
+                          a.qs, a.ks, a.vs, a.ys, a.dys, a.seqlen, a.heads, a.kvheads,
                           a.window, a.sinks, p.sink_tiles, p.chunk, p.nchunks, p.rows, a.scale, a.scale * kLog2e};
     return a.headdim == 32   ? attn_bwd_sized<T, 32>(in, a.batch, stream)
            : a.headdim == 64 ? attn_bwd_sized<T, 64>(in, a.batch, stream)

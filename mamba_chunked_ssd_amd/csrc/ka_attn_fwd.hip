@@ -10,15 +10,14 @@
 // and rescaling are the lane's own but for one exchange of the two halves, and P
 // stays in registers as the second product's operand.
 #include <algorithm>
-#include <limits>
 
 #include "ka_attn.h"
 
 namespace ssd {
 namespace {
 
-constexpr float kInf = std::numeric_limits<float>::infinity();
 constexpr int kQueries = 128;  // of a block
+constexpr int64_t kAttnShared = 256;  // fewer blocks of 128 queries: the waves of a block share 32
 
 template <typename T>
 struct AttnIn {
@@ -29,7 +28,7 @@ struct AttnIn {
     float *lse;
     HeadStrides qs, ks, vs;
     int64_t slots;  // of the cache
-    int L, heads, kvheads, tiles;
+    int L, heads, kvheads;
     int window, sinks;
     float c;  // scale log2(e)
 };
@@ -46,86 +45,156 @@ struct Keys {
     }
 };
 
+template <typename T, int D, int KB>
+__device__ __forceinline__ void hide(floatx16 (&s)[KB], const Walk<32 * KB> &w, int n, int j0, int t, int h, int window, int sinks) {
+    const Mask mask(t, j0, h, window, sinks);
+    if (n < w.nsink) {
+        const int sunk = w.sunk - j0 - 4 * h;
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[kb][r] = place(kb, r) < sunk ? s[kb][r] : -kInf;
+        return;
+    }
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[kb][r] = mask.seen(place(kb, r)) ? s[kb][r] : -kInf;
+    if (j0 < 0) {
+        const int none = -j0 - 4 * h;
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[kb][r] = place(kb, r) >= none ? s[kb][r] : -kInf;
+    }
+}
+
+// A value that is not finite makes 0 times it NaN in the rows of its tile that
+// do not see it.  Such a row (with a sound softmax: reference `ref`, sum 1 /
+// inv) is formed again by a wave, from the tokens that it sees alone: 64 keys'
+// weights at a time, a lane each, then their values one after the other, a lane
+// to an element.
 template <typename T, int D>
-__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(const AttnIn<T> a) {
+__device__ void attend_row(const AttnIn<T> &a, const Keys<T, D> &keys, const Keys<T, D> &values, const T *q, T *y, int t,
+                           float ref, float inv) {
+    const int lane = threadIdx.x & 63;
+    float acc[(D + 63) / 64] = {};
+    const int near = max(t - a.window + 1, 0), far = min(a.sinks, near), seen = far + t - near + 1;
+    for (int base = 0; base < seen; base += 64) {
+        const int at = base + lane, j = at < far ? at : near + at - far;
+        float p = 0.f;
+        if (at < seen) {
+            const T *kr = keys.of(j);
+            float s = 0.f;
+            for (int e = 0; e < D; ++e) s = fmaf(widen(q[e]), widen(kr[e]), s);
+            p = fast_exp2(fmaf(s, a.c, -ref));
+        }
+        for (int u = 0; u < min(64, seen - base); ++u) {
+            const float pu = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(p), u));
+            const T *vr = values.of(base + u < far ? base + u : near + base + u - far);
+#pragma unroll
+            for (int k = 0; k < (D + 63) / 64; ++k)
+                if (lane + 64 * k < D) acc[k] = fmaf(pu, widen(vr[lane + 64 * k]), acc[k]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < (D + 63) / 64; ++k)
+        if (lane + 64 * k < D) narrow(y + lane + 64 * k, acc[k] * inv);
+}
+
+// What a block works on.
+template <typename T, int D>
+struct Place {
+    int head, kvh, b, q0, len, first, end;
+    // queries: of a block; the longest rows of keys come first
+    __device__ Place(const AttnIn<T> &a, int queries) {
+        const int group = a.heads / a.kvheads, tiles = (a.L + queries - 1) / queries;
+        int n = xcd_remap((int)blockIdx.x, (int)gridDim.x);
+        const int gh = n % group;
+        n /= group;
+        q0 = (tiles - 1 - n % tiles) * queries;
+        n /= tiles;
+        kvh = n % a.kvheads;
+        b = n / a.kvheads;
+        head = kvh * group + gh;
+        len = a.lengths == nullptr ? a.L : min(max(a.lengths[b], 0), a.L);
+        first = a.positions == nullptr ? 0 : min(max(a.positions[b], 0), kAttnLast);
+        end = first + len;
+    }
+    __device__ Keys<T, D> keys(const AttnIn<T> &a) const {
+        return Keys<T, D>{a.k + (int64_t)b * a.ks.batch + kvh * a.ks.head, a.kc + ((int64_t)b * a.kvheads + kvh) * a.slots * D,
+                          a.ks.row, first, a.window, a.sinks};
+    }
+    __device__ Keys<T, D> values(const AttnIn<T> &a) const {
+        return Keys<T, D>{a.v + (int64_t)b * a.vs.batch + kvh * a.vs.head, a.vc + ((int64_t)b * a.kvheads + kvh) * a.slots * D,
+                          a.vs.row, first, a.window, a.sinks};
+    }
+    __device__ const T *query(const AttnIn<T> &a, int i) const {
+        return a.q + (int64_t)b * a.qs.batch + (int64_t)i * a.qs.row + head * a.qs.head;
+    }
+    __device__ T *result(const AttnIn<T> &a, int i) const {
+        return a.y + ((int64_t)b * a.L + i) * a.heads * D + (int64_t)head * D;
+    }
+    __device__ float *sums(const AttnIn<T> &a, int i) const {
+        return a.lse + ((int64_t)b * a.heads + head) * a.L + i;
+    }
+};
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <typename T, int D>
+__global__ __launch_bounds__(256, (sizeof(T) == 2 ? (D == 32 ? 4 : D == 64 ? 3 : 2) : (D == 128 ? 1 : 2))) void attn_fwd_kernel(const AttnIn<T> a) {
     constexpr int KT = sizeof(T) == 2 ? 64 : 32, KB = KT / 32, NS = D / 16, DB = D / 32;
     typedef Tile<T, D, KT> Tl;
     extern __shared__ __align__(16) unsigned char lds[];  // (2 stages, keys and values)
 
-    const int group = a.heads / a.kvheads;
-    int n = xcd_remap((int)blockIdx.x, (int)gridDim.x);
-    const int gh = n % group;
-    n /= group;
-    const int q0 = (a.tiles - 1 - n % a.tiles) * kQueries;  // the longest rows of keys first
-    n /= a.tiles;
-    const int kvh = n % a.kvheads, b = n / a.kvheads, head = kvh * group + gh;
-    const int len = a.lengths == nullptr ? a.L : min(max(a.lengths[b], 0), a.L);
-    const int first = a.positions == nullptr ? 0 : min(max(a.positions[b], 0), kAttnLast);
-    const int end = first + len;
-
+    const Place<T, D> p(a, kQueries);
     const int lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int i = q0 + 32 * wave + col, t = first + i;
-    const bool live = i < len;
-    T *yrow = a.y + ((int64_t)b * a.L + i) * a.heads * D + (int64_t)head * D;
-    float *lse = a.lse != nullptr ? a.lse + ((int64_t)b * a.heads + head) * a.L + i : nullptr;
-    if (q0 >= len) {
+    const int i = p.q0 + 32 * wave + col, t = p.first + i;
+    const bool live = i < p.len;
+    if (p.q0 >= p.len) {
         if (i < a.L) {
             const float z[16] = {};
-            for (int db = 0; db < DB; ++db) store_column(yrow, db, h, z, true);
-            if (lse != nullptr && h == 0) *lse = 0.f;
+            for (int db = 0; db < DB; ++db) store_column(p.result(a, i), db, h, z, true);
+            if (a.lse != nullptr && h == 0) *p.sums(a, i) = 0.f;
         }
         return;
     }
-
     Frag<T> qf[NS];
-    const T *qrow = a.q + (int64_t)b * a.qs.batch + (int64_t)i * a.qs.row + head * a.qs.head;
 #pragma unroll
-    for (int s = 0; s < NS; ++s) load_frag(qf[s], qrow + 16 * s + 8 * h, live);
+    for (int s = 0; s < NS; ++s) load_frag(qf[s], p.query(a, i) + 16 * s + 8 * h, live);
 
-    // Tiles of keys: those of the window from `from`, on a grid that `first` lies on, and before them the sinks
-    // below `from`.
-    const int t0 = first + q0, t1 = min(t0 + kQueries, end) - 1;
-    const int lo = max(t0 - a.window + 1, 0);
-    const int from = lo >= first ? first + (lo - first) / KT * KT : first - (first - lo + KT - 1) / KT * KT;
-    const int sunk = min(a.sinks, max(from, 0));
-    const int nsink = (sunk + KT - 1) / KT, ntiles = nsink + (t1 - from) / KT + 1;
-    const Keys<T, D> keys{a.k + (int64_t)b * a.ks.batch + kvh * a.ks.head, a.kc + ((int64_t)b * a.kvheads + kvh) * a.slots * D,
-                          a.ks.row, first, a.window, a.sinks};
-    const Keys<T, D> values{a.v + (int64_t)b * a.vs.batch + kvh * a.vs.head,
-                            a.vc + ((int64_t)b * a.kvheads + kvh) * a.slots * D, a.vs.row, first, a.window, a.sinks};
-    const auto start_of = [&](int n) { return n < nsink ? n * KT : from + (n - nsink) * KT; };
+    const int t0 = p.first + p.q0;
+    const Walk<KT> walk(t0, min(t0 + kQueries, p.end) - 1, p.first, a.window, a.sinks);
+    const Keys<T, D> keys = p.keys(a), values = p.values(a);
+    Copier<Tl, 4> kcopy, vcopy;
+    kcopy.init(a.ks.row * (int64_t)sizeof(T), wave, lane);
+    vcopy.init(a.vs.row * (int64_t)sizeof(T), wave, lane);
     const auto stage = [&](int n) {
-        const int j0 = start_of(n), stop = n < nsink ? sunk : end;
+        const int j0 = walk.start(n);
         unsigned char *kl = lds + (n & 1) * 2 * Tl::kBytes, *vl = kl + Tl::kBytes;
-        if (j0 >= first) {
-            const int rows = min(stop - j0, KT);
-            Tl::template copy<256>(lds_addr(kl), (const unsigned char *)(keys.fresh + (int64_t)(j0 - first) * a.ks.row),
-                                   a.ks.row * (int64_t)sizeof(T), rows);
-            Tl::template copy<256>(lds_addr(vl), (const unsigned char *)(values.fresh + (int64_t)(j0 - first) * a.vs.row),
-                                   a.vs.row * (int64_t)sizeof(T), rows);
+        if (j0 >= p.first) {
+            const int rows = min((n < walk.nsink ? walk.sunk : p.end) - j0, KT);
+            kcopy.copy(lds_addr(kl), keys.of(j0), rows);
+            vcopy.copy(lds_addr(vl), values.of(j0), rows);
         } else {
-            // the cache holds what some query of this call may see, and no older token
-            const auto held = [&](int j) { return j >= 0 && j < stop && (n < nsink || j >= lo || j < a.sinks); };
-            Tl::template gather<256>(kl, [&](int r) { return held(j0 + r) ? keys.of(j0 + r) : nullptr; });
-            Tl::template gather<256>(vl, [&](int r) { return held(j0 + r) ? values.of(j0 + r) : nullptr; });
+            Tl::template gather<256>(kl, [&](int r) { return walk.held(n, j0 + r, a.sinks, p.end) ? keys.of(j0 + r) : nullptr; });
+            Tl::template gather<256>(vl, [&](int r) { return walk.held(n, j0 + r, a.sinks, p.end) ? values.of(j0 + r) : nullptr; });
         }
     };
 
-    floatx16 o[DB];
-#pragma unroll
-    for (int db = 0; db < DB; ++db) o[db] = zero16();
-    float m = -kInf, l = 0.f;  // in units of log 2; l of this lane's half of the keys
-    const int w0 = t0 + 32 * wave, w1 = min(w0 + 31, end - 1);  // the wave's queries
-
-    stage(0);
-    for (int n = 0; n < ntiles; ++n) {
-        lds_dma_wait();
-        __syncthreads();
-        if (n + 1 < ntiles) stage(n + 1);
-        const int j0 = start_of(n);
-        if (w0 >= end || j0 > w1) continue;
-        if (n >= nsink && j0 + KT <= w0 - a.window + 1 && j0 >= a.sinks) continue;
+    Running<T, D> run;
+    run.init();
+    const int w0 = t0 + 32 * wave, w1 = min(w0 + 31, p.end - 1);  // the wave's queries
+    for (int n = -1; n < walk.ntiles; ++n) {
+        if (n >= 0) {
+            lds_dma_wait();
+            __syncthreads();
+        }
+        if (n + 1 < walk.ntiles) stage(n + 1);
+        const int j0 = walk.start(n);
+        if (n < 0 || w0 >= p.end || j0 > w1) continue;
+        if (n >= walk.nsink && j0 + KT <= w0 - a.window + 1 && j0 >= a.sinks) continue;
         const unsigned char *kl = lds + (n & 1) * 2 * Tl::kBytes, *vl = kl + Tl::kBytes;
         floatx16 s[KB];
 #pragma unroll
@@ -138,111 +207,117 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(const AttnIn<T> a) {
                 s[kb] = mma(kf, qf[ks], s[kb]);
             }
         }
-        const bool whole = n < nsink ? j0 + KT <= sunk
-                                     : j0 >= 0 && j0 + KT - 1 <= w0 && (w0 + 31 - j0 < a.window || j0 + KT <= a.sinks);
-        if (!whole) {
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int j = j0 + 32 * kb + 8 * (r / 4) + 4 * h + r % 4;
-                    const bool on = n < nsink ? j < sunk : j >= 0 && sees(t, j, a.window, a.sinks);
-                    s[kb][r] = on ? s[kb][r] : -kInf;
-                }
-        }
-        float top = s[0][0];
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) top = fmaxf(top, s[kb][r]);
-        top = fmaxf(top, other_half(top)) * a.c;
-        // The reference of the exponentials follows the maximum only where it has fallen 2^8 behind: p stays below
-        // 2^8, which costs no precision, and most tiles rescale nothing.
-        if (__any(top > m + 8.f)) {
-            const float next = fmaxf(m, top);
-            const float by = next == -kInf ? 1.f : fast_exp2(m - next);
-            l *= by;
-#pragma unroll
-            for (int db = 0; db < DB; ++db)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) o[db][r] *= by;
-            m = next;
-        }
-        const float ref = m == -kInf ? 0.f : m;
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-            float p[16];
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                p[r] = fast_exp2(fmaf(s[kb][r], a.c, -ref));
-                l += p[r];
-            }
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                Frag<T> pf;
-                to_frag(p, ks, pf);
-#pragma unroll
-                for (int db = 0; db < DB; ++db) {
-                    Frag<T> vf;
-                    Tl::across(vl, 32 * kb + 16 * ks, 32 * db, lane, vf);
-                    o[db] = mma(vf, pf, o[db]);
-                }
-            }
-        }
+        const bool whole = n < walk.nsink ? j0 + KT <= walk.sunk
+                                          : j0 >= 0 && j0 + KT - 1 <= w0 && (w0 + 31 - j0 < a.window || j0 + KT <= a.sinks);
+        if (!whole) hide<T, D, KB>(s, walk, n, j0, t, h, a.window, a.sinks);
+        run.template take<Tl, KB>(s, a.c, vl, 0, lane);
     }
-    if (w0 - first >= a.L) return;  // (no barrier follows)
+    if (w0 - p.first >= a.L) return;  // (no barrier follows)
 
-    l = both_halves(l);
-    const float ref = m == -kInf ? 0.f : m, inv = 1.f / l;
+    const float l = both_halves(run.l), ref = run.ref(), inv = 1.f / l;
     float check = 0.f;  // NaN if a sum is not finite
 #pragma unroll
     for (int db = 0; db < DB; ++db) {
         float v[16];
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            check = fmaf(o[db][r], 0.f, check);
-            v[r] = live ? o[db][r] * inv : 0.f;
+            check = fmaf(run.o[db][r], 0.f, check);
+            v[r] = live ? run.o[db][r] * inv : 0.f;
         }
-        store_column(yrow, db, h, v, i < a.L);
+        store_column(p.result(a, i), db, h, v, i < a.L);
     }
-    if (lse != nullptr && h == 0 && i < a.L) *lse = live ? (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f : 0.f;
-
-    // A value that is not finite makes 0 times it NaN in the rows of its tile that do not see it.  Such rows (with
-    // a sound softmax) are formed again, each from the tokens that it sees alone: 64 keys' weights at a time, a lane
-    // each, then their values one after the other, a lane to an element.
+    if (a.lse != nullptr && h == 0 && i < a.L) *p.sums(a, i) = live ? (run.m + __builtin_amdgcn_logf(l)) * kLn2 : 0.f;
     check = both_halves(check);
     uint64_t again = __ballot(live && check != check && l > 0.f && l < kInf) & 0xffffffffull;
     while (again != 0) {
-        const int c = __builtin_ctzll(again);
+        const int c = __builtin_ctzll(again), ic = p.q0 + 32 * wave + c;
         again &= again - 1;
-        const int tt = w0 + c;
-        const float rm = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ref), c));
-        const float rl = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv), c));
-        const T *qr = a.q + (int64_t)b * a.qs.batch + (int64_t)(tt - first) * a.qs.row + head * a.qs.head;
-        float acc[(D + 63) / 64] = {};
-        const int near = max(tt - a.window + 1, 0), far = min(a.sinks, near), seen = far + tt - near + 1;
-        for (int base = 0; base < seen; base += 64) {
-            const int at = base + lane, j = at < far ? at : near + at - far;
-            float p = 0.f;
-            if (at < seen) {
-                const T *kr = keys.of(j);
-                float s = 0.f;
-                for (int e = 0; e < D; ++e) s = fmaf(widen(qr[e]), widen(kr[e]), s);
-                p = fast_exp2(fmaf(s, a.c, -rm));
-            }
-            for (int u = 0; u < min(64, seen - base); ++u) {
-                const float pu = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(p), u));
-                const int ju = base + u < far ? base + u : near + base + u - far;
-                const T *vr = values.of(ju);
+        attend_row<T, D>(a, keys, values, p.query(a, ic), p.result(a, ic), w0 + c,
+                         __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ref), c)),
+                         __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv), c)));
+    }
+}
+
+// The same for few queries: the waves of a block share 32 of them and take the
+// tiles of 32 keys in turn, each with stages of its own in LDS (no barrier
+// between tiles), and are joined at the end.
+template <typename T, int D>
+__global__ __launch_bounds__((64 * WaveLds<T, D>::kWaves), 1) void attn_fwd_shared_kernel(const AttnIn<T> a) {
+    constexpr int NS = D / 16, NW = WaveLds<T, D>::kWaves, kStage = WaveLds<T, D>::kStage;
+    typedef Tile<T, D, 32> Tl;
+    extern __shared__ __align__(16) unsigned char lds[];
+    float2 *stats = reinterpret_cast<float2 *>(lds + WaveLds<T, D>::kBytes);  // reference and 1 / sum of each query
+    uint32_t &again = *reinterpret_cast<uint32_t *>(stats + 32);              // queries to form again
+
+    const Place<T, D> p(a, 32);
+    const int lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int i = p.q0 + col, t = p.first + i, columns = min(32, a.L - p.q0);
+    if (p.q0 >= p.len) {
+        for (int e = threadIdx.x; e < columns * D; e += 64 * NW) narrow(p.result(a, p.q0 + e / D) + e % D, 0.f);
+        if (a.lse != nullptr && (int)threadIdx.x < columns) *p.sums(a, p.q0 + threadIdx.x) = 0.f;
+        return;
+    }
+    Frag<T> qf[NS];
 #pragma unroll
-                for (int k = 0; k < (D + 63) / 64; ++k)
-                    if (lane + 64 * k < D) acc[k] = fmaf(pu, widen(vr[lane + 64 * k]), acc[k]);
-            }
+    for (int s = 0; s < NS; ++s) load_frag(qf[s], p.query(a, i) + 16 * s + 8 * h, i < p.len);
+    const int t0 = p.first + p.q0, t1 = min(t0 + 32, p.end) - 1;
+    const Walk<32> walk(t0, t1, p.first, a.window, a.sinks);
+    const Keys<T, D> keys = p.keys(a), values = p.values(a);
+    unsigned char *own = lds + wave * 2 * kStage;
+    Copier<Tl, 1> kcopy, vcopy;
+    kcopy.init(a.ks.row * (int64_t)sizeof(T), 0, lane);
+    vcopy.init(a.vs.row * (int64_t)sizeof(T), 0, lane);
+    const auto stage = [&](int n, unsigned char *kl) {
+        const int j0 = walk.start(n);
+        if (j0 >= p.first) {
+            const int rows = min((n < walk.nsink ? walk.sunk : p.end) - j0, 32);
+            kcopy.copy(lds_addr(kl), keys.of(j0), rows);
+            vcopy.copy(lds_addr(kl + Tl::kBytes), values.of(j0), rows);
+        } else {
+            Tl::template gather<64>(kl, [&](int r) { return walk.held(n, j0 + r, a.sinks, p.end) ? keys.of(j0 + r) : nullptr; });
+            Tl::template gather<64>(kl + Tl::kBytes, [&](int r) { return walk.held(n, j0 + r, a.sinks, p.end) ? values.of(j0 + r) : nullptr; });
         }
-        T *yr = a.y + ((int64_t)b * a.L + (tt - first)) * a.heads * D + (int64_t)head * D;
+    };
+    Running<T, D> run;
+    run.init();
+    int buf = 0;
+    for (int n = wave - NW; n < walk.ntiles; n += NW, buf ^= 1) {
+        // the copies of this tile are the oldest; what was read of the other stage has arrived
+        if (n >= 0) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        if (n + NW < walk.ntiles) stage(n + NW, own + (buf ^ 1) * kStage);
+        if (n < 0) continue;
+        const unsigned char *kl = own + buf * kStage;
+        const int j0 = walk.start(n);
+        floatx16 s[1] = {zero16()};
 #pragma unroll
-        for (int k = 0; k < (D + 63) / 64; ++k)
-            if (lane + 64 * k < D) narrow(yr + lane + 64 * k, acc[k] * rl);
+        for (int ks = 0; ks < NS; ++ks) {
+            Frag<T> kf;
+            Tl::down(kl, 0, ks, lane, kf);
+            s[0] = mma(kf, qf[ks], s[0]);
+        }
+        const bool whole = n < walk.nsink ? j0 + 32 <= walk.sunk
+                                          : j0 >= 0 && j0 + 31 <= t0 && (t0 + 31 - j0 < a.window || j0 + 32 <= a.sinks);
+        if (!whole) hide<T, D, 1>(s, walk, n, j0, t, h, a.window, a.sinks);
+        run.template take<Tl, 1>(s, a.c, kl + Tl::kBytes, 0, lane);
+    }
+    if (threadIdx.x == 0) again = 0;  // (Join's barriers come before its use)
+    Join<T, D, NW>::run(lds, run, wave, lane, columns, [&](int c, int d, float y, float m, float l) {
+        const int ic = p.q0 + c;
+        const bool live = ic < p.len;
+        const float inv = 1.f / l;
+        narrow(p.result(a, ic) + d, live ? y * inv : 0.f);
+        if (d == 0) {
+            stats[c] = float2{m == -kInf ? 0.f : m, inv};
+            if (a.lse != nullptr) *p.sums(a, ic) = live ? (m + __builtin_amdgcn_logf(l)) * kLn2 : 0.f;
+        }
+        if (live && y - y != 0.f && l > 0.f && l < kInf) atomicOr(&again, 1u << c);
+    });
+    __syncthreads();
+    for (uint32_t rest = again; rest != 0; rest &= rest - 1) {
+        const int c = __builtin_ctz(rest);
+        if (c % NW != wave) continue;
+        attend_row<T, D>(a, keys, values, p.query(a, p.q0 + c), p.result(a, p.q0 + c), t0 + c, stats[c].x, stats[c].y);
     }
 }
 
@@ -270,10 +345,18 @@ __global__ __launch_bounds__(256) void attn_put_kernel(const AttnIn<T> a, int D,
 
 template <typename T, int D>
 hipError_t attn_fwd_sized(const AttnIn<T> &in, int64_t batch, hipStream_t stream) {
+    const int64_t blocks = batch * in.heads * ((in.L + kQueries - 1) / kQueries);
+    if (blocks < kAttnShared) {
+        constexpr int kLds = WaveLds<T, D>::kBytes + 32 * (int)sizeof(float2) + 16;
+        const hipError_t e = allow_lds<attn_fwd_shared_kernel<T, D>>(kLds);
+        if (e != hipSuccess) return e;
+        attn_fwd_shared_kernel<T, D><<<dim3((uint32_t)(batch * in.heads * ((in.L + 31) / 32))), dim3(64 * WaveLds<T, D>::kWaves), kLds, stream>>>(in);
+        return hipGetLastError();
+    }
     constexpr int kLds = 2 * 2 * Tile<T, D, sizeof(T) == 2 ? 64 : 32>::kBytes;
     const hipError_t e = allow_lds<attn_fwd_kernel<T, D>>(kLds);
     if (e != hipSuccess) return e;
-    attn_fwd_kernel<T, D><<<dim3((uint32_t)(batch * in.heads * in.tiles)), dim3(256), kLds, stream>>>(in);
+    attn_fwd_kernel<T, D><<<dim3((uint32_t)blocks), dim3(256), kLds, stream>>>(in);
     return hipGetLastError();
 }
 
@@ -282,7 +365,7 @@ hipError_t attn_fwd_typed(const AttnArgs &a, hipStream_t stream) {
     const AttnIn<T> in{static_cast<const T *>(a.q), static_cast<const T *>(a.k), static_cast<const T *>(a.v),
                        static_cast<T *>(a.kc), static_cast<T *>(a.vc), a.positions, a.lengths, static_cast<T *>(a.y), a.lse,
                        a.qs, a.ks, a.vs, (int64_t)a.window + a.sinks, a.seqlen, a.heads, a.kvheads,
-                       (a.seqlen + kQueries - 1) / kQueries, a.window, a.sinks, a.scale * kLog2e};
+                       a.window, a.sinks, a.scale * kLog2e};
     hipError_t e = a.headdim == 32   ? attn_fwd_sized<T, 32>(in, a.batch, stream)
                    : a.headdim == 64 ? attn_fwd_sized<T, 64>(in, a.batch, stream)
                                      : attn_fwd_sized<T, 128>(in, a.batch, stream);

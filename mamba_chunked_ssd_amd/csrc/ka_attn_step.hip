@@ -11,15 +11,10 @@
 // LDS, with its own running maximum and sum; the waves' results are joined in
 // LDS, and where few sequences leave compute units idle, so that a sequence's
 // slots are split over blocks, those of the blocks by a second kernel.
-#include <algorithm>
-#include <limits>
-
 #include "ka_attn.h"
 
 namespace ssd {
 namespace {
-
-constexpr float kInf = std::numeric_limits<float>::infinity();
 
 template <typename T>
 struct AttnStepIn {
@@ -37,21 +32,11 @@ struct AttnStepIn {
 
 __device__ __forceinline__ int slot_of(int j, int window, int sinks) { return j < sinks ? j : sinks + (j - sinks) % window; }
 
-// A wave's two stages of 32 keys and values; four waves to a block where they
-// fit its 128 KB (fp32 rows of 128 elements: two).
 template <typename T, int D>
-struct StepLds {
-    static constexpr int kStage = 2 * Tile<T, D, 32>::kBytes, kWaves = 8 * kStage <= 131072 ? 4 : 2;
-    static constexpr int kPad = D + 4;  // floats to a row of the waves' results
-    static constexpr int kResults = kWaves * 32 * (2 + kPad) * (int)sizeof(float), kCopies = kWaves * 2 * kStage;
-    static constexpr int kBytes = kCopies > kResults ? kCopies : kResults;
-};
-
-template <typename T, int D>
-__global__ __launch_bounds__((64 * StepLds<T, D>::kWaves), 1) void attn_step_kernel(const AttnStepIn<T> a) {
-    constexpr int NS = D / 16, DB = D / 32, NW = StepLds<T, D>::kWaves;
+__global__ __launch_bounds__((64 * WaveLds<T, D>::kWaves), 1) void attn_step_kernel(const AttnStepIn<T> a) {
+    constexpr int NS = D / 16, NW = WaveLds<T, D>::kWaves;
     typedef Tile<T, D, 32> Tl;
-    constexpr int kStage = StepLds<T, D>::kStage, kCopies = kStage / 16 / 64;
+    constexpr int kStage = WaveLds<T, D>::kStage, kCopies = 2 * Copier<Tl, 1>::kEach;
     extern __shared__ __align__(16) unsigned char lds[];  // (waves, 2 stages, keys and values); then the waves' results
 
     const int group = a.heads / a.kvheads, hblocks = (group + 31) / 32;
@@ -80,17 +65,16 @@ __global__ __launch_bounds__((64 * StepLds<T, D>::kWaves), 1) void attn_step_ker
 
     const int64_t cache = ((int64_t)b * a.kvheads + kvh) * a.slots * D;
     unsigned char *own = lds + wave * 2 * kStage;
+    Copier<Tl, 1> copier;
+    copier.init(Tl::kRow, 0, lane);
     const auto stage = [&](int at, int buf) {
-        const int rows = min(s1 - at, 32);
         const uint32_t kl = lds_addr(own + buf * kStage);
-        Tl::copy_wave(kl, (const unsigned char *)(a.kc + cache + (int64_t)at * D), rows, lane);
-        Tl::copy_wave(kl + Tl::kBytes, (const unsigned char *)(a.vc + cache + (int64_t)at * D), rows, lane);
+        copier.copy(kl, a.kc + cache + (int64_t)at * D, min(s1 - at, 32));
+        copier.copy(kl + Tl::kBytes, a.vc + cache + (int64_t)at * D, min(s1 - at, 32));
     };
 
-    floatx16 o[DB];
-#pragma unroll
-    for (int db = 0; db < DB; ++db) o[db] = zero16();
-    float m = -kInf, l = 0.f;
+    Running<T, D> run;
+    run.init();
     int at = s0 + 32 * wave, buf = 0;
     if (at < s1) stage(at, 0);
     for (; at < s1; at += 32 * NW, buf ^= 1) {
@@ -114,124 +98,57 @@ __global__ __launch_bounds__((64 * StepLds<T, D>::kWaves), 1) void attn_step_ker
             }
             lds_dma_wait();
         }
-        floatx16 s = zero16();
+        floatx16 s[1] = {zero16()};
 #pragma unroll
         for (int ks = 0; ks < NS; ++ks) {
             Frag<T> kf;
             Tl::down(kl, 0, ks, lane, kf);
-            s = mma(kf, qf[ks], s);
+            s[0] = mma(kf, qf[ks], s[0]);
         }
         if (at + 32 > s1) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s[r] = at + 8 * (r / 4) + 4 * h + r % 4 < s1 ? s[r] : -kInf;
+            for (int r = 0; r < 16; ++r) s[0][r] = place(0, r) < s1 - at - 4 * h ? s[0][r] : -kInf;
         }
-        float top = s[0];
-#pragma unroll
-        for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
-        top = fmaxf(top, other_half(top)) * a.c;
-        if (__any(top > m + 8.f)) {
-            const float next = fmaxf(m, top), by = next == -kInf ? 1.f : fast_exp2(m - next);
-            l *= by;
-#pragma unroll
-            for (int db = 0; db < DB; ++db)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) o[db][r] *= by;
-            m = next;
-        }
-        const float ref = m == -kInf ? 0.f : m;
-        float p[16];
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            p[r] = fast_exp2(fmaf(s[r], a.c, -ref));
-            l += p[r];
-        }
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            Frag<T> pf;
-            to_frag(p, ks, pf);
-#pragma unroll
-            for (int db = 0; db < DB; ++db) {
-                Frag<T> vf;
-                Tl::across(vl, 16 * ks, 32 * db, lane, vf);
-                o[db] = mma(vf, pf, o[db]);
-            }
-        }
+        run.template take<Tl, 1>(s, a.c, vl, 0, lane);
     }
-    l = both_halves(l);
-
-    // The waves' results: (wave, head, maximum and sum), (wave, head, element)
-    constexpr int kPad = StepLds<T, D>::kPad;
-    float *ml = reinterpret_cast<float *>(lds), *os = ml + NW * 32 * 2;
-    __syncthreads();
-    if (col < nh) {
-        if (h == 0) {
-            ml[(wave * 32 + col) * 2] = m;
-            ml[(wave * 32 + col) * 2 + 1] = l;
-        }
-        float *row = os + (wave * 32 + col) * kPad;
-#pragma unroll
-        for (int db = 0; db < DB; ++db)
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-                *reinterpret_cast<floatx4 *>(row + 32 * db + 8 * g + 4 * h) =
-                    floatx4{o[db][4 * g], o[db][4 * g + 1], o[db][4 * g + 2], o[db][4 * g + 3]};
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < nh * D; e += 64 * NW) {
-        const int c = e / D, d = e % D;
-        float most = -kInf, w[NW], sum = 0.f, y = 0.f;
-#pragma unroll
-        for (int k = 0; k < NW; ++k) most = fmaxf(most, ml[(k * 32 + c) * 2]);
-        const float ref = most == -kInf ? 0.f : most;
-#pragma unroll
-        for (int k = 0; k < NW; ++k) {
-            w[k] = fast_exp2(ml[(k * 32 + c) * 2] - ref);
-            sum = fmaf(ml[(k * 32 + c) * 2 + 1], w[k], sum);
-            y = fmaf(os[(k * 32 + c) * kPad + d], w[k], y);
-        }
+    Join<T, D, NW>::run(lds, run, wave, lane, nh, [&](int c, int d, float y, float m, float l) {
         const int64_t head = (int64_t)b * a.heads + head0 + c;
         if (a.splits == 1) {
-            narrow(a.y + head * D + d, y / sum);
+            narrow(a.y + head * D + d, y / l);
         } else {
             a.part_y[(head * a.splits + split) * D + d] = y;
-            if (d == 0) {
-                a.part_ml[(head * a.splits + split) * 2] = most;
-                a.part_ml[(head * a.splits + split) * 2 + 1] = sum;
-            }
+            if (d == 0) *reinterpret_cast<float2 *>(a.part_ml + (head * a.splits + split) * 2) = float2{m, l};
         }
-    }
+    });
 }
 
-// Joins the blocks' results, a wave to a head of a sequence.
+// Joins the blocks' results, a block of D threads to a head of a sequence.
 template <typename T>
-__global__ __launch_bounds__(256) void attn_join_kernel(const AttnStepIn<T> a, int64_t all, int D) {
-    const int lane = threadIdx.x & 63;
-    const int64_t head = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (head >= all || a.positions[head / a.heads] < 0) return;
-    const float *ml = a.part_ml + head * a.splits * 2;
-    float most = -kInf, sum = 0.f;
-    for (int k = 0; k < a.splits; ++k) most = fmaxf(most, ml[2 * k]);
-    const float ref = most == -kInf ? 0.f : most;
-    float y[2] = {0.f, 0.f};
+__global__ __launch_bounds__(128) void attn_join_kernel(const AttnStepIn<T> a, int D) {
+    const int64_t head = blockIdx.x;
+    const int d = threadIdx.x;
+    if (a.positions[head / a.heads] < 0) return;
+    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + head * a.splits;
+    const float *py = a.part_y + head * a.splits * D + d;
+    float most = -kInf, sum = 0.f, y = 0.f;
+    for (int k = 0; k < a.splits; ++k) most = fmaxf(most, ml[k].x);
+    const float from = most == -kInf ? 0.f : most;
+#pragma unroll 8
     for (int k = 0; k < a.splits; ++k) {
-        const float w = fast_exp2(ml[2 * k] - ref);
-        sum = fmaf(ml[2 * k + 1], w, sum);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (lane + 64 * i < D) y[i] = fmaf(a.part_y[(head * a.splits + k) * D + lane + 64 * i], w, y[i]);
+        const float w = fast_exp2(ml[k].x - from);
+        sum = fmaf(ml[k].y, w, sum);
+        y = fmaf(py[(int64_t)k * D], w, y);
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (lane + 64 * i < D) narrow(a.y + head * D + lane + 64 * i, y[i] / sum);
+    narrow(a.y + head * D + d, y / sum);
 }
 
 template <typename T, int D>
 hipError_t attn_step_sized(const AttnStepIn<T> &in, int64_t batch, hipStream_t stream) {
-    constexpr int kLds = StepLds<T, D>::kBytes;
+    constexpr int kLds = WaveLds<T, D>::kBytes;
     const hipError_t e = allow_lds<attn_step_kernel<T, D>>(kLds);
     if (e != hipSuccess) return e;
     const int64_t hblocks = (in.heads / in.kvheads + 31) / 32;
-    attn_step_kernel<T, D><<<dim3((uint32_t)(batch * in.kvheads * hblocks * in.splits)), dim3(64 * StepLds<T, D>::kWaves), kLds, stream>>>(in);
+    attn_step_kernel<T, D><<<dim3((uint32_t)(batch * in.kvheads * hblocks * in.splits)), dim3(64 * WaveLds<T, D>::kWaves), kLds, stream>>>(in);
     return hipGetLastError();
 }
 
@@ -245,8 +162,7 @@ hipError_t attn_step_typed(const AttnArgs &a, const AttnStepPlan &p, hipStream_t
                          : a.headdim == 64 ? attn_step_sized<T, 64>(in, a.batch, stream)
                                            : attn_step_sized<T, 128>(in, a.batch, stream);
     if (e != hipSuccess || p.splits == 1) return e;
-    const int64_t all = a.batch * a.heads;
-    attn_join_kernel<T><<<dim3((uint32_t)((all + 3) / 4)), dim3(256), 0, stream>>>(in, all, a.headdim);
+    attn_join_kernel<T><<<dim3((uint32_t)(a.batch * a.heads)), dim3(a.headdim), 0, stream>>>(in, a.headdim);
     return hipGetLastError();
 }
 

@@ -20,11 +20,11 @@ AttnBwdPlan attn_bwd_plan(const AttnArgs &a) {
     const int far = a.seqlen - a.window;  // queries that see token 0 as a sink only
     if (a.sinks == 0 || far <= 0) return p;
     const int keys = std::min(a.sinks, far);
-    p.sink_tiles = (keys + kAttnKeys - 1) / kAttnKeys;
-    p.chunk = 512;
+    p.sink_tiles = (keys + kSinkKeys - 1) / kSinkKeys;
+    p.chunk = std::max(128, (far + 64 * 128 - 1) / (64 * 128) * 128);
     p.nchunks = (far + p.chunk - 1) / p.chunk;
     p.parts = 1 + p.nchunks;
-    p.rows = (int64_t)p.sink_tiles * kAttnKeys;
+    p.rows = (int64_t)p.sink_tiles * kSinkKeys;
     return p;
 }
 
@@ -141,7 +141,7 @@ ssd_status check_attn(const ssd_attn_shape *s, bool cached, AttnArgs *a, AttnByt
 
 size_t attn_bwd_carve(AttnArgs *a, const AttnBwdPlan &p, void *ws) {
     Carver w{static_cast<unsigned char *>(ws), 0};
-    a->delta = w.take((size_t)a->batch * a->heads * a->seqlen);
+    a->stats = w.take((size_t)a->batch * a->heads * a->seqlen * 2);
     a->partials = w.take((size_t)a->batch * a->kvheads * p.parts * 2 * p.rows * a->headdim);
     return w.off;
 }
@@ -162,7 +162,7 @@ ssd_status check_attn_bwd(const ssd_attn_shape *s, AttnArgs *a, AttnBytes *n) {
     const AttnBwdPlan p = attn_bwd_plan(*a);
     int64_t t;
     if (!product({a->batch, a->kvheads, p.parts, 2 * p.rows, a->headdim, 4}, &t)) return SSD_ERROR_UNSUPPORTED;
-    if (!product({a->batch * a->kvheads, a->seqlen / kAttnKeys + 1 + (int64_t)p.sink_tiles * p.nchunks}, &t) ||
+    if (!product({a->batch * a->kvheads, (int64_t)p.sink_tiles * p.nchunks}, &t) ||
         t >= (int64_t)1 << 24)
         return SSD_ERROR_UNSUPPORTED;
     return SSD_OK;

@@ -150,7 +150,7 @@ struct AttnArgs {
     // backward
     const void *dy;
     void *dq, *dk, *dv;
-    float *delta;     // (batch, heads, seqlen): sum_d dy y
+    float *stats;     // (batch, heads, seqlen, 2): lse / log(2), sum_d dy y
     float *partials;  // (batch, kvheads, AttnBwdPlan::parts, 2, AttnBwdPlan::rows, headdim)
     // one token
     float *part_y, *part_ml;  // (batch, heads, splits, headdim), (batch, heads, splits, 2)
@@ -158,15 +158,15 @@ struct AttnArgs {
 constexpr int kAttnFar = 1 << 30;   // farther than any token sees
 constexpr int kAttnLast = 1 << 29;  // the largest position that a call begins at: tokens and what is added to them fit 32 bits
 
-// Keys of the backward pass's blocks and how the sinks' far queries (those that
-// see them as sinks only) are cut: chunks of `chunk` queries beside each other.
+// How the backward pass cuts the sinks' far queries (those that see them as
+// sinks only): chunks of `chunk` queries beside each other.
 struct AttnBwdPlan {
-    int sink_tiles;  // tiles of kAttnKeys keys that hold sinks with far queries
+    int sink_tiles;  // tiles of kSinkKeys keys that hold sinks with far queries
     int chunk, nchunks;
-    int parts;       // partial sums of a sink tile's rows: its own block's, then the chunks'
-    int64_t rows;    // sink_tiles * kAttnKeys
+    int parts;       // partial sums of these tiles' rows: their window's, then the chunks'
+    int64_t rows;    // sink_tiles * kSinkKeys
 };
-constexpr int kAttnKeys = 128;
+constexpr int kSinkKeys = 32;
 AttnBwdPlan attn_bwd_plan(const AttnArgs &a);
 
 // Blocks that share the slots of one sequence and head of keys, and the slots of each.
