@@ -46,9 +46,15 @@ def flags() -> list[str]:
     ]
 
 
+def flags_of(src: str) -> list[str]:
+    # The attention kernels carry whole result tiles of the matrix units through loops and branches: as single
+    # registers, they would be copied in every turn.
+    return ["-mllvm", "-amdgpu-codegenprepare-break-large-phis=false"] if src.startswith("ka_") else []
+
+
 def _compile(src: str, verbose: bool) -> str:
     obj = os.path.join(OBJ_DIR, os.path.splitext(src)[0] + ".o")
-    cmd = [hipcc(), "-x", "hip", "-c", os.path.join(CSRC, src), "-o", obj] + flags()
+    cmd = [hipcc(), "-x", "hip", "-c", os.path.join(CSRC, src), "-o", obj] + flags() + flags_of(src)
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)

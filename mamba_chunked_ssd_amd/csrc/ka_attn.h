@@ -46,15 +46,15 @@ __device__ __forceinline__ floatx16 zero16() {
     return floatx16{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 }
 
-// Registers 8 s .. 8 s + 7 of a result as the next product's B operand (bf16:
-// rounded to nearest even, relative 2^-9; the sums they enter are fp32).
-__device__ __forceinline__ void to_frag(const float (&p)[16], int s, Frag<uint16_t> &f) {
+// Eight registers of a result (8 s .. 8 s + 7) as the next product's B operand
+// (bf16: rounded to nearest even, by 2^-8 at most; the sums they enter are fp32).
+__device__ __forceinline__ void to_frag(const float (&p)[8], Frag<uint16_t> &f) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f.v[i] = pack_bf16(p[8 * s + 2 * i], p[8 * s + 2 * i + 1]);
+    for (int i = 0; i < 4; ++i) f.v[i] = pack_bf16(p[2 * i], p[2 * i + 1]);
 }
-__device__ __forceinline__ void to_frag(const float (&p)[16], int s, Frag<float> &f) {
+__device__ __forceinline__ void to_frag(const float (&p)[8], Frag<float> &f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f.v[i] = p[8 * s + i];
+    for (int i = 0; i < 8; ++i) f.v[i] = p[i];
 }
 
 // Eight consecutive elements from memory (16-byte aligned), or 0.
@@ -70,6 +70,19 @@ __device__ __forceinline__ void load_frag(Frag<float> &f, const float *p, bool o
         f.v[4 + i] = b[i];
     }
 }
+// The loads of f have arrived.  Said before a loop that uses f beside copies
+// (lds_dma_x4) in flight: the compiler, which does not count those, would wait
+// in every turn for the loads, and so for the copies.
+__device__ __forceinline__ void arrived(Frag<uint16_t> &f) { asm volatile("" : "+v"(f.v)); }
+__device__ __forceinline__ void arrived(Frag<float> &f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(f.v[i]));
+}
+// Nothing is scheduled across.  Between groups of LDS reads and products: left
+// alone, the compiler reuses one operand's registers and waits for each read
+// right before its product.
+__device__ __forceinline__ void group_end() { __builtin_amdgcn_sched_barrier(0); }
+
 __device__ __forceinline__ float dot_frag(const Frag<uint16_t> &a, const Frag<uint16_t> &b, float s) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -148,10 +161,12 @@ struct Tile {
     // Filled through registers, row r from row(r), null: 0.
     template <int THREADS, typename F>
     __device__ static void gather(unsigned char *lds, F &&row) {
-        static_assert(kBytes / 16 % THREADS == 0, "every thread takes as many pieces");
+        
 #pragma unroll 2
-        for (int k = 0; k < kBytes / 16 / THREADS; ++k) {
-            const int n = k * THREADS + (int)threadIdx.x % THREADS, r = n / kPieces, piece = n % kPieces;
+        for (int k = 0; k < (kBytes / 16 + THREADS - 1) / THREADS; ++k) {
+            const int n = k * THREADS + (int)threadIdx.x % THREADS;
+            if (kBytes / 16 % THREADS != 0 && n >= kBytes / 16) break;
+            const int r = n / kPieces, piece = n % kPieces;
             const T *p = row(r);
             u32x4 v = {0, 0, 0, 0};
             if (p != nullptr) v = *reinterpret_cast<const u32x4 *>(p + piece * kPer);
@@ -194,14 +209,21 @@ __device__ __forceinline__ void lds_dma_wait_but() {
 }
 
 // The mask of a block of keys whose first is token j0, for the lane's query t:
-// register r of block kb is key j0 + 4 h + place(kb, r), which t sees if seen().
-// Without branches: three comparisons, and the rest on scalar registers.
+// register r of block kb is key j0 + 4 h + place(kb, r), which t sees if it is
+// none of those behind `last` and, but for the sinks, after `before`.
 __device__ constexpr int place(int kb, int r) { return 32 * kb + 8 * (r / 4) + r % 4; }
 struct Mask {
     int last, before, sunk;
     __device__ Mask(int t, int j0, int h, int window, int sinks)
         : last(t - j0 - 4 * h), before(last - window), sunk(sinks - j0 - 4 * h) {}
+    // without branches: comparisons, and the rest on scalar registers
     __device__ bool seen(int at) const { return (at <= last) & ((at > before) | (at < sunk)); }
+};
+// Masks of 32 KB keys for the queries w0 .. w0 + 31 of a wave: which comparisons they need.
+struct Needs {
+    bool last, before;
+    __device__ Needs(int j0, int keys, int w0, int window, int sinks)
+        : last(j0 + keys - 1 > w0), before(w0 + 31 - j0 >= window && j0 + keys > sinks) {}
 };
 
 // Which tiles of KT keys a run of queries from token t0 to t1 takes: those of
@@ -255,34 +277,55 @@ struct Running {
             const float by = next == -kInf ? 1.f : fast_exp2(m - next);
             l *= by;
 #pragma unroll
-            for (int db = 0; db < DB; ++db)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) o[db][r] *= by;
+            for (int db = 0; db < DB; ++db) o[db] *= by;
             m = next;
         }
         const float from = ref();
+        // 16 keys at a time: their values are read while the weights of those before them are formed
+        constexpr int kSteps = 2 * KB;
+        Frag<T> vf[2][DB];
+        const auto read = [&](int step) {
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-            float p[16];
+            for (int db = 0; db < DB; ++db) Tl::across(v, r0 + 16 * step, 32 * db, lane, vf[step & 1][db]);
+        };
+        read(0);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                p[r] = fast_exp2(fmaf(s[kb][r], c, -from));
+        for (int step = 0; step < kSteps; ++step) {
+            if (step + 1 < kSteps) read(step + 1);
+            float p[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                p[r] = fast_exp2(fmaf(s[step / 2][8 * (step % 2) + r], c, -from));
                 l += p[r];
             }
+            Frag<T> pf;
+            to_frag(p, pf);
+            group_end();
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                Frag<T> pf;
-                to_frag(p, ks, pf);
-#pragma unroll
-                for (int db = 0; db < DB; ++db) {
-                    Frag<T> vf;
-                    Tl::across(v, r0 + 32 * kb + 16 * ks, 32 * db, lane, vf);
-                    o[db] = mma(vf, pf, o[db]);
-                }
-            }
+            for (int db = 0; db < DB; ++db) o[db] = mma(vf[step & 1][db], pf, o[db]);
         }
     }
 };
+
+// S^T = K Q^T of 32 KB keys, the rows of the tile at k.
+template <typename Tl, typename T, int NS, int KB>
+__device__ __forceinline__ void scores(const unsigned char *k, const Frag<T> (&q)[NS], int lane, floatx16 (&s)[KB]) {
+    Frag<T> kf[KB > 1 ? 2 : 1][NS];
+#pragma unroll
+    for (int ks = 0; ks < NS; ++ks) Tl::down(k, 0, ks, lane, kf[0][ks]);
+    group_end();
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+        if (kb + 1 < KB) {
+#pragma unroll
+            for (int ks = 0; ks < NS; ++ks) Tl::down(k, 32 * (kb + 1), ks, lane, kf[(kb + 1) & 1][ks]);
+        }
+        s[kb] = zero16();
+#pragma unroll
+        for (int ks = 0; ks < NS; ++ks) s[kb] = mma(kf[kb & 1][ks], q[ks], s[kb]);
+        group_end();
+    }
+}
 
 // Results of NW waves over the same 32 columns joined through LDS: (wave,
 // column, m and l), then (wave, column, D values).  write(column, element,

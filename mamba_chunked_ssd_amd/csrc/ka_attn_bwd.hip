@@ -23,6 +23,7 @@ namespace ssd {
 namespace {
 
 constexpr int kQueries = 128;
+constexpr int64_t kFewBlocks = 256;
 
 template <typename T>
 struct AttnBwdIn {
@@ -51,28 +52,34 @@ __device__ __forceinline__ float row_dot(const T *a, const T *b) {
     return s;
 }
 
-template <typename T, int D>
-__global__ __launch_bounds__(256, (D * sizeof(T) <= 256 ? 2 : 1)) void attn_dq_kernel(const AttnBwdIn<T> a) {
-    constexpr int KT = sizeof(T) == 2 ? 64 : 32, KB = KT / 32, NS = D / 16, DB = D / 32;
+// SHARED (few queries): the waves of a block share 32 queries and take the
+// tiles in turn, with stages of their own; their sums are added at the end, in
+// order.  Else each has 32, and all use the same tiles.
+template <typename T, int D, bool SHARED>
+__global__ __launch_bounds__((SHARED ? 64 * WaveLds<T, D>::kWaves : 256), (!SHARED && D * sizeof(T) <= 256 ? 2 : 1)) void attn_dq_kernel(
+    const AttnBwdIn<T> a) {
+    constexpr int KT = sizeof(T) == 2 && !SHARED ? 64 : 32, KB = KT / 32, NS = D / 16, DB = D / 32;
+    constexpr int NW = SHARED ? WaveLds<T, D>::kWaves : 4, kRun = SHARED ? 32 : kQueries;
     typedef Tile<T, D, KT> Tl;
     extern __shared__ __align__(16) unsigned char lds[];
 
     const int group = a.heads / a.kvheads;
-    const int tiles = (a.L + kQueries - 1) / kQueries;
+    const int tiles = (a.L + kRun - 1) / kRun;
     int n = xcd_remap((int)blockIdx.x, (int)gridDim.x);
     const int gh = n % group;
     n /= group;
-    const int q0 = (tiles - 1 - n % tiles) * kQueries;
+    const int q0 = (tiles - 1 - n % tiles) * kRun;
     n /= tiles;
     const int kvh = n % a.kvheads, b = n / a.kvheads, head = kvh * group + gh;
     const int len = length_of(a.lengths, b, a.L);
     const int lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int t = q0 + 32 * wave + col;
+    const int w0 = SHARED ? q0 : q0 + 32 * wave, t = w0 + col;  // the wave's queries
     const bool live = t < len;
     const int64_t dense = ((int64_t)b * a.L + t) * a.heads * D + (int64_t)head * D;
     const int64_t stat = ((int64_t)b * a.heads + head) * a.L + t;
     if (q0 >= len) {
+        if (SHARED && wave > 0) return;
         const float z[16] = {};
         for (int db = 0; db < DB; ++db) store_column(a.dq + dense, db, h, z, t < a.L);
         return;
@@ -96,69 +103,93 @@ __global__ __launch_bounds__(256, (D * sizeof(T) <= 256 ? 2 : 1)) void attn_dq_k
     }
     delta = both_halves(delta);
     const float lse = live ? a.lse[stat] * kLog2e : 0.f;
-    if (live && h == 0) a.stats[stat] = float2{lse, delta};
+    if (live && h == 0 && (!SHARED || wave == 0)) a.stats[stat] = float2{lse, delta};
 
-    const Walk<KT> walk(q0, min(q0 + kQueries, len) - 1, 0, a.window, a.sinks);
+    const Walk<KT> walk(q0, min(q0 + kRun, len) - 1, 0, a.window, a.sinks);
     const T *kh = a.k + (int64_t)b * a.ks.batch + kvh * a.ks.head, *vh = a.v + (int64_t)b * a.vs.batch + kvh * a.vs.head;
-    Copier<Tl, 4> kcopy, vcopy;
-    kcopy.init(a.ks.row * (int64_t)sizeof(T), wave, lane);
-    vcopy.init(a.vs.row * (int64_t)sizeof(T), wave, lane);
-    const auto stage = [&](int n) {
+    Copier<Tl, SHARED ? 1 : 4> kcopy, vcopy;
+    kcopy.init(a.ks.row * (int64_t)sizeof(T), SHARED ? 0 : wave, lane);
+    vcopy.init(a.vs.row * (int64_t)sizeof(T), SHARED ? 0 : wave, lane);
+    unsigned char *own = lds + (SHARED ? wave * 4 * Tl::kBytes : 0);  // (2 stages, keys and values)
+    const auto stage = [&](int n, int buf) {
         const int j0 = walk.start(n), rows = min((n < walk.nsink ? walk.sunk : len) - j0, KT);
-        const uint32_t kl = lds_addr(lds + (n & 1) * 2 * Tl::kBytes);
+        const uint32_t kl = lds_addr(own + buf * 2 * Tl::kBytes);
         kcopy.copy(kl, kh + (int64_t)j0 * a.ks.row, rows);
         vcopy.copy(kl + Tl::kBytes, vh + (int64_t)j0 * a.vs.row, rows);
     };
 
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+        arrived(qf[s]);
+        arrived(df[s]);
+    }
     floatx16 o[DB];
 #pragma unroll
     for (int db = 0; db < DB; ++db) o[db] = zero16();
-    const int w0 = q0 + 32 * wave, w1 = min(w0 + 31, len - 1);
+    const int w1 = min(w0 + 31, len - 1);
     const bool alone = t == 0 || (a.window == 1 && a.sinks == 0);  // (such a row's tile is never whole)
-    for (int n = -1; n < walk.ntiles; ++n) {
+    constexpr int kStep = SHARED ? NW : 1;
+    int buf = 0;
+    for (int n = SHARED ? wave - NW : -1; n < walk.ntiles; n += kStep, buf ^= 1) {
         if (n >= 0) {
-            lds_dma_wait();
-            __syncthreads();
+            // (what was read of the other stage has arrived too)
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+            if constexpr (!SHARED) __syncthreads();
         }
-        if (n + 1 < walk.ntiles) stage(n + 1);
+        if (n + kStep < walk.ntiles) stage(n + kStep, buf ^ 1);
         const int j0 = walk.start(n);
         if (n < 0 || w0 >= len || j0 > w1) continue;
         if (n >= walk.nsink && j0 + KT <= w0 - a.window + 1 && j0 >= a.sinks) continue;
-        const unsigned char *kl = lds + (n & 1) * 2 * Tl::kBytes, *vl = kl + Tl::kBytes;
+        const unsigned char *kl = own + buf * 2 * Tl::kBytes, *vl = kl + Tl::kBytes;
         const bool whole = n < walk.nsink ? j0 + KT <= walk.sunk
                                           : j0 + KT - 1 <= w0 && (w0 + 31 - j0 < a.window || j0 + KT <= a.sinks);
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
-            floatx16 s = zero16(), g = zero16();
-#pragma unroll
-            for (int ks = 0; ks < NS; ++ks) {
-                Frag<T> kf, vf;
-                Tl::down(kl, 32 * kb, ks, lane, kf);
-                s = mma(kf, qf[ks], s);
-                Tl::down(vl, 32 * kb, ks, lane, vf);
-                g = mma(vf, df[ks], g);
-            }
+            floatx16 s[1], g[1];
+            scores<Tl>(kl + Tl::at(32 * kb, 0), qf, lane, s);
+            scores<Tl>(vl + Tl::at(32 * kb, 0), df, lane, g);
             float ds[16];
 #pragma unroll
-            for (int r = 0; r < 16; ++r) ds[r] = fast_exp2(fmaf(s[r], a.c, -lse)) * (g[r] - delta);
+            for (int r = 0; r < 16; ++r) ds[r] = fast_exp2(fmaf(s[0][r], a.c, -lse)) * (g[0][r] - delta);
             if (!whole) {
                 // (a tile of sinks: all of them, up to its end)
                 const Mask mask(n < walk.nsink ? walk.sunk - 1 : t, j0, h, n < walk.nsink ? kAttnFar : a.window, a.sinks);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) ds[r] = (mask.seen(place(kb, r)) & !alone) ? ds[r] : 0.f;
             }
+            Frag<T> kf[2][DB];
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                for (int db = 0; db < DB; ++db) Tl::across(kl, 32 * kb + 16 * ks, 32 * db, lane, kf[ks][db]);
+            group_end();
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 Frag<T> sf;
-                to_frag(ds, ks, sf);
+                to_frag(reinterpret_cast<const float(&)[8]>(ds[8 * ks]), sf);
 #pragma unroll
-                for (int db = 0; db < DB; ++db) {
-                    Frag<T> kf;
-                    Tl::across(kl, 32 * kb + 16 * ks, 32 * db, lane, kf);
-                    o[db] = mma(kf, sf, o[db]);
-                }
+                for (int db = 0; db < DB; ++db) o[db] = mma(kf[ks][db], sf, o[db]);
             }
         }
+    }
+    if constexpr (SHARED) {
+        floatx4 *sums = reinterpret_cast<floatx4 *>(lds) + lane;  // (wave, register quad, lane)
+        __syncthreads();
+        if (wave > 0) {
+#pragma unroll
+            for (int q = 0; q < DB * 4; ++q)
+                sums[((wave - 1) * DB * 4 + q) * 64] = floatx4{o[q / 4][4 * (q % 4)], o[q / 4][4 * (q % 4) + 1], o[q / 4][4 * (q % 4) + 2], o[q / 4][4 * (q % 4) + 3]};
+        }
+        __syncthreads();
+        if (wave > 0) return;
+#pragma unroll
+        for (int of = 0; of < NW - 1; ++of)
+#pragma unroll
+            for (int q = 0; q < DB * 4; ++q) {
+                const floatx4 x = sums[(of * DB * 4 + q) * 64];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[q / 4][4 * (q % 4) + e] += x[e];
+            }
     }
     if (w0 >= a.L) return;  // (no barrier follows)
 
@@ -274,6 +305,11 @@ __global__ __launch_bounds__((64 * KW * G), 1) void attn_dkv_kernel(const AttnBw
         }
     };
 
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+        arrived(kf[s]);
+        arrived(vf[s]);
+    }
     const bool lone = a.window == 1 && a.sinks == 0;
     floatx16 dk[DB], dv[DB];
 #pragma unroll
@@ -294,15 +330,10 @@ __global__ __launch_bounds__((64 * KW * G), 1) void attn_dkv_kernel(const AttnBw
             if (SINKS ? w0 >= a.sinks || t0 + 31 - w0 < a.window : t0 + 31 < w0 || t0 - w0 - 31 >= a.window) continue;
             if (t0 >= hi) continue;
             const bool whole = SINKS ? w0 + 32 <= a.sinks && t0 - w0 - 31 >= a.window : t0 >= w0 + 31 && t0 + 31 - w0 < a.window;
-            floatx16 s = zero16(), g = zero16();
-#pragma unroll
-            for (int ks = 0; ks < NS; ++ks) {
-                Frag<T> f;
-                Tl::down(ql, q0, ks, lane, f);
-                s = mma(f, kf[ks], s);
-                Tl::down(dl, q0, ks, lane, f);
-                g = mma(f, vf[ks], g);
-            }
+            floatx16 sc[1], gr[1];
+            scores<Tl>(ql + Tl::at(q0, 0), kf, lane, sc);
+            scores<Tl>(dl + Tl::at(q0, 0), vf, lane, gr);
+            const floatx16 &s = sc[0], &g = gr[0];
             float p[16], ds[16];
 #pragma unroll
             for (int r = 0; r < 16; r += 2) {
@@ -325,19 +356,30 @@ __global__ __launch_bounds__((64 * KW * G), 1) void attn_dkv_kernel(const AttnBw
                     ds[r] = (on & (at != first) & !lone) ? ds[r] : 0.f;
                 }
             }
+            Frag<T> f[2][DB];
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                for (int db = 0; db < DB; ++db) Tl::across(dl, q0 + 16 * ks, 32 * db, lane, f[ks][db]);
+            group_end();
+            Frag<T> f2[2][DB];
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-                Frag<T> pf, sf;
-                to_frag(p, ks, pf);
-                to_frag(ds, ks, sf);
+                Frag<T> pf;
+                to_frag(reinterpret_cast<const float(&)[8]>(p[8 * ks]), pf);
 #pragma unroll
                 for (int db = 0; db < DB; ++db) {
-                    Frag<T> f;
-                    Tl::across(dl, q0 + 16 * ks, 32 * db, lane, f);
-                    dv[db] = mma(f, pf, dv[db]);
-                    Tl::across(ql, q0 + 16 * ks, 32 * db, lane, f);
-                    dk[db] = mma(f, sf, dk[db]);
+                    Tl::across(ql, q0 + 16 * ks, 32 * db, lane, f2[ks][db]);
+                    dv[db] = mma(f[ks][db], pf, dv[db]);
                 }
+            }
+            group_end();
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                Frag<T> sf;
+                to_frag(reinterpret_cast<const float(&)[8]>(ds[8 * ks]), sf);
+#pragma unroll
+                for (int db = 0; db < DB; ++db) dk[db] = mma(f2[ks][db], sf, dk[db]);
             }
         }
         tile += QT;
@@ -478,12 +520,24 @@ hipError_t attn_bwd_sized(const AttnBwdIn<T> &in, int64_t batch, hipStream_t str
     // two groups of waves where a wave's registers (keys, values, their gradients) leave room for two on a SIMD
     constexpr bool kSmall = D * sizeof(T) <= 128;
     constexpr int G = kSmall ? 2 : 1, QB = sizeof(T) == 2 && !kSmall ? 2 : 1, GS = D * sizeof(T) <= 256 ? 4 : 2;
-    hipError_t e = allow_lds<attn_dq_kernel<T, D>>(kLds);
-    if (e != hipSuccess) return e;
-    attn_dq_kernel<T, D><<<dim3((uint32_t)(batch * in.heads * ((in.L + kQueries - 1) / kQueries))), dim3(256), kLds, stream>>>(in);
+    // fewer blocks of 128 than compute units: blocks of 32, whose waves share them and part the rest
+    const int64_t rows = batch * in.heads, qblocks = rows * ((in.L + kQueries - 1) / kQueries);
+    hipError_t e;
+    if (qblocks < kFewBlocks) {
+        constexpr int kWaveLds = WaveLds<T, D>::kCopies;
+        e = allow_lds<attn_dq_kernel<T, D, true>>(kWaveLds);
+        if (e != hipSuccess) return e;
+        attn_dq_kernel<T, D, true><<<dim3((uint32_t)(rows * ((in.L + 31) / 32))), dim3(64 * WaveLds<T, D>::kWaves), kWaveLds, stream>>>(in);
+    } else {
+        e = allow_lds<attn_dq_kernel<T, D, false>>(kLds);
+        if (e != hipSuccess) return e;
+        attn_dq_kernel<T, D, false><<<dim3((uint32_t)qblocks), dim3(256), kLds, stream>>>(in);
+    }
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const int64_t heads = batch * in.kvheads;
-    e = attn_dkv_launch<T, D, 4, G, QB, false>(in, heads * ((in.L + 127) / 128), stream);
+    const int64_t blocks = heads * ((in.L + 127) / 128);
+    e = blocks < kFewBlocks ? attn_dkv_launch<T, D, 1, GS, 1, false>(in, heads * ((in.L + 31) / 32), stream)
+                            : attn_dkv_launch<T, D, 4, G, QB, false>(in, blocks, stream);
     if (e != hipSuccess || in.sink_tiles == 0) return e;
     e = attn_dkv_launch<T, D, 1, GS, 1, true>(in, heads * in.sink_tiles * in.nchunks, stream);
     if (e != hipSuccess) return e;

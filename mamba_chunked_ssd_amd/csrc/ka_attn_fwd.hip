@@ -45,8 +45,11 @@ struct Keys {
     }
 };
 
-template <typename T, int D, int KB>
-__device__ __forceinline__ void hide(floatx16 (&s)[KB], const Walk<32 * KB> &w, int n, int j0, int t, int h, int window, int sinks) {
+// What a lane's query t, one of the wave's from w0 on, does not see of 32 KB keys from token j0, of tile n, becomes
+// -infinity.
+template <int KT, int KB>
+__device__ __forceinline__ void hide(floatx16 (&s)[KB], const Walk<KT> &w, int n, int j0, int t, int w0, int h, int window, int sinks) {
+    const Needs need(j0, 32 * KB, w0, window, sinks);
     const Mask mask(t, j0, h, window, sinks);
     if (n < w.nsink) {
         const int sunk = w.sunk - j0 - 4 * h;
@@ -54,12 +57,22 @@ __device__ __forceinline__ void hide(floatx16 (&s)[KB], const Walk<32 * KB> &w, 
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[kb][r] = place(kb, r) < sunk ? s[kb][r] : -kInf;
-        return;
+    } else if (!need.before) {
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[kb][r] = place(kb, r) <= mask.last ? s[kb][r] : -kInf;
+    } else if (!need.last && j0 >= sinks) {
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[kb][r] = place(kb, r) > mask.before ? s[kb][r] : -kInf;
+    } else {
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[kb][r] = mask.seen(place(kb, r)) ? s[kb][r] : -kInf;
     }
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s[kb][r] = mask.seen(place(kb, r)) ? s[kb][r] : -kInf;
     if (j0 < 0) {
         const int none = -j0 - 4 * h;
 #pragma unroll
@@ -183,6 +196,8 @@ __global__ __launch_bounds__(256, (sizeof(T) == 2 ? (D == 32 ? 4 : D == 64 ? 3 :
         }
     };
 
+#pragma unroll
+    for (int s = 0; s < NS; ++s) arrived(qf[s]);
     Running<T, D> run;
     run.init();
     const int w0 = t0 + 32 * wave, w1 = min(w0 + 31, p.end - 1);  // the wave's queries
@@ -192,24 +207,15 @@ __global__ __launch_bounds__(256, (sizeof(T) == 2 ? (D == 32 ? 4 : D == 64 ? 3 :
             __syncthreads();
         }
         if (n + 1 < walk.ntiles) stage(n + 1);
-        const int j0 = walk.start(n);
-        if (n < 0 || w0 >= p.end || j0 > w1) continue;
-        if (n >= walk.nsink && j0 + KT <= w0 - a.window + 1 && j0 >= a.sinks) continue;
+        if (n < 0 || w0 >= p.end) continue;
         const unsigned char *kl = lds + (n & 1) * 2 * Tl::kBytes, *vl = kl + Tl::kBytes;
+        const int j0 = walk.start(n);
+        if (j0 > w1 || (n >= walk.nsink && j0 + KT <= w0 - a.window + 1 && j0 >= a.sinks)) continue;
         floatx16 s[KB];
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-            s[kb] = zero16();
-#pragma unroll
-            for (int ks = 0; ks < NS; ++ks) {
-                Frag<T> kf;
-                Tl::down(kl, 32 * kb, ks, lane, kf);
-                s[kb] = mma(kf, qf[ks], s[kb]);
-            }
-        }
+        scores<Tl>(kl, qf, lane, s);
         const bool whole = n < walk.nsink ? j0 + KT <= walk.sunk
                                           : j0 >= 0 && j0 + KT - 1 <= w0 && (w0 + 31 - j0 < a.window || j0 + KT <= a.sinks);
-        if (!whole) hide<T, D, KB>(s, walk, n, j0, t, h, a.window, a.sinks);
+        if (!whole) hide(s, walk, n, j0, t, w0, h, a.window, a.sinks);
         run.template take<Tl, KB>(s, a.c, vl, 0, lane);
     }
     if (w0 - p.first >= a.L) return;  // (no barrier follows)
@@ -279,6 +285,8 @@ __global__ __launch_bounds__((64 * WaveLds<T, D>::kWaves), 1) void attn_fwd_shar
             Tl::template gather<64>(kl + Tl::kBytes, [&](int r) { return walk.held(n, j0 + r, a.sinks, p.end) ? values.of(j0 + r) : nullptr; });
         }
     };
+#pragma unroll
+    for (int s = 0; s < NS; ++s) arrived(qf[s]);
     Running<T, D> run;
     run.init();
     int buf = 0;
@@ -289,16 +297,11 @@ __global__ __launch_bounds__((64 * WaveLds<T, D>::kWaves), 1) void attn_fwd_shar
         if (n < 0) continue;
         const unsigned char *kl = own + buf * kStage;
         const int j0 = walk.start(n);
-        floatx16 s[1] = {zero16()};
-#pragma unroll
-        for (int ks = 0; ks < NS; ++ks) {
-            Frag<T> kf;
-            Tl::down(kl, 0, ks, lane, kf);
-            s[0] = mma(kf, qf[ks], s[0]);
-        }
+        floatx16 s[1];
+        scores<Tl>(kl, qf, lane, s);
         const bool whole = n < walk.nsink ? j0 + 32 <= walk.sunk
                                           : j0 >= 0 && j0 + 31 <= t0 && (t0 + 31 - j0 < a.window || j0 + 32 <= a.sinks);
-        if (!whole) hide<T, D, 1>(s, walk, n, j0, t, h, a.window, a.sinks);
+        if (!whole) hide(s, walk, n, j0, t, t0, h, a.window, a.sinks);
         run.template take<Tl, 1>(s, a.c, kl + Tl::kBytes, 0, lane);
     }
     if (threadIdx.x == 0) again = 0;  // (Join's barriers come before its use)

@@ -73,6 +73,8 @@ __global__ __launch_bounds__((64 * WaveLds<T, D>::kWaves), 1) void attn_step_ker
         copier.copy(kl + Tl::kBytes, a.vc + cache + (int64_t)at * D, min(s1 - at, 32));
     };
 
+#pragma unroll
+    for (int s = 0; s < NS; ++s) arrived(qf[s]);
     Running<T, D> run;
     run.init();
     int at = s0 + 32 * wave, buf = 0;
@@ -98,13 +100,8 @@ __global__ __launch_bounds__((64 * WaveLds<T, D>::kWaves), 1) void attn_step_ker
             }
             lds_dma_wait();
         }
-        floatx16 s[1] = {zero16()};
-#pragma unroll
-        for (int ks = 0; ks < NS; ++ks) {
-            Frag<T> kf;
-            Tl::down(kl, 0, ks, lane, kf);
-            s[0] = mma(kf, qf[ks], s[0]);
-        }
+        floatx16 s[1];
+        scores<Tl>(kl, qf, lane, s);
         if (at + 32 > s1) {
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[0][r] = place(0, r) < s1 - at - 4 * h ? s[0][r] : -kInf;

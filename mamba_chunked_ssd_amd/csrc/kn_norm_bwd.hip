@@ -213,18 +213,29 @@ __global__ __launch_bounds__(256) void norm_bwd_long_kernel(const NormBwdIn a) {
     }
 }
 
-// dweight: the blocks' partial sums, 16 threads a column, in 64 bits.
-__global__ __launch_bounds__(256) void norm_dweight_kernel(const float *partials, int parts, int C, float *dweight) {
-    __shared__ double room[16][16];
-    const int col = threadIdx.x & 15, slice = threadIdx.x >> 4;
-    for (int base = blockIdx.x * 16; base < C; base += gridDim.x * 16) {
+// dweight: the blocks' partial sums, a wave's width of columns by 16 slices of
+// the blocks, in 64 bits.  Loads of several blocks are on their way at a time.
+__global__ __launch_bounds__(1024) void norm_dweight_kernel(const float *partials, int parts, int C, float *dweight) {
+    __shared__ double room[16][64];
+    const int col = threadIdx.x & 63, slice = threadIdx.x >> 6;
+    for (int base = blockIdx.x * 64; base < C; base += gridDim.x * 64) {
         const int c = base + col;
         double s = 0.0;
-        if (c < C)
-            for (int p = slice; p < parts; p += 16) s += (double)partials[(int64_t)p * C + c];
+        if (c < C) {
+            int p = slice;
+            for (; p + 16 * 7 < parts; p += 16 * 8) {
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = partials[(int64_t)(p + 16 * k) * C + c];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) s += (double)v[k];
+            }
+            for (; p < parts; p += 16) s += (double)partials[(int64_t)p * C + c];
+        }
         room[slice][col] = s;
         __syncthreads();
         if (slice == 0 && c < C) {
+#pragma unroll
             for (int k = 1; k < 16; ++k) s += room[k][col];
             dweight[c] = (float)s;
         }
@@ -257,7 +268,7 @@ hipError_t launch_norm_bwd(const NormArgs &a, const NormBwdPlan &plan, hipStream
     if (y16) e = u16 ? norm_bwd_typed<uint16_t, uint16_t>(in, plan.parts, stream) : norm_bwd_typed<uint16_t, float>(in, plan.parts, stream);
     else e = u16 ? norm_bwd_typed<float, uint16_t>(in, plan.parts, stream) : norm_bwd_typed<float, float>(in, plan.parts, stream);
     if (e != hipSuccess || a.dweight == nullptr) return e;
-    norm_dweight_kernel<<<dim3(std::min((a.channels + 15) / 16, 1 << 16)), dim3(256), 0, stream>>>(a.partials, plan.parts, a.channels, a.dweight);
+    norm_dweight_kernel<<<dim3(std::min((a.channels + 63) / 64, 1 << 16)), dim3(1024), 0, stream>>>(a.partials, plan.parts, a.channels, a.dweight);
     return hipGetLastError();
 }
 
