@@ -1109,7 +1109,7 @@ def window_attention_fwd(q, k, v, window=None, sinks: int = 0, *, scale=None, le
         _dense(out, "out", dtype, (b, L, h, d), dev, torch.Tensor)
 
     def run(handle):
-        y = out if out is not None else torch.empty((b, L, h, d), dtype=dtype, device=dev)
+        y = out if out is not None else _rows_like(q, shape.q, (b, L, h, d), dtype, dev, torch)
         lse = torch.empty((b, h, L), dtype=torch.float32, device=dev) if return_lse else None
         st = load_library().ssd_window_attn_fwd(ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                                 _addr(positions), _addr(lengths), _addr(k_cache), _addr(v_cache),
@@ -1139,7 +1139,8 @@ def window_attention_bwd(q, k, v, y, lse, dy, window=None, sinks: int = 0, *, sc
         _dense(lengths, "lengths", torch.int32, (b,), dev, torch.Tensor)
 
     def run(handle):
-        res = {"dq": torch.empty((b, L, h, d), dtype=dtype, device=dev), "dk": torch.empty((b, L, kv, d), dtype=dtype, device=dev)}
+        res = {"dq": _rows_like(q, shape.q, (b, L, h, d), dtype, dev, torch),
+               "dk": _rows_like(k, shape.k, (b, L, kv, d), dtype, dev, torch)}
         res["dv"] = torch.empty_like(res["dk"])
         ws, size, _keep = _workspace(workspace, lib.ssd_window_attn_bwd_workspace_size(ctypes.byref(shape)), dev, torch)
         st = lib.ssd_window_attn_bwd(ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(), y.data_ptr(),
@@ -1171,7 +1172,7 @@ def window_attention_step(q, k, v, k_cache, v_cache, positions, window, sinks: i
         _dense(out, "out", dtype, (b, h, d), dev, torch.Tensor)
 
     def run(handle):
-        y = out if out is not None else torch.empty((b, h, d), dtype=dtype, device=dev)
+        y = out if out is not None else _rows_like(q, shape.q, (b, h, d), dtype, dev, torch)
         ws, size, _keep = _workspace(workspace, lib.ssd_window_attn_step_workspace_size(ctypes.byref(shape)), dev, torch)
         st = lib.ssd_window_attn_step(ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                       positions.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), y.data_ptr(), ws,
@@ -1211,6 +1212,9 @@ def _norm_args(x, name, weight, eps, lengths, torch):
 
 def _norm_rows(t, name, dtype, shape, device, torch):
     """:func:`_rows` of tokens in one or two dimensions."""
+    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.get_device() == device.index \
+            and t.is_contiguous():
+        return None
     if len(shape) == 2 and isinstance(t, torch.Tensor) and t.dim() == 2:
         return _rows(t[None], name, dtype, (1, *shape), device, torch.Tensor, 2)
     return _rows(t, name, dtype, shape, device, torch.Tensor, 2)
@@ -1265,12 +1269,13 @@ def rms_norm_fwd(x, weight=None, residual=None, *, eps: float = 1e-5, lengths=No
         _dense(residual_out, "residual_out", rtype, dims, dev, torch.Tensor)
 
     def run(handle):
-        y = out if out is not None else torch.empty(dims, dtype=ytype, device=dev)
+        y = out if out is not None else _rows_like(x, shape.x, dims, ytype, dev, torch)
         scales, u = scales_out, residual_out
         if codes and scales is None:
             scales = torch.empty(sdims, dtype=torch.float32, device=dev)
         if u is None and return_residual:
-            u = torch.empty(dims, dtype=rtype, device=dev)
+            u = torch.empty(dims, dtype=rtype, device=dev) if residual is None else \
+                _rows_like(residual, shape.residual, dims, rtype, dev, torch)
         st = load_library().ssd_rms_norm_fwd(ctypes.byref(shape), x.data_ptr(), _addr(residual), _addr(weight),
                                              _addr(lengths), y.data_ptr(), _addr(scales), _addr(u), handle)
         got = (y,) + ((scales,) if codes else ()) + ((u,) if return_residual else ())
@@ -1306,11 +1311,12 @@ def rms_norm_bwd(dy, u, weight=None, d_residual=None, *, eps: float = 1e-5, leng
     shape.dtype = SSD_DTYPE_F32 if xtype == torch.float32 else SSD_DTYPE_BF16
 
     def run(handle):
-        res = {"dx": torch.empty(dims, dtype=xtype, device=dev)}
+        res = {"dx": _rows_like(u, shape.residual, dims, xtype, dev, torch)}
         if want_dresidual:
-            res["dresidual"] = torch.empty(dims, dtype=u.dtype, device=dev)
+            res["dresidual"] = _rows_like(u, shape.residual, dims, u.dtype, dev, torch)
         if want_dweight:
-            res["dweight"] = torch.empty((dims[-1],), dtype=torch.float32, device=dev)
+            res["dweight"] = torch.empty((dims[-1],), dtype=torch.float32, device=dev) if weight is None else \
+                torch.empty_like(weight)
         ws, size, _keep = _workspace(workspace, lib.ssd_rms_norm_bwd_workspace_size(ctypes.byref(shape)), dev, torch)
         st = lib.ssd_rms_norm_bwd(ctypes.byref(shape), dy.data_ptr(), u.data_ptr(), _addr(weight), _addr(d_residual),
                                   _addr(lengths), res["dx"].data_ptr(), _addr(res.get("dresidual")),

@@ -327,6 +327,31 @@ __device__ __forceinline__ void scores(const unsigned char *k, const Frag<T> (&q
     }
 }
 
+// s = X A^T and g = Y B^T of 32 rows of the tiles at x and y, side by side: neither chain of products waits for itself,
+// and where registers hold them all, both operands are read at once.
+template <typename Tl, typename T, int NS>
+__device__ __forceinline__ void both_scores(const unsigned char *x, const unsigned char *y, const Frag<T> (&a)[NS],
+                                            const Frag<T> (&b)[NS], int lane, floatx16 &s, floatx16 &g) {
+    constexpr int kAtOnce = NS * sizeof(T) <= 8 ? NS : NS / 2;
+    s = zero16();
+    g = zero16();
+#pragma unroll
+    for (int k0 = 0; k0 < NS; k0 += kAtOnce) {
+        Frag<T> xf[kAtOnce], yf[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            Tl::down(x, 0, k0 + k, lane, xf[k]);
+            Tl::down(y, 0, k0 + k, lane, yf[k]);
+        }
+        group_end();
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            s = mma(xf[k], a[k0 + k], s);
+            g = mma(yf[k], b[k0 + k], g);
+        }
+    }
+}
+
 // Results of NW waves over the same 32 columns joined through LDS: (wave,
 // column, m and l), then (wave, column, D values).  write(column, element,
 // value, m, l) gets the joined sums, not yet divided, of the first `columns`.

@@ -23,7 +23,9 @@ namespace ssd {
 namespace {
 
 constexpr int kQueries = 128;
-constexpr int64_t kFewBlocks = 256;
+constexpr int64_t kFewQueries = 160;
+template <typename T>
+constexpr int64_t kFewKeys = sizeof(T) == 2 ? 100 : 200;
 
 template <typename T>
 struct AttnBwdIn {
@@ -145,24 +147,23 @@ __global__ __launch_bounds__((SHARED ? 64 * WaveLds<T, D>::kWaves : 256), (!SHAR
                                           : j0 + KT - 1 <= w0 && (w0 + 31 - j0 < a.window || j0 + KT <= a.sinks);
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
-            floatx16 s[1], g[1];
-            scores<Tl>(kl + Tl::at(32 * kb, 0), qf, lane, s);
-            scores<Tl>(vl + Tl::at(32 * kb, 0), df, lane, g);
-            float ds[16];
-#pragma unroll
-            for (int r = 0; r < 16; ++r) ds[r] = fast_exp2(fmaf(s[0][r], a.c, -lse)) * (g[0][r] - delta);
-            if (!whole) {
-                // (a tile of sinks: all of them, up to its end)
-                const Mask mask(n < walk.nsink ? walk.sunk - 1 : t, j0, h, n < walk.nsink ? kAttnFar : a.window, a.sinks);
-#pragma unroll
-                for (int r = 0; r < 16; ++r) ds[r] = (mask.seen(place(kb, r)) & !alone) ? ds[r] : 0.f;
-            }
+            floatx16 s, g;
+            both_scores<Tl>(kl + Tl::at(32 * kb, 0), vl + Tl::at(32 * kb, 0), qf, df, lane, s, g);
             Frag<T> kf[2][DB];
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
                 for (int db = 0; db < DB; ++db) Tl::across(kl, 32 * kb + 16 * ks, 32 * db, lane, kf[ks][db]);
             group_end();
+            float ds[16];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) ds[r] = fast_exp2(fmaf(s[r], a.c, -lse)) * (g[r] - delta);
+            if (!whole) {
+                // (a tile of sinks: all of them, up to its end)
+                const Mask mask(n < walk.nsink ? walk.sunk - 1 : t, j0, h, n < walk.nsink ? kAttnFar : a.window, a.sinks);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) ds[r] = (mask.seen(place(kb, r)) & !alone) ? ds[r] : 0.f;
+            }
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 Frag<T> sf;
@@ -244,8 +245,9 @@ __global__ __launch_bounds__((SHARED ? 64 * WaveLds<T, D>::kWaves : 256), (!SHAR
 // the way while another is in use.  dv^T += dY^T P and dk^T += Q^T dS take the
 // same tiles across.  The groups' sums are added at the end, in order.
 //
-// SINKS: the queries are a chunk of those that see the block's keys as sinks
-// alone; else all those that see them through the window.
+// A block's queries are all those that see its keys through the window, or a
+// chunk of those that see them as sinks alone (blocks behind `tiles`).
+enum class Part { window, sinks, both };
 template <typename T, int D, int KW, int G, int QB>
 struct KeyLds {
     typedef Tile<T, D, 32 * G * QB> Tl;
@@ -254,22 +256,24 @@ struct KeyLds {
     static constexpr int kBytes = 2 * kStage > kSums ? 2 * kStage : kSums;
 };
 
-template <typename T, int D, int KW, int G, int QB, bool SINKS>
+template <typename T, int D, int KW, int G, int QB, Part PART>
 __global__ __launch_bounds__((64 * KW * G), 1) void attn_dkv_kernel(const AttnBwdIn<T> a) {
     constexpr int NS = D / 16, DB = D / 32, NW = KW * G, QT = 32 * G * QB;
     typedef KeyLds<T, D, KW, G, QB> Lds;
     typedef typename Lds::Tl Tl;
     extern __shared__ __align__(16) unsigned char lds[];  // (2 stages: queries, dy, stats); then a group's sums
 
-    const int group = a.heads / a.kvheads, tiles = SINKS ? a.sink_tiles * a.nchunks : (a.L + 32 * KW - 1) / (32 * KW);
+    const int group = a.heads / a.kvheads, tiles = PART == Part::sinks ? 0 : (a.L + 32 * KW - 1) / (32 * KW);
+    const int items = tiles + (PART == Part::window ? 0 : a.sink_tiles * a.nchunks);
     int n = xcd_remap((int)blockIdx.x, (int)gridDim.x);
-    const int item = n % tiles;
-    n /= tiles;
+    const int item = n % items;
+    n /= items;
     const int kvh = n % a.kvheads, b = n / a.kvheads;
     const int len = length_of(a.lengths, b, a.L);
-    const int part = SINKS ? 1 + item % a.nchunks : 0, j0 = (SINKS ? item / a.nchunks : item) * 32 * KW;
-    const int lo = SINKS ? max(a.window + (part - 1) * a.chunk, a.window + j0) : j0;
-    const int hi = SINKS ? min(len, a.window + part * a.chunk) : (int)min((int64_t)len, (int64_t)j0 + 32 * KW - 1 + a.window);
+    const bool far = PART == Part::both ? item >= tiles : PART == Part::sinks;
+    const int part = far ? 1 + (item - tiles) % a.nchunks : 0, j0 = (far ? (item - tiles) / a.nchunks : item) * 32 * KW;
+    const int lo = far ? max(a.window + (part - 1) * a.chunk, a.window + j0) : j0;
+    const int hi = far ? min(len, a.window + part * a.chunk) : (int)min((int64_t)len, (int64_t)j0 + 32 * KW - 1 + a.window);
     const int turns = hi > lo ? (hi - lo + QT - 1) / QT * group : 0;
 
     const int lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
@@ -327,22 +331,25 @@ __global__ __launch_bounds__((64 * KW * G), 1) void attn_dkv_kernel(const AttnBw
 #pragma unroll
         for (int qi = 0; qi < QB; ++qi) {
             const int q0 = 32 * (part_of * QB + qi), t0 = tile + q0;
-            if (SINKS ? w0 >= a.sinks || t0 + 31 - w0 < a.window : t0 + 31 < w0 || t0 - w0 - 31 >= a.window) continue;
+            if (far ? w0 >= a.sinks || t0 + 31 - w0 < a.window : t0 + 31 < w0 || t0 - w0 - 31 >= a.window) continue;
             if (t0 >= hi) continue;
-            const bool whole = SINKS ? w0 + 32 <= a.sinks && t0 - w0 - 31 >= a.window : t0 >= w0 + 31 && t0 + 31 - w0 < a.window;
-            floatx16 sc[1], gr[1];
-            scores<Tl>(ql + Tl::at(q0, 0), kf, lane, sc);
-            scores<Tl>(dl + Tl::at(q0, 0), vf, lane, gr);
-            const floatx16 &s = sc[0], &g = gr[0];
+            const bool whole = far ? w0 + 32 <= a.sinks && t0 - w0 - 31 >= a.window : t0 >= w0 + 31 && t0 + 31 - w0 < a.window;
+            floatx16 s, g;
+            both_scores<Tl>(ql + Tl::at(q0, 0), dl + Tl::at(q0, 0), kf, vf, lane, s, g);
+            floatx4 st[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) st[r] = *reinterpret_cast<const floatx4 *>(stats + q0 + place(0, 2 * r) + 4 * h);
+            Frag<T> f[2][DB];
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                for (int db = 0; db < DB; ++db) Tl::across(dl, q0 + 16 * ks, 32 * db, lane, f[ks][db]);
+            group_end();
             float p[16], ds[16];
 #pragma unroll
-            for (int r = 0; r < 16; r += 2) {
-                const floatx4 st = *reinterpret_cast<const floatx4 *>(stats + q0 + place(0, r) + 4 * h);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    p[r + e] = fast_exp2(fmaf(s[r + e], a.c, -st[2 * e]));
-                    ds[r + e] = p[r + e] * (g[r + e] - st[2 * e + 1]);
-                }
+            for (int r = 0; r < 16; ++r) {
+                p[r] = fast_exp2(fmaf(s[r], a.c, -st[r / 2][2 * (r % 2)]));
+                ds[r] = p[r] * (g[r] - st[r / 2][2 * (r % 2) + 1]);
             }
             if (!whole) {
                 // rows are queries here: t - j within a window of the key's
@@ -351,17 +358,11 @@ __global__ __launch_bounds__((64 * KW * G), 1) void attn_dkv_kernel(const AttnBw
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const int at = place(0, r), d = at + back;
-                    const bool on = SINKS ? (at < left) & (d >= a.window + sunk) : (at < left) & (d >= 0) & (d < a.window);
+                    const bool on = far ? (at < left) & (d >= a.window + sunk) : (at < left) & (d >= 0) & (d < a.window);
                     p[r] = on ? p[r] : 0.f;
                     ds[r] = (on & (at != first) & !lone) ? ds[r] : 0.f;
                 }
             }
-            Frag<T> f[2][DB];
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-                for (int db = 0; db < DB; ++db) Tl::across(dl, q0 + 16 * ks, 32 * db, lane, f[ks][db]);
-            group_end();
             Frag<T> f2[2][DB];
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
@@ -415,7 +416,7 @@ __global__ __launch_bounds__((64 * KW * G), 1) void attn_dkv_kernel(const AttnBw
     }
     if (part_of != 0 || w0 >= a.L) return;  // (no barrier follows)
 
-    const bool partial = SINKS || w0 < a.rows;
+    const bool partial = far || w0 < a.rows;
     const int64_t dense = ((int64_t)b * a.L + j) * a.kvheads * D + (int64_t)kvh * D;
     float *pk = a.partials + ((((int64_t)b * a.kvheads + kvh) * (1 + a.nchunks) + part) * 2 * a.rows + j) * D;
     float *pv = pk + a.rows * D;
@@ -445,7 +446,7 @@ __global__ __launch_bounds__((64 * KW * G), 1) void attn_dkv_kernel(const AttnBw
         again &= again - 1;
         const int jj = w0 + c;
         const T *kr = kh + (int64_t)jj * a.ks.row, *vr = vh + (int64_t)jj * a.vs.row;
-        const int t_lo = SINKS ? max(lo, jj + a.window) : jj, t_hi = SINKS ? (jj < a.sinks ? hi : t_lo) : (int)min((int64_t)hi, (int64_t)jj + a.window);
+        const int t_lo = far ? max(lo, jj + a.window) : jj, t_hi = far ? (jj < a.sinks ? hi : t_lo) : (int)min((int64_t)hi, (int64_t)jj + a.window);
         float acc[2][(D + 63) / 64] = {};
         for (int gh = 0; gh < group; ++gh) {
             const int of = kvh * group + gh;
@@ -505,12 +506,12 @@ __global__ __launch_bounds__(256) void attn_sinks_kernel(const AttnBwdIn<T> a, i
     }
 }
 
-template <typename T, int D, int KW, int G, int QB, bool SINKS>
+template <typename T, int D, int KW, int G, int QB, Part PART>
 hipError_t attn_dkv_launch(const AttnBwdIn<T> &in, int64_t blocks, hipStream_t stream) {
     constexpr int kLds = KeyLds<T, D, KW, G, QB>::kBytes;
-    const hipError_t e = allow_lds<attn_dkv_kernel<T, D, KW, G, QB, SINKS>>(kLds);
+    const hipError_t e = allow_lds<attn_dkv_kernel<T, D, KW, G, QB, PART>>(kLds);
     if (e != hipSuccess) return e;
-    attn_dkv_kernel<T, D, KW, G, QB, SINKS><<<dim3((uint32_t)blocks), dim3(64 * KW * G), kLds, stream>>>(in);
+    attn_dkv_kernel<T, D, KW, G, QB, PART><<<dim3((uint32_t)blocks), dim3(64 * KW * G), kLds, stream>>>(in);
     return hipGetLastError();
 }
 
@@ -523,7 +524,7 @@ hipError_t attn_bwd_sized(const AttnBwdIn<T> &in, int64_t batch, hipStream_t str
     // fewer blocks of 128 than compute units: blocks of 32, whose waves share them and part the rest
     const int64_t rows = batch * in.heads, qblocks = rows * ((in.L + kQueries - 1) / kQueries);
     hipError_t e;
-    if (qblocks < kFewBlocks) {
+    if (qblocks < kFewQueries) {
         constexpr int kWaveLds = WaveLds<T, D>::kCopies;
         e = allow_lds<attn_dq_kernel<T, D, true>>(kWaveLds);
         if (e != hipSuccess) return e;
@@ -536,11 +537,15 @@ hipError_t attn_bwd_sized(const AttnBwdIn<T> &in, int64_t batch, hipStream_t str
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const int64_t heads = batch * in.kvheads;
     const int64_t blocks = heads * ((in.L + 127) / 128);
-    e = blocks < kFewBlocks ? attn_dkv_launch<T, D, 1, GS, 1, false>(in, heads * ((in.L + 31) / 32), stream)
-                            : attn_dkv_launch<T, D, 4, G, QB, false>(in, blocks, stream);
-    if (e != hipSuccess || in.sink_tiles == 0) return e;
-    e = attn_dkv_launch<T, D, 1, GS, 1, true>(in, heads * in.sink_tiles * in.nchunks, stream);
-    if (e != hipSuccess) return e;
+    const int64_t chunks = heads * in.sink_tiles * in.nchunks;
+    if (blocks < kFewKeys<T>) {
+        // blocks of 32 keys, whose waves share them and part the queries; the sinks' among them
+        e = attn_dkv_launch<T, D, 1, GS, 1, Part::both>(in, heads * ((in.L + 31) / 32) + chunks, stream);
+    } else {
+        e = attn_dkv_launch<T, D, 4, G, QB, Part::window>(in, blocks, stream);
+        if (e == hipSuccess && chunks > 0) e = attn_dkv_launch<T, D, 1, GS, 1, Part::sinks>(in, chunks, stream);
+    }
+    if (e != hipSuccess || chunks == 0) return e;
     const int64_t n = 2 * heads * std::min<int64_t>(in.L, in.rows) * D;
     attn_sinks_kernel<T><<<dim3((uint32_t)std::min<int64_t>((n + 255) / 256, 1 << 16)), dim3(256), 0, stream>>>(in, heads, D);
     return hipGetLastError();

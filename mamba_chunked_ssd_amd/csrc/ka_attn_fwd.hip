@@ -17,7 +17,7 @@ namespace ssd {
 namespace {
 
 constexpr int kQueries = 128;  // of a block
-constexpr int64_t kAttnShared = 256;  // fewer blocks of 128 queries: the waves of a block share 32
+constexpr int64_t kAttnShared = 160;  // fewer blocks of 128 queries: the waves of a block share 32
 
 template <typename T>
 struct AttnIn {
