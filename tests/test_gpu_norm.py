@@ -142,28 +142,6 @@ def test_backward(case):
             assert not got["dx"][i, end:].any() and not got["dresidual"][i, end:].any()
 
 
-def test_gradients_against_differences():
-    # the fp64 oracle's own gradients, by central differences of its forward pass: error h^2 f''' / 6 and rounding
-    # 2^-53 |f| / h, with h = 1e-5 below 1e-8 here
-    rng = np.random.default_rng(1)
-    x, w, dy, dres = rng.standard_normal((1, 3, 6)), rng.standard_normal(6), rng.standard_normal((1, 3, 6)), rng.standard_normal((1, 3, 6))
-    du, dw, _, _ = mo.norm_bwd(dy, x, w, dres)
-
-    def loss(x, w):
-        u, y = mo.norm(x, w)
-        return (y * dy).sum() + (u * dres).sum()
-
-    h = 1e-5
-    for i in np.ndindex(x.shape):
-        e = np.zeros(x.shape)
-        e[i] = h
-        assert abs((loss(x + e, w) - loss(x - e, w)) / (2 * h) - du[i]) < 1e-7
-    for i in range(6):
-        e = np.zeros(6)
-        e[i] = h
-        assert abs((loss(x, w + e) - loss(x, w - e)) / (2 * h) - dw[i]) < 1e-7
-
-
 @pytest.mark.parametrize("c", [7, 200, 5000, 17000])
 def test_without_weight_stream_or_requests(c):
     d = inputs(2, 3, c, "f32", "f32", "f32")
