@@ -594,7 +594,8 @@ ssd_status ssd_selective_scan_step(const ssd_selective_shape *shape, const void 
  * lie outside tokens too; a head's elements are contiguous, row is at least
  * headdim where seqlen > 1 and below 2^22, all are >= 0 and multiples of 16 bytes
  * where there is more than one of their kind.  Inputs, outputs and caches are
- * 16-byte aligned (lse, positions, lengths 4).  Products of bf16
+ * 16-byte aligned (lse, positions, lengths 4); batch x nheads x (seqlen / 32 + 4)
+ * must stay below 2^25.  Products of bf16
  * inputs run on the matrix cores with fp32 sums; the weights p and the
  * gradients of the scores are rounded to bf16 as operands of the next product,
  * never the softmax's maxima and sums.  Products of fp32 inputs are fp32.

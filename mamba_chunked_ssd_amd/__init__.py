@@ -731,9 +731,9 @@ def _addr(t):
 
 
 def _rows_like(x, stride, shape, dtype, device, torch):
-    """A new dense tensor; ``empty_like`` is the cheaper call where x has that shape, type and layout."""
-    if dtype == x.dtype and stride.row == 0:
-        return torch.empty_like(x)
+    """A new dense tensor of x's shape; ``empty_like`` is the cheaper call where x is dense."""
+    if stride.row == 0:
+        return torch.empty_like(x) if dtype == x.dtype else torch.empty_like(x, dtype=dtype)
     return torch.empty(shape, dtype=dtype, device=device)
 
 

@@ -9,6 +9,13 @@
 // O^T = V^T P^T, so that a query is a lane's column throughout: its maximum, sum
 // and rescaling are the lane's own but for one exchange of the two halves, and P
 // stays in registers as the second product's operand.
+//
+// Bound by the waves' own chain of products, exponentials and waits at two (heads
+// of 128) or three (64) waves to a SIMD.  16 384 tokens, 8 heads of 128 over 2, a
+// window of 2048: 155 to 166 us, 780 to 840 TFLOP/s (an 8192^3 product of the
+// library: 1170); alone on its SIMD a wave takes 218.  2 x 2048 tokens, 40 heads of
+// 64 over 8, a window of 512: 41 us (one, two, three blocks to a compute unit: 77,
+// 49, 41).  LDS is no limit: its pipe is busy 17 % of the time, without conflicts.
 #include <algorithm>
 
 #include "ka_attn.h"
@@ -17,7 +24,10 @@ namespace ssd {
 namespace {
 
 constexpr int kQueries = 128;  // of a block
-constexpr int64_t kAttnShared = 160;  // fewer blocks of 128 queries: the waves of a block share 32
+// Fewer blocks of 128 queries than this: the waves of a block share 32.  8 heads
+// of 64 over 2, a window of 512: 128 blocks 21.3 us, shared 18.1; 256 blocks 22.8,
+// shared 27.3.  fp32, a window of 256: 128 blocks 39 and 32, 256 blocks 42 and 59.
+constexpr int64_t kAttnShared = 160;
 
 template <typename T>
 struct AttnIn {

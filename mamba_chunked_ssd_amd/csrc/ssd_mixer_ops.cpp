@@ -15,12 +15,15 @@
 
 namespace ssd {
 
+constexpr int64_t kStepTurns = 9;
+
 AttnBwdPlan attn_bwd_plan(const AttnArgs &a) {
     AttnBwdPlan p{};
     const int far = a.seqlen - a.window;  // queries that see token 0 as a sink only
     if (a.sinks == 0 || far <= 0) return p;
     const int keys = std::min(a.sinks, far);
     p.sink_tiles = (keys + kSinkKeys - 1) / kSinkKeys;
+    // one tile of the kernel's, or as many as leave 64 partial sums to add
     p.chunk = std::max(128, (far + 64 * 128 - 1) / (64 * 128) * 128);
     p.nchunks = (far + p.chunk - 1) / p.chunk;
     p.parts = 1 + p.nchunks;
@@ -28,15 +31,19 @@ AttnBwdPlan attn_bwd_plan(const AttnArgs &a) {
     return p;
 }
 
+// A block for all slots where that is a few turns of its waves, of 32 slots each:
+// a split takes a second launch and a workspace, some 5 us of the host's time.
+// One sequence, 8 heads of 64, 2052 slots (9 turns of eight waves, bf16): a call
+// 10.9 us, its kernel 10.5; in 17 blocks 15.1, its two kernels 5.3 and 4.3.
 AttnStepPlan attn_step_plan(const AttnArgs &a) {
-    const int64_t slots = (int64_t)a.window + a.sinks;
-    const int64_t units = std::max<int64_t>(1, a.batch * a.kvheads);
-    // four waves of 32 slots at the least
-    int64_t splits = std::min<int64_t>((slots + 127) / 128, std::max<int64_t>(1, 1024 / units));
-    const int64_t run = ((slots + splits - 1) / splits + 127) / 128 * 128;
+    const int64_t slots = (int64_t)a.window + a.sinks, turn = 32 * attn_step_waves(a.headdim, a.bf16 ? 2 : 4);
+    const int64_t units = std::max<int64_t>(1, a.batch * a.kvheads), turns = (slots + turn - 1) / turn;
+    const int64_t splits = turns <= kStepTurns ? 1 : std::min<int64_t>(turns, std::max<int64_t>(1, 1024 / units));
+    const int64_t run = (turns + splits - 1) / splits * turn;
     return AttnStepPlan{(int)((slots + run - 1) / run), (int)run};
 }
 
+// 512 blocks: two for each compute unit (a wave's registers leave one to a SIMD).
 NormBwdPlan norm_bwd_plan(const NormArgs &a) {
     const int64_t rows = a.batch * a.seqlen;
     const int64_t beside = a.channels <= kNormWaveRow ? 4 : 1;  // rows of a block at a time
@@ -115,11 +122,11 @@ ssd_status check_attn(const ssd_attn_shape *s, bool cached, AttnArgs *a, AttnByt
     }
     if (!whole) return SSD_ERROR_MISALIGNED;
     int64_t t;
-    // every buffer within int64, and fewer than 2^24 blocks of 128 queries (32 bits of threads)
+    // every buffer within int64, and fewer than 2^23 blocks of 128 queries or keys (and 512 threads at most: 32 bits)
     const int64_t slots = cached ? s->window + s->sinks : 0;
     if (!product({s->batch, s->nkvheads, slots, s->headdim, 4}, &t) ||
         !product({s->batch, s->seqlen, qw, 4}, &t) || !product({s->batch, s->nheads, s->seqlen / 32 + 4}, &t) ||
-        t >= (int64_t)1 << 26)
+        t >= (int64_t)1 << 25)
         return SSD_ERROR_UNSUPPORTED;
     a->batch = s->batch;
     a->seqlen = (int)s->seqlen;
@@ -155,7 +162,7 @@ size_t attn_step_carve(AttnArgs *a, const AttnStepPlan &p, void *ws) {
     return w.off;
 }
 
-// The backward pass's partial sums within int64, its blocks below 2^24.
+// The backward pass's partial sums within int64, its sinks' blocks below 2^23.
 ssd_status check_attn_bwd(const ssd_attn_shape *s, AttnArgs *a, AttnBytes *n) {
     const ssd_status st = check_attn(s, false, a, n);
     if (st != SSD_OK) return st;
@@ -163,7 +170,7 @@ ssd_status check_attn_bwd(const ssd_attn_shape *s, AttnArgs *a, AttnBytes *n) {
     int64_t t;
     if (!product({a->batch, a->kvheads, p.parts, 2 * p.rows, a->headdim, 4}, &t)) return SSD_ERROR_UNSUPPORTED;
     if (!product({a->batch * a->kvheads, (int64_t)p.sink_tiles * p.nchunks}, &t) ||
-        t >= (int64_t)1 << 24)
+        t >= (int64_t)1 << 23)
         return SSD_ERROR_UNSUPPORTED;
     return SSD_OK;
 }

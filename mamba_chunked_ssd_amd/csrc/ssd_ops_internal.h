@@ -173,6 +173,11 @@ AttnBwdPlan attn_bwd_plan(const AttnArgs &a);
 struct AttnStepPlan {
     int splits, run;
 };
+// Waves of a block: each has two stages of 32 keys and values in LDS, all of them 128 KB at most.
+constexpr int attn_step_waves(int headdim, int esz) {
+    const int stage = 2 * 32 * headdim * esz;
+    return stage <= 8192 ? 8 : stage <= 16384 ? 4 : 2;
+}
 AttnStepPlan attn_step_plan(const AttnArgs &a);
 
 hipError_t launch_attn_fwd(const AttnArgs &a, hipStream_t stream);

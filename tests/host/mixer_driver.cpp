@@ -106,9 +106,9 @@ static void plans() {
     for (int64_t b : {1, 3, 128, 65535})
         for (int64_t slots : {1, 31, 128, 129, 2052, 65536, 1 << 29}) {
             ssd::AttnArgs a{};
-            a.batch = b; a.window = (int)slots; a.heads = a.kvheads = 8;
+            a.batch = b; a.window = (int)slots; a.heads = a.kvheads = 8; a.headdim = 128; a.bf16 = b == 1;
             const ssd::AttnStepPlan p = ssd::attn_step_plan(a);
-            CHECK(p.splits >= 1 && p.run % 128 == 0 && (int64_t)p.splits * p.run >= slots && (int64_t)(p.splits - 1) * p.run < slots);
+            CHECK(p.splits >= 1 && p.run % (32 * ssd::attn_step_waves(128, a.bf16 ? 2 : 4)) == 0 && (int64_t)p.splits * p.run >= slots && (int64_t)(p.splits - 1) * p.run < slots);
             CHECK(p.splits == 1 || b * 8 * p.splits <= 1024 + b * 8);
         }
     for (int64_t rows : {0, 1, 5, 4096, 1 << 20, (1 << 30) - 1})

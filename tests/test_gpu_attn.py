@@ -188,6 +188,62 @@ def test_queries_that_see_one_token_alone(dtype):
                 assert bool(((y[0].double() - v).abs() <= (e + 2 * ROUND[dtype]) * v.abs()).all())
 
 
+# enough blocks of 128 queries, and of 128 keys, that none of the kernels for few is taken
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("h,kv,w,n,layout", [(8, 8, 40, 3, "sliced"), (24, 8, 200, 70, "dense"), (8, 8, 1, 0, "heads"),
+                                             (8, 8, 129, 0, "turned"), (16, 8, 9, 1, "dense")])
+def test_many_blocks(h, kv, w, n, layout, d, dtype):
+    b, L = 9, 300
+    lengths = [300, 0, 1, 299, 129, 128, 127, 33, 200]
+    s = inputs(b, L, h, kv, d, dtype, layout, lengths, seed=14)
+    y, lse = ssd.window_attention_fwd(s["q"], s["k"], s["v"], w, n, lengths=s["lengths"], return_lse=True)
+    got = ssd.window_attention_bwd(s["q"], s["k"], s["v"], y, lse, s["dy"], w, n, lengths=s["lengths"])
+    x = [s[m].double().nan_to_num().requires_grad_() for m in "qkv"]
+    ref, rlse, mag = dense(x, w, n, d ** -0.5)
+    on = (torch.arange(L, device="cuda")[None, :] < s["lengths"][:, None])[..., None, None]
+    (torch.where(on, ref, 0) * s["dy"].double()).sum().backward()
+    e, a = spread(s, d ** -0.5, w, n, d)
+    r = ROUND[dtype]
+    assert bool(((y.double() - torch.where(on, ref, 0)).abs() <= (e + r) * mag * on + r * ref.abs() * on).all())
+    live = on[..., 0].transpose(1, 2)
+    assert bool(((lse.double() - torch.where(live, rlse, 0)).abs() <= live * (2 * (d + 8) * a + L + 8 + 4 * rlse.abs()) * EPS).all())
+    for name, z in zip(("dq", "dk", "dv"), x):
+        if (w, n) == (1, 0) and name != "dv":
+            assert not bool(got[name].any())
+            continue
+        # 2-norms, whose errors average: the operands' roundings (a few short windows: no more than four of them)
+        off = float((got[name].double() - z.grad).norm() / z.grad.norm())
+        assert off <= (4 * r if r else 4e-6), (name, off)
+        for i, end in enumerate(lengths):
+            assert not bool(got[name][i, end:].any())
+
+
+@pytest.mark.parametrize("d,dtype", [(32, "f32"), (64, "bf16"), (128, "bf16"), (128, "f32")])
+@pytest.mark.parametrize("w,n,positions", [(16, 4, [0, 3, 17, 500]), (100, 0, [64, 99, 100, 333]), (33, 80, [10, 81, 200, 0])])
+def test_many_blocks_with_a_past(w, n, positions, d, dtype):
+    # the same four sequences once (few blocks) and twelve times (many): every copy gives the same
+    L, h, kv = 200, 4, 2
+    s = inputs(4, L, h, kv, d, dtype, "dense", [200, 131, 0, 64], w + n, positions, seed=15)
+    many = {k: v.repeat(12, *[1] * (v.dim() - 1)) for k, v in s.items()}
+
+    def call(z):
+        y, lse = ssd.window_attention_fwd(z["q"], z["k"], z["v"], w, n, lengths=z["lengths"], positions=z["positions"],
+                                          k_cache=z["kc"], v_cache=z["vc"], return_lse=True)
+        return y, lse, z["kc"], z["vc"]
+
+    few, all_ = call(s), call(many)
+    e, _ = spread(s, d ** -0.5, w, n, d)
+    most = max(1.0, float(s["vc"].abs().max()), float(s["v"].abs().max()))
+    for k, (p, q) in enumerate(zip(few, all_)):
+        q = q.unflatten(0, (12, 4))
+        assert all(torch.equal(q[0], c) for c in q[1:])
+        if k >= 2:
+            assert torch.equal(q[0], p)
+        else:  # two calculations, each within its bound
+            assert float((q[0].double() - p.double()).abs().max()) <= 2 * (e + 2 * ROUND[dtype]) * (most if k == 0 else 20)
+
+
 # (b, L, h, kv, d, window, sinks, dtype, lengths, positions): nothing behind, less than the sinks, than the window, a
 # ring that has turned, one far along; new tokens that fill the sinks, that overrun the whole ring
 PAST = [
@@ -253,7 +309,7 @@ def test_steps(h, kv, d, dtype, w, n):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("b,h,kv,d,w,n", [(1, 8, 2, 64, 1500, 4), (3, 4, 4, 128, 700, 0), (2, 70, 2, 32, 900, 130)])
+@pytest.mark.parametrize("b,h,kv,d,w,n", [(1, 8, 2, 64, 1500, 4), (1, 8, 2, 64, 4000, 4), (3, 4, 4, 128, 1700, 0), (2, 70, 2, 32, 2900, 130)])
 def test_steps_over_split_caches(b, h, kv, d, w, n, dtype):
     # few sequences: their slots are split over blocks.  Against the prompts' kernel
     s = inputs(b, 2, h, kv, d, dtype, "dense", None, w + n, [w + n + 5 + i for i in range(b)], seed=2)
@@ -314,9 +370,10 @@ def test_rows_behind_the_end_are_not_read():
 @pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 128), ("bf16", 32)])
 @pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan"), "largest"])
 @pytest.mark.parametrize("which", ["k", "v", "q", "dy"])
-def test_values_not_finite_reach_only_who_sees_them(dtype, d, value, which):
+@pytest.mark.parametrize("b", [1, 34])  # the kernels for few blocks, and the others
+def test_values_not_finite_reach_only_who_sees_them(b, dtype, d, value, which):
     # one token of the sequence holds them; rows that do not see it (and keys that it does not see) are as if it did not
-    b, L, h, kv, w, n, at = 1, 300, 4, 2, 20, 3, 150
+    L, h, kv, w, n, at = 300, 4, 2, 20, 3, 150
     s = inputs(b, L, h, kv, d, dtype, seed=8)
     value = torch.finfo(TYPES[dtype]).max if value == "largest" else value
     clean = {}
