@@ -531,7 +531,7 @@ hipError_t attn_bwd_sized(const AttnBwdIn<T> &in, int64_t batch, hipStream_t str
     constexpr int kLds = 2 * 2 * Tile<T, D, sizeof(T) == 2 ? 64 : 32>::kBytes;
     // two groups of waves where a wave's registers (keys, values, their gradients) leave room for two on a SIMD
     constexpr bool kSmall = D * sizeof(T) <= 128;
-    constexpr int G = kSmall ? 2 : 1, QB = sizeof(T) == 2 && !kSmall ? 2 : 1, GS = D * sizeof(T) <= 256 ? 4 : 2;
+    constexpr int G = kSmall ? 2 : 1, QB = sizeof(T) == 2 ? 2 : 1, GS = D * sizeof(T) <= 256 ? 4 : 2;
     // fewer blocks of 128 than compute units: blocks of 32, whose waves share them and part the rest
     const int64_t rows = batch * in.heads, qblocks = rows * ((in.L + kQueries - 1) / kQueries);
     hipError_t e;
