@@ -16,12 +16,15 @@
 // seen by every later query of the sequence too: those are cut into chunks, a
 // block each, and their sums added by a third kernel.
 //
-// 2 x 2048 tokens, 40 heads of 64 over 8, a window of 512, 4 sinks: 59 us over the
-// queries, 75 over the keys, 8 and 4 for the sinks; 10 products of headdim a pair
-// of tokens instead of 14 would need dq or dk and dv added up in memory.  Matrix
-// instructions take 17 and 20 % of that time, vector ones 41 and 20 %: the rest is
-// the waves' waiting, for LDS reads and for each other at the tiles' barriers
-// (three or four tiles on their way instead of one: no faster, so not for copies).
+// 2 x 2048 tokens, 40 heads of 64 over 8, a window of 512, 4 sinks, bf16: 55 us over
+// the queries, 64 over the keys, 8 and 4 for the sinks, 127 the call (372 TFLOP/s of
+// 10 products of headdim a pair of tokens); the 14 that two kernels form could only be
+// 10 with dq, or dk and dv, added up in memory.  Matrix instructions take 22 and 25 % of
+// that time, vector ones 34 and 29 %: the rest is the waves' waiting, for LDS reads and
+// for each other at the tiles' barriers (three or four tiles on their way instead of
+// one: no faster, so not for copies).  Over the queries, a wave leaves out blocks of 32
+// keys that none of its queries sees, not only whole tiles of 64: 59 to 55 us; tiles
+// of 128 keys took 68.
 #include <algorithm>
 
 #include "ka_attn.h"
@@ -30,10 +33,10 @@ namespace ssd {
 namespace {
 
 constexpr int kQueries = 128;
-// Fewer blocks of 128 queries, or of 128 keys, than these: blocks of 32.  Keys, in
-// all for bf16 heads of 64 over a window of 512: 64 blocks 102 us, of 32 keys 82; 128
-// blocks 123 and 133 (heads of 128: 274 and 301).  fp32: 128 blocks 104 and 85.
-// Queries: as in the forward pass.
+// Fewer blocks of 128 queries, or of 128 keys, than these: blocks of 32.  Keys, the
+// whole backward pass, bf16 heads of 64 over a window of 512: 64 blocks 90 us, of 32
+// keys 76; 128 blocks 111 and 124 (heads of 128: 259 and 289).  fp32, a window of 256:
+// 128 blocks 99 and 83, 256 blocks 114 and 139.  Queries: as in the forward pass.
 constexpr int64_t kFewQueries = 160;
 template <typename T>
 constexpr int64_t kFewKeys = sizeof(T) == 2 ? 100 : 200;
@@ -150,14 +153,14 @@ __global__ __launch_bounds__((SHARED ? 64 * WaveLds<T, D>::kWaves : 256), (!SHAR
             if constexpr (!SHARED) __syncthreads();
         }
         if (n + kStep < walk.ntiles) stage(n + kStep, buf ^ 1);
-        const int j0 = walk.start(n);
-        if (n < 0 || w0 >= len || j0 > w1) continue;
-        if (n >= walk.nsink && j0 + KT <= w0 - a.window + 1 && j0 >= a.sinks) continue;
+        if (n < 0 || w0 >= len) continue;
         const unsigned char *kl = own + buf * 2 * Tl::kBytes, *vl = kl + Tl::kBytes;
-        const bool whole = n < walk.nsink ? j0 + KT <= walk.sunk
-                                          : j0 + KT - 1 <= w0 && (w0 + 31 - j0 < a.window || j0 + KT <= a.sinks);
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
+            const int j0 = walk.start(n) + 32 * kb;
+            if (j0 > w1 || (n < walk.nsink ? j0 >= walk.sunk : j0 + 32 <= w0 - a.window + 1 && j0 >= a.sinks)) continue;
+            const bool whole = n < walk.nsink ? j0 + 32 <= walk.sunk
+                                              : j0 + 31 <= w0 && (w0 + 31 - j0 < a.window || j0 + 32 <= a.sinks);
             floatx16 s, g;
             both_scores<Tl>(kl + Tl::at(32 * kb, 0), vl + Tl::at(32 * kb, 0), qf, df, lane, s, g);
             Frag<T> kf[2][DB];
@@ -173,7 +176,7 @@ __global__ __launch_bounds__((SHARED ? 64 * WaveLds<T, D>::kWaves : 256), (!SHAR
                 // (a tile of sinks: all of them, up to its end)
                 const Mask mask(n < walk.nsink ? walk.sunk - 1 : t, j0, h, n < walk.nsink ? kAttnFar : a.window, a.sinks);
 #pragma unroll
-                for (int r = 0; r < 16; ++r) ds[r] = (mask.seen(place(kb, r)) & !alone) ? ds[r] : 0.f;
+                for (int r = 0; r < 16; ++r) ds[r] = (mask.seen(place(0, r)) & !alone) ? ds[r] : 0.f;
             }
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
@@ -531,6 +534,7 @@ hipError_t attn_bwd_sized(const AttnBwdIn<T> &in, int64_t batch, hipStream_t str
     constexpr int kLds = 2 * 2 * Tile<T, D, sizeof(T) == 2 ? 64 : 32>::kBytes;
     // two groups of waves where a wave's registers (keys, values, their gradients) leave room for two on a SIMD
     constexpr bool kSmall = D * sizeof(T) <= 128;
+    // blocks of queries for a wave and tile, bf16 heads of 64: one 75 us, two 64, four 67
     constexpr int G = kSmall ? 2 : 1, QB = sizeof(T) == 2 ? 2 : 1, GS = D * sizeof(T) <= 256 ? 4 : 2;
     // fewer blocks of 128 than compute units: blocks of 32, whose waves share them and part the rest
     const int64_t rows = batch * in.heads, qblocks = rows * ((in.L + kQueries - 1) / kQueries);
