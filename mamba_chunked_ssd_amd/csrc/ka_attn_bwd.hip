@@ -17,7 +17,7 @@
 // block each, and their sums added by a third kernel.
 //
 // 2 x 2048 tokens, 40 heads of 64 over 8, a window of 512, 4 sinks, bf16: 55 us over
-// the queries, 64 over the keys, 8 and 4 for the sinks, 127 the call (372 TFLOP/s of
+// the queries, 64 over the keys, 8 and 4 for the sinks, 125 the call (378 TFLOP/s of
 // 10 products of headdim a pair of tokens); the 14 that two kernels form could only be
 // 10 with dq, or dk and dv, added up in memory.  Matrix instructions take 22 and 25 % of
 // that time, vector ones 34 and 29 %: the rest is the waves' waiting, for LDS reads and
@@ -133,6 +133,9 @@ __global__ __launch_bounds__((SHARED ? 64 * WaveLds<T, D>::kWaves : 256), (!SHAR
         kcopy.copy(kl, kh + (int64_t)j0 * a.ks.row, rows);
         vcopy.copy(kl + Tl::kBytes, vh + (int64_t)j0 * a.vs.row, rows);
     };
+    constexpr int kStep = SHARED ? NW : 1;
+    const int first = SHARED ? wave : 0;
+    if (first < walk.ntiles) stage(first, 0);
 
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
@@ -144,16 +147,13 @@ __global__ __launch_bounds__((SHARED ? 64 * WaveLds<T, D>::kWaves : 256), (!SHAR
     for (int db = 0; db < DB; ++db) o[db] = zero16();
     const int w1 = min(w0 + 31, len - 1);
     const bool alone = t == 0 || (a.window == 1 && a.sinks == 0);  // (such a row's tile is never whole)
-    constexpr int kStep = SHARED ? NW : 1;
     int buf = 0;
-    for (int n = SHARED ? wave - NW : -1; n < walk.ntiles; n += kStep, buf ^= 1) {
-        if (n >= 0) {
-            // (what was read of the other stage has arrived too)
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-            if constexpr (!SHARED) __syncthreads();
-        }
+    for (int n = first; n < walk.ntiles; n += kStep, buf ^= 1) {
+        // (what was read of the other stage has arrived too)
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        if constexpr (!SHARED) __syncthreads();
         if (n + kStep < walk.ntiles) stage(n + kStep, buf ^ 1);
-        if (n < 0 || w0 >= len) continue;
+        if (w0 >= len) continue;
         const unsigned char *kl = own + buf * 2 * Tl::kBytes, *vl = kl + Tl::kBytes;
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
@@ -322,6 +322,7 @@ __global__ __launch_bounds__((64 * KW * G), 1) void attn_dkv_kernel(const AttnBw
             ++head;
         }
     };
+    if (turns > 0) stage(0);
 
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
@@ -333,13 +334,10 @@ __global__ __launch_bounds__((64 * KW * G), 1) void attn_dkv_kernel(const AttnBw
 #pragma unroll
     for (int db = 0; db < DB; ++db) dk[db] = dv[db] = zero16();
     int tile = lo;
-    for (int n = -1; n < turns; ++n) {
-        if (n >= 0) {
-            lds_dma_wait();
-            __syncthreads();
-        }
+    for (int n = 0; n < turns; ++n) {
+        lds_dma_wait();
+        __syncthreads();
         if (n + 1 < turns) stage((n + 1) & 1);
-        if (n < 0) continue;
         const unsigned char *ql = lds + (n & 1) * Lds::kStage, *dl = ql + Tl::kBytes;
         const float2 *stats = reinterpret_cast<const float2 *>(ql + Lds::kStats);
 #pragma unroll
@@ -515,6 +513,7 @@ __global__ __launch_bounds__(256) void attn_sinks_kernel(const AttnBwdIn<T> a, i
         const bool second = (rest & 1) != 0;
         const float *p = a.partials + ((of * parts * 2 + second) * a.rows + j) * D + e;
         float s = 0.f;
+#pragma unroll 8
         for (int k = 0; k < parts; ++k) s += p[k * 2 * a.rows * D];
         narrow((second ? a.dv : a.dk) + ((b * a.L + j) * a.kvheads + kvh) * D + e, s);
     }

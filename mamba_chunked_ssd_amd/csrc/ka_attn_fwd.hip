@@ -12,10 +12,10 @@
 //
 // Bound by the waves' own chain of products, exponentials and waits at two (heads
 // of 128) or three (64) waves to a SIMD.  16 384 tokens, 8 heads of 128 over 2, a
-// window of 2048: 155 to 166 us, 780 to 840 TFLOP/s (an 8192^3 product of the
+// window of 2048: 153 to 166 us, 780 to 847 TFLOP/s (an 8192^3 product of the
 // library: 1170); alone on its SIMD a wave takes 218.  2 x 2048 tokens, 40 heads of
-// 64 over 8, a window of 512: 41 us (one, two, three blocks to a compute unit: 77,
-// 49, 41).  LDS is no limit: its pipe is busy 17 % of the time, without conflicts.
+// 64 over 8, a window of 512: 40 us (one, two, three blocks to a compute unit: 77,
+// 49, 40).  LDS is no limit: its pipe is busy 17 % of the time, without conflicts.
 #include <algorithm>
 
 #include "ka_attn.h"
@@ -206,18 +206,17 @@ __global__ __launch_bounds__(256, (sizeof(T) == 2 ? (D == 32 ? 4 : D == 64 ? 3 :
         }
     };
 
+    if (walk.ntiles > 0) stage(0);
 #pragma unroll
     for (int s = 0; s < NS; ++s) arrived(qf[s]);
     Running<T, D> run;
     run.init();
     const int w0 = t0 + 32 * wave, w1 = min(w0 + 31, p.end - 1);  // the wave's queries
-    for (int n = -1; n < walk.ntiles; ++n) {
-        if (n >= 0) {
-            lds_dma_wait();
-            __syncthreads();
-        }
+    for (int n = 0; n < walk.ntiles; ++n) {
+        lds_dma_wait();
+        __syncthreads();
         if (n + 1 < walk.ntiles) stage(n + 1);
-        if (n < 0 || w0 >= p.end) continue;
+        if (w0 >= p.end) continue;
         const unsigned char *kl = lds + (n & 1) * 2 * Tl::kBytes, *vl = kl + Tl::kBytes;
         const int j0 = walk.start(n);
         if (j0 > w1 || (n >= walk.nsink && j0 + KT <= w0 - a.window + 1 && j0 >= a.sinks)) continue;
@@ -295,16 +294,16 @@ __global__ __launch_bounds__((64 * WaveLds<T, D>::kWaves), 1) void attn_fwd_shar
             Tl::template gather<64>(kl + Tl::kBytes, [&](int r) { return walk.held(n, j0 + r, a.sinks, p.end) ? values.of(j0 + r) : nullptr; });
         }
     };
+    if (wave < walk.ntiles) stage(wave, own);
 #pragma unroll
     for (int s = 0; s < NS; ++s) arrived(qf[s]);
     Running<T, D> run;
     run.init();
     int buf = 0;
-    for (int n = wave - NW; n < walk.ntiles; n += NW, buf ^= 1) {
+    for (int n = wave; n < walk.ntiles; n += NW, buf ^= 1) {
         // the copies of this tile are the oldest; what was read of the other stage has arrived
-        if (n >= 0) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
         if (n + NW < walk.ntiles) stage(n + NW, own + (buf ^ 1) * kStage);
-        if (n < 0) continue;
         const unsigned char *kl = own + buf * kStage;
         const int j0 = walk.start(n);
         floatx16 s[1];

@@ -83,12 +83,12 @@ __global__ __launch_bounds__((64 * StepLds<T, D>::kWaves), 1) void attn_step_ker
         copier.copy(kl + Tl::kBytes, a.vc + cache + (int64_t)at * D, min(s1 - at, 32));
     };
 
+    int at = s0 + 32 * wave, buf = 0;
+    if (at < s1) stage(at, 0);
 #pragma unroll
     for (int s = 0; s < NS; ++s) arrived(qf[s]);
     Running<T, D> run;
     run.init();
-    int at = s0 + 32 * wave, buf = 0;
-    if (at < s1) stage(at, 0);
     for (; at < s1; at += 32 * NW, buf ^= 1) {
         if (at + 32 * NW < s1) {
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // what was read of the other stage has arrived
