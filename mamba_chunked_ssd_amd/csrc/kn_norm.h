@@ -98,35 +98,43 @@ __device__ __forceinline__ void zero_row(Stored t, void *base, int64_t at, int C
 __device__ __forceinline__ float larger(float a, float b) {
     return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
 }
+__device__ __forceinline__ double larger(double a, double b) {
+    return __longlong_as_double(max(__double_as_longlong(a), __double_as_longlong(b)));
+}
 
-// sum and largest magnitude over the threads that hold a row: a wave, or a
-// block of four with `room` in LDS.  A block's rows follow one another, so the
-// rooms alternate: a wave writes one again only after the next row's barrier.
-__device__ __forceinline__ void wave_reduce(float &sum, float &most) {
-    sum = lane_total<16>(sum);
-    most = larger(most, lane_swap<1>(most));
-    most = larger(most, lane_swap<2>(most));
-    most = larger(most, lane_swap<4>(most));
-    most = larger(most, lane_swap<8>(most));
-    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(sum), __float_as_uint(sum), false, false);
-    const auto m = __builtin_amdgcn_permlane16_swap(__float_as_uint(most), __float_as_uint(most), false, false);
-    sum = __uint_as_float(s[0]) + __uint_as_float(s[1]);
-    most = larger(__uint_as_float(m[0]), __uint_as_float(m[1]));
-    const auto t = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum), __float_as_uint(sum), false, false);
-    const auto n = __builtin_amdgcn_permlane32_swap(__float_as_uint(most), __float_as_uint(most), false, false);
-    sum = __uint_as_float(t[0]) + __uint_as_float(t[1]);
-    most = larger(__uint_as_float(n[0]), __uint_as_float(n[1]));
+// The sum, or the largest magnitude, over the threads that hold a row: a wave,
+// or a block of four with `room` in LDS.  Reductions follow one another, so the
+// rooms alternate: a wave writes one again only after the next one's barrier.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float *room) {
+    v = lane_total<16>(v);
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+    const auto t = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(t[0]) + __uint_as_float(t[1]);
+    if constexpr (TPR > 64) {
+        if ((threadIdx.x & 63) == 0) room[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = (room[0] + room[1]) + (room[2] + room[3]);
+    }
+    return v;
 }
 template <int TPR>
-__device__ __forceinline__ void row_reduce(float &sum, float &most, float2 *room) {
-    wave_reduce(sum, most);
+__device__ __forceinline__ float row_most(float v, float *room) {
+    v = larger(v, lane_swap<1>(v));
+    v = larger(v, lane_swap<2>(v));
+    v = larger(v, lane_swap<4>(v));
+    v = larger(v, lane_swap<8>(v));
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = larger(__uint_as_float(s[0]), __uint_as_float(s[1]));
+    const auto t = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = larger(__uint_as_float(t[0]), __uint_as_float(t[1]));
     if constexpr (TPR > 64) {
-        const int w = threadIdx.x >> 6;
-        if ((threadIdx.x & 63) == 0) room[w] = float2{sum, most};
+        if ((threadIdx.x & 63) == 0) room[threadIdx.x >> 6] = v;
         __syncthreads();
-        sum = (room[0].x + room[1].x) + (room[2].x + room[3].x);
-        most = larger(larger(room[0].y, room[1].y), larger(room[2].y, room[3].y));
+        v = larger(larger(room[0], room[1]), larger(room[2], room[3]));
     }
+    return v;
 }
 
 // f(i, whether the piece is a row's last) for its NV pieces.

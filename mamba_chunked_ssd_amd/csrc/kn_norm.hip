@@ -65,7 +65,7 @@ template <typename TX, typename TR, int TPR, int NV>
 __global__ __launch_bounds__(256) void norm_fwd_kernel(const NormIn a) {
     constexpr bool kRes = !std::is_same<TR, void>::value;
     typedef typename std::conditional<kRes, TR, float>::type R;
-    __shared__ float2 room[2][4];
+    __shared__ float room[2][4];
     const int lane = threadIdx.x % TPR, C = a.C;
     uint32_t row = blockIdx.x, step = gridDim.x;
     if constexpr (TPR == 64) {
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(const NormIn a) {
             for_pieces<NV>([&](auto i, auto last) { load_piece<last>(wt[i], a.weight, at_piece(i), C); });
         else
             for_pieces<NV>([&](auto i, auto) { wt[i].v[0] = wt[i].v[1] = floatx4{1.f, 1.f, 1.f, 1.f}; });
-        float u[NV][8], sum = 0.f, most = 0.f;
+        float u[NV][8], sum = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -103,13 +103,22 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(const NormIn a) {
                 u[i][e] = x[i].get(e);
                 if constexpr (kRes) u[i][e] += res[i].get(e);
                 sum = fmaf(u[i][e], u[i][e], sum);
-                most = larger(most, __builtin_fabsf(u[i][e] * wt[i].get(e)));
             }
-        row_reduce<TPR>(sum, most, room[turn]);
+        sum = row_sum<TPR>(sum, room[turn]);
         turn ^= 1;
         const float r = rsqrtf(sum / (float)C + a.eps);
-        const float row_scale = larger(__builtin_fabsf(most * r / kE4m3Max), kLeastScale);
-        if (a.out == Stored::e4m3 && a.block == 0 && lane == 0) a.scales[at] = row_scale;
+        float row_scale = 0.f;
+        if (a.out == Stored::e4m3 && a.block == 0) {
+            // over y itself: u w alone, taken beside the sum, may leave fp32's range where y does not
+            float most = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) most = larger(most, __builtin_fabsf(u[i][e] * r * wt[i].get(e)));
+            row_scale = larger(row_most<TPR>(most, room[turn]) / kE4m3Max, kLeastScale);
+            turn ^= 1;
+            if (lane == 0) a.scales[at] = row_scale;
+        }
         if (a.residual_out != nullptr)
             for_pieces<NV>([&](auto i, auto last) { store_as<last>(a.res, a.residual_out, out, at_piece(i), C, u[i]); });
         for_pieces<NV>([&](auto i, auto last) {
@@ -123,15 +132,17 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(const NormIn a) {
 }
 
 // Rows of any length, a block each: once for the sum, once for the output.  A
-// lane's sum is over up to 2^16 elements and is held in 64 bits.
+// lane's sum is over up to 2^16 elements and is held in 64 bits, and so is, for
+// the row's scale, the largest |u w|, whose product may leave fp32's range where
+// y does not.
 template <typename TX, typename TR>
 __global__ __launch_bounds__(256) void norm_fwd_long_kernel(const NormIn a) {
     constexpr bool kRes = !std::is_same<TR, void>::value;
     typedef typename std::conditional<kRes, TR, float>::type R;
-    __shared__ float2 room[2][4];
+    __shared__ float room[2][4];
     const int C = a.C;
     int turn = 0;
-    for (uint64_t at = blockIdx.x; at < a.rows; at += gridDim.x, turn ^= 1) {
+    for (uint64_t at = blockIdx.x; at < a.rows; at += gridDim.x) {
         const Place p = place_of((uint32_t)at, (uint32_t)a.L, a.lengths);
         const TX *xr = static_cast<const TX *>(a.x) + p.b * a.xs.batch + p.t * a.xs.row;
         const R *rr = static_cast<const R *>(a.residual) + p.b * a.rs.batch + p.t * a.rs.row;
@@ -150,23 +161,29 @@ __global__ __launch_bounds__(256) void norm_fwd_long_kernel(const NormIn a) {
                 w[e] = a.weight != nullptr ? v.get(e) : 1.f;
             }
         };
-        double total = 0.0;
-        float most = 0.f, u[8], w[8];
+        const bool by_row = a.out == Stored::e4m3 && a.block == 0;
+        double total = 0.0, most = 0.0;
+        float u[8], w[8];
         for (int c0 = threadIdx.x * 8; c0 < stop; c0 += 2048) {
             piece(c0, u, w);
             float s = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                s = fmaf(u[e], u[e], s);
-                most = larger(most, __builtin_fabsf(u[e] * w[e]));
-            }
+            for (int e = 0; e < 8; ++e) s = fmaf(u[e], u[e], s);
             total += s;
+            if (by_row) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) most = larger(most, __builtin_fabs((double)u[e] * (double)w[e]));
+            }
         }
-        float sum = (float)total;
-        row_reduce<256>(sum, most, room[turn]);
+        const float sum = row_sum<256>((float)total, room[turn]);
+        turn ^= 1;
         const float r = p.live ? rsqrtf(sum / (float)C + a.eps) : 0.f;
-        const float row_scale = larger(__builtin_fabsf(most * r / kE4m3Max), kLeastScale);
-        if (a.out == Stored::e4m3 && a.block == 0 && threadIdx.x == 0) a.scales[at] = row_scale;
+        float row_scale = 0.f;
+        if (by_row) {
+            row_scale = larger(row_most<256>(__builtin_fabsf((float)(most * (double)r)), room[turn]) / kE4m3Max, kLeastScale);
+            turn ^= 1;
+            if (threadIdx.x == 0) a.scales[at] = row_scale;
+        }
         const int64_t out = (int64_t)at * C;
         // every lane takes every turn: a block of columns is shared by lanes
         for (int base = 0; base < C; base += 2048) {

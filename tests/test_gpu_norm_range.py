@@ -53,3 +53,21 @@ def test_backward_along_u(c, size):
     got = ssd.rms_norm_bwd(u / size, u, eps=0.0)
     du, _, mag, _ = mo.norm_bwd(host(u / size), host(u), eps=0.0)
     assert np.all(np.abs(host(got["dx"]) - du) <= 256 * EPS * mag)
+
+
+@pytest.mark.parametrize("c", [200, 2560, 5000, 17000])
+@pytest.mark.parametrize("size,weight", [(1e17, 1e22), (1e-13, 1e-28), (1e-13, 1e20), (1e16, 1e-30)])
+@pytest.mark.parametrize("block", [0, 128])
+def test_scales_where_u_times_weight_leaves_the_range(c, size, weight, block):
+    # y = u r w is of order w; the scale is off by 64 EPS of itself, a code by half a step of e4m3 and 130 EPS
+    g = torch.Generator().manual_seed(c)
+    x = (size * torch.randn((2, 3, c), generator=g)).cuda()
+    w = (weight * (1 + 0.3 * torch.randn(c, generator=g))).cuda()
+    q, s = ssd.rms_norm_fwd(x, w, eps=0.0, y_dtype=torch.float8_e4m3fn, scale_block=block)
+    _, y = mo.norm(host(x), host(w), eps=0.0)
+    want, per = mo.scales(y, block)
+    assert np.all(np.abs(host(s) - want) <= 64 * EPS * want)
+    z = y / per
+    assert np.all(np.abs(host(q.float()) - z) <= 2.0 ** -4 * np.maximum(np.abs(z), 2.0 ** -6) + 130 * EPS * np.abs(z))
+    # in fp32 the same y
+    assert np.all(np.abs(host(ssd.rms_norm_fwd(x, w, eps=0.0)) - y) <= 64 * EPS * np.abs(y))
