@@ -434,4 +434,49 @@ __device__ __forceinline__ float widen(float v) { return v; }
 __device__ __forceinline__ void narrow(uint16_t *p, float v) { *p = (uint16_t)(pack_bf16(v, 0.f) & 0xffffu); }
 __device__ __forceinline__ void narrow(float *p, float v) { *p = v; }
 
+// ---------------------------------------------------------------------------
+// Results of columns that may not see all rows which a product takes: a row's
+// value that is not finite makes 0 times it NaN where it is not seen.  A wave
+// with a result that is not finite forms it again from memory, 32 rows at a
+// time as before, but with such values taken out of the product, and beside it a
+// product of their kinds with 1 where a column sees the row, else 0, which tells
+// what of them each result has seen.  So a diverged step costs some times a sound
+// one, however many of its values are not finite.
+// ---------------------------------------------------------------------------
+
+// Kinds, which sums over 32 rows keep apart: infinity 1, -infinity 2^7, NaN 2^14.
+// A weight of kOddNan makes a NaN of each (0 times infinity).
+constexpr float kOddMinus = 128.f, kOddNan = 16384.f;
+
+// Element c of eight rows in the order of Tile::across (row(i) for the lane's rows i = 0 .. 3, 8 .. 11; null: 0).
+template <typename T, typename F>
+__device__ __forceinline__ void load_apart(Frag<T> &finite, Frag<T> &kind, int c, F &&row) {
+    float x[8], k[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const T *p = row((j & 3) + 8 * (j >> 2));
+        const float v = p != nullptr ? widen(p[c]) : 0.f;
+        const bool sound = v - v == 0.f;
+        x[j] = sound ? v : 0.f;
+        k[j] = sound ? 0.f : v != v ? kOddNan : v > 0.f ? 1.f : kOddMinus;
+    }
+    to_frag(x, finite);
+    to_frag(k, kind);
+}
+// What a product of kinds says of each register: bit r infinity, bit 16 + r -infinity, both NaN.
+__device__ __forceinline__ uint32_t odd_of(const floatx16 &n) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        const uint32_t sum = n[r] >= kOddNan ? (uint32_t)kOddMinus + 1u : (uint32_t)n[r];
+        bits |= ((sum & 127u) != 0 ? 1u << r : 0u) | (sum >> 7 != 0 ? 1u << (16 + r) : 0u);
+    }
+    return bits;
+}
+__device__ __forceinline__ float with_odd(float v, uint32_t odd, int r) {
+    if ((odd >> r & 1) != 0) v += kInf;
+    if ((odd >> (16 + r) & 1) != 0) v -= kInf;
+    return v;
+}
+
 }  // namespace ssd

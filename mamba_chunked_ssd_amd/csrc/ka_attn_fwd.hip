@@ -92,37 +92,56 @@ __device__ __forceinline__ void hide(floatx16 (&s)[KB], const Walk<KT> &w, int n
     }
 }
 
-// A value that is not finite makes 0 times it NaN in the rows of its tile that
-// do not see it.  Such a row (with a sound softmax: reference `ref`, sum 1 /
-// inv) is formed again by a wave, from the tokens that it sees alone: 64 keys'
-// weights at a time, a lane each, then their values one after the other, a lane
-// to an element.
+// Elements 32 db .. of a wave's rows formed again (see with_odd): queries w0 ..
+// w0 + 31 below `end`, a lane's t with its softmax's reference and 1 / sum, over
+// the sinks and the window's tokens, 32 at a time.  A score of -infinity has a
+// weight of 0, which makes NaN of a value that is not finite.
 template <typename T, int D>
-__device__ void attend_row(const AttnIn<T> &a, const Keys<T, D> &keys, const Keys<T, D> &values, const T *q, T *y, int t,
-                           float ref, float inv) {
-    const int lane = threadIdx.x & 63;
-    float acc[(D + 63) / 64] = {};
-    const int near = max(t - a.window + 1, 0), far = min(a.sinks, near), seen = far + t - near + 1;
-    for (int base = 0; base < seen; base += 64) {
-        const int at = base + lane, j = at < far ? at : near + at - far;
-        float p = 0.f;
-        if (at < seen) {
-            const T *kr = keys.of(j);
-            float s = 0.f;
-            for (int e = 0; e < D; ++e) s = fmaf(widen(q[e]), widen(kr[e]), s);
-            p = fast_exp2(fmaf(s, a.c, -ref));
-        }
-        for (int u = 0; u < min(64, seen - base); ++u) {
-            const float pu = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(p), u));
-            const T *vr = values.of(base + u < far ? base + u : near + base + u - far);
+__device__ __forceinline__ void attend_again(const AttnIn<T> &a, const Keys<T, D> &keys, const Keys<T, D> &values,
+                                             const Frag<T> (&q)[D / 16], int w0, int end, int t, int db, float ref, float inv,
+                                             T *row, bool on) {
+    const int lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
+    const int near = max(w0 - a.window + 1, 0), last = min(w0 + 31, end - 1), far = min(a.sinks, near);
+    const int nfar = (far + 31) / 32, blocks = nfar + (last - near) / 32 + 1;
+    floatx16 o = zero16();
+    uint32_t odd = 0;
+#pragma unroll 1
+    for (int n = 0; n < blocks; ++n) {
+        const int j0 = n < nfar ? 32 * n : near + 32 * (n - nfar), stop = n < nfar ? far : last + 1;
+        floatx16 s = zero16(), kinds = zero16();
 #pragma unroll
-            for (int k = 0; k < (D + 63) / 64; ++k)
-                if (lane + 64 * k < D) acc[k] = fmaf(pu, widen(vr[lane + 64 * k]), acc[k]);
+        for (int ks = 0; ks < D / 16; ++ks) {
+            Frag<T> kf;
+            load_frag(kf, keys.of(j0 + col) + 16 * ks + 8 * h, j0 + col < stop);
+            s = mma(kf, q[ks], s);
         }
+        const int upto = min(t, stop - 1) - j0 - 4 * h, before = t - a.window - j0 - 4 * h, sunk = a.sinks - j0 - 4 * h;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            float p[8], u[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = 8 * ks + i, at = place(0, r);
+                const bool seen = (at <= upto) & ((at > before) | (at < sunk));
+                p[i] = seen ? fast_exp2(fmaf(s[r], a.c, -ref)) : 0.f;
+                u[i] = !seen ? 0.f : s[r] == -kInf ? kOddNan : 1.f;
+            }
+            Frag<T> pf, uf, vf, kind;
+            to_frag(p, pf);
+            to_frag(u, uf);
+            load_apart(vf, kind, 32 * db + col, [&](int i) {
+                const int j = j0 + 16 * ks + 4 * h + i;
+                return j < stop ? values.of(j) : nullptr;
+            });
+            o = mma(vf, pf, o);
+            kinds = mma(kind, uf, kinds);
+        }
+        odd |= odd_of(kinds);
     }
+    float v[16];
 #pragma unroll
-    for (int k = 0; k < (D + 63) / 64; ++k)
-        if (lane + 64 * k < D) narrow(y + lane + 64 * k, acc[k] * inv);
+    for (int r = 0; r < 16; ++r) v[r] = with_odd(o[r] * inv, odd, r);
+    store_column(row, db, h, v, on);
 }
 
 // What a block works on.
@@ -243,13 +262,10 @@ __global__ __launch_bounds__(256, (sizeof(T) == 2 ? (D == 32 ? 4 : D == 64 ? 3 :
     }
     if (a.lse != nullptr && h == 0 && i < a.L) *p.sums(a, i) = live ? (run.m + __builtin_amdgcn_logf(l)) * kLn2 : 0.f;
     check = both_halves(check);
-    uint64_t again = __ballot(live && check != check && l > 0.f && l < kInf) & 0xffffffffull;
-    while (again != 0) {
-        const int c = __builtin_ctzll(again), ic = p.q0 + 32 * wave + c;
-        again &= again - 1;
-        attend_row<T, D>(a, keys, values, p.query(a, ic), p.result(a, ic), w0 + c,
-                         __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ref), c)),
-                         __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv), c)));
+    const bool redo = live && check != check && l > 0.f && l < kInf;
+    if (__any(redo)) {
+#pragma unroll 1
+        for (int db = 0; db < DB; ++db) attend_again<T, D>(a, keys, values, qf, w0, p.end, t, db, ref, inv, p.result(a, i), redo);
     }
 }
 
@@ -326,10 +342,12 @@ __global__ __launch_bounds__((64 * WaveLds<T, D>::kWaves), 1) void attn_fwd_shar
         if (live && y - y != 0.f && l > 0.f && l < kInf) atomicOr(&again, 1u << c);
     });
     __syncthreads();
-    for (uint32_t rest = again; rest != 0; rest &= rest - 1) {
-        const int c = __builtin_ctz(rest);
-        if (c % NW != wave) continue;
-        attend_row<T, D>(a, keys, values, p.query(a, p.q0 + c), p.result(a, p.q0 + c), t0 + c, stats[c].x, stats[c].y);
+    // (a wave takes some of the elements)
+    if (again != 0) {
+        const bool redo = (again >> col & 1) != 0;
+#pragma unroll 1
+        for (int db = wave; db < D / 32; db += NW)
+            attend_again<T, D>(a, keys, values, qf, t0, p.end, t, db, stats[col].x, stats[col].y, p.result(a, i), redo);
     }
 }
 

@@ -1,0 +1,128 @@
+"""Sliding-window attention over values that are not finite: each element of a
+result has what its row sees and nothing else, and a step that has diverged
+takes some times a sound one's time.
+
+The reference is in fp64: sums over the finite values, and beside them what of
+infinities and NaN a row sees.  Weights of seen tokens are above 0 there (scores
+are of order 1).  Bounds as in test_gpu_attn.py.
+"""
+from __future__ import annotations
+
+import math
+import statistics
+
+import pytest
+import torch
+
+import mamba_chunked_ssd_amd as ssd
+
+pytestmark = pytest.mark.gpu
+
+EPS = 2.0 ** -24
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+ROUND = {"bf16": 2.0 ** -8, "f32": 0.0}
+INF, NAN = math.inf, math.nan
+
+
+def inputs(b, L, h, kv, d, dtype, seed=0):
+    g = torch.Generator().manual_seed(seed + 7 * L + d)
+    return [torch.randn((b, L, n, d), generator=g).to(TYPES[dtype]).cuda() for n in (h, kv, kv, h)]
+
+
+def seen_by(first, L, w, n):
+    """(query, token) of a sequence with `first` tokens behind it."""
+    t = first + torch.arange(L, device="cuda")[:, None]
+    j = torch.arange(first + L, device="cuda")[None]
+    return (j <= t) & ((t - j < w) | (j < n))
+
+
+def spread(q, k, scale, tokens):
+    """E of test_gpu_attn.py."""
+    d = q.shape[-1]
+    q, k = (x.double().nan_to_num(0, 0, 0).abs().flatten(0, -2).amax(0) for x in (q, k))
+    return (2 * (d + 8) * scale * float(q @ k) + 2 * tokens + 32) * EPS
+
+
+def apart(p, x):
+    """p @ x where x may hold anything: p above 0 where it counts."""
+    plus, minus, none = (x == INF).double(), (x == -INF).double(), x.isnan().double()
+    on = (p > 0).double()
+    plus, minus, none = ((on @ z) > 0 for z in (plus, minus, none))
+    y = p @ x.nan_to_num(0, 0, 0)
+    y = torch.where(plus, INF, y)
+    y = torch.where(minus, -INF, y)
+    return torch.where(none | (plus & minus), NAN, y)
+
+
+def same(got, want, bound):
+    got = got.double()
+    odd = ~want.isfinite()
+    return torch.equal(got.isnan(), want.isnan()) and torch.equal(got == INF, want == INF) and \
+        torch.equal(got == -INF, want == -INF) and bool(((got - want).abs() <= bound)[~odd].all())
+
+
+# one block of queries and many; sequences whose windows end inside tiles
+@pytest.mark.parametrize("b", [1, 34])
+@pytest.mark.parametrize("d,dtype", [(32, "bf16"), (64, "bf16"), (128, "bf16"), (32, "f32"), (64, "f32"), (128, "f32")])
+@pytest.mark.parametrize("w,n", [(20, 3), (75, 0), (1000, 0), (33, 40)])
+def test_forward_has_what_it_sees(b, d, dtype, w, n):
+    L, h, kv = 260, 4, 2
+    q, k, v, _ = inputs(b, L, h, kv, d, dtype)
+    for at, kind in ((1, INF), (34, -INF), (100, NAN), (130, INF), (131, -INF), (200, INF), (259, NAN)):
+        v[:, at, :, at % 7::5] = kind
+    y = ssd.window_attention_fwd(q, k, v, w, n)
+    on = seen_by(0, L, w, n)
+    kk, vv = (x.double().repeat_interleave(h // kv, 2).transpose(1, 2) for x in (k, v))
+    z = (q.double().transpose(1, 2) @ kk.transpose(2, 3).contiguous() * d ** -0.5).masked_fill(~on, -INF)
+    p = torch.softmax(z, -1)
+    want, mag = apart(p, vv), p @ vv.nan_to_num(0, 0, 0).abs()
+    e, r = spread(q, k, d ** -0.5, min(w, L) + n), ROUND[dtype]
+    assert same(y.transpose(1, 2), want, (e + r) * mag + r * want.abs())
+
+
+@pytest.mark.parametrize("b", [3, 48])
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "f32")])
+@pytest.mark.parametrize("w,n", [(20, 3), (75, 0), (33, 40)])
+def test_forward_from_a_cache(b, d, dtype, w, n):
+    first, L, h, kv = 150, 150, 4, 2
+    q, k, v, _ = inputs(b, first + L, h, kv, d, dtype, 1)
+    for at, kind in ((2, INF), (30, NAN), (120, -INF), (149, NAN), (151, INF), (152, -INF), (290, INF)):
+        v[:, at, :, at % 7::5] = kind
+    kc, vc = (torch.zeros((b, kv, w + n, d), dtype=TYPES[dtype], device="cuda") for _ in range(2))
+    ssd.window_attention_fwd(q[:, :first], k[:, :first], v[:, :first], w, n, k_cache=kc, v_cache=vc)
+    at = torch.full((b,), first, dtype=torch.int32, device="cuda")
+    y = ssd.window_attention_fwd(q[:, first:], k[:, first:], v[:, first:], w, n, positions=at, k_cache=kc, v_cache=vc)
+    on = seen_by(first, L, w, n)
+    kk, vv = (x.double().repeat_interleave(h // kv, 2).transpose(1, 2) for x in (k, v))
+    z = (q[:, first:].double().transpose(1, 2) @ kk.transpose(2, 3).contiguous() * d ** -0.5).masked_fill(~on, -INF)
+    p = torch.softmax(z, -1)
+    want, mag = apart(p, vv), p @ vv.nan_to_num(0, 0, 0).abs()
+    e, r = spread(q, k, d ** -0.5, w + n), ROUND[dtype]
+    assert same(y.transpose(1, 2), want, (e + r) * mag + r * want.abs())
+
+
+def took(call):
+    for _ in range(2):
+        call()
+    times = []
+    for _ in range(3):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        call()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b))
+    return statistics.median(times)
+
+
+# everything is not finite, or one sink that every query sees
+ODD = [("all", slice(None), NAN), ("all", slice(None), INF), ("sink", slice(1, 2), NAN), ("sink", slice(1, 2), INF)]
+
+
+@pytest.mark.parametrize("L,h,kv,d,dtype", [(4096, 32, 8, 64, "bf16"), (8192, 16, 4, 128, "bf16"), (4096, 16, 8, 64, "f32")])
+@pytest.mark.parametrize("where", ODD, ids=lambda o: "%s_%s" % (o[0], o[2]))
+def test_a_diverged_forward_takes_some_times_a_sound_one(L, h, kv, d, dtype, where):
+    q, k, v, _ = inputs(1, L, h, kv, d, dtype)
+    sound = took(lambda: ssd.window_attention_fwd(q, k, v, 512, 4))
+    v[:, where[1]] = where[2]
+    assert took(lambda: ssd.window_attention_fwd(q, k, v, 512, 4)) <= 20 * sound
