@@ -61,23 +61,79 @@ __device__ __forceinline__ int length_of(const int32_t *lengths, int b, int L) {
     return lengths == nullptr ? L : min(max(lengths[b], 0), L);
 }
 
+// Elements 32 db .. of a wave's dq formed again (see with_odd): queries w0 .. w0
+// + 31 below `len`, a lane's t.  Under a finite lse a key that is not finite has a
+// weight and a dS of 0, which make NaN of it.
 template <typename T, int D>
-__device__ __forceinline__ float row_dot(const T *a, const T *b) {
-    float s = 0.f;
-    for (int e = 0; e < D; ++e) s = fmaf(widen(a[e]), widen(b[e]), s);
-    return s;
+__device__ __forceinline__ void query_again(const AttnBwdIn<T> &a, const T *kh, const T *vh, const Frag<T> (&q)[D / 16],
+                                            const Frag<T> (&dy)[D / 16], int w0, int len, int t, int db, float lse, float delta,
+                                            T *row, bool on) {
+    const int lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
+    const int near = max(w0 - a.window + 1, 0), last = min(w0 + 31, len - 1), far = min(a.sinks, near);
+    const int nfar = (far + 31) / 32, blocks = nfar + (last - near) / 32 + 1;
+    const bool alone = t == 0 || (a.window == 1 && a.sinks == 0);
+    floatx16 o = zero16();
+    uint32_t odd = 0;
+#pragma unroll 1
+    for (int n = 0; n < blocks; ++n) {
+        const int j0 = n < nfar ? 32 * n : near + 32 * (n - nfar), stop = n < nfar ? far : last + 1;
+        floatx16 s = zero16(), g = zero16();
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            Frag<T> f;
+            load_frag(f, kh + (int64_t)(j0 + col) * a.ks.row + 16 * ks + 8 * h, j0 + col < stop);
+            s = mma(f, q[ks], s);
+            load_frag(f, vh + (int64_t)(j0 + col) * a.vs.row + 16 * ks + 8 * h, j0 + col < stop);
+            g = mma(f, dy[ks], g);
+        }
+        const int upto = min(t, stop - 1) - j0 - 4 * h, before = t - a.window - j0 - 4 * h, sunk = a.sinks - j0 - 4 * h;
+        Frag<T> sf[2], uf[2];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            float ds[8], u[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = 8 * ks + i, at = place(0, r);
+                const bool seen = (at <= upto) & ((at > before) | (at < sunk));
+                ds[i] = (seen & !alone) ? fast_exp2(fmaf(s[r], a.c, -lse)) * (g[r] - delta) : 0.f;
+                u[i] = seen ? kOddNan : 0.f;
+            }
+            to_frag(ds, sf[ks]);
+            to_frag(u, uf[ks]);
+        }
+        group_end();
+        floatx16 kinds = zero16();
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            Frag<T> kf, kind;
+            load_apart(kf, kind, 32 * db + col, [&](int i) {
+                const int j = j0 + 16 * ks + 4 * h + i;
+                return j < stop ? kh + (int64_t)j * a.ks.row : nullptr;
+            });
+            o = mma(kf, sf[ks], o);
+            kinds = mma(kind, uf[ks], kinds);
+            group_end();
+        }
+        odd |= odd_of(kinds);
+    }
+    float v[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) v[r] = with_odd(o[r] * a.scale, odd, r);
+    store_column(row, db, h, v, on);
 }
 
 // SHARED (few queries): the waves of a block share 32 queries and take the
 // tiles in turn, with stages of their own; their sums are added at the end, in
 // order.  Else each has 32, and all use the same tiles.
+// (bf16 heads of 32 are held to four waves a SIMD: at five, what forms rows again
+// spills into the loop, 86 us the backward pass of 4 x 2048 tokens for 83.)
 template <typename T, int D, bool SHARED>
-__global__ __launch_bounds__((SHARED ? 64 * WaveLds<T, D>::kWaves : 256), (!SHARED && D * sizeof(T) <= 256 ? 2 : 1)) void attn_dq_kernel(
+__global__ __launch_bounds__((SHARED ? 64 * WaveLds<T, D>::kWaves : 256), (SHARED || D * sizeof(T) > 256 ? 1 : D * sizeof(T) > 64 ? 2 : 4)) void attn_dq_kernel(
     const AttnBwdIn<T> a) {
     constexpr int KT = sizeof(T) == 2 && !SHARED ? 64 : 32, KB = KT / 32, NS = D / 16, DB = D / 32;
     constexpr int NW = SHARED ? WaveLds<T, D>::kWaves : 4, kRun = SHARED ? 32 : kQueries;
     typedef Tile<T, D, KT> Tl;
-    extern __shared__ __align__(16) unsigned char lds[];
+    extern __shared__ __align__(16) unsigned char lds[];  // (the stages; SHARED: which queries to form again)
 
     const int group = a.heads / a.kvheads;
     const int tiles = (a.L + kRun - 1) / kRun;
@@ -196,60 +252,46 @@ __global__ __launch_bounds__((SHARED ? 64 * WaveLds<T, D>::kWaves : 256), (!SHAR
                 sums[((wave - 1) * DB * 4 + q) * 64] = floatx4{o[q / 4][4 * (q % 4)], o[q / 4][4 * (q % 4) + 1], o[q / 4][4 * (q % 4) + 2], o[q / 4][4 * (q % 4) + 3]};
         }
         __syncthreads();
-        if (wave > 0) return;
+        if (wave == 0) {
 #pragma unroll
-        for (int of = 0; of < NW - 1; ++of)
+            for (int of = 0; of < NW - 1; ++of)
 #pragma unroll
-            for (int q = 0; q < DB * 4; ++q) {
-                const floatx4 x = sums[(of * DB * 4 + q) * 64];
+                for (int q = 0; q < DB * 4; ++q) {
+                    const floatx4 x = sums[(of * DB * 4 + q) * 64];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[q / 4][4 * (q % 4) + e] += x[e];
-            }
+                    for (int e = 0; e < 4; ++e) o[q / 4][4 * (q % 4) + e] += x[e];
+                }
+        }
     }
-    if (w0 >= a.L) return;  // (no barrier follows)
+    if (w0 >= a.L) return;  // (not SHARED: no barrier follows)
 
     float check = 0.f;
+    if (!SHARED || wave == 0) {
 #pragma unroll
-    for (int db = 0; db < DB; ++db) {
-        float v[16];
+        for (int db = 0; db < DB; ++db) {
+            float v[16];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            check = fmaf(o[db][r], 0.f, check);
-            v[r] = live ? o[db][r] * a.scale : 0.f;
-        }
-        store_column(a.dq + dense, db, h, v, t < a.L);
-    }
-    // As in the forward pass: rows that a value they do not see may have spoiled, once more from what they see.
-    check = both_halves(check);
-    uint64_t again = __ballot(live && check != check && delta - delta == 0.f && lse - lse == 0.f) & 0xffffffffull;
-    while (again != 0) {
-        const int c = __builtin_ctzll(again);
-        again &= again - 1;
-        const int tt = w0 + c;
-        const float rd = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(delta), c));
-        const float rl = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lse), c));
-        const T *qr = a.q + (int64_t)b * a.qs.batch + (int64_t)tt * a.qs.row + head * a.qs.head;
-        const T *dr = a.dy + (int64_t)b * a.dys.batch + (int64_t)tt * a.dys.row + head * a.dys.head;
-        float acc[(D + 63) / 64] = {};
-        const int near = max(tt - a.window + 1, 0), far = min(a.sinks, near), seen = far + tt - near + 1;
-        for (int base = 0; base < seen; base += 64) {
-            const int at = base + lane, j = at < far ? at : near + at - far;
-            float ds = 0.f;
-            if (at < seen && seen > 1)
-                ds = fast_exp2(fmaf(row_dot<T, D>(qr, kh + (int64_t)j * a.ks.row), a.c, -rl)) *
-                     (row_dot<T, D>(dr, vh + (int64_t)j * a.vs.row) - rd);
-            for (int u = 0; u < min(64, seen - base); ++u) {
-                const float du = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ds), u));
-                const T *kr = kh + (int64_t)(base + u < far ? base + u : near + base + u - far) * a.ks.row;
-#pragma unroll
-                for (int k = 0; k < (D + 63) / 64; ++k)
-                    if (lane + 64 * k < D) acc[k] = fmaf(du, widen(kr[lane + 64 * k]), acc[k]);
+            for (int r = 0; r < 16; ++r) {
+                check = fmaf(o[db][r], 0.f, check);
+                v[r] = live ? o[db][r] * a.scale : 0.f;
             }
+            store_column(a.dq + dense, db, h, v, t < a.L);
         }
-        T *out = a.dq + ((int64_t)b * a.L + tt) * a.heads * D + (int64_t)head * D;
-#pragma unroll
-        for (int k = 0; k < (D + 63) / 64; ++k)
-            if (lane + 64 * k < D) narrow(out + lane + 64 * k, acc[k] * a.scale);
+    }
+    // As in the forward pass: rows that a value they do not see may have spoiled.
+    check = both_halves(check);
+    uint32_t again = (uint32_t)__ballot(live && check != check && delta - delta == 0.f && lse - lse == 0.f);
+    if constexpr (SHARED) {
+        // by all waves, which take some of the elements each
+        uint32_t *told = reinterpret_cast<uint32_t *>(lds + WaveLds<T, D>::kCopies);
+        if (threadIdx.x == 0) *told = again;
+        __syncthreads();
+        again = *told;
+    }
+    if (again != 0) {
+#pragma unroll 1
+        for (int db = SHARED ? wave : 0; db < DB; db += SHARED ? NW : 1)
+            query_again<T, D>(a, kh, vh, qf, df, w0, len, t, db, lse, delta, a.dq + dense, (again >> col & 1) != 0);
     }
 }
 
@@ -262,12 +304,88 @@ __global__ __launch_bounds__((SHARED ? 64 * WaveLds<T, D>::kWaves : 256), (!SHAR
 // A block's queries are all those that see its keys through the window, or a
 // chunk of those that see them as sinks alone (blocks behind `tiles`).
 enum class Part { window, sinks, both };
+
+// Elements 32 db .. of a wave's dk and dv formed again (see with_odd): a lane's
+// key j of w0 .. w0 + 31, over the queries lo .. hi - 1 of the group's heads that
+// see it through the window (far: as a sink alone).  A query that is not finite
+// makes NaN of every weight in its row; where its own key is all that it sees, dS
+// is 0 and 0 times it is NaN.
+template <typename T, int D>
+__device__ __forceinline__ void keys_again(const AttnBwdIn<T> &a, const T *q, const T *dy, const float2 *stats, int group,
+                                           const Frag<T> (&k)[D / 16], const Frag<T> (&v)[D / 16], int w0, int j, int lo, int hi,
+                                           bool far, int db, floatx16 &dk, floatx16 &dv) {
+    const int lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
+    const bool lone = a.window == 1 && a.sinks == 0;
+    // of the wave's keys; a lane's own
+    const int from = max(lo, far ? w0 + a.window : w0);
+    const int to = far ? (w0 < a.sinks ? hi : from) : (int)min((int64_t)hi, (int64_t)w0 + 31 + a.window);
+    const int first = far ? j + a.window : j;
+    const int last = far ? (j < a.sinks ? to : first) - 1 : (int)min((int64_t)to, (int64_t)j + a.window) - 1;
+    uint32_t kodd = 0, vodd = 0;
+    dk = dv = zero16();
+    for (int head = 0; head < group; ++head, q += a.qs.head, dy += a.dys.head, stats += a.L) {
+#pragma unroll 1
+        for (int t0 = from; t0 < to; t0 += 32) {
+            floatx16 s = zero16(), g = zero16(), kinds = zero16(), vinds = zero16();
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                Frag<T> f;
+                load_frag(f, q + (int64_t)(t0 + col) * a.qs.row + 16 * ks + 8 * h, t0 + col < to);
+                s = mma(f, k[ks], s);
+                load_frag(f, dy + (int64_t)(t0 + col) * a.dys.row + 16 * ks + 8 * h, t0 + col < to);
+                g = mma(f, v[ks], g);
+            }
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                float p[8], ds[8], pu[8], su[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 8 * ks + i, t = t0 + 4 * h + place(0, r);
+                    const bool seen = (t >= first) & (t <= last);
+                    const float2 st = seen ? stats[t] : float2{0.f, 0.f};
+                    p[i] = seen ? fast_exp2(fmaf(s[r], a.c, -st.x)) : 0.f;
+                    ds[i] = (seen & (t > 0) & !lone) ? p[i] * (g[r] - st.y) : 0.f;
+                    pu[i] = !seen ? 0.f : s[r] == -kInf ? kOddNan : 1.f;
+                    su[i] = seen ? kOddNan : 0.f;
+                }
+                const auto add = [&](const T *x, int64_t stride, const float (&weight)[8], const float (&one)[8], floatx16 &sum,
+                                     floatx16 &kinds, uint32_t &odd) {
+                    Frag<T> w, u, f, kind;
+                    to_frag(weight, w);
+                    to_frag(one, u);
+                    load_apart(f, kind, 32 * db + col, [&](int i) {
+                        const int t = t0 + 16 * ks + 4 * h + i;
+                        return t < to ? x + (int64_t)t * stride : nullptr;
+                    });
+                    sum = mma(f, w, sum);
+                    // (fp32 heads of 128 have no registers to hold kinds in)
+                    if constexpr (D * sizeof(T) > 256) odd |= odd_of(mma(kind, u, zero16()));
+                    else kinds = mma(kind, u, kinds);
+                    group_end();
+                };
+                add(dy, a.dys.row, p, pu, dv, vinds, vodd);
+                add(q, a.qs.row, ds, su, dk, kinds, kodd);
+            }
+            if constexpr (D * sizeof(T) <= 256) {
+                kodd |= odd_of(kinds);
+                vodd |= odd_of(vinds);
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        dk[r] = with_odd(dk[r] * a.scale, kodd, r);
+        dv[r] = with_odd(dv[r], vodd, r);
+    }
+}
+
 template <typename T, int D, int KW, int G, int QB>
 struct KeyLds {
     typedef Tile<T, D, 32 * G * QB> Tl;
     static constexpr int kStats = Tl::kBytes * 2, kStage = kStats + 32 * G * QB * (int)sizeof(float2);
     static constexpr int kSums = G > 1 ? KW * D * 256 : 0;  // of one group
-    static constexpr int kBytes = 2 * kStage > kSums ? 2 * kStage : kSums;
+    static constexpr int kTold = 2 * kStage > kSums ? 2 * kStage : kSums;  // which keys to form again, a word for each KW
+    static constexpr int kBytes = kTold + 16;
 };
 
 template <typename T, int D, int KW, int G, int QB, Part PART>
@@ -426,76 +544,51 @@ __global__ __launch_bounds__((64 * KW * G), 1) void attn_dkv_kernel(const AttnBw
                 }
         }
     }
-    if (part_of != 0 || w0 >= a.L) return;  // (no barrier follows)
 
     const bool partial = far || w0 < a.rows;
     const int64_t dense = ((int64_t)b * a.L + j) * a.kvheads * D + (int64_t)kvh * D;
     float *pk = a.partials + ((((int64_t)b * a.kvheads + kvh) * (1 + a.nchunks) + part) * 2 * a.rows + j) * D;
     float *pv = pk + a.rows * D;
-    float check = 0.f;
-#pragma unroll
-    for (int db = 0; db < DB; ++db) {
+    const auto write = [&](int db, const floatx16 &dk, const floatx16 &dv, float k_scale, bool on) {
         float x[16], z[16];
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            check = fmaf(dk[db][r], 0.f, fmaf(dv[db][r], 0.f, check));
-            x[r] = live ? dk[db][r] * a.scale : 0.f;
-            z[r] = live ? dv[db][r] : 0.f;
+            x[r] = live ? dk[r] * k_scale : 0.f;
+            z[r] = live ? dv[r] : 0.f;
         }
         if (partial) {
-            store_column(pk, db, h, x, true);
-            store_column(pv, db, h, z, true);
+            store_column(pk, db, h, x, on);
+            store_column(pv, db, h, z, on);
         } else {
-            store_column(a.dk + dense, db, h, x, j < a.L);
-            store_column(a.dv + dense, db, h, z, j < a.L);
+            store_column(a.dk + dense, db, h, x, on && j < a.L);
+            store_column(a.dv + dense, db, h, z, on && j < a.L);
+        }
+    };
+    float check = 0.f;
+    if (part_of == 0 && w0 < a.L) {
+#pragma unroll
+        for (int db = 0; db < DB; ++db) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) check = fmaf(dk[db][r], 0.f, fmaf(dv[db][r], 0.f, check));
+            write(db, dk[db], dv[db], a.scale, true);
         }
     }
-    // Keys that a query which does not see them may have spoiled, once more from those that do.
+    // Keys that a query which does not see them may have spoiled, by all groups, which take some of the elements each.
     check = both_halves(check);
-    uint64_t again = __ballot(live && check != check) & 0xffffffffull;
-    while (again != 0) {
-        const int c = __builtin_ctzll(again);
-        again &= again - 1;
-        const int jj = w0 + c;
-        const T *kr = kh + (int64_t)jj * a.ks.row, *vr = vh + (int64_t)jj * a.vs.row;
-        const int t_lo = far ? max(lo, jj + a.window) : jj, t_hi = far ? (jj < a.sinks ? hi : t_lo) : (int)min((int64_t)hi, (int64_t)jj + a.window);
-        float acc[2][(D + 63) / 64] = {};
-        for (int gh = 0; gh < group; ++gh) {
-            const int of = kvh * group + gh;
-            const T *qr = qb + of * a.qs.head, *dr = db_ + of * a.dys.head;
-            for (int base = t_lo; base < t_hi; base += 64) {
-                const int t = base + lane;
-                float p = 0.f, ds = 0.f;
-                if (t < t_hi) {
-                    const float2 st = a.stats[((int64_t)b * a.heads + of) * a.L + t];
-                    p = fast_exp2(fmaf(row_dot<T, D>(qr + (int64_t)t * a.qs.row, kr), a.c, -st.x));
-                    if (t > 0 && !lone) ds = p * (row_dot<T, D>(dr + (int64_t)t * a.dys.row, vr) - st.y);
-                }
-                for (int u = 0; u < min(64, t_hi - base); ++u) {
-                    const float pu = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(p), u));
-                    const float su = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ds), u));
-#pragma unroll
-                    for (int k = 0; k < (D + 63) / 64; ++k)
-                        if (lane + 64 * k < D) {
-                            acc[0][k] = fmaf(su, widen(qr[(int64_t)(base + u) * a.qs.row + lane + 64 * k]), acc[0][k]);
-                            acc[1][k] = fmaf(pu, widen(dr[(int64_t)(base + u) * a.dys.row + lane + 64 * k]), acc[1][k]);
-                        }
-                }
-            }
-        }
-        const int64_t out = ((int64_t)b * a.L + jj) * a.kvheads * D + (int64_t)kvh * D;
-        float *qk = a.partials + ((((int64_t)b * a.kvheads + kvh) * (1 + a.nchunks) + part) * 2 * a.rows + jj) * D;
-#pragma unroll
-        for (int k = 0; k < (D + 63) / 64; ++k) {
-            const int e = lane + 64 * k;
-            if (e >= D) continue;
-            if (partial) {
-                qk[e] = acc[0][k] * a.scale;
-                qk[a.rows * D + e] = acc[1][k];
-            } else {
-                narrow(a.dk + out + e, acc[0][k] * a.scale);
-                narrow(a.dv + out + e, acc[1][k]);
-            }
+    uint32_t again = (uint32_t)__ballot(live && check != check);
+    if constexpr (G > 1) {
+        uint32_t *told = reinterpret_cast<uint32_t *>(lds + Lds::kTold) + wave % KW;
+        if (part_of == 0 && lane == 0) *told = again;
+        __syncthreads();
+        again = *told;
+    }
+    if (again != 0) {
+#pragma unroll 1
+        for (int db = part_of; db < DB; db += G) {
+            floatx16 x, z;
+            keys_again<T, D>(a, qb + kvh * group * a.qs.head, db_ + kvh * group * a.dys.head,
+                             a.stats + ((int64_t)b * a.heads + kvh * group) * a.L, group, kf, vf, w0, j, lo, hi, far, db, x, z);
+            write(db, x, z, 1.f, (again >> col & 1) != 0);
         }
     }
 }
@@ -539,7 +632,7 @@ hipError_t attn_bwd_sized(const AttnBwdIn<T> &in, int64_t batch, hipStream_t str
     const int64_t rows = batch * in.heads, qblocks = rows * ((in.L + kQueries - 1) / kQueries);
     hipError_t e;
     if (qblocks < kFewQueries) {
-        constexpr int kWaveLds = WaveLds<T, D>::kCopies;
+        constexpr int kWaveLds = WaveLds<T, D>::kCopies + 16;
         e = allow_lds<attn_dq_kernel<T, D, true>>(kWaveLds);
         if (e != hipSuccess) return e;
         attn_dq_kernel<T, D, true><<<dim3((uint32_t)(rows * ((in.L + 31) / 32))), dim3(64 * WaveLds<T, D>::kWaves), kWaveLds, stream>>>(in);

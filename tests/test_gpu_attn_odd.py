@@ -126,3 +126,75 @@ def test_a_diverged_forward_takes_some_times_a_sound_one(L, h, kv, d, dtype, whe
     sound = took(lambda: ssd.window_attention_fwd(q, k, v, 512, 4))
     v[:, where[1]] = where[2]
     assert took(lambda: ssd.window_attention_fwd(q, k, v, 512, 4)) <= 20 * sound
+
+
+def terms(q, k, v, dy, on, scale, g):
+    """P, and the gradients with their terms' magnitudes, in fp64; heads first.  What is not finite in dy, v counts as 0."""
+    q, dy = (x.double().transpose(1, 2) for x in (q, dy.nan_to_num(0, 0, 0)))
+    k, v = (x.double().repeat_interleave(g, 2).transpose(1, 2) for x in (k, v.nan_to_num(0, 0, 0)))
+    across = lambda x: x.transpose(2, 3).contiguous()  # noqa: E731
+    p = torch.softmax((q @ across(k) * scale).masked_fill(~on, -INF), -1)
+    dp, part = dy @ across(v), dy.abs() @ across(v.abs())
+    ds = scale * p * (dp - (p * dp).sum(-1, keepdim=True))
+    dsm = scale * p * (part + (p * part).sum(-1, keepdim=True))
+    share = lambda x: x.unflatten(1, (-1, g)).sum(2)  # noqa: E731
+    return p, dict(dq=ds @ k, dk=share(across(ds) @ q), dv=share(across(p) @ dy)), \
+        dict(dq=dsm @ k.abs(), dk=share(across(dsm) @ q.abs()), dv=share(across(p) @ dy.abs()))
+
+
+KINDS = ((1, INF), (34, -INF), (100, NAN), (130, INF), (131, -INF), (200, INF), (259, NAN))
+
+
+# few blocks and many
+@pytest.mark.parametrize("b", [1, 34])
+@pytest.mark.parametrize("d,dtype", [(32, "bf16"), (64, "bf16"), (128, "bf16"), (32, "f32"), (64, "f32"), (128, "f32")])
+@pytest.mark.parametrize("w,n", [(20, 3), (75, 0), (33, 40)])
+@pytest.mark.parametrize("which", ["dy", "v", "k", "q"])
+def test_backward_has_what_it_sees(which, b, d, dtype, w, n):
+    L, h, kv = 260, 4, 2
+    z = dict(zip(("q", "k", "v", "dy"), inputs(b, L, h, kv, d, dtype, 2)))
+    clean = {x: t.clone() for x, t in z.items()}
+    for at, kind in KINDS[3:] if which in "kq" else KINDS:
+        z[which][:, at, :, at % 7::5] = kind
+    y, lse = ssd.window_attention_fwd(z["q"], z["k"], z["v"], w, n, return_lse=True)
+    got = ssd.window_attention_bwd(z["q"], z["k"], z["v"], y, lse, z["dy"], w, n)
+    on = seen_by(0, L, w, n)
+    held = clean if which in "kq" else z
+    p, ref, mag = terms(held["q"], held["k"], held["v"], held["dy"], on, d ** -0.5, h // kv)
+    odd = torch.zeros(L, dtype=torch.bool, device="cuda")
+    odd[[at for at, _ in (KINDS[3:] if which in "kq" else KINDS)]] = True
+    rows = (on & odd).any(1) if which in "kv" else odd  # queries whose weights or dP are not finite
+    keys = (on & rows[:, None]).any(0)  # keys that such a query sees
+    e, r = spread(clean["q"], clean["k"], d ** -0.5, min(w, L) + n), ROUND[dtype]
+    for name in ref:
+        out = got[name].transpose(1, 2).double()
+        m = 1 if name == "dv" else 4
+        bound = m * (e + r) * mag[name] + (r + EPS) * ref[name].abs()
+        if name == "dv" and which in ("dy", "v"):
+            # P is sound: each element has the kinds that its key sees, and no others
+            want = ref[name]
+            if which == "dy":
+                both = apart(p.transpose(2, 3).contiguous(), z["dy"].double().transpose(1, 2)).unflatten(1, (kv, -1)).sum(2)
+                want = torch.where(both.isfinite(), want, both)
+            assert same(out, want, bound)
+            continue
+        sel = ~(rows if name == "dq" else keys)
+        assert bool(sel.any()) or name != "dq"
+        assert bool(((out - ref[name]).abs() <= bound)[:, :, sel].all()), name
+        # and the others are as far from sound as the input is
+        assert not bool(out[:, :, ~sel].isfinite().all()), name
+
+
+@pytest.mark.parametrize("L,h,kv,d,dtype", [(4096, 32, 8, 64, "bf16"), (4096, 16, 4, 128, "bf16"), (2048, 16, 8, 64, "f32"), (1024, 4, 1, 128, "bf16")])
+@pytest.mark.parametrize("which", ["q", "k", "v", "dy"])
+@pytest.mark.parametrize("where", [ODD[0], ODD[3]], ids=lambda o: "%s_%s" % (o[0], o[2]))
+def test_a_diverged_backward_takes_some_times_a_sound_one(L, h, kv, d, dtype, which, where):
+    z = dict(zip(("q", "k", "v", "dy"), inputs(1, L, h, kv, d, dtype)))
+
+    def time():
+        y, lse = ssd.window_attention_fwd(z["q"], z["k"], z["v"], 512, 4, return_lse=True)
+        return took(lambda: ssd.window_attention_bwd(z["q"], z["k"], z["v"], y, lse, z["dy"], 512, 4))
+
+    sound = time()
+    z[which][:, where[1]] = where[2]
+    assert time() <= 40 * sound
