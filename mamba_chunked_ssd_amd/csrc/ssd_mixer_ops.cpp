@@ -15,8 +15,6 @@
 
 namespace ssd {
 
-constexpr int64_t kStepTurns = 9;
-
 AttnBwdPlan attn_bwd_plan(const AttnArgs &a) {
     AttnBwdPlan p{};
     const int far = a.seqlen - a.window;  // queries that see token 0 as a sink only
@@ -31,14 +29,53 @@ AttnBwdPlan attn_bwd_plan(const AttnArgs &a) {
     return p;
 }
 
-// A block for all slots where that is a few turns of its waves, of 32 slots each:
-// a split takes a second launch and a workspace, some 5 us of the host's time.
-// One sequence, 8 heads of 64, 2052 slots (9 turns of eight waves, bf16): a call
-// 10.9 us, its kernel 10.5; in 17 blocks 15.1, its two kernels 5.3 and 4.3.
+// One block walks all slots of a sequence and head of keys, or several blocks do
+// and a second kernel joins them.  Times of one block and of several, us on the
+// device (many calls in a captured graph) and, from Python, a call:
+//   bf16 heads of 64, 8 walks:    6 turns  9.1, 8.6 and 11.3, 15.2
+//     (a turn is 256 slots)       9       11.6, 8.1     12.2, 15.4
+//                                12       14.5, 8.7     14.8, 15.2
+//                                24       24.2, 9.1     24.7, 15.1
+//     64 walks                   16       18.7, 17.6    18.6, 17.6
+//     128 walks                  24       32.0, 35.8    31.9, 35.5
+//   bf16 heads of 128, 8 walks:   8       12.6, 7.7     13.1, 15.1
+//     (128 slots)                12       16.7, 9.1     17.1, 15.2
+//   bf16 heads of 32, 8 walks:   12       11.4, 8.0     11.9, 15.2
+//   fp32 heads of 128, 8 walks:   2       13.8, 11.5    14.4, 15.3
+//     (64 slots)                  4       22.9, 11.8    23.4, 15.3
+//     128 walks                   4       24.1, 18.9    24.2, 19.1
+//   fp32 heads of 64, 8 walks:    4       14.0, 9.3     14.5, 15.5
+// So a turn takes kTurnUs, a walk is not faster than memory (kBytesPerUs, caches
+// that the last-level cache holds), and several blocks cost 3 us of the device's
+// time and 4 more of the host's: kSplitUs lies where what a captured graph loses by
+// one block and what a call from Python loses by several are alike.
+constexpr float kTurnUs[2][3] = {{0.67f, 0.83f, 0.97f}, {2.2f, 2.4f, 4.45f}};  // bf16, fp32: heads of 32, 64, 128
+constexpr float kSplitUs = 6.7f, kBytesPerUs = 8e6f;
+// A block takes a compute unit's LDS, so that blocks run in rounds of 256 (128 walks, fp32 heads of 64, 12 turns: 256
+// blocks 26.8 us, 512 32.5, 1024 36.3; 384 walks, fp32 heads of 128, 128 turns: 384 blocks, two rounds, 1167 us, 768 of
+// half the turns, three rounds, 895).
+constexpr int64_t kStepBlocks = 256, kStepRounds = 4;
+
 AttnStepPlan attn_step_plan(const AttnArgs &a) {
-    const int64_t slots = (int64_t)a.window + a.sinks, turn = 32 * attn_step_waves(a.headdim, a.bf16 ? 2 : 4);
-    const int64_t units = std::max<int64_t>(1, a.batch * a.kvheads), turns = (slots + turn - 1) / turn;
-    const int64_t splits = turns <= kStepTurns ? 1 : std::min<int64_t>(turns, std::max<int64_t>(1, 1024 / units));
+    const int64_t esz = a.bf16 ? 2 : 4, slots = (int64_t)a.window + a.sinks, turn = 32 * attn_step_waves(a.headdim, (int)esz);
+    const int64_t turns = (slots + turn - 1) / turn;
+    // sequences, heads of keys, and blocks of 32 heads that share one
+    const int64_t walks = std::max<int64_t>(1, a.batch * a.kvheads * ((a.heads / a.kvheads + 31) / 32));
+    const float us = kTurnUs[a.bf16 ? 0 : 1][a.headdim / 64];
+    const float least = (float)walks * (float)turns * (float)(turn * 2 * a.headdim * esz) / kBytesPerUs;
+    const auto walk = [&](int64_t n) {
+        const int64_t rounds = (walks * n + kStepBlocks - 1) / kStepBlocks, each = (turns + n - 1) / n;
+        return std::max((float)rounds * (float)each * us, least);
+    };
+    int64_t splits = 1;
+    float best = walk(1) - kSplitUs;
+    for (int64_t rounds = 1; rounds <= kStepRounds; ++rounds) {
+        const int64_t n = std::min(turns, rounds * kStepBlocks / walks);
+        if (n > 1 && walk(n) < best) {
+            best = walk(n);
+            splits = n;
+        }
+    }
     const int64_t run = (turns + splits - 1) / splits * turn;
     return AttnStepPlan{(int)((slots + run - 1) / run), (int)run};
 }
