@@ -416,6 +416,24 @@ struct WaveLds {
     static constexpr int kBytes = kCopies > kResults ? kCopies : kResults;
 };
 
+// Blocks of 128 queries up to which the waves of a block share 32 of them instead:
+// about what the compute units hold at once of those blocks (four for one of 128),
+// and twice as many where the window covers the sequence, whose blocks of 128 are
+// unlike one another.  One sequence, 8 heads over 2, 4 sinks, us of the forward
+// pass by 128 and by 32, and what 32 change in the backward pass:
+//   bf16 heads of 32, window 128: 192 blocks 10, 9, 0; 384 blocks 12, 14, +4
+//     of 64:  128 blocks 11, 10, 0; 160 blocks 11, 16, +6; all tokens: 256 blocks 71, 66, -3; 320 blocks 95, 96, +9
+//     of 128: 64 blocks 14, 13, -5; 96 blocks 14, 23, +5; all tokens: 128 blocks 54, 50, -9; 160 blocks 66, 82, +6
+//   fp32 heads of 32, window 128: 192 blocks 20, 18, 0; 224 blocks 20, 21, +4
+//     of 64:  128 blocks 29, 24, -8; 160 blocks 29, 35, +7; all tokens: 192 blocks 244, 190, -56; 256 blocks 326, 324, +19
+//     of 128: 64 blocks 52, 28, -42; 96 blocks 52, 53, -15; all tokens: 128 blocks 321, 298, -21; 160 blocks 402, 533, +187
+// (windows of 16 and 512 cross where 128 does, within a step of 32 blocks.)
+template <typename T, int D>
+inline bool few_queries(int64_t blocks, int seqlen, int window) {
+    constexpr int64_t most = D == 128 ? 64 : D == 64 ? 128 : sizeof(T) == 2 ? 320 : 192;
+    return blocks <= (window >= seqlen ? 2 * most : most);
+}
+
 // A result whose columns are rows of memory: lane l's column is row l % 32, its
 // values the elements 32 b + 8 (r / 4) + 4 (l / 32) + r % 4 of it.  Lanes l and l
 // + 32 exchange halves, so that each stores whole pieces of eight.

@@ -33,13 +33,21 @@ namespace ssd {
 namespace {
 
 constexpr int kQueries = 128;
-// Fewer blocks of 128 queries, or of 128 keys, than these: blocks of 32.  Keys, the
-// whole backward pass, bf16 heads of 64 over a window of 512: 64 blocks 90 us, of 32
-// keys 76; 128 blocks 111 and 124 (heads of 128: 259 and 289).  fp32, a window of 256:
-// 128 blocks 99 and 83, 256 blocks 114 and 139.  Queries: as in the forward pass.
-constexpr int64_t kFewQueries = 160;
-template <typename T>
-constexpr int64_t kFewKeys = sizeof(T) == 2 ? 100 : 200;
+// Blocks of 128 keys up to which blocks of 32 are taken, twice as many where the
+// window covers the sequence.  One sequence, 16 heads over 8, 4 sinks, us of the
+// backward pass by 128 and by 32:
+//   bf16 heads of 32, window 512: 128 blocks 47, 42; 160 blocks 47, 48; all tokens: 256 blocks 156, 144; 320 blocks 181, 189
+//     of 64:  128 blocks 59, 53; 160 blocks 60, 63; all tokens: 256 blocks 203, 196; 320 blocks 243, 266
+//     of 128: 96 blocks 92, 80; 128 blocks 95, 93 (window 128: 62, 72); all tokens: 192 blocks 284, 240; 320 blocks 447, 511
+//   fp32 heads of 32, window 128: 192 blocks 95, 85; 224 blocks 96, 99; all tokens: 384 blocks 1124, 1093
+//     of 64:  160 blocks 162, 159; 224 blocks 165, 188; all tokens: 320 blocks 1779, 1661; 384 blocks 2155, 2247
+//     of 128: 96 blocks 266, 209; 128 blocks 270, 256; 160 blocks 342, 364; all tokens: 192 blocks 2182, 2055; 256 blocks
+//             2980, 3223
+template <typename T, int D>
+inline bool few_keys(int64_t blocks, int seqlen, int window) {
+    constexpr int64_t most = sizeof(T) == 2 ? (D == 128 ? 96 : 128) : (D == 128 ? 112 : 192);
+    return blocks <= (window >= seqlen ? 2 * most : most);
+}
 
 template <typename T>
 struct AttnBwdIn {
@@ -631,7 +639,7 @@ hipError_t attn_bwd_sized(const AttnBwdIn<T> &in, int64_t batch, hipStream_t str
     // fewer blocks of 128 than compute units: blocks of 32, whose waves share them and part the rest
     const int64_t rows = batch * in.heads, qblocks = rows * ((in.L + kQueries - 1) / kQueries);
     hipError_t e;
-    if (qblocks < kFewQueries) {
+    if (few_queries<T, D>(qblocks, in.L, in.window)) {
         constexpr int kWaveLds = WaveLds<T, D>::kCopies + 16;
         e = allow_lds<attn_dq_kernel<T, D, true>>(kWaveLds);
         if (e != hipSuccess) return e;
@@ -645,7 +653,7 @@ hipError_t attn_bwd_sized(const AttnBwdIn<T> &in, int64_t batch, hipStream_t str
     const int64_t heads = batch * in.kvheads;
     const int64_t blocks = heads * ((in.L + 127) / 128);
     const int64_t chunks = heads * in.sink_tiles * in.nchunks;
-    if (blocks < kFewKeys<T>) {
+    if (few_keys<T, D>(blocks, in.L, in.window)) {
         // blocks of 32 keys, whose waves share them and part the queries; the sinks' among them
         e = attn_dkv_launch<T, D, 1, GS, 1, Part::both>(in, heads * ((in.L + 31) / 32) + chunks, stream);
     } else {

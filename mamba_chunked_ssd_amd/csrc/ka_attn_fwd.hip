@@ -24,10 +24,6 @@ namespace ssd {
 namespace {
 
 constexpr int kQueries = 128;  // of a block
-// Fewer blocks of 128 queries than this: the waves of a block share 32.  8 heads
-// of 64 over 2, a window of 512: 128 blocks 21.3 us, shared 18.1; 256 blocks 22.8,
-// shared 27.3.  fp32, a window of 256: 128 blocks 39 and 32, 256 blocks 42 and 59.
-constexpr int64_t kAttnShared = 160;
 
 template <typename T>
 struct AttnIn {
@@ -376,7 +372,7 @@ __global__ __launch_bounds__(256) void attn_put_kernel(const AttnIn<T> a, int D,
 template <typename T, int D>
 hipError_t attn_fwd_sized(const AttnIn<T> &in, int64_t batch, hipStream_t stream) {
     const int64_t blocks = batch * in.heads * ((in.L + kQueries - 1) / kQueries);
-    if (blocks < kAttnShared) {
+    if (few_queries<T, D>(blocks, in.L, in.window)) {
         constexpr int kLds = WaveLds<T, D>::kBytes + 32 * (int)sizeof(float2) + 16;
         const hipError_t e = allow_lds<attn_fwd_shared_kernel<T, D>>(kLds);
         if (e != hipSuccess) return e;
