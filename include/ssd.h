@@ -597,8 +597,7 @@ ssd_status ssd_selective_scan_step(const ssd_selective_shape *shape, const void 
  * 16-byte aligned (lse, positions, lengths 4); batch x nheads x (seqlen / 32 + 4)
  * must stay below 2^25.  Products of bf16
  * inputs run on the matrix cores with fp32 sums; the weights p and the
- * gradients of the scores are rounded to bf16 as operands of the next product
- * (one token's step: the weights to 16 bits, where its time is memory's),
+ * gradients of the scores are rounded to bf16 as operands of the next product,
  * never the softmax's maxima and sums.  Products of fp32 inputs are fp32.
  * ------------------------------------------------------------------------- */
 typedef struct {

@@ -56,11 +56,6 @@ __device__ __forceinline__ void to_frag(const float (&p)[8], Frag<float> &f) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) f.v[i] = p[i];
 }
-// What to_frag has rounded off, as an operand of its own (bf16: the two hold 16 bits).
-__device__ __forceinline__ void rest_frag(const float (&p)[8], const Frag<uint16_t> &f, Frag<uint16_t> &rest) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) rest.v[i] = pack_bf16(p[2 * i] - bf16lo(f.v[i]), p[2 * i + 1] - bf16hi(f.v[i]));
-}
 
 // Eight consecutive elements from memory (16-byte aligned), or 0.
 __device__ __forceinline__ void load_frag(Frag<uint16_t> &f, const uint16_t *p, bool on) {
@@ -266,9 +261,8 @@ struct Running {
         for (int db = 0; db < DB; ++db) o[db] = zero16();
     }
     __device__ float ref() const { return m == -kInf ? 0.f : m; }
-    // Scores of 32 KB keys (-infinity: not seen), whose values are rows r0 .. of the tile at v.  FINE: bf16 weights as
-    // two operands, of 16 bits together.
-    template <typename Tl, int KB, bool FINE = false>
+    // Scores of 32 KB keys (-infinity: not seen), whose values are rows r0 .. of the tile at v.
+    template <typename Tl, int KB>
     __device__ void take(const floatx16 (&s)[KB], float c, const unsigned char *v, int r0, int lane) {
         float top = s[0][0];
 #pragma unroll
@@ -309,12 +303,6 @@ struct Running {
             group_end();
 #pragma unroll
             for (int db = 0; db < DB; ++db) o[db] = mma(vf[step & 1][db], pf, o[db]);
-            if constexpr (FINE && sizeof(T) == 2) {
-                Frag<T> rest;
-                rest_frag(p, pf, rest);
-#pragma unroll
-                for (int db = 0; db < DB; ++db) o[db] = mma(vf[step & 1][db], rest, o[db]);
-            }
         }
     }
 };

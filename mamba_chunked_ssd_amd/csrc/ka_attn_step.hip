@@ -11,10 +11,11 @@
 // LDS, with its own running maximum and sum; the waves' results are joined in
 // LDS, and where few sequences leave compute units idle, so that a sequence's
 // slots are split over blocks, those of the blocks by a second kernel.
-// bf16 weights enter their product as two operands, of 16 bits together, and the
-// result is the plain form's to its rounding: 1.7e-3 from 64 bits, with weights of
-// 8 bits 2.4e-3.  A batch of heads of 64 or 128 takes the same time by either, heads
-// of 32 up to 6 % more by two, one sequence's walk over 2052 slots 10.8 us for 9.4.
+//
+// bf16 weights are rounded to 8 bits for their product, as over prompts.  In two
+// operands, 16 bits together (and once more in one where a value is infinite, of
+// which the second operand makes NaN), one sequence's 2052 slots took 11.4 us for
+// 9.4, 128 walks over 1024 slots of heads of 128 16.2 for 13.9.
 //
 // Measured: 128 sequences, 40 heads of 64 over 8, 2052 slots 77.6 us, 5.8 TB/s (a
 // large copy: 5.1); one sequence 10.5 us.
@@ -120,7 +121,7 @@ __global__ __launch_bounds__((64 * StepLds<T, D>::kWaves), 1) void attn_step_ker
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[0][r] = place(0, r) < s1 - at - 4 * h ? s[0][r] : -kInf;
         }
-        run.template take<Tl, 1, true>(s, a.c, vl, 0, lane);
+        run.template take<Tl, 1>(s, a.c, vl, 0, lane);
     }
     Join<T, D, NW>::run(lds, run, wave, lane, nh, [&](int c, int d, float y, float m, float l) {
         const int64_t head = (int64_t)b * a.heads + head0 + c;
