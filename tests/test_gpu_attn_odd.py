@@ -101,6 +101,26 @@ def test_forward_from_a_cache(b, d, dtype, w, n):
     assert same(y.transpose(1, 2), want, (e + r) * mag + r * want.abs())
 
 
+# one block for a cache and several; several tokens, so that the cache's own odd values and new ones are met
+@pytest.mark.parametrize("b,h,kv,d,dtype,w,n", [(3, 4, 2, 64, "bf16", 40, 3), (2, 8, 8, 128, "bf16", 300, 0), (4, 40, 1, 32, "bf16", 90, 2),
+                                                (1, 8, 2, 64, "bf16", 6000, 4), (3, 6, 2, 64, "f32", 50, 3), (1, 4, 2, 128, "f32", 3000, 4)])
+def test_step_has_what_it_sees(b, h, kv, d, dtype, w, n):
+    q, k, v, _ = inputs(b, w + n + 4, h, kv, d, dtype, 3)
+    for at, kind in ((0, INF), (1, -INF), (w // 2, NAN), (w // 2 + 1, INF), (w + n - 1, -INF), (w + n + 1, INF), (w + n + 2, NAN)):
+        v[:, at, :, at % 7::9] = kind
+    kc, vc = (torch.zeros((b, kv, w + n, d), dtype=TYPES[dtype], device="cuda") for _ in range(2))
+    ssd.window_attention_fwd(q[:, :-4], k[:, :-4], v[:, :-4], w, n, k_cache=kc, v_cache=vc)
+    pos = torch.full((b,), w + n, dtype=torch.int32, device="cuda")
+    e, r = spread(q, k, d ** -0.5, w + n), ROUND[dtype]
+    for t in range(w + n, w + n + 4):
+        y = ssd.window_attention_step(q[:, t], k[:, t], v[:, t], kc, vc, pos, w, n)
+        pos += 1
+        kk, vv = (x.double().repeat_interleave(h // kv, 1) for x in (kc, vc))
+        p = torch.softmax((kk * q[:, t].double()[:, :, None]).sum(-1) * d ** -0.5, -1)[:, :, None]
+        want, mag = apart(p, vv)[:, :, 0], (p @ vv.nan_to_num(0, 0, 0).abs())[:, :, 0]
+        assert same(y, want, (e + r) * mag + r * want.abs())
+
+
 def took(call):
     for _ in range(2):
         call()
