@@ -35,15 +35,15 @@ AttnBwdPlan attn_bwd_plan(const AttnArgs &a) {
 // One block walks all slots of a sequence and head of keys, or several blocks do
 // and a second kernel joins them.  Times of one block and of several, us on the
 // device (many calls in a captured graph) and, from Python, a call:
-//   bf16 heads of 64, 8 walks:    6 turns  9.1, 8.6 and 11.3, 15.2
-//     (a turn is 256 slots)       9       11.6, 8.1     12.2, 15.4
-//                                12       14.5, 8.7     14.8, 15.2
-//                                24       24.2, 9.1     24.7, 15.1
-//     64 walks                   16       18.7, 17.6    18.6, 17.6
-//     128 walks                  24       32.0, 35.8    31.9, 35.5
-//   bf16 heads of 128, 8 walks:   8       12.6, 7.7     13.1, 15.1
-//     (128 slots)                12       16.7, 9.1     17.1, 15.2
-//   bf16 heads of 32, 8 walks:   12       11.4, 8.0     11.9, 15.2
+//   bf16 heads of 64, 8 walks:    6 turns  8.0, 8.7 and 11.3, 15.7
+//     (a turn is 256 slots)       9       10.0, 7.8     11.6, 15.4
+//                                12       12.0, 8.6     12.6, 15.1
+//                                24       20.2, 8.7     20.8, 15.2
+//     64 walks                   32       27.3, 26.9    27.4, 26.8
+//     128 walks                  24       31.0, 34.5    31.0, 34.4
+//   bf16 heads of 128, 8 walks:   8       11.8, 7.7     12.4, 15.4
+//     (128 slots)                12       15.4, 9.0     16.0, 15.4
+//   bf16 heads of 32, 8 walks:   14       10.8, 8.8     11.4, 15.4
 //   fp32 heads of 128, 8 walks:   2       13.8, 11.5    14.4, 15.3
 //     (64 slots)                  4       22.9, 11.8    23.4, 15.3
 //     128 walks                   4       24.1, 18.9    24.2, 19.1
@@ -52,7 +52,7 @@ AttnBwdPlan attn_bwd_plan(const AttnArgs &a) {
 // that the last-level cache holds), and several blocks cost 3 us of the device's
 // time and 4 more of the host's: kSplitUs lies where what a captured graph loses by
 // one block and what a call from Python loses by several are alike.
-constexpr float kTurnUs[2][3] = {{0.67f, 0.83f, 0.97f}, {2.2f, 2.4f, 4.45f}};  // bf16, fp32: heads of 32, 64, 128
+constexpr float kTurnUs[2][3] = {{0.52f, 0.67f, 0.88f}, {2.2f, 2.4f, 4.45f}};  // bf16, fp32: heads of 32, 64, 128
 constexpr float kSplitUs = 6.7f, kBytesPerUs = 8e6f;
 // A block takes a compute unit's LDS, so that blocks run in rounds of 256 (128 walks, fp32 heads of 64, 12 turns: 256
 // blocks 26.8 us, 512 32.5, 1024 36.3; 384 walks, fp32 heads of 128, 128 turns: 384 blocks, two rounds, 1167 us, 768 of
