@@ -611,7 +611,7 @@ typedef struct {
     int64_t headdim;       /* supported 32, 64, 128 */
     int64_t window;        /* >= 1; seqlen or more without a cache: every earlier token */
     int64_t sinks;         /* >= 0 */
-    float scale;           /* > 0 and finite, usually headdim^-1/2 */
+    float scale;           /* > 0, below 2.3e38 (times log2(e) finite), usually headdim^-1/2 */
     int32_t dtype;         /* ssd_dtype of q, k, v, y, their gradients and the cache */
     int32_t reserved[2];   /* must be 0 */
     ssd_head_stride q, k, v, y, dy; /* (y, dy: inputs of the backward pass) */

@@ -136,7 +136,8 @@ ssd_status check_attn(const ssd_attn_shape *s, bool cached, AttnArgs *a, AttnByt
         s->sinks < 0 || s->reserved[0] != 0 || s->reserved[1] != 0)
         return SSD_ERROR_INVALID_VALUE;
     if (s->nheads % s->nkvheads != 0 || !dtype_ok(s->dtype)) return SSD_ERROR_INVALID_VALUE;
-    if (!(s->scale > 0.f) || !std::isfinite(s->scale)) return SSD_ERROR_INVALID_VALUE;
+    // (the kernels multiply scores by scale log2(e))
+    if (!(s->scale > 0.f) || !std::isfinite(s->scale * 1.4426950408889634f)) return SSD_ERROR_INVALID_VALUE;
     if (s->headdim != 32 && s->headdim != 64 && s->headdim != 128) return SSD_ERROR_UNSUPPORTED;
     if (s->batch > 65535 || s->seqlen > kMaxLen || s->nheads > 65535) return SSD_ERROR_UNSUPPORTED;
     if (cached && (s->window > kMaxLen || s->sinks > kMaxLen || s->window + s->sinks > kMaxLen))
