@@ -1061,6 +1061,9 @@ def _attn_args(q, k, v, window, sinks, scale, lead, torch):
     if len(dims) != lead + 2 or len(of_k) != lead + 2:
         raise ValueError("q must be (batch, %snheads, headdim) and k (batch, %snkvheads, headdim)"
                          % (("seqlen, ",) * 2 if lead == 2 else ("", "")))
+    for name, n in (("window", window), ("sinks", sinks)):
+        if n is not None and not -1 << 63 <= n < 1 << 63:  # (ctypes would drop the bits above)
+            raise ValueError("%s must fit 64 bits" % name)
     dev, dtype, b, h, d, kv = q.device, q.dtype, dims[0], dims[-2], dims[-1], of_k[-2]
     L = dims[1] if lead == 2 else 1
     shape = AttnShape(b, L, h, kv, d, max(L, 1) if window is None else window, sinks, d ** -0.5 if scale is None else scale,

@@ -30,3 +30,18 @@ def test_scale_times_log2_e(lib, scale, ok):
         a = [(1 << 44) + (i << 36) for i in range(5)]
         st = lib.ssd_window_attn_fwd(ctypes.byref(shape), a[0], a[1], a[2], None, None, None, None, a[3], a[4], None)
         assert st == INVALID
+
+
+@pytest.mark.gpu
+def test_window_and_sinks_beyond_64_bits():
+    q = torch.randn((1, 20, 2, 32), device="cuda")
+    k = torch.randn((1, 20, 1, 32), device="cuda")
+    want = ssd.window_attention_fwd(q, k, k)
+    assert torch.equal(ssd.window_attention_fwd(q, k, k, (1 << 63) - 1), want)
+    for kw in (dict(window=(1 << 64) + 5), dict(window=1 << 63), dict(window=5, sinks=(1 << 64) + 2), dict(window=-(1 << 64) + 5)):
+        with pytest.raises(ValueError, match="64 bits"):
+            ssd.window_attention_fwd(q, k, k, **kw)
+    kc = torch.zeros((1, 1, 5, 32), device="cuda")
+    at = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="64 bits"):
+        ssd.window_attention_step(q[:, 0], k[:, 0], k[:, 0], kc, kc.clone(), at, (1 << 64) + 5)
