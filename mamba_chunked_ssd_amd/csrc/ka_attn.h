@@ -106,11 +106,6 @@ __device__ __forceinline__ float both_halves(float x) {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
-__device__ __forceinline__ float wave_sum(float v) {
-    v = lane_total<16>(v);
-    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return both_halves(__uint_as_float(s[0]) + __uint_as_float(s[1]));
-}
 
 // ROWS rows of D elements in LDS, in pieces of 16 bytes.  A row's pieces are
 // permuted by an exclusive or with bits of the row's number, so that the reads
@@ -161,7 +156,6 @@ struct Tile {
     // Filled through registers, row r from row(r), null: 0.
     template <int THREADS, typename F>
     __device__ static void gather(unsigned char *lds, F &&row) {
-        
 #pragma unroll 2
         for (int k = 0; k < (kBytes / 16 + THREADS - 1) / THREADS; ++k) {
             const int n = k * THREADS + (int)threadIdx.x % THREADS;
@@ -261,9 +255,9 @@ struct Running {
         for (int db = 0; db < DB; ++db) o[db] = zero16();
     }
     __device__ float ref() const { return m == -kInf ? 0.f : m; }
-    // Scores of 32 KB keys (-infinity: not seen), whose values are rows r0 .. of the tile at v.
+    // Scores of 32 KB keys (-infinity: not seen), whose values are the rows of the tile at v.
     template <typename Tl, int KB>
-    __device__ void take(const floatx16 (&s)[KB], float c, const unsigned char *v, int r0, int lane) {
+    __device__ void take(const floatx16 (&s)[KB], float c, const unsigned char *v, int lane) {
         float top = s[0][0];
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
@@ -286,7 +280,7 @@ struct Running {
         Frag<T> vf[2][DB];
         const auto read = [&](int step) {
 #pragma unroll
-            for (int db = 0; db < DB; ++db) Tl::across(v, r0 + 16 * step, 32 * db, lane, vf[step & 1][db]);
+            for (int db = 0; db < DB; ++db) Tl::across(v, 16 * step, 32 * db, lane, vf[step & 1][db]);
         };
         read(0);
 #pragma unroll

@@ -240,7 +240,7 @@ __global__ __launch_bounds__(256, (sizeof(T) == 2 ? (D == 32 ? 4 : D == 64 ? 3 :
         const bool whole = n < walk.nsink ? j0 + KT <= walk.sunk
                                           : j0 >= 0 && j0 + KT - 1 <= w0 && (w0 + 31 - j0 < a.window || j0 + KT <= a.sinks);
         if (!whole) hide(s, walk, n, j0, t, w0, h, a.window, a.sinks);
-        run.template take<Tl, KB>(s, a.c, vl, 0, lane);
+        run.template take<Tl, KB>(s, a.c, vl, lane);
     }
     if (w0 - p.first >= a.L) return;  // (no barrier follows)
 
@@ -323,7 +323,7 @@ __global__ __launch_bounds__((64 * WaveLds<T, D>::kWaves), 1) void attn_fwd_shar
         const bool whole = n < walk.nsink ? j0 + 32 <= walk.sunk
                                           : j0 >= 0 && j0 + 31 <= t0 && (t0 + 31 - j0 < a.window || j0 + 32 <= a.sinks);
         if (!whole) hide(s, walk, n, j0, t, t0, h, a.window, a.sinks);
-        run.template take<Tl, 1>(s, a.c, kl + Tl::kBytes, 0, lane);
+        run.template take<Tl, 1>(s, a.c, kl + Tl::kBytes, lane);
     }
     if (threadIdx.x == 0) again = 0;  // (Join's barriers come before its use)
     Join<T, D, NW>::run(lds, run, wave, lane, columns, [&](int c, int d, float y, float m, float l) {

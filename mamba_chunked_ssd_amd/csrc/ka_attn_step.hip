@@ -121,7 +121,7 @@ __global__ __launch_bounds__((64 * StepLds<T, D>::kWaves), 1) void attn_step_ker
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[0][r] = place(0, r) < s1 - at - 4 * h ? s[0][r] : -kInf;
         }
-        run.template take<Tl, 1>(s, a.c, vl, 0, lane);
+        run.template take<Tl, 1>(s, a.c, vl, lane);
     }
     Join<T, D, NW>::run(lds, run, wave, lane, nh, [&](int c, int d, float y, float m, float l) {
         const int64_t head = (int64_t)b * a.heads + head0 + c;
