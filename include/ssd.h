@@ -672,7 +672,8 @@ ssd_status ssd_window_attn_step(const ssd_attn_shape *shape, const void *q, cons
  * row, or of each scale_block consecutive columns of it (the last may be
  * shorter), scale = max(m / 448, 2^-126) and the code e4m3(y_c / scale), rounded
  * to nearest even.  A NaN among them makes the scale NaN.  Sums of squares that
- * leave fp32's range (|u| from about 1e18) give r = 0.
+ * leave fp32's range (|u| from about 1e18) give r = 0; with eps 0, squares lose
+ * bits where |u| is below about 1e-19, and a row of zeros gives NaN.
  * The conventions of the operators above hold; pointers need their element
  * type's alignment only.  batch x seqlen must stay below 2^31.
  * ------------------------------------------------------------------------- */

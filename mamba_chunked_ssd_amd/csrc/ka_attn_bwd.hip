@@ -16,9 +16,10 @@
 // seen by every later query of the sequence too: those are cut into chunks, a
 // block each, and their sums added by a third kernel.
 //
-// 2 x 2048 tokens, 40 heads of 64 over 8, a window of 512, 4 sinks, bf16: 55 us over
-// the queries, 64 over the keys, 8 and 4 for the sinks, 125 the call (378 TFLOP/s of
-// 10 products of headdim a pair of tokens); the 14 that two kernels form could only be
+// 2 x 2048 tokens, 40 heads of 64 over 8, a window of 512, 4 sinks, bf16: the call 124
+// to 129 us (up to 382 TFLOP/s of 10 products of headdim a pair of tokens); under a
+// kernel trace, which slows them, 54 us over the queries, 64 over the keys, 15 and 5
+// for the sinks.  The 14 products that two kernels form could only be
 // 10 with dq, or dk and dv, added up in memory.  Matrix instructions take 22 and 25 % of
 // that time, vector ones 34 and 29 %: the rest is the waves' waiting, for LDS reads and
 // for each other at the tiles' barriers (three or four tiles on their way instead of
