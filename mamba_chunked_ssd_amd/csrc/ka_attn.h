@@ -282,6 +282,7 @@ struct Running {
         const float from = ref();
         // 16 keys at a time: their values are read while the weights of those before them are formed
         constexpr int kSteps = 2 * KB;
+        float sum;  // of the tile's weights: the running sum takes one term a tile
         Frag<T> vf[2][DB];
         const auto read = [&](int step) {
 #pragma unroll
@@ -295,7 +296,7 @@ struct Running {
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
                 p[r] = fast_exp2(fmaf(s[step / 2][8 * (step % 2) + r], c, -from));
-                l += p[r];
+                sum = step + r == 0 ? p[0] : sum + p[r];
             }
             Frag<T> pf;
             to_frag(p, pf);
@@ -303,6 +304,7 @@ struct Running {
 #pragma unroll
             for (int db = 0; db < DB; ++db) o[db] = mma(vf[step & 1][db], pf, o[db]);
         }
+        l += sum;
     }
 };
 
