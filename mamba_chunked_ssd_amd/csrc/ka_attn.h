@@ -417,10 +417,19 @@ struct WaveLds {
 //     of 64:  128 blocks 29, 24, -8; 160 blocks 29, 35, +7; all tokens: 192 blocks 244, 190, -56; 256 blocks 326, 324, +19
 //     of 128: 64 blocks 52, 28, -42; 96 blocks 52, 53, -15; all tokens: 128 blocks 321, 298, -21; 160 blocks 402, 533, +187
 // (windows of 16 and 512 cross where 128 does, within a step of 32 blocks.)
+// Tokens with a past all have a window behind them, so that its length plays no
+// part.  512 tokens a sequence behind a window of 2048, the forward pass:
+//   bf16 heads of 32: 256 blocks 61, 53; 320 blocks 70, 74
+//     of 64:  128 blocks 85, 66; 160 blocks 88, 114     of 128: 64 blocks 133, 106; 96 blocks 139, 197
+//   fp32 heads of 32: 128 blocks 144, 94; 160 blocks 148, 167
+//     of 64:  96 blocks 256, 250 (256 behind 4096: 64 blocks 478, 256; 96 blocks 549, 604)
+//     of 128: 64 blocks 490, 469; 96 blocks 555, 1018
 template <typename T, int D>
-inline bool few_queries(int64_t blocks, int seqlen, int window) {
-    constexpr int64_t most = D == 128 ? 64 : D == 64 ? 128 : sizeof(T) == 2 ? 320 : 192;
-    return blocks <= (window >= seqlen ? 2 * most : most);
+inline bool few_queries(int64_t blocks, int seqlen, int window, bool past) {
+    constexpr bool bf16 = sizeof(T) == 2;
+    constexpr int64_t most = D == 128 ? 64 : D == 64 ? 128 : bf16 ? 320 : 192;
+    constexpr int64_t most_past = D == 128 ? 64 : D == 64 ? (bf16 ? 128 : 64) : bf16 ? 256 : 128;
+    return blocks <= (past ? most_past : window >= seqlen ? 2 * most : most);
 }
 
 // A result whose columns are rows of memory: lane l's column is row l % 32, its

@@ -640,7 +640,7 @@ hipError_t attn_bwd_sized(const AttnBwdIn<T> &in, int64_t batch, hipStream_t str
     // fewer blocks of 128 than compute units: blocks of 32, whose waves share them and part the rest
     const int64_t rows = batch * in.heads, qblocks = rows * ((in.L + kQueries - 1) / kQueries);
     hipError_t e;
-    if (few_queries<T, D>(qblocks, in.L, in.window)) {
+    if (few_queries<T, D>(qblocks, in.L, in.window, false)) {
         constexpr int kWaveLds = WaveLds<T, D>::kCopies + 16;
         e = allow_lds<attn_dq_kernel<T, D, true>>(kWaveLds);
         if (e != hipSuccess) return e;

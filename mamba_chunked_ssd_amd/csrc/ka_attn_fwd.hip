@@ -372,7 +372,7 @@ __global__ __launch_bounds__(256) void attn_put_kernel(const AttnIn<T> a, int D,
 template <typename T, int D>
 hipError_t attn_fwd_sized(const AttnIn<T> &in, int64_t batch, hipStream_t stream) {
     const int64_t blocks = batch * in.heads * ((in.L + kQueries - 1) / kQueries);
-    if (few_queries<T, D>(blocks, in.L, in.window)) {
+    if (few_queries<T, D>(blocks, in.L, in.window, in.positions != nullptr)) {
         constexpr int kLds = WaveLds<T, D>::kBytes + 32 * (int)sizeof(float2) + 16;
         const hipError_t e = allow_lds<attn_fwd_shared_kernel<T, D>>(kLds);
         if (e != hipSuccess) return e;
