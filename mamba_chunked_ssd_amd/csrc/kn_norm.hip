@@ -7,7 +7,7 @@
 // vector operations, so a row stays in registers between its sum and its
 // output.  Up to 4096 channels a wave holds a row, eight channels a lane and
 // piece, and sums by lane moves alone; up to 16384 a block of four waves does,
-// through LDS once a row; longer rows are read twice (the second time from the
+// through LDS once a row (twice with a scale for the row); longer rows are read twice (the second time from the
 // caches).  Rows need no alignment: the loads of 16 bytes are unaligned ones
 // where they must be, and only a row's last channels (channels mod 8) come one
 // by one.
